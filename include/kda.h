@@ -358,6 +358,90 @@ kda_status kda_linear(int32_t M, int32_t N, int32_t K, const void *x, const void
                       int32_t ysplit, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The gated delta rule: the mixer's recurrence with one decay per head instead of one per
+ * channel, without the convolution and the output norm (the delta rule is that of the kimi_k3.c
+ * header, "KDA per-head recurrence"; the pages have no counterpart with a scalar decay). Per
+ * token and value head h, with key head h / (H / Hk) and state S[key][value] in FP32:
+ *   alpha = exp(-exp(A_log[h]) softplus(a + dt_bias[h])),  beta = sigmoid(b)
+ *   k^ = k / sqrt(|k|^2 + l2_eps),  q^ = q_scale q / sqrt(|q|^2 + l2_eps)
+ *                                   (qk_l2norm == 0: k^ = k, q^ = q_scale q)
+ *   S = alpha S;  u = beta (v - S^T k^);  S = S + k^ u^T;  out = S^T q^
+ * -inf and very negative decay logits are allowed (alpha = 1), as are those that make alpha 0.
+ *
+ * States are caller-owned: S device FP32 [max_slots][H][d][d], 16-byte aligned (the S part of a
+ * kda_state's slots, without the conv history). A call reads row r's state from slot
+ * src_slots[r] (-1: a zero state, nothing is read) and writes it to dst_slots[r], which may be
+ * the same slot; another slot forks the sequence and keeps the old state, so that rejected draft
+ * tokens are taken back by reading the old slot again. Within a call the dst slots must be
+ * distinct, and no row's dst may be another row's src.
+ *   src_slots, dst_slots  device int32. A row with an id out of range is skipped (its out rows
+ *                         and slots keep their contents) and KDA_ERR_DEVICE is recorded.
+ *   err     device int32 word or NULL. Receives KDA_ERR_DEVICE (a bad slot id, or a cu_seqlens
+ *           that disagrees with cu_seqlens_host; the call then leaves out and S as they are) or
+ *           KDA_ERR_TIMEOUT (a bounded wait gave up). Never cleared by the library.
+ */
+typedef struct {
+    int32_t num_heads;     /* H value heads, a multiple of num_qk_heads, <= 65536 */
+    int32_t num_qk_heads;  /* Hk key heads */
+    int32_t head_dim;      /* d; this build supports 128 */
+    int32_t io_dtype;      /* kda_dtype of q, k, v, a, b, out */
+    int32_t qk_l2norm;     /* default 1 */
+    float l2_eps;          /* default 1e-6, inside the sqrt */
+    float q_scale;         /* default d^-1/2 */
+} kda_gdr_config_t;
+
+/* Per-layer parameters, device FP32 [H] each, caller-owned. */
+typedef struct {
+    const float *A_log;
+    const float *dt_bias;
+} kda_gdr_params;
+
+/*
+ * The per-token rows, device io_dtype, with the distance between tokens in elements (so that
+ * they may be columns of one projection's output):
+ *   q, k [.][Hk*d]   v, out [.][H*d]   a, b [.][H]
+ * q, k, v and out: 16-byte aligned, the stride a multiple of 16 bytes; a and b: element-aligned.
+ * A stride is at least its row's width (it is not used with one token). out must not overlap an
+ * input.
+ */
+typedef struct {
+    const void *q, *k, *v, *a, *b;
+    void *out;
+    int64_t q_stride, k_stride, v_stride, a_stride, b_stride, out_stride;
+} kda_gdr_rows;
+
+/* Fill *cfg with the defaults. KDA_ERR_INVALID (cfg untouched) for cfg == NULL or an unsupported geometry. */
+kda_status kda_gdr_config(kda_gdr_config_t *cfg, int32_t num_heads, int32_t num_qk_heads, int32_t head_dim,
+                          int32_t io_dtype);
+
+/*
+ * n consecutive tokens (1 .. KDA_DECODE_MAX_TOKENS) for each of B sequences, token by token; token
+ * t of sequence r is row r*n + t. B == 0 is a no-op. Errors: KDA_ERR_INVALID, KDA_ERR_CUDA.
+ */
+kda_status kda_gdr_decode(const kda_gdr_config_t *cfg, const kda_gdr_params *params, float *S, int32_t max_slots,
+                          const int32_t *src_slots, const int32_t *dst_slots, int32_t B, int32_t n,
+                          const kda_gdr_rows *rows, int32_t *err, void *stream);
+
+/*
+ * N sequences packed along the token axis; cu_seqlens (device int32 [N+1]) and cu_seqlens_host as
+ * for kda_prefill. An empty sequence copies its src state (or zeros) to its dst. With BF16 rows
+ * the tokens are taken in chunks of 64 on the tensor cores, with the state, its updates and all
+ * sums held in FP32; with FP32 rows they are taken one by one in FP32. Nothing outside the rows
+ * [0, cu[N]) of out is written.
+ *   workspace  device scratch of at least kda_gdr_workspace_bytes(cfg, cu_seqlens_host, N) bytes,
+ *              16-byte aligned, caller-owned (25.6 KB per chunk and value head; with FP32 rows it is
+ *              not touched). Calls that share one must be ordered, captured graphs that are replayed
+ *              at the same time need one each. The query returns 0 for invalid arguments and does
+ *              not touch the device.
+ * Errors: KDA_ERR_INVALID, KDA_ERR_CUDA.
+ */
+size_t kda_gdr_workspace_bytes(const kda_gdr_config_t *cfg, const int32_t *cu_seqlens_host, int32_t N);
+kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *params, float *S, int32_t max_slots,
+                           const int32_t *src_slots, const int32_t *dst_slots, const int32_t *cu_seqlens,
+                           const int32_t *cu_seqlens_host, int32_t N, const kda_gdr_rows *rows, void *workspace,
+                           size_t workspace_bytes, int32_t *err, void *stream);
+
+/*
  * Recurrent-state photos (kimi_k3.c header, the COLI_K3_CKPT and
  * COLI_K3_CKPT_DIR serve options). A store keeps up to `capacity` photos of
  * one sequence slot across a stack of KDA layers (one kda_state per layer),

@@ -1,0 +1,371 @@
+// kda_gdr.cu - the gated delta rule, token by token (decode, and prefill of FP32 rows), and the
+// host side of its entry points.
+//
+// One warp owns 16 value columns of one (row, head) state: columns of S do not interact, so a warp
+// runs its tokens alone, with no barrier and no shared memory. Lane (rg, cg) = (lane / 4, lane % 4)
+// holds the 16 key rows 16 rg .. 16 rg + 15 of the 4 columns 4 cg .. 4 cg + 3 in registers from the
+// first token to the last. With the raw k, q and the scalars rk = 1 / sqrt(|k|^2 + eps),
+// rq = q_scale / sqrt(|q|^2 + eps) a token is
+//   p = S^T k, r = S^T q                       8 partial sums a lane, added over rg by halving exchanges
+//   u = beta (v - alpha rk p)
+//   o = rq (alpha r + rk (k . q) u),  S = alpha S + k (rk u)^T
+// so that the normalised vectors are never formed.
+#include <climits>
+#include <cstdarg>
+#include <cstdio>
+
+#include "kda_gdr.cuh"
+
+namespace kda {
+namespace gdr {
+namespace {
+
+constexpr int kRecWarps = 4;  // warps a block: half of one (row, head)
+
+// 16 consecutive elements as FP32
+template <typename T> struct Vec16;
+template <> struct Vec16<__nv_bfloat16> {
+    uint4 r[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
+    {
+        r[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+        r[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float (&f)[16]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+                f[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+        }
+    }
+};
+template <> struct Vec16<float> {
+    float4 r[4];
+    __device__ __forceinline__ void load(const float *p)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = __ldg(reinterpret_cast<const float4 *>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&f)[16]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[4 * i] = r[i].x; f[4 * i + 1] = r[i].y; f[4 * i + 2] = r[i].z; f[4 * i + 3] = r[i].w;
+        }
+    }
+};
+
+template <typename T>
+struct Token {
+    Vec16<T> k, q;
+    float v, a, b;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kRecWarps)
+gdr_recurrent_kernel(const __grid_constant__ Args p, int64_t n_units)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * kRecWarps + (threadIdx.x >> 5);  // (row, head, 16 columns)
+    if (unit >= n_units) return;
+    const int cb = (int)(unit & 7);
+    const int64_t rh = unit >> 3;
+    const int h = (int)(rh % p.H), row = (int)(rh / p.H);
+    const int rg = lane >> 2, cg = lane & 3, c = rg & 3;
+    int src, dst;
+    if (!slots_ok(p, row, src, dst)) {
+        if (lane == 0) set_err(p.err);
+        return;
+    }
+    int64_t t0 = (int64_t)row * p.n, t1 = t0 + p.n;
+    if (p.cu) {
+        t0 = __ldg(p.cu + row);
+        t1 = __ldg(p.cu + row + 1);
+        if (t0 < 0 || t1 < t0 || t1 > p.total_T) {
+            if (lane == 0) set_err(p.err);
+            return;
+        }
+    }
+    const size_t at = (size_t)(16 * rg) * kD + 16 * cb + 4 * cg;
+    float4 s[16];
+    if (src >= 0) {
+        const float *S = p.S + ((size_t)src * p.H + h) * kD * kD + at;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = ld_stream(reinterpret_cast<const float4 *>(S + i * kD));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int hk = h / p.G, col = 16 * cb + 4 * cg + c;
+    const float expA = expf(__ldg(p.A_log + h)), dt_bias = __ldg(p.dt_bias + h);
+    const T *kp = static_cast<const T *>(p.rows.k) + (size_t)hk * kD + 16 * rg;
+    const T *qp = static_cast<const T *>(p.rows.q) + (size_t)hk * kD + 16 * rg;
+    const T *vp = static_cast<const T *>(p.rows.v) + (size_t)h * kD + col;
+    const T *ap = static_cast<const T *>(p.rows.a) + h;
+    const T *bp = static_cast<const T *>(p.rows.b) + h;
+    T *op = static_cast<T *>(p.rows.out) + (size_t)h * kD + col;
+    auto load = [&](int64_t t, Token<T> &x) {
+        x.k.load(kp + t * p.rows.k_stride);
+        x.q.load(qp + t * p.rows.q_stride);
+        x.v = IO<T>::ld(vp + t * p.rows.v_stride);
+        x.a = IO<T>::ld(ap + t * p.rows.a_stride);
+        x.b = IO<T>::ld(bp + t * p.rows.b_stride);
+    };
+    Token<T> next;
+    if (t0 < t1) load(t0, next);
+#pragma unroll 1
+    for (int64_t t = t0; t < t1; ++t) {
+        float k[16], q[16];
+        next.k.get(k);
+        next.q.get(q);
+        const float v = next.v;
+        const float alpha = expf(log_decay(next.a, dt_bias, expA)), beta = sigmoidf_(next.b);
+        if (t + 1 < t1) load(t + 1, next);
+        // |k|^2, |q|^2, k.q: the 16 rows of this lane, then over rg (lane bits 2..4)
+        float2 kk2 = make_float2(0.f, 0.f), qq2 = kk2, kq2 = kk2;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float2 k2 = make_float2(k[i], k[i + 1]), q2 = make_float2(q[i], q[i + 1]);
+            kk2 = f2_fma(k2, k2, kk2);
+            qq2 = f2_fma(q2, q2, qq2);
+            kq2 = f2_fma(k2, q2, kq2);
+        }
+        float kk = kk2.x + kk2.y, qq = qq2.x + qq2.y, kq = kq2.x + kq2.y;
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+            kk += __shfl_xor_sync(0xFFFFFFFFu, kk, o);
+            qq += __shfl_xor_sync(0xFFFFFFFFu, qq, o);
+            kq += __shfl_xor_sync(0xFFFFFFFFu, kq, o);
+        }
+        const float rk = p.l2norm ? rsqrtf(kk + p.l2_eps) : 1.f;
+        const float rq = p.l2norm ? p.q_scale * rsqrtf(qq + p.l2_eps) : p.q_scale;
+        float2 p01 = make_float2(0.f, 0.f), p23 = p01, r01 = p01, r23 = p01;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 k2 = make_float2(k[i], k[i]), q2 = make_float2(q[i], q[i]);
+            const float2 s01 = make_float2(s[i].x, s[i].y), s23 = make_float2(s[i].z, s[i].w);
+            p01 = f2_fma(k2, s01, p01);
+            p23 = f2_fma(k2, s23, p23);
+            r01 = f2_fma(q2, s01, r01);
+            r23 = f2_fma(q2, s23, r23);
+        }
+        // halving exchanges over rg: lane bit 4 keeps p (0) or r (1), bits 3 and 2 pick the column c = rg & 3
+        const bool hi = lane & 16, b3 = lane & 8, b2 = lane & 4;
+        float x0 = hi ? r01.x : p01.x, x1 = hi ? r01.y : p01.y, x2 = hi ? r23.x : p23.x, x3 = hi ? r23.y : p23.y;
+        x0 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p01.x : r01.x, 16);
+        x1 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p01.y : r01.y, 16);
+        x2 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p23.x : r23.x, 16);
+        x3 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p23.y : r23.y, 16);
+        float y0 = b3 ? x2 : x0, y1 = b3 ? x3 : x1;
+        y0 += __shfl_xor_sync(0xFFFFFFFFu, b3 ? x0 : x2, 8);
+        y1 += __shfl_xor_sync(0xFFFFFFFFu, b3 ? x1 : x3, 8);
+        float z = b2 ? y1 : y0;
+        z += __shfl_xor_sync(0xFFFFFFFFu, b2 ? y0 : y1, 4);
+        const float z2 = __shfl_xor_sync(0xFFFFFFFFu, z, 16);
+        const float ps = hi ? z2 : z, rs = hi ? z : z2;
+        const float u = beta * fmaf(-alpha * rk, ps, v);
+        const float o = rq * fmaf(rk * kq, u, alpha * rs);
+        if (!hi) IO<T>::st(op + t * p.rows.out_stride, o);
+        const float w = rk * u;  // of column c; this lane updates its columns 0 .. 3
+        const float w0 = __shfl_sync(0xFFFFFFFFu, w, cg), w1 = __shfl_sync(0xFFFFFFFFu, w, cg + 4);
+        const float w2 = __shfl_sync(0xFFFFFFFFu, w, cg + 8), w3 = __shfl_sync(0xFFFFFFFFu, w, cg + 12);
+        const float2 w01 = make_float2(w0, w1), w23 = make_float2(w2, w3), al = make_float2(alpha, alpha);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 k2 = make_float2(k[i], k[i]);
+            const float2 s01 = f2_fma(k2, w01, f2_mul(al, make_float2(s[i].x, s[i].y)));
+            const float2 s23 = f2_fma(k2, w23, f2_mul(al, make_float2(s[i].z, s[i].w)));
+            s[i] = make_float4(s01.x, s01.y, s23.x, s23.y);
+        }
+    }
+    float *D = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st_stream(reinterpret_cast<float4 *>(D + i * kD), s[i]);
+}
+
+thread_local char g_msg[256];
+
+kda_status fail(kda_status s, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+    va_end(ap);
+    return record_error(s, g_msg);
+}
+
+bool cfg_ok(const kda_gdr_config_t *c)
+{
+    if (!c) return fail(KDA_ERR_INVALID, "config is NULL"), false;
+    if (c->num_heads < 1 || c->num_qk_heads < 1 || c->num_heads % c->num_qk_heads != 0)
+        return fail(KDA_ERR_INVALID, "num_heads must be a positive multiple of num_qk_heads (got %d, %d)", c->num_heads,
+                    c->num_qk_heads), false;
+    if (c->num_heads > 65536) return fail(KDA_ERR_INVALID, "num_heads must be <= 65536 (got %d)", c->num_heads), false;
+    if (c->head_dim != kD) return fail(KDA_ERR_INVALID, "head_dim must be %d (got %d)", kD, c->head_dim), false;
+    if (c->io_dtype != KDA_F32 && c->io_dtype != KDA_BF16)
+        return fail(KDA_ERR_INVALID, "io_dtype must be KDA_F32 or KDA_BF16"), false;
+    if (c->qk_l2norm && !(c->l2_eps > 0.f && c->l2_eps < INFINITY))
+        return fail(KDA_ERR_INVALID, "l2_eps must be finite and > 0"), false;
+    if (!(fabsf(c->q_scale) < INFINITY)) return fail(KDA_ERR_INVALID, "q_scale must be finite"), false;
+    return true;
+}
+
+bool row_ok(const char *name, const void *ptr, int64_t stride, int64_t width, int64_t T, int esize, bool vec)
+{
+    if (!ptr) return fail(KDA_ERR_INVALID, "%s is NULL", name), false;
+    if (T > 1 && stride < width)
+        return fail(KDA_ERR_INVALID, "%s_stride must be >= %lld (got %lld)", name, (long long)width, (long long)stride), false;
+    if (stride < 0 || stride > ((int64_t)1 << 38))
+        return fail(KDA_ERR_INVALID, "%s_stride out of range (%lld)", name, (long long)stride), false;
+    const uintptr_t u = reinterpret_cast<uintptr_t>(ptr);
+    if (u % (vec ? 16 : esize)) return fail(KDA_ERR_INVALID, "%s must be %d-byte aligned", name, vec ? 16 : esize), false;
+    if (vec && (stride * esize) % 16)
+        return fail(KDA_ERR_INVALID, "%s_stride must be a multiple of %d elements (got %lld)", name, 16 / esize,
+                    (long long)stride), false;
+    return true;
+}
+
+// Everything but the token counts. T: rows of q, k, v, a, b and out.
+bool call_ok(const kda_gdr_config_t *c, const kda_gdr_params *prm, const float *S, int32_t max_slots,
+             const int32_t *src, const int32_t *dst, const kda_gdr_rows *r, int64_t T)
+{
+    if (!prm || !prm->A_log || !prm->dt_bias) return fail(KDA_ERR_INVALID, "params (or one of its pointers) is NULL"), false;
+    if (!S || (reinterpret_cast<uintptr_t>(S) & 15u)) return fail(KDA_ERR_INVALID, "S is NULL or not 16-byte aligned"), false;
+    if (max_slots < 1) return fail(KDA_ERR_INVALID, "max_slots must be >= 1 (got %d)", max_slots), false;
+    if (!src || !dst) return fail(KDA_ERR_INVALID, "src_slots or dst_slots is NULL"), false;
+    if (!r) return fail(KDA_ERR_INVALID, "rows is NULL"), false;
+    if (T == 0) return true;
+    const int e = c->io_dtype == KDA_BF16 ? 2 : 4;
+    const int64_t Dk = (int64_t)c->num_qk_heads * kD, Dv = (int64_t)c->num_heads * kD;
+    return row_ok("q", r->q, r->q_stride, Dk, T, e, true) && row_ok("k", r->k, r->k_stride, Dk, T, e, true) &&
+           row_ok("v", r->v, r->v_stride, Dv, T, e, true) && row_ok("a", r->a, r->a_stride, c->num_heads, T, e, false) &&
+           row_ok("b", r->b, r->b_stride, c->num_heads, T, e, false) && row_ok("out", r->out, r->out_stride, Dv, T, e, true);
+}
+
+Args make_args(const kda_gdr_config_t *c, const kda_gdr_params *prm, float *S, int32_t max_slots, const int32_t *src,
+               const int32_t *dst, int32_t N, const kda_gdr_rows *r, int32_t *err)
+{
+    Args p;
+    p.S = S; p.max_slots = max_slots; p.src = src; p.dst = dst; p.err = err;
+    p.cu = nullptr; p.N = N; p.n = 0; p.total_T = 0;
+    p.H = c->num_heads; p.G = c->num_heads / c->num_qk_heads;
+    p.A_log = prm->A_log; p.dt_bias = prm->dt_bias;
+    p.rows = *r;
+    p.l2norm = c->qk_l2norm != 0; p.l2_eps = c->l2_eps; p.q_scale = c->q_scale;
+    return p;
+}
+
+// host cu_seqlens: total chunks (or -1 with the error set)
+int64_t count_chunks(const int32_t *cu, int32_t N)
+{
+    if (cu[0] != 0) return fail(KDA_ERR_INVALID, "cu_seqlens[0] must be 0 (got %d)", cu[0]), -1;
+    int64_t n = 0;
+    for (int32_t i = 0; i < N; ++i) {
+        if (cu[i + 1] < cu[i]) return fail(KDA_ERR_INVALID, "cu_seqlens decreases at %d", i + 1), -1;
+        n += ((int64_t)cu[i + 1] - cu[i] + kC - 1) / kC;
+    }
+    return n;
+}
+
+}  // namespace
+
+cudaError_t launch_recurrent(const Args &p, bool f32, int64_t n_rows, cudaStream_t stream)
+{
+    const int64_t units = n_rows * p.H * (kD / 16);
+    const unsigned grid = (unsigned)((units + kRecWarps - 1) / kRecWarps);
+    if (f32) gdr_recurrent_kernel<float><<<grid, 32 * kRecWarps, 0, stream>>>(p, units);
+    else gdr_recurrent_kernel<__nv_bfloat16><<<grid, 32 * kRecWarps, 0, stream>>>(p, units);
+    return cudaGetLastError();
+}
+
+}  // namespace gdr
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+kda_status kda_gdr_config(kda_gdr_config_t *cfg, int32_t num_heads, int32_t num_qk_heads, int32_t head_dim,
+                          int32_t io_dtype)
+{
+    if (!cfg) return gdr::fail(KDA_ERR_INVALID, "cfg is NULL");
+    kda_gdr_config_t c;
+    c.num_heads = num_heads;
+    c.num_qk_heads = num_qk_heads;
+    c.head_dim = head_dim;
+    c.io_dtype = io_dtype;
+    c.qk_l2norm = 1;
+    c.l2_eps = 1e-6f;
+    c.q_scale = 0.08838834764831845f;  // 128^-1/2
+    if (!gdr::cfg_ok(&c)) return KDA_ERR_INVALID;
+    *cfg = c;
+    return KDA_OK;
+}
+
+kda_status kda_gdr_decode(const kda_gdr_config_t *cfg, const kda_gdr_params *params, float *S, int32_t max_slots,
+                          const int32_t *src_slots, const int32_t *dst_slots, int32_t B, int32_t n,
+                          const kda_gdr_rows *rows, int32_t *err, void *stream)
+{
+    if (!gdr::cfg_ok(cfg)) return KDA_ERR_INVALID;
+    if (B < 0) return gdr::fail(KDA_ERR_INVALID, "B must be >= 0 (got %d)", B);
+    if (n < 1 || n > KDA_DECODE_MAX_TOKENS)
+        return gdr::fail(KDA_ERR_INVALID, "n must be in 1 .. %d (got %d)", KDA_DECODE_MAX_TOKENS, n);
+    if (B == 0) return KDA_OK;
+    if ((int64_t)B * cfg->num_heads > INT_MAX / 8) return gdr::fail(KDA_ERR_INVALID, "B * num_heads is too large");
+    if (!gdr::call_ok(cfg, params, S, max_slots, src_slots, dst_slots, rows, (int64_t)B * n)) return KDA_ERR_INVALID;
+    gdr::Args p = gdr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, B, rows, err);
+    p.n = n;
+    p.total_T = (int64_t)B * n;
+    const cudaError_t e = gdr::launch_recurrent(p, cfg->io_dtype == KDA_F32, B, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : gdr::fail(KDA_ERR_CUDA, "kda_gdr_decode: %s", cudaGetErrorString(e));
+}
+
+size_t kda_gdr_workspace_bytes(const kda_gdr_config_t *cfg, const int32_t *cu_seqlens_host, int32_t N)
+{
+    if (!gdr::cfg_ok(cfg)) return 0;
+    if (N < 0 || (N > 0 && !cu_seqlens_host)) return gdr::fail(KDA_ERR_INVALID, "cu_seqlens_host is NULL or N < 0"), 0;
+    if (N == 0 || cfg->io_dtype == KDA_F32) return 256;
+    const int64_t nc = gdr::count_chunks(cu_seqlens_host, N);
+    return nc < 0 ? 0 : gdr::chunked_workspace_bytes(nc, cfg->num_heads);
+}
+
+kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *params, float *S, int32_t max_slots,
+                           const int32_t *src_slots, const int32_t *dst_slots, const int32_t *cu_seqlens,
+                           const int32_t *cu_seqlens_host, int32_t N, const kda_gdr_rows *rows, void *workspace,
+                           size_t workspace_bytes, int32_t *err, void *stream)
+{
+    if (!gdr::cfg_ok(cfg)) return KDA_ERR_INVALID;
+    if (N < 0) return gdr::fail(KDA_ERR_INVALID, "N must be >= 0 (got %d)", N);
+    if (N == 0) return KDA_OK;
+    if (!cu_seqlens || !cu_seqlens_host) return gdr::fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL");
+    if ((int64_t)N * cfg->num_heads > INT_MAX / 8) return gdr::fail(KDA_ERR_INVALID, "N * num_heads is too large");
+    const int64_t nc = gdr::count_chunks(cu_seqlens_host, N);
+    if (nc < 0) return KDA_ERR_INVALID;
+    if (nc * cfg->num_heads > INT_MAX / 8) return gdr::fail(KDA_ERR_INVALID, "chunks * num_heads is too large");
+    const int64_t T = cu_seqlens_host[N];
+    if (!gdr::call_ok(cfg, params, S, max_slots, src_slots, dst_slots, rows, T)) return KDA_ERR_INVALID;
+    gdr::Args p = gdr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, N, rows, err);
+    p.cu = cu_seqlens;
+    p.total_T = T;
+    cudaError_t e;
+    if (cfg->io_dtype == KDA_F32) {
+        e = gdr::launch_recurrent(p, true, N, static_cast<cudaStream_t>(stream));
+    } else {
+        const size_t need = gdr::chunked_workspace_bytes(nc, cfg->num_heads);
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need)
+            return gdr::fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed",
+                             workspace_bytes, need);
+        int dev = 0, sms = 0;
+        if ((e = cudaGetDevice(&dev)) == cudaSuccess &&
+            (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) == cudaSuccess)
+            e = gdr::launch_chunked(p, nc, workspace, sms, static_cast<cudaStream_t>(stream));
+    }
+    return e == cudaSuccess ? KDA_OK : gdr::fail(KDA_ERR_CUDA, "kda_gdr_prefill: %s", cudaGetErrorString(e));
+}
+
+}  // extern "C"

@@ -45,6 +45,21 @@ class kda_layer_params(ctypes.Structure):
                 ("A_log", ctypes.c_void_p), ("norm_w", ctypes.c_void_p)]
 
 
+class kda_gdr_config_t(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_qk_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("qk_l2norm", ctypes.c_int32), ("l2_eps", ctypes.c_float),
+                ("q_scale", ctypes.c_float)]
+
+
+class kda_gdr_params(ctypes.Structure):
+    _fields_ = [("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class kda_gdr_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "a", "b", "out")] + \
+        [(n + "_stride", ctypes.c_int64) for n in ("q", "k", "v", "a", "b", "out")]
+
+
 class kda_blob_header(ctypes.Structure):
     _fields_ = [("magic", ctypes.c_uint32), ("version", ctypes.c_uint32),
                 ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
@@ -87,6 +102,12 @@ SIGNATURES = [
                                       _PI32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
     ("kda_linear_workspace_bytes", ctypes.c_size_t, [_I32, _I32, _I32]),
     ("kda_linear", _I32, [_I32, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, ctypes.c_size_t, _VP]),
+    ("kda_gdr_config", _I32, [ctypes.POINTER(kda_gdr_config_t), _I32, _I32, _I32, _I32]),
+    ("kda_gdr_decode", _I32, [ctypes.POINTER(kda_gdr_config_t), ctypes.POINTER(kda_gdr_params), _VP, _I32, _VP, _VP,
+                              _I32, _I32, ctypes.POINTER(kda_gdr_rows), _VP, _VP]),
+    ("kda_gdr_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(kda_gdr_config_t), _PI32, _I32]),
+    ("kda_gdr_prefill", _I32, [ctypes.POINTER(kda_gdr_config_t), ctypes.POINTER(kda_gdr_params), _VP, _I32, _VP, _VP,
+                               _VP, _PI32, _I32, ctypes.POINTER(kda_gdr_rows), _VP, ctypes.c_size_t, _VP, _VP]),
     ("kda_photo_store_create", _I32, [_I32, ctypes.c_char_p, ctypes.POINTER(_VP)]),
     ("kda_photo_store_free", _I32, [_VP]),
     ("kda_photo_count", _I32, [_VP]),
@@ -372,6 +393,88 @@ def kda_linear(x, w, y, workspace: torch.Tensor, r=None, ysplit: int = 0, stream
                             _VP(None) if r is None else _dev(r, bf, "r"), _dev(y, bf, "y"), int(ysplit),
                             _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
                             _stream(stream)))
+
+
+def kda_gdr_config(num_heads: int, num_qk_heads: int | None = None, head_dim: int = 128,
+                   io_dtype: int = KDA_BF16) -> kda_gdr_config_t:
+    cfg = kda_gdr_config_t()
+    _check(lib().kda_gdr_config(ctypes.byref(cfg), num_heads, num_heads if num_qk_heads is None else num_qk_heads,
+                                head_dim, io_dtype))
+    return cfg
+
+
+def kda_gdr_params_from(A_log: torch.Tensor, dt_bias: torch.Tensor) -> kda_gdr_params:
+    if A_log.shape != dt_bias.shape or A_log.dim() != 1:
+        raise ValueError("A_log and dt_bias must both be [H]")
+    p = kda_gdr_params(_dev(A_log, torch.float32, "A_log"), _dev(dt_bias, torch.float32, "dt_bias"))
+    p._keep = (A_log, dt_bias)
+    return p
+
+
+def _gdr_args(cfg, params, S, src_slots, dst_slots, T, q, k, v, a, b, out, err):
+    """Checked rows, slots and states of a gated delta rule call, and T, the tokens of each row tensor."""
+    H, Hk, d = cfg.num_heads, cfg.num_qk_heads, cfg.head_dim
+    dt = _torch_io_dtype(cfg)
+    dev = torch.cuda.current_device()
+    if S.dim() != 4 or tuple(S.shape[1:]) != (H, d, d):
+        raise ValueError(f"S must be [max_slots, {H}, {d}, {d}], got {tuple(S.shape)}")
+    if params._keep[0].numel() != H:
+        raise ValueError(f"A_log and dt_bias must hold {H} elements")
+    if src_slots.numel() != dst_slots.numel():
+        raise ValueError("src_slots and dst_slots must have the same length")
+    r = kda_gdr_rows()
+    for name, t, width in (("q", q, Hk * d), ("k", k, Hk * d), ("v", v, H * d), ("a", a, H), ("b", b, H),
+                           ("out", out, H * d)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dt:
+            raise TypeError(f"{name} must be a CUDA tensor of {dt}")
+        if tuple(t.shape) != (T, width):
+            raise ValueError(f"{name} must be [{T}, {width}], got {tuple(t.shape)}")
+        if T > 0 and t.stride(1) != 1 and width > 1:
+            raise ValueError(f"{name} must be contiguous within a token")
+        setattr(r, name, t.data_ptr())
+        setattr(r, name + "_stride", t.stride(0) if T > 1 else width)
+    for t in (S, src_slots, dst_slots, q, k, v, a, b, out, *params._keep, *(() if err is None else (err,))):
+        if t.is_cuda and t.device.index != dev:
+            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on {t.device}")
+    return (_dev(S, torch.float32, "S"), int(S.shape[0]), _dev(src_slots, torch.int32, "src_slots"),
+            _dev(dst_slots, torch.int32, "dst_slots"), r, _VP(None) if err is None else _dev(err, torch.int32, "err"))
+
+
+def kda_gdr_decode(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tensor, src_slots: torch.Tensor,
+                   dst_slots: torch.Tensor, n: int, q, k, v, a, b, out, err=None, stream=None) -> None:
+    """n tokens for each row: q, k [B n, Hk d], v, out [B n, H d], a, b [B n, H], contiguous within a
+    token; S FP32 [max_slots, H, d, d], read at src_slots (-1: zeros) and written at dst_slots."""
+    B = int(src_slots.numel())
+    Sp, slots, sp, dp, r, ep = _gdr_args(cfg, params, S, src_slots, dst_slots, B * int(n), q, k, v, a, b, out, err)
+    _check(lib().kda_gdr_decode(ctypes.byref(cfg), ctypes.byref(params), Sp, slots, sp, dp, B, int(n), ctypes.byref(r),
+                                ep, _stream(stream)))
+
+
+def kda_gdr_workspace_bytes(cfg: kda_gdr_config_t, cu_seqlens_host) -> int:
+    cu_h, cu_p = _host_i32(cu_seqlens_host)
+    need = int(lib().kda_gdr_workspace_bytes(ctypes.byref(cfg), cu_p, len(cu_h) - 1))
+    if need == 0:
+        raise KdaError(KDA_ERR_INVALID, kda_last_error())
+    return need
+
+
+def kda_gdr_prefill(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tensor, src_slots: torch.Tensor,
+                    dst_slots: torch.Tensor, cu_seqlens: torch.Tensor, cu_seqlens_host, q, k, v, a, b, out,
+                    workspace: torch.Tensor, err=None, stream=None) -> None:
+    """Packed sequences, rows as in kda_gdr_decode with T = cu_seqlens[-1]; workspace of at least
+    kda_gdr_workspace_bytes(cfg, cu_seqlens_host) bytes."""
+    N = int(src_slots.numel())
+    cu_h, cu_p = _host_i32(cu_seqlens_host)
+    if len(cu_h) != N + 1 or cu_seqlens.numel() != N + 1:
+        raise ValueError("cu_seqlens must hold N + 1 entries")
+    Sp, slots, sp, dp, r, ep = _gdr_args(cfg, params, S, src_slots, dst_slots, int(cu_h[-1]), q, k, v, a, b, out, err)
+    for t in (cu_seqlens, workspace):
+        if t.is_cuda and t.device != S.device:
+            raise ValueError(f"every tensor must be on {S.device}, got one on {t.device}")
+    _check(lib().kda_gdr_prefill(ctypes.byref(cfg), ctypes.byref(params), Sp, slots, sp, dp,
+                                 _dev(cu_seqlens, torch.int32, "cu_seqlens"), cu_p, N, ctypes.byref(r),
+                                 _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size(), ep,
+                                 _stream(stream)))
 
 
 def _layers(layers):
