@@ -358,6 +358,39 @@ kda_status kda_linear(int32_t M, int32_t N, int32_t K, const void *x, const void
                       int32_t ysplit, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The dense projections in 8-bit floating point (E4M3), with one FP32 scale for each group of 128
+ * columns: of one row for activations (block_rows 1), of 128 rows for weights (block_rows 128). It is
+ * kda_linear's product for weights of half the bytes (the pages keep 8- and 4-bit weights with
+ * group scales for their CPU products: kimi_k3.c, w_load).
+ *
+ * kda_quant_fp8: the operands from BF16 or FP32. Per group s = 2^e with e the smallest integer (>= -126)
+ * for which every finite |x| <= 448 s (s = 1 when all are 0), q = x / s rounded to the nearest E4M3
+ * (ties to even; x / s is exact, so one rounding). NaN and infinities become NaN and do not set s.
+ *   M, K      rows and columns; M >= 0 (0 is a no-op), K a multiple of 16 (a last group may be short)
+ *   x         device x_dtype [M], rows x_stride elements apart, 16-byte aligned, x_stride a multiple of
+ *             16 bytes and >= K (not used when M == 1)
+ *   q         device E4M3 [M][K], 16-byte aligned      out
+ *   s         device FP32 [ceil(M / block_rows)][ceil(K / 128)]      out
+ * kda_linear_fp8: y = x W^T (+ r) in BF16, each block's product accumulated in FP32 on the tensor cores,
+ * scaled by xs * ws and added in FP32, in the blocks' order. The scales may be any FP32 numbers.
+ *   M, N, K   as for kda_linear, with N a multiple of 8 and K a multiple of 16
+ *   xq, xs    device E4M3 [M][K], FP32 [M][ceil(K / 128)]
+ *   wq, ws    device E4M3 [N][K], FP32 [ceil(N / 128)][ceil(K / 128)]
+ *   r, y, ysplit   as for kda_linear (a ysplit other than 0 and N: a multiple of 128 that divides N)
+ *   workspace device scratch of at least kda_linear_fp8_workspace_bytes(M, N, K) bytes (query with the
+ *             call's device current; 0 for invalid arguments), 16-byte aligned. Its first int32 is set to
+ *             KDA_ERR_TIMEOUT if a bounded wait gave up and never cleared: zero it once before use. Calls
+ *             that share a workspace must be ordered.
+ * xq, wq, r and y 16-byte aligned. Results do not depend on timing. Errors: KDA_ERR_INVALID, KDA_ERR_CUDA.
+ */
+kda_status kda_quant_fp8(int64_t M, int32_t K, const void *x, int64_t x_stride, int32_t x_dtype, int32_t block_rows,
+                         void *q, float *s, void *stream);
+size_t kda_linear_fp8_workspace_bytes(int32_t M, int32_t N, int32_t K);
+kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void *xq, const float *xs, const void *wq,
+                          const float *ws, const void *r, void *y, int32_t ysplit, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
  * The gated delta rule: the mixer's recurrence with one decay per head instead of one per
  * channel, without the convolution and the output norm (the delta rule is that of the kimi_k3.c
  * header, "KDA per-head recurrence"; the pages have no counterpart with a scalar decay). Per

@@ -102,6 +102,9 @@ SIGNATURES = [
                                       _PI32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
     ("kda_linear_workspace_bytes", ctypes.c_size_t, [_I32, _I32, _I32]),
     ("kda_linear", _I32, [_I32, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, ctypes.c_size_t, _VP]),
+    ("kda_quant_fp8", _I32, [ctypes.c_int64, _I32, _VP, ctypes.c_int64, _I32, _I32, _VP, _VP, _VP]),
+    ("kda_linear_fp8_workspace_bytes", ctypes.c_size_t, [_I32, _I32, _I32]),
+    ("kda_linear_fp8", _I32, [_I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, ctypes.c_size_t, _VP]),
     ("kda_gdr_config", _I32, [ctypes.POINTER(kda_gdr_config_t), _I32, _I32, _I32, _I32]),
     ("kda_gdr_decode", _I32, [ctypes.POINTER(kda_gdr_config_t), ctypes.POINTER(kda_gdr_params), _VP, _I32, _VP, _VP,
                               _I32, _I32, ctypes.POINTER(kda_gdr_rows), _VP, _VP]),
@@ -395,6 +398,59 @@ def kda_linear(x, w, y, workspace: torch.Tensor, r=None, ysplit: int = 0, stream
                             _stream(stream)))
 
 
+def _same_device(*tensors) -> None:
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on {t.device}")
+
+
+def kda_quant_fp8(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, block_rows: int = 1, stream=None) -> None:
+    """q [M, K] (float8_e4m3fn) and s [ceil(M / block_rows), ceil(K / 128)] (FP32) from x [M, K] (BF16 or
+    FP32, contiguous within a row): one power-of-two scale for each 1 x 128 or 128 x 128 block."""
+    if x.dim() != 2 or not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be a CUDA tensor [M, K] of bfloat16 or float32")
+    M, K = int(x.shape[0]), int(x.shape[1])
+    if M > 0 and K > 1 and x.stride(1) != 1:
+        raise ValueError("x must be contiguous within a row")
+    rows = int(block_rows)
+    if rows < 1:
+        raise ValueError("block_rows must be 1 or 128")
+    if tuple(q.shape) != (M, K) or tuple(s.shape) != (-(-M // rows), -(-K // 128)):
+        raise ValueError(f"q must be [{M}, {K}] and s [{-(-M // rows)}, {-(-K // 128)}], got {tuple(q.shape)}, {tuple(s.shape)}")
+    _same_device(x, q, s)
+    _check(lib().kda_quant_fp8(M, K, _VP(x.data_ptr()), x.stride(0) if M > 1 else K,
+                               KDA_BF16 if x.dtype == torch.bfloat16 else KDA_F32, rows, _dev(q, torch.float8_e4m3fn, "q"),
+                               _dev(s, torch.float32, "s"), _stream(stream)))
+
+
+def kda_linear_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    need = int(lib().kda_linear_fp8_workspace_bytes(int(M), int(N), int(K)))
+    if need == 0:
+        raise KdaError(KDA_ERR_INVALID, kda_last_error())
+    return need
+
+
+def kda_linear_fp8(xq, xs, wq, ws, y, workspace: torch.Tensor, r=None, ysplit: int = 0, stream=None) -> None:
+    """y = x w^T (+ r) in BF16 from E4M3 xq [M, K], wq [N, K] and their scales xs [M, ceil(K / 128)],
+    ws [ceil(N / 128), ceil(K / 128)]; y [M, N] (or [N / ysplit, M, ysplit] with ysplit)."""
+    f8, bf = torch.float8_e4m3fn, torch.bfloat16
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError("xq must be [M, K] and wq [N, K]")
+    M, K = int(xq.shape[0]), int(xq.shape[1])
+    N = int(wq.shape[0])
+    if tuple(xs.shape) != (M, -(-K // 128)) or tuple(ws.shape) != (-(-N // 128), -(-K // 128)):
+        raise ValueError(f"xs must be [{M}, {-(-K // 128)}] and ws [{-(-N // 128)}, {-(-K // 128)}], "
+                         f"got {tuple(xs.shape)}, {tuple(ws.shape)}")
+    if y.numel() != M * N or (r is not None and r.numel() != M * N):
+        raise ValueError(f"y and r must hold {M} x {N} elements")
+    _same_device(xq, xs, wq, ws, y, r, workspace)
+    _check(lib().kda_linear_fp8(M, N, K, _dev(xq, f8, "xq"), _dev(xs, torch.float32, "xs"), _dev(wq, f8, "wq"),
+                                _dev(ws, torch.float32, "ws"), _VP(None) if r is None else _dev(r, bf, "r"),
+                                _dev(y, bf, "y"), int(ysplit), _dev(workspace, None, "workspace"),
+                                workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
 def kda_gdr_config(num_heads: int, num_qk_heads: int | None = None, head_dim: int = 128,
                    io_dtype: int = KDA_BF16) -> kda_gdr_config_t:
     cfg = kda_gdr_config_t()
@@ -415,7 +471,6 @@ def _gdr_args(cfg, params, S, src_slots, dst_slots, T, q, k, v, a, b, out, err):
     """Checked rows, slots and states of a gated delta rule call, and T, the tokens of each row tensor."""
     H, Hk, d = cfg.num_heads, cfg.num_qk_heads, cfg.head_dim
     dt = _torch_io_dtype(cfg)
-    dev = torch.cuda.current_device()
     if S.dim() != 4 or tuple(S.shape[1:]) != (H, d, d):
         raise ValueError(f"S must be [max_slots, {H}, {d}, {d}], got {tuple(S.shape)}")
     if params._keep[0].numel() != H:
@@ -433,9 +488,7 @@ def _gdr_args(cfg, params, S, src_slots, dst_slots, T, q, k, v, a, b, out, err):
             raise ValueError(f"{name} must be contiguous within a token")
         setattr(r, name, t.data_ptr())
         setattr(r, name + "_stride", t.stride(0) if T > 1 else width)
-    for t in (S, src_slots, dst_slots, q, k, v, a, b, out, *params._keep, *(() if err is None else (err,))):
-        if t.is_cuda and t.device.index != dev:
-            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on {t.device}")
+    _same_device(S, src_slots, dst_slots, q, k, v, a, b, out, err, *params._keep)
     return (_dev(S, torch.float32, "S"), int(S.shape[0]), _dev(src_slots, torch.int32, "src_slots"),
             _dev(dst_slots, torch.int32, "dst_slots"), r, _VP(None) if err is None else _dev(err, torch.int32, "err"))
 
@@ -468,9 +521,7 @@ def kda_gdr_prefill(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tens
     if len(cu_h) != N + 1 or cu_seqlens.numel() != N + 1:
         raise ValueError("cu_seqlens must hold N + 1 entries")
     Sp, slots, sp, dp, r, ep = _gdr_args(cfg, params, S, src_slots, dst_slots, int(cu_h[-1]), q, k, v, a, b, out, err)
-    for t in (cu_seqlens, workspace):
-        if t.is_cuda and t.device != S.device:
-            raise ValueError(f"every tensor must be on {S.device}, got one on {t.device}")
+    _same_device(cu_seqlens, workspace)
     _check(lib().kda_gdr_prefill(ctypes.byref(cfg), ctypes.byref(params), Sp, slots, sp, dp,
                                  _dev(cu_seqlens, torch.int32, "cu_seqlens"), cu_p, N, ctypes.byref(r),
                                  _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size(), ep,
