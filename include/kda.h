@@ -462,7 +462,7 @@ kda_status kda_gdr_decode(const kda_gdr_config_t *cfg, const kda_gdr_params *par
  * sums held in FP32; with FP32 rows they are taken one by one in FP32. Nothing outside the rows
  * [0, cu[N]) of out is written.
  *   workspace  device scratch of at least kda_gdr_workspace_bytes(cfg, cu_seqlens_host, N) bytes,
- *              16-byte aligned, caller-owned (25.6 KB per chunk and value head; with FP32 rows it is
+ *              16-byte aligned, caller-owned (25,856 bytes per chunk and value head; with FP32 rows it is
  *              not touched). Calls that share one must be ordered, captured graphs that are replayed
  *              at the same time need one each. The query returns 0 for invalid arguments and does
  *              not touch the device.

@@ -2,21 +2,21 @@
 // C = 64 tokens.
 //
 // With G the cumulative log decay inside a chunk (a scalar per token) and S0 the state before it,
-//   A[t][i] = beta_t (k^_t . k^_i) exp(G_t - G_i)  (i < t),   T = (I + A)^-1 Diag(beta)
-//   U = T (V - Diag(exp G) K^ S0)
+//   A[t][i] = beta_t (k^_t . k^_i) exp(G_t - G_i)  (i < t),   T = (I + A)^-1
+//   U = T Diag(beta) (V - Diag(exp G) K^ S0)
 //   O = Diag(exp G) Q^ S0 + P U,   P[t][i] = (q^_t . k^_i) exp(G_t - G_i)  (i <= t)
 //   S = exp(G_last) S0 + (Diag(exp(G_last - G)) K^)^T U
 // which is the token recurrence exactly in real arithmetic. Every exponent is <= 0.
 //
 // Two kernels:
 //   gdr_prep_kernel   per (chunk, key head): the products K K^T and Q K^T once, then for each of its
-//                     value heads the decays, A, its inverse by forward substitution, and one block of
-//                     T, P and three scalars a token for the second kernel
-//   gdr_state_kernel  per (sequence, head, VB value columns): the serial pass over the chunks
+//                     value heads the decays, A, T, and one block of T, P and four scalars a token for
+//                     the second kernel
+//   gdr_state_kernel  per (sequence, head, 32 value columns): the serial pass over the chunks
 //
 // The raw BF16 rows of K, Q and V are the matrix operands as they are, so those operands are exact;
 // the norms and the decays are FP32 scalars a token, applied to FP32 accumulators. What carries the
-// state is kept to about 16 bits: S, V - .., T and U go into the products as a BF16 high part and a
+// state is kept to about 16 bits: S, beta (V - ..), T and U go into the products as a BF16 high part and a
 // BF16 low part (x - high), products of two such factors as hi hi + lo hi + hi lo, and sums are FP32.
 // With single BF16 operands the state would be off by 2^-9 a chunk. The output, which is rounded to
 // BF16 itself, takes the high parts of S and U and P in one BF16.
@@ -24,28 +24,34 @@
 #include <cudaTypedefs.h>
 
 #include "kda_gdr.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 namespace gdr {
 namespace {
 
-// One block per (chunk, value head): BF16 tiles of 64 rows t of 64 columns i (128 bytes), 16-byte
-// piece c of row t at c ^ (t & 7), then FP32 scalars.
-constexpr int kBlkTl = 8192, kBlkP = 16384;  // T high at 0, T low, P
-constexpr int kBlkX = 24576;                 // rk exp G | rq exp G | rk exp(G_last - G) | exp G_last
-constexpr int kBlkBytes = 25600;
+// One block per (chunk, value head), in two parts that go to different rings of the second kernel.
+// Tiles: BF16, 64 rows t of 64 columns i (128 bytes), 16-byte piece c of row t at c ^ (t & 7); only the
+// 16 x 16 blocks on and below the diagonal are meaningful.
+//   T high | T low | FP32 scalars: beta rk exp G [64], beta [64], rk exp(G_last - G) [64], exp G_last
+//   P | rq exp G [64]
+constexpr int kTl = 8192, kTx = 16384, kPartT = kTx + 1024;
+constexpr int kPx = 8192, kPartP = kPx + 256;
+constexpr int kBlkBytes = kPartT + kPartP;
 
 __device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
 
+// Shared memory read as matrix operands. Volatile keeps these behind the barrier that the data came with;
+// what this thread's warp wrote itself is followed by __syncwarp.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void stsm2t(uint32_t addr, uint32_t a, uint32_t b)
 {
@@ -55,7 +61,7 @@ __device__ __forceinline__ void stsm2t(uint32_t addr, uint32_t a, uint32_t b)
 // g, g + 8 at columns 2q, 2q + 1; a = those rows at k 2q, 2q + 1 (+ 8); b = k 2q, 2q + 1 (+ 8) of column g.
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -123,22 +129,36 @@ __device__ __forceinline__ bool find_place(const int32_t *cu, int N, int64_t tot
 }
 
 // ---------------------------------------------------------------- prep
-// 128 threads. Shared memory: K and Q rows (swizzled 128-byte halves), later two FP32 T matrices in
-// their place; two FP32 A^T matrices; per-token scalars of the two value heads in work.
+// 128 threads; warp w has the rows t = 16 w .. 16 w + 15. T by blocks of 16 rows: the diagonal blocks
+// D_w = (I + A_ww)^-1 by forward substitution in FP32, a warp each, one column a lane; below them
+//   T[w][:] = -D_w sum_{j < w} A[w][j] T[j][:]
+// on the tensor cores with split factors, three barriers deep. (The whole inverse by forward
+// substitution, a column a lane, took 92 us for 4096 (chunk, value head) pairs; see the launch below.)
+// Shared memory: K and Q rows, in whose place the first block is then built; a second block when there
+// is more than one value head a key head; A's diagonal blocks; scalars of up to four value heads.
 constexpr int kPrepThreads = 128;
-constexpr int kAp = kC + 4;                    // row pitch of A^T (16-byte rows, a step of 4 banks)
-constexpr int kPsK = 0, kPsQ = 16384, kPsA = 32768;
-constexpr int kPsS = kPsA + 2 * kC * kAp * 4;  // [2 heads][Gh, Gl, beta][64]
-constexpr int kPsN = kPsS + 2 * 3 * kC * 4;    // rk[64], rq[64]
-constexpr int kPrepSmem = kPsN + 2 * kC * 4 + 64;
+constexpr int kPsQ = 16384, kPsB1 = 32768;
+constexpr int kDp = 20;                               // row pitch of a diagonal block of A^T
+constexpr int kPsDiag = 0, kPsScal = 4 * 16 * kDp * 4;  // relative to the end of the blocks
+constexpr int kScal = 5 * kC;                         // per head: G high, G low, beta, exp G, exp(G_last - G)
+constexpr int kPsNorm = kPsScal + 4 * (kScal + 4) * 4;
+constexpr int kPsPlace = kPsNorm + 2 * kC * 4, kPsTail = kPsPlace + 64;
+constexpr int prep_smem(int G) { return kPsB1 + (G > 1 ? kBlkBytes : 0) + kPsTail; }
 
-__global__ void __launch_bounds__(kPrepThreads)
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 4)
 gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ blocks, int64_t n_chunks, int Hk)
 {
-    extern __shared__ __align__(128) unsigned char sm[];
-    Place *place = reinterpret_cast<Place *>(sm + kPsN + 2 * kC * 4);
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char *tail = sm + kPsB1 + (p.G > 1 ? kBlkBytes : 0);
+    Place *place = reinterpret_cast<Place *>(tail + kPsPlace);
     int *ok = reinterpret_cast<int *>(place + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q2 = 2 * (lane & 3);
     const int64_t chunk = blockIdx.x / Hk;
     const int hk = (int)(blockIdx.x - chunk * Hk);
     if (warp == 0) {
@@ -155,10 +175,10 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
     const int pos = (int)(chunk - place->first) * kC;
     const int64_t t0 = (int64_t)place->t0 + pos;
     const int n = min(kC, place->len - pos);
-    const uint32_t sK = smem_u32(sm + kPsK), sQ = smem_u32(sm + kPsQ);
-    float *sA = reinterpret_cast<float *>(sm + kPsA);
-    float *sS = reinterpret_cast<float *>(sm + kPsS);
-    float *sRk = reinterpret_cast<float *>(sm + kPsN), *sRq = sRk + kC;
+    const uint32_t sK = smem_u32(sm), sQ = sK + kPsQ;
+    float *sRk = reinterpret_cast<float *>(tail + kPsNorm), *sRq = sRk + kC;
+    float *scal = reinterpret_cast<float *>(tail + kPsScal);
+    float *diag = reinterpret_cast<float *>(tail + kPsDiag) + warp * 16 * kDp;
 
     // rows n .. 63 read as zeros
     const __nv_bfloat16 *kg = static_cast<const __nv_bfloat16 *>(p.rows.k) + t0 * p.rows.k_stride + (size_t)hk * kD;
@@ -168,9 +188,51 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
         const int x = tid + i * kPrepThreads, r = x >> 4, c = x & 15;  // 16 pieces of 16 bytes a row
         const uint32_t off = (uint32_t)(c >> 3) * 8192 + swz(r, c & 7);
         const int rr = r < n ? r : 0;
-        cp_async16(sm + kPsK + off, kg + rr * p.rows.k_stride + 8 * c, r < n ? 16 : 0);
+        cp_async16(sm + off, kg + rr * p.rows.k_stride + 8 * c, r < n ? 16 : 0);
         cp_async16(sm + kPsQ + off, qg + rr * p.rows.q_stride + 8 * c, r < n ? 16 : 0);
     }
+    // decays of value head j + warp, two tokens a lane. The sums are taken in 64 bits and kept as two FP32,
+    // so that differences of tokens far down a strongly decaying chunk stay exact.
+    auto decays = [&](int j) {
+        if (j + warp >= p.G) return;
+        const int h = hk * p.G + j + warp;
+        const float expA = expf(__ldg(p.A_log + h)), dtb = __ldg(p.dt_bias + h);
+        const __nv_bfloat16 *ag = static_cast<const __nv_bfloat16 *>(p.rows.a) + t0 * p.rows.a_stride + h;
+        const __nv_bfloat16 *bg = static_cast<const __nv_bfloat16 *>(p.rows.b) + t0 * p.rows.b_stride + h;
+        float *s = scal + warp * (kScal + 4);
+        double ga[2];
+        float be[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            ga[e] = 0.0;
+            be[e] = 0.f;
+            if (t < n) {
+                ga[e] = (double)log_decay(__bfloat162float(ag[t * p.rows.a_stride]), dtb, expA) * 1.4426950408889634;
+                be[e] = sigmoidf_(__bfloat162float(bg[t * p.rows.b_stride]));
+            }
+        }
+        double c = ga[0] + ga[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double x = __shfl_up_sync(0xFFFFFFFFu, c, o);
+            if (lane >= o) c += x;
+        }
+        const double last = __shfl_sync(0xFFFFFFFFu, c, 31);
+        const double Gs[2] = {c - ga[1], c};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            const float h0 = (float)Gs[e];
+            s[t] = h0;
+            s[kC + t] = (float)(Gs[e] - (double)h0);
+            s[2 * kC + t] = be[e];
+            s[3 * kC + t] = ex2(h0);
+            s[4 * kC + t] = ex2((float)(last - Gs[e]));
+        }
+        if (lane == 0) s[5 * kC] = ex2((float)last);
+    };
+    decays(0);
     cp_async_wait_all();
     __syncthreads();
     {  // norms: two threads a row of K and of Q
@@ -179,7 +241,7 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const uint32_t off = (uint32_t)half * 8192 + swz(r, c);
-            const uint4 a = *reinterpret_cast<const uint4 *>(sm + kPsK + off);
+            const uint4 a = *reinterpret_cast<const uint4 *>(sm + off);
             const uint4 b = *reinterpret_cast<const uint4 *>(sm + kPsQ + off);
             const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -195,7 +257,7 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
             sRq[r] = p.l2norm ? p.q_scale * rsqrtf(qq + p.l2_eps) : p.q_scale;
         }
     }
-    // K K^T and Q K^T: warp w has rows t = 16 w .. 16 w + 15, columns i <= 16 w + 15
+    // K K^T and Q K^T: rows t of this warp, columns i <= 16 w + 15
     float kk[8][4], qk[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -219,59 +281,30 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
             mma(qk[2 * jp + 1], aq, b[2], b[3]);
         }
     }
-    float *sT = reinterpret_cast<float *>(sm);  // [2][64][64], in the place of K and Q
-    for (int j0 = 0; j0 < p.G; j0 += 2) {
-        const int nh = min(2, p.G - j0);
-        __syncthreads();  // K, Q (first time), A, T and the scalars are free
-        if (warp < nh) {  // decays of value head j0 + warp: two tokens a lane
-            const int h = hk * p.G + j0 + warp;
-            const float expA = expf(__ldg(p.A_log + h)), dtb = __ldg(p.dt_bias + h);
-            const __nv_bfloat16 *ag = static_cast<const __nv_bfloat16 *>(p.rows.a) + t0 * p.rows.a_stride + h;
-            const __nv_bfloat16 *bg = static_cast<const __nv_bfloat16 *>(p.rows.b) + t0 * p.rows.b_stride + h;
-            float *s = sS + warp * 3 * kC;
-            unsigned char *blk = blocks + ((size_t)chunk * p.H + h) * kBlkBytes;
-            double g[2];
-            float be[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                g[e] = 0.0;
-                be[e] = 0.f;
-                if (t < n) {
-                    g[e] = (double)log_decay(__bfloat162float(ag[t * p.rows.a_stride]), dtb, expA) * 1.4426950408889634;
-                    be[e] = sigmoidf_(__bfloat162float(bg[t * p.rows.b_stride]));
-                }
-            }
-            // sums in 64 bits, kept as two FP32: differences of tokens far down a strongly decaying chunk stay exact
-            double c = g[0] + g[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_up_sync(0xFFFFFFFFu, c, o);
-                if (lane >= o) c += x;
-            }
-            const double last = __shfl_sync(0xFFFFFFFFu, c, 31);
-            float *bx = reinterpret_cast<float *>(blk + kBlkX);
-            const double Gs[2] = {c - g[1], c};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const float h0 = (float)Gs[e];
-                s[t] = h0;
-                s[kC + t] = (float)(Gs[e] - (double)h0);
-                s[2 * kC + t] = be[e];
-                const float eg = ex2((float)Gs[e]);
-                bx[t] = t < n ? sRk[t] * eg : 0.f;
-                bx[kC + t] = t < n ? sRq[t] * eg : 0.f;
-                bx[2 * kC + t] = t < n ? sRk[t] * ex2((float)(last - Gs[e])) : 0.f;
-            }
-            if (lane == 0) bx[3 * kC] = ex2((float)last);
+    const int rowT = (lane & 7) + (((lane >> 3) & 1) << 3), pcT = lane >> 4;  // ldmatrix.trans of B operands
+#pragma unroll 1
+    for (int j = 0; j < p.G; ++j) {
+        unsigned char *blk = j & 1 ? sm + kPsB1 : sm;
+        const uint32_t sT = smem_u32(blk);
+        if (j && (j & 3) == 0) {
+            __syncthreads();  // every warp has read the last four heads' scalars
+            decays(j);
         }
-        __syncthreads();
-        for (int j = 0; j < nh; ++j) {  // A^T to shared memory, P to the block
-            const float *s = sS + j * 3 * kC;
-            float *A = sA + j * kC * kAp;
-            unsigned char *P = blocks + ((size_t)chunk * p.H + hk * p.G + j0 + j) * kBlkBytes + kBlkP;
-            const int ta = 16 * warp + (lane >> 2);
+        if (tid == 0 && j > 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncthreads();  // K, Q are read, the scalars are written, this block's last store has read it
+        const float *s = scal + (j & 3) * (kScal + 4);
+        if (tid < kC) {
+            float *x = reinterpret_cast<float *>(blk + kTx);
+            x[tid] = s[2 * kC + tid] * sRk[tid] * s[3 * kC + tid];
+            x[kC + tid] = s[2 * kC + tid];
+            x[2 * kC + tid] = sRk[tid] * s[4 * kC + tid];
+            if (tid == 0) x[3 * kC] = s[5 * kC];
+            reinterpret_cast<float *>(blk + kPartT + kPx)[tid] = sRq[tid] * s[3 * kC + tid];
+        }
+        // A and P from the products: A's blocks left of the diagonal stay in registers as split A operands
+        uint32_t ah[3][4], al[3][4];
+        {
+            const int ta = 16 * warp + g;
             float Gh[2], Gl[2], fb[2], fq[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -283,349 +316,484 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
             }
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
-                float pv[2][2];
+                if ((nt >> 1) > warp) break;
+                const int i = 8 * nt + q2;
+                const float2 gh = *reinterpret_cast<const float2 *>(s + i), gl = *reinterpret_cast<const float2 *>(s + kC + i);
+                const float2 rk = *reinterpret_cast<const float2 *>(sRk + i);
+                float av[2][2], pv[2][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
-                        const int t = ta + 8 * e, i = 8 * nt + 2 * (lane & 3) + f;
-                        float av = 0.f, x = 0.f;
-                        if (i <= t) {
-                            const float d = ex2((Gh[e] - s[i]) + (Gl[e] - s[kC + i])) * sRk[i];
-                            x = fq[e] * d * qk[nt][2 * e + f];
-                            if (i < t) av = fb[e] * d * kk[nt][2 * e + f];
+                        const float x = (Gh[e] - (f ? gh.y : gh.x)) + (Gl[e] - (f ? gl.y : gl.x));
+                        const float d = ex2(x) * (f ? rk.y : rk.x);
+                        av[e][f] = i + f < ta + 8 * e ? fb[e] * d * kk[nt][2 * e + f] : 0.f;
+                        pv[e][f] = i + f <= ta + 8 * e ? fq[e] * d * qk[nt][2 * e + f] : 0.f;
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    *reinterpret_cast<uint32_t *>(blk + kPartT + swz(ta + 8 * e, nt) + 2 * q2) = pack2(pv[e][0], pv[e][1]);
+                    if ((nt >> 1) < warp) {
+                        if (nt < 6) split2(av[e][0], av[e][1], ah[(nt >> 1) % 3][2 * (nt & 1) + e], al[(nt >> 1) % 3][2 * (nt & 1) + e]);
+                    } else {
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) diag[(8 * (nt & 1) + q2 + f) * kDp + g + 8 * e] = av[e][f];
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        {  // the diagonal block: column lane & 15; lanes 0..15 store its high part, lanes 16..31 its low part
+            const int jc = lane & 15;
+            float acc[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[r] = r == jc ? 1.f : 0.f;
+#pragma unroll
+            for (int r = 0; r < 15; ++r) {
+                float a[16];
+#pragma unroll
+                for (int e = (r + 1) / 4; e < 4; ++e)
+                    *reinterpret_cast<float4 *>(a + 4 * e) = *reinterpret_cast<const float4 *>(diag + r * kDp + 4 * e);
+#pragma unroll
+                for (int r2 = r + 1; r2 < 16; ++r2) acc[r2] = fmaf(-a[r2], acc[r], acc[r2]);
+            }
+            unsigned char *dst = blk + (lane & 16 ? kTl : 0) + 2 * (jc & 7);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const __nv_bfloat16 hi = __float2bfloat16_rn(acc[r]);
+                const __nv_bfloat16 lo = __float2bfloat16_rn(acc[r] - __bfloat162float(hi));
+                *reinterpret_cast<__nv_bfloat16 *>(dst + swz(16 * warp + r, 2 * warp + (jc >> 3))) = lane & 16 ? lo : hi;
+            }
+        }
+        float Y[6][4];
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Y[i][e] = 0.f;
+#pragma unroll
+        for (int jb = 0; jb < 3; ++jb) {
+            __syncthreads();  // block row jb of T is complete
+            if (warp <= jb) continue;
+#pragma unroll
+            for (int np = 0; np <= jb; ++np) {
+                uint32_t bh[4], bl[4];
+                const uint32_t off = swz(16 * jb + rowT, 2 * np + pcT);
+                ldsm4t(bh, sT + off);
+                ldsm4t(bl, sT + kTl + off);
+                mma(Y[2 * np], ah[jb], bh[0], bh[1]);
+                mma(Y[2 * np + 1], ah[jb], bh[2], bh[3]);
+                mma(Y[2 * np], al[jb], bh[0], bh[1]);
+                mma(Y[2 * np + 1], al[jb], bh[2], bh[3]);
+                mma(Y[2 * np], ah[jb], bl[0], bl[1]);
+                mma(Y[2 * np + 1], ah[jb], bl[2], bl[3]);
+            }
+            if (warp == jb + 1) {  // T[w][:] = -D Y: Y goes to its own place in T first, to be read as a B operand
+                uint32_t dh[4], dl[4];
+                const uint32_t od = swz(16 * warp + (lane & 15), 2 * warp + (lane >> 4));
+                ldsm4(dh, sT + od);
+                ldsm4(dl, sT + kTl + od);
+#pragma unroll
+                for (int nt = 0; nt < 2 * jb + 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t h, l;
+                        split2(-Y[nt][2 * e], -Y[nt][2 * e + 1], h, l);
+                        unsigned char *dst = blk + swz(16 * warp + g + 8 * e, nt) + 2 * q2;
+                        *reinterpret_cast<uint32_t *>(dst) = h;
+                        *reinterpret_cast<uint32_t *>(dst + kTl) = l;
+                    }
+                __syncwarp();
+#pragma unroll
+                for (int np = 0; np <= jb; ++np) {
+                    uint32_t bh[4], bl[4];
+                    const uint32_t off = swz(16 * warp + rowT, 2 * np + pcT);
+                    ldsm4t(bh, sT + off);
+                    ldsm4t(bl, sT + kTl + off);
+                    __syncwarp();
+                    float z[2][4] = {};
+                    mma(z[0], dh, bh[0], bh[1]);
+                    mma(z[1], dh, bh[2], bh[3]);
+                    mma(z[0], dl, bh[0], bh[1]);
+                    mma(z[1], dl, bh[2], bh[3]);
+                    mma(z[0], dh, bl[0], bl[1]);
+                    mma(z[1], dh, bl[2], bl[3]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t h, l;
+                            split2(z[x][2 * e], z[x][2 * e + 1], h, l);
+                            unsigned char *dst = blk + swz(16 * warp + g + 8 * e, 2 * np + x) + 2 * q2;
+                            *reinterpret_cast<uint32_t *>(dst) = h;
+                            *reinterpret_cast<uint32_t *>(dst + kTl) = l;
                         }
-                        A[i * kAp + t] = av;
-                        pv[e][f] = x;
-                    }
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<uint32_t *>(P + swz(ta + 8 * e, nt) + 4 * (lane & 3)) = pack2(pv[e][0], pv[e][1]);
-            }
-        }
-        __syncthreads();
-        if ((warp >> 1) < nh) {  // column jc of (I + A)^-1 by forward substitution, 16 rows at a time
-            const float *A = sA + (warp >> 1) * kC * kAp;
-            float *Tm = sT + (warp >> 1) * kC * kC;
-            const int half = warp & 1, jc = 32 * half + lane;
-            if (half)
-#pragma unroll
-                for (int t = 0; t < 32; ++t) Tm[t * kC + jc] = 0.f;
-#pragma unroll 1
-            for (int b = 2 * half; b < 4; ++b) {
-                float acc[16];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[r] = 16 * b + r == jc ? 1.f : 0.f;
-#pragma unroll 4
-                for (int i = 32 * half; i < 16 * b; ++i) {
-                    const float x = Tm[i * kC + jc];
-                    const float4 *a4 = reinterpret_cast<const float4 *>(A + i * kAp + 16 * b);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float4 a = a4[r];
-                        acc[4 * r] = fmaf(-a.x, x, acc[4 * r]);
-                        acc[4 * r + 1] = fmaf(-a.y, x, acc[4 * r + 1]);
-                        acc[4 * r + 2] = fmaf(-a.z, x, acc[4 * r + 2]);
-                        acc[4 * r + 3] = fmaf(-a.w, x, acc[4 * r + 3]);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float x = acc[r];
-                    Tm[(16 * b + r) * kC + jc] = x;
-#pragma unroll
-                    for (int r2 = r + 1; r2 < 16; ++r2) acc[r2] = fmaf(-A[(16 * b + r) * kAp + 16 * b + r2], x, acc[r2]);
                 }
             }
         }
+        tc::fence_smem_to_async();
         __syncthreads();
-        for (int x = tid; x < nh * 512; x += kPrepThreads) {  // T Diag(beta), high and low
-            const int j = x >> 9, t = (x >> 3) & 63, c = x & 7;
-            const float4 *T4 = reinterpret_cast<const float4 *>(sT + j * kC * kC + t * kC + 8 * c);
-            const float4 *b4 = reinterpret_cast<const float4 *>(sS + j * 3 * kC + 2 * kC + 8 * c);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float4 a = T4[e], b = b4[e];
-                split2(a.x * b.x, a.y * b.y, hi[2 * e], lo[2 * e]);
-                split2(a.z * b.z, a.w * b.w, hi[2 * e + 1], lo[2 * e + 1]);
-            }
-            unsigned char *blk = blocks + ((size_t)chunk * p.H + hk * p.G + j0 + j) * kBlkBytes + swz(t, c);
-            *reinterpret_cast<uint4 *>(blk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(blk + kBlkTl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (tid == 0) {
+            bulk_s2g(blocks + ((size_t)chunk * p.H + hk * p.G + j) * kBlkBytes, blk, kBlkBytes);
+            bulk_commit_group();
         }
     }
+    if (tid == 0) bulk_wait_all();
 }
 
 // ---------------------------------------------------------------- state
-// Everything is held transposed, with the 16 value columns of a unit as the 16 rows of the MMA: the
-// FP32 accumulators of S^T, X^T = S0^T K^T, U^T and O^T then have the register layout of the next
-// product's A operand, and the operands in shared memory are only read. Two warps share a unit: warp kw
-// has the key rows 64 kw .. 64 kw + 63 of S (its partial sums of X and O go to the other through shared
-// memory) and half of the token tiles of U and O. The tiles are dealt so that both halves of the
-// triangular products are equal: tokens 0..15 and 48..63 to warp 0, 16..47 to warp 1.
-// A further warp copies: a ring of stages, each K | Q | block | V of one chunk.
-template <int VB> struct St {
-    static constexpr int kUnits = VB / 16, kWarps = 2 * kUnits, kThreads = 32 * (kWarps + 1);
-    static constexpr int kStages = VB == 32 ? 3 : 2;
-    static constexpr int kQ = 16384, kBlk = 32768, kV = kBlk + kBlkBytes, kStage = kV + kC * VB * 2;
-    static constexpr int kXBytes = 2 * 8 * 512, kOBytes = 2 * 4 * 512, kUBytes = 2 * 4 * 512;  // per unit
-    static constexpr int kX = kStages * kStage, kUnit = kXBytes + kOBytes + kUBytes;
-    static constexpr int kBar = kX + kUnits * kUnit;
-    static constexpr int kSmem = kBar + 2 * kStages * 8 + 64 + 1024;
-};
-static_assert(St<32>::kSmem <= 232448 && St<64>::kSmem <= 232448, "state kernel shared memory");
-static_assert(St<32>::kStage % 1024 == 0 && St<64>::kStage % 1024 == 0, "swizzled boxes");
+// A block takes 32 value columns of one (sequence, head) through its chunks. Everything is held
+// transposed, with 16 value columns (a unit) as the 16 rows of the MMA: the FP32 accumulators of S^T, X^T
+// = S0^T K^T and U^T then have the register layout of the next product's A operand, and the operands in
+// shared memory are only read.
+//   warps 0-3  the chain: warp 2 u + kw has unit u and the key rows 64 kw .. 64 kw + 63 of S. Its partial
+//              sums of X, then half of the token tiles of U, go to the unit's other warp through shared
+//              memory. Of each pair of 8-token tiles a warp has one, in turn the first and the second, so
+//              that both halves of the triangular product are equal.
+//   warps 4-7  the output, one chunk behind the chain at most: unit and token tiles as above, O^T from the
+//              high parts of S0 and U that the chain hands over (two buffers)
+//   warp 8     (of a third warpgroup, which leaves its registers to the first) copies: a ring of K, T and V for the chain, one of Q and P for the output
+// What bounds it is the chain of a chunk, 158 MMAs a warp (m16n8k16, 8 cycles each on its quarter of the
+// SM) with the exchanges between them. Tcgen05 would run the same products in tiles of 64 or 128 rows at
+// four times that rate, but the four dependent products of a chunk (64 x 128 x 32 and smaller) would each
+// pay for the way through tensor memory and back into shared memory.
+constexpr int kVB = 32, kStThreads = 384;
+constexpr int kNa = 3, kNo = 2;  // stages of the two rings
+constexpr int kSaT = 16384, kSaV = kSaT + kPartT, kSa = kSaV + kC * kVB * 2;
+constexpr int kSoP = 16384, kSo = 25600;
+constexpr int kSmO = kNa * kSa, kSmX = kSmO + kNo * kSo;  // X: [2 units][2 kw][8 tiles][32 lanes] float4
+constexpr int kSmU = kSmX + 16384, kSmH = kSmU + 8192;    // U: [2][2][4][32] float4; hand-over buffers
+constexpr int kHand = 12288;                              // S [2][8 k steps][32] uint4, U [2][4][32] uint4
+constexpr int kSmSt = kSmH + 2 * kHand, kSmBar = kSmSt + 4096;
+constexpr int kStSmem = kSmBar + 256 + 1024;
+static_assert(kSa % 1024 == 0 && kSo % 1024 == 0 && kSaV % 512 == 0 && kSoP + kPartP <= kSo, "stages");
+static_assert(kStSmem <= 232448, "state kernel shared memory");
 constexpr uint32_t kStSpin = 1u << 26;
 
-// byte offset of 16-byte piece c of row r of the V tile (rows of 64 or 128 bytes, TMA's swizzle)
-template <int VB> __device__ __forceinline__ uint32_t v_off(int r, int c)
+struct StateMaps { CUtensorMap k, q, v; };
+// full and empty of the two rings; S0 handed over, U handed over, both read
+struct StBars { uint64_t fa[kNa], ea[kNa], fo[kNo], eo[kNo], fs[2], fh[2], eh[2]; };
+
+// byte offset of 16-byte piece c of row r of the V tile (rows of 64 bytes, TMA's 64-byte swizzle)
+__device__ __forceinline__ uint32_t v_off(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// Token tiles (8 tokens) of the unit's warp kw: one of each pair, 2 p + own(p).
+__device__ __forceinline__ int own(int kw, int p) { return (p ^ kw) & 1; }
+
+// Two barriers at once: even lanes wait for one, odd lanes for the other.
+__device__ __forceinline__ bool wait_both(uint64_t *x, uint32_t px, uint64_t *y, uint32_t py)
 {
-    return VB == 64 ? swz(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    const bool odd = threadIdx.x & 1;
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odd ? y : x, odd ? py : px, kStSpin));
 }
 
-struct StateMaps { CUtensorMap k, q, v; };
-
-// The chunks of one sequence for one warp of a unit.
-template <int VB, int KW>
-__device__ __forceinline__ bool state_pass(const Args &p, unsigned char *sm, uint64_t *full, uint64_t *empty, int u,
-                                           const Place &pl, int h, int v0, float (&S)[8][4])
+// The two k halves of a fragment of 16 values rows by 16, from FP32 pairs, split
+__device__ __forceinline__ void split_tile(float2 x, float2 y, uint32_t *h, uint32_t *l)
 {
-    using L = St<VB>;
+    split2(x.x, x.y, h[0], l[0]);
+    split2(y.x, y.y, h[1], l[1]);
+}
+
+__device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u, int kw, int len, float2 (&S)[8][2])
+{
     const int lane = threadIdx.x & 31, q2 = 2 * (lane & 3);
-    float4 *xb = reinterpret_cast<float4 *>(sm + L::kX + u * L::kUnit);  // [2][8][32]
-    float4 *ob = xb + 2 * 8 * 32, *ub = ob + 2 * 4 * 32;                 // [2][4][32]
-    const int nc = (pl.len + kC - 1) / kC;
+    float4 *xb = reinterpret_cast<float4 *>(sm + kSmX) + u * 512 + lane;
+    float4 *ub = reinterpret_cast<float4 *>(sm + kSmU) + u * 256 + lane;
+    const int nc = (len + kC - 1) / kC;
     bool good = true;
-    // row within an ldmatrix of B operands: tokens in rows (lane / 16 picks the second tile), or key rows transposed
+    // row and 16-byte piece within an ldmatrix of B operands: two tiles of tokens in rows, or tokens as k
+    // (transposed; own tile first), or one tile of tokens with two k steps
     const int rowB = (lane & 7) + ((lane >> 4) << 3), pcB = (lane >> 3) & 1;
-    const int rowT = (lane & 7) + (((lane >> 3) & 1) << 3), pcT = lane >> 4;
-    constexpr int pr0 = KW == 0 ? 0 : 1, pr1 = KW == 0 ? 3 : 2;   // this warp's pairs of token tiles
-    constexpr int or0 = KW == 0 ? 1 : 0, or1 = KW == 0 ? 2 : 3;   // the other's
+    uint32_t offT[4];  // T rows of this warp's tile of pair p, k steps 0 and 1 (steps 2 and 3: ^ 64)
+#pragma unroll
+    for (int pr = 0; pr < 4; ++pr) offT[pr] = swz(16 * pr + 8 * own(kw, pr) + (lane & 7), lane >> 3);
+    int st = 0, pa = 0;
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
-        const int st = c % L::kStages;
-        unsigned char *base = sm + st * L::kStage;
-        const uint32_t sb = smem_u32(base);
-        const int n = min(kC, pl.len - c * kC);
+        const int hb = c & 1;
+        unsigned char *base = sm + st * kSa;
+        const uint32_t sb = smem_u32(base), sk = sb + kw * 8192;
+        uint4 *hs = reinterpret_cast<uint4 *>(sm + kSmH + hb * kHand) + u * 256 + kw * 128 + lane;
+        uint2 *hu = reinterpret_cast<uint2 *>(sm + kSmH + hb * kHand + 8192 + u * 2048) + lane;
+        const int n = min(kC, len - c * kC);
         // after a wait that gave up the warp goes on without waiting, so that every barrier is met
-        if (good) good = mbar_wait_bounded(&full[st], (uint32_t)((c / L::kStages) & 1), kStSpin);
+        if (good)
+            good = c < 2 ? mbar_wait_bounded(&bar->fa[st], (uint32_t)pa, kStSpin)
+                         : wait_both(&bar->fa[st], (uint32_t)pa, &bar->eh[hb], (uint32_t)(((c >> 1) - 1) & 1));
         if (n < kC) {  // the last chunk: what follows the sequence in K and V counts as zero
-            const int t = threadIdx.x;
-            for (int x = t; x < (kC - n) * 16; x += 32 * L::kWarps)
+            for (int x = threadIdx.x; x < (kC - n) * 16; x += 128)
                 *reinterpret_cast<uint4 *>(base + ((x >> 3) & 1) * 8192 + (n + (x >> 4)) * 128 + (x & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
-            for (int x = t; x < (kC - n) * (VB / 8); x += 32 * L::kWarps)
-                *reinterpret_cast<uint4 *>(base + L::kV + n * VB * 2 + x * 16) = make_uint4(0, 0, 0, 0);
-            named_bar_sync(1 + L::kUnits, 32 * L::kWarps);
+            for (int x = threadIdx.x; x < (kC - n) * (kVB / 8); x += 128)
+                *reinterpret_cast<uint4 *>(base + kSaV + n * kVB * 2 + x * 16) = make_uint4(0, 0, 0, 0);
+            named_bar_sync(3, 128);
         }
-        const float *sx = reinterpret_cast<const float *>(base + L::kBlk + kBlkX);
-        // X^T and Q S0, over this warp's 64 key rows
-        float X[8][4], O[8][4];
+        const float *sx = reinterpret_cast<const float *>(base + kSaT + kTx);
+        uint32_t b[2][4][4];      // B operands of a k step, fetched a step ahead
+        uint32_t ah[2][4], al[2][4];  // A operand of a k step, split a step ahead
+        // X^T over this warp's 64 key rows
+        float X[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) X[j][e] = O[j][e] = 0.f;
-        {
-            uint32_t ah[4][4], al[4][4];
+            for (int e = 0; e < 4; ++e) X[j][e] = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
+        for (int jp = 0; jp < 4; ++jp) ldsm4(b[0][jp], sk + swz(16 * jp + rowB, pcB));
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    split2(S[2 * ks + e][0], S[2 * ks + e][1], ah[ks][2 * e], al[ks][2 * e]);
-                    split2(S[2 * ks + e][2], S[2 * ks + e][3], ah[ks][2 * e + 1], al[ks][2 * e + 1]);
-                }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-                for (int jp = 0; jp < 4; ++jp) {
-                    uint32_t b[4];
-                    ldsm4(b, sb + KW * 8192 + swz(16 * jp + rowB, 2 * ks + pcB));
-                    mma(X[2 * jp], ah[ks], b[0], b[1]);
-                    mma(X[2 * jp + 1], ah[ks], b[2], b[3]);
-                    mma(X[2 * jp], al[ks], b[0], b[1]);
-                    mma(X[2 * jp + 1], al[ks], b[2], b[3]);
-                }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) xb[(KW * 8 + j) * 32 + lane] = make_float4(X[j][0], X[j][1], X[j][2], X[j][3]);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-                for (int jp = 0; jp < 4; ++jp) {
-                    uint32_t b[4];
-                    ldsm4(b, sb + L::kQ + KW * 8192 + swz(16 * jp + rowB, 2 * ks + pcB));
-                    mma(O[2 * jp], ah[ks], b[0], b[1]);
-                    mma(O[2 * jp + 1], ah[ks], b[2], b[3]);
-                }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            ob[(KW * 4 + e) * 32 + lane] = make_float4(O[2 * or0 + e][0], O[2 * or0 + e][1], O[2 * or0 + e][2], O[2 * or0 + e][3]);
-            ob[(KW * 4 + 2 + e) * 32 + lane] = make_float4(O[2 * or1 + e][0], O[2 * or1 + e][1], O[2 * or1 + e][2], O[2 * or1 + e][3]);
-        }
-        named_bar_sync(1 + u, 64);
-        // right side V - x X, split; token tiles 2 ks, 2 ks + 1 are k step ks of the next product
-        uint32_t rh[4][4], rl[4][4];
+        for (int e = 0; e < 2; ++e) split_tile(S[e][0], S[e][1], ah[0] + 2 * e, al[0] + 2 * e);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            uint32_t vv[4];  // V^T of tiles 2 ks, 2 ks + 1: value rows g (0, 2) and g + 8 (1, 3)
-            ldsm4t(vv, sb + L::kV + v_off<VB>(16 * ks + rowB, 2 * u + pcB));
+            const int x = ks & 1, y = x ^ 1;
+            hs[ks * 32] = make_uint4(ah[x][0], ah[x][1], ah[x][2], ah[x][3]);
+            if (ks < 3) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = 2 * ks + e;
-                const float4 o = xb[((1 - KW) * 8 + j) * 32 + lane];
-                const float2 cx = *reinterpret_cast<const float2 *>(sx + 8 * j + q2);
-                const float r0 = fmaf(-cx.x, X[j][0] + o.x, lo_f(vv[2 * e])), r1 = fmaf(-cx.y, X[j][1] + o.y, hi_f(vv[2 * e]));
-                const float r2 = fmaf(-cx.x, X[j][2] + o.z, lo_f(vv[2 * e + 1])), r3 = fmaf(-cx.y, X[j][3] + o.w, hi_f(vv[2 * e + 1]));
-                split2(r0, r1, rh[ks][2 * e], rl[ks][2 * e]);
-                split2(r2, r3, rh[ks][2 * e + 1], rl[ks][2 * e + 1]);
+                for (int jp = 0; jp < 4; ++jp) ldsm4(b[y][jp], sk + swz(16 * jp + rowB, 2 * (ks + 1) + pcB));
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    split_tile(S[2 * ks + 2 + e][0], S[2 * ks + 2 + e][1], ah[y] + 2 * e, al[y] + 2 * e);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mma(X[j], ah[x], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mma(X[j], al[x], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
         }
-        // U^T of this warp's token tiles
-        float U[8][4];
+        // fetched while the products drain: V^T (value rows g and g + 8 of a tile), the scalars, T
+        uint32_t vv[4][4], th[2][4][4], tl[2][4][4];
 #pragma unroll
-        for (int pi = 0; pi < 2; ++pi) {
-            const int pr = pi ? pr1 : pr0;
+        for (int ks = 0; ks < 4; ++ks) ldsm4t(vv[ks], sb + kSaV + v_off(16 * ks + rowB, 2 * u + pcB));
+        float2 cx[8], be[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) U[2 * pr][e] = U[2 * pr + 1][e] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks <= pr; ++ks) {
-                uint32_t bh[4], bl[4];
-                const uint32_t off = swz(16 * pr + rowB, 2 * ks + pcB);
-                ldsm4(bh, sb + L::kBlk + off);
-                ldsm4(bl, sb + L::kBlk + kBlkTl + off);
-                mma(U[2 * pr], rh[ks], bh[0], bh[1]);
-                mma(U[2 * pr + 1], rh[ks], bh[2], bh[3]);
-                mma(U[2 * pr], rl[ks], bh[0], bh[1]);
-                mma(U[2 * pr + 1], rl[ks], bh[2], bh[3]);
-                mma(U[2 * pr], rh[ks], bl[0], bl[1]);
-                mma(U[2 * pr + 1], rh[ks], bl[2], bl[3]);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                ub[(KW * 4 + 2 * pi + e) * 32 + lane] =
-                    make_float4(U[2 * pr + e][0], U[2 * pr + e][1], U[2 * pr + e][2], U[2 * pr + e][3]);
+        for (int j = 0; j < 8; ++j) {
+            cx[j] = *reinterpret_cast<const float2 *>(sx + 8 * j + q2);
+            be[j] = *reinterpret_cast<const float2 *>(sx + kC + 8 * j + q2);
         }
-        named_bar_sync(1 + u, 64);
-#pragma unroll
-        for (int pi = 0; pi < 2; ++pi)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = 2 * (pi ? or1 : or0) + e;
-                const float4 o = ub[((1 - KW) * 4 + 2 * pi + e) * 32 + lane];
-                U[j][0] = o.x; U[j][1] = o.y; U[j][2] = o.z; U[j][3] = o.w;
-            }
-        // S^T = exp(G_last) S^T + (x U)^T K over this warp's key rows
         const float gl = sx[3 * kC];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int pr = 0; pr < 4; ++pr) {
+            ldsm4(th[0][pr], sb + kSaT + offT[pr]);
+            ldsm4(tl[0][pr], sb + kSaT + kTl + offT[pr]);
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[j][e] *= gl;
+        for (int j = 0; j < 8; ++j) xb[(kw * 8 + j) * 32] = make_float4(X[j][0], X[j][1], X[j][2], X[j][3]);
+        named_bar_sync(1 + u, 64);
+        if (lane == 0) mbar_arrive(&bar->fs[hb]);
+        // right side beta V - x X, split; token tiles 2 ks, 2 ks + 1 are k step ks of the next product
+        uint32_t rh[4][4], rl[4][4];
+        {
+            float4 o[8];
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t ah[4], al[4];
+            for (int j = 0; j < 8; ++j) o[j] = xb[((1 - kw) * 8 + j) * 32];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = 2 * ks + e;
-                const float2 cu = *reinterpret_cast<const float2 *>(sx + 2 * kC + 8 * j + q2);
-                split2(cu.x * U[j][0], cu.y * U[j][1], ah[2 * e], al[2 * e]);
-                split2(cu.x * U[j][2], cu.y * U[j][3], ah[2 * e + 1], al[2 * e + 1]);
-            }
-#pragma unroll
-            for (int jp = 0; jp < 4; ++jp) {
-                uint32_t b[4];
-                ldsm4t(b, sb + KW * 8192 + swz(16 * ks + rowT, 2 * jp + pcT));
-                mma(S[2 * jp], ah, b[0], b[1]);
-                mma(S[2 * jp + 1], ah, b[2], b[3]);
-                mma(S[2 * jp], al, b[0], b[1]);
-                mma(S[2 * jp + 1], al, b[2], b[3]);
+            for (int j = 0; j < 8; ++j) {
+                const int ks = j >> 1, e = j & 1;
+                const float2 m = make_float2(-cx[j].x, -cx[j].y);
+                const float2 v0 = make_float2(lo_f(vv[ks][2 * e]), hi_f(vv[ks][2 * e]));
+                const float2 v1 = make_float2(lo_f(vv[ks][2 * e + 1]), hi_f(vv[ks][2 * e + 1]));
+                const float2 x0 = f2_add(make_float2(X[j][0], X[j][1]), make_float2(o[j].x, o[j].y));
+                const float2 x1 = f2_add(make_float2(X[j][2], X[j][3]), make_float2(o[j].z, o[j].w));
+                split_tile(f2_fma(m, x0, f2_mul(be[j], v0)), f2_fma(m, x1, f2_mul(be[j], v1)), rh[ks] + 2 * e, rl[ks] + 2 * e);
             }
         }
-        // O^T of this warp's token tiles: x (Q S0) + P U
-        uint32_t uh[4][4];
+        // U^T of this warp's tiles, the high products and the mixed ones apart (shorter chains of MMAs)
+        float U[4][4], W[4][4];
 #pragma unroll
-        for (int ks = 0; ks <= pr1; ++ks)
+        for (int pr = 0; pr < 4; ++pr)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uh[ks][2 * e] = pack2(U[2 * ks + e][0], U[2 * ks + e][1]);
-                uh[ks][2 * e + 1] = pack2(U[2 * ks + e][2], U[2 * ks + e][3]);
+            for (int e = 0; e < 4; ++e) U[pr][e] = W[pr][e] = 0.f;
+#pragma unroll
+        for (int pr = 2; pr < 4; ++pr) {
+            ldsm4(th[1][pr], sb + kSaT + (offT[pr] ^ 64));
+            ldsm4(tl[1][pr], sb + kSaT + kTl + (offT[pr] ^ 64));
+        }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const int kp = ks >> 1, k2 = 2 * (ks & 1);
+#pragma unroll
+            for (int pr = ks; pr < 4; ++pr) mma(U[pr], rh[ks], th[kp][pr][k2], th[kp][pr][k2 + 1]);
+#pragma unroll
+            for (int pr = ks; pr < 4; ++pr) mma(W[pr], rl[ks], th[kp][pr][k2], th[kp][pr][k2 + 1]);
+#pragma unroll
+            for (int pr = ks; pr < 4; ++pr) mma(W[pr], rh[ks], tl[kp][pr][k2], tl[kp][pr][k2 + 1]);
+        }
+        // while they run: the state's decay, K as the next B operand, the scalars of U
+        const float2 gl2 = make_float2(gl, gl);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            S[j][0] = f2_mul(S[j][0], gl2);
+            S[j][1] = f2_mul(S[j][1], gl2);
+        }
+        const uint32_t rowT[2] = {(uint32_t)((lane & 7) + ((((lane >> 3) & 1) ^ own(kw, 0)) << 3)),
+                                  (uint32_t)((lane & 7) + ((((lane >> 3) & 1) ^ own(kw, 1)) << 3))};
+        const int pcT = lane >> 4;
+#pragma unroll
+        for (int jp = 0; jp < 4; ++jp) ldsm4t(b[0][jp], sk + swz(rowT[0], 2 * jp + pcT));
+        float2 cu[4][2];  // of the own tile of a pair, of the other's
+#pragma unroll
+        for (int pr = 0; pr < 4; ++pr) {
+            cu[pr][0] = *reinterpret_cast<const float2 *>(sx + 2 * kC + 16 * pr + 8 * own(kw, pr) + q2);
+            cu[pr][1] = *reinterpret_cast<const float2 *>(sx + 2 * kC + 16 * pr + 8 - 8 * own(kw, pr) + q2);
+        }
+#pragma unroll
+        for (int pr = 0; pr < 4; ++pr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) U[pr][e] += W[pr][e];
+            ub[(kw * 4 + pr) * 32] = make_float4(U[pr][0], U[pr][1], U[pr][2], U[pr][3]);
+            hu[(2 * pr + own(kw, pr)) * 32] = make_uint2(pack2(U[pr][0], U[pr][1]), pack2(U[pr][2], U[pr][3]));
+        }
+        uint32_t uh[4][4], ul[4][4];  // (x U)^T of a pair, own tile first
+#pragma unroll
+        for (int pr = 0; pr < 4; ++pr)
+            split_tile(f2_mul(cu[pr][0], make_float2(U[pr][0], U[pr][1])), f2_mul(cu[pr][0], make_float2(U[pr][2], U[pr][3])),
+                       uh[pr], ul[pr]);
+        named_bar_sync(1 + u, 64);
+        if (lane == 0) mbar_arrive(&bar->fh[hb]);
+        // S^T = exp(G_last) S^T + (x U)^T K over this warp's key rows
+        {
+            float4 o[4];
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr) o[pr] = ub[((1 - kw) * 4 + pr) * 32];
+            float acc[8][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                acc[j][0] = S[j][0].x; acc[j][1] = S[j][0].y; acc[j][2] = S[j][1].x; acc[j][3] = S[j][1].y;
             }
-        uint32_t om[4][2];
+            split_tile(f2_mul(cu[0][1], make_float2(o[0].x, o[0].y)), f2_mul(cu[0][1], make_float2(o[0].z, o[0].w)), uh[0] + 2, ul[0] + 2);
 #pragma unroll
-        for (int pi = 0; pi < 2; ++pi) {
-            const int pr = pi ? pr1 : pr0;
-            float o[2][4];
+            for (int ks = 0; ks < 4; ++ks) {
+                const int x = ks & 1, y = x ^ 1;
+                if (ks < 3) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = 2 * pr + e;
-                const float4 w = ob[((1 - KW) * 4 + 2 * pi + e) * 32 + lane];
-                const float2 co = *reinterpret_cast<const float2 *>(sx + kC + 8 * j + q2);
-                o[e][0] = co.x * (O[j][0] + w.x);
-                o[e][1] = co.y * (O[j][1] + w.y);
-                o[e][2] = co.x * (O[j][2] + w.z);
-                o[e][3] = co.y * (O[j][3] + w.w);
+                    for (int jp = 0; jp < 4; ++jp) ldsm4t(b[y][jp], sk + swz(16 * (ks + 1) + rowT[y], 2 * jp + pcT));
+                    split_tile(f2_mul(cu[ks + 1][1], make_float2(o[ks + 1].x, o[ks + 1].y)),
+                               f2_mul(cu[ks + 1][1], make_float2(o[ks + 1].z, o[ks + 1].w)), uh[ks + 1] + 2, ul[ks + 1] + 2);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mma(acc[j], uh[ks], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mma(acc[j], ul[ks], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
             }
 #pragma unroll
-            for (int ks = 0; ks <= pr; ++ks) {
-                uint32_t b[4];
-                ldsm4(b, sb + L::kBlk + kBlkP + swz(16 * pr + rowB, 2 * ks + pcB));
-                mma(o[0], uh[ks], b[0], b[1]);
-                mma(o[1], uh[ks], b[2], b[3]);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                om[2 * pi + e][0] = pack2(o[e][0], o[e][1]);
-                om[2 * pi + e][1] = pack2(o[e][2], o[e][3]);
+            for (int j = 0; j < 8; ++j) {
+                S[j][0] = make_float2(acc[j][0], acc[j][1]);
+                S[j][1] = make_float2(acc[j][2], acc[j][3]);
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
-        // the 32 tokens x 16 values as rows of 32 bytes, staged in this warp's own part of xb: the other
-        // warp read it before the second barrier
-        unsigned char *stg = reinterpret_cast<unsigned char *>(xb + KW * 8 * 32);
+        if (lane == 0) mbar_arrive(&bar->ea[st]);
+        if (++st == kNa) st = 0, pa ^= 1;
+    }
+    return good;
+}
+
+__device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, StBars *bar, int u, int kw, const Place &pl, int h, int v0)
+{
+    const int lane = threadIdx.x & 31, q2 = 2 * (lane & 3);
+    unsigned char *stg = sm + kSmSt + (2 * u + kw) * 1024;
+    const int nc = (pl.len + kC - 1) / kC;
+    uint32_t off[4];  // rows of this warp's tile of pair p, pieces 0..3 (4..7: ^ 64)
+#pragma unroll
+    for (int pr = 0; pr < 4; ++pr) off[pr] = swz(16 * pr + 8 * own(kw, pr) + (lane & 7), lane >> 3);
+    bool good = true;
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c) {
+        const int st = c & 1, hb = c & 1;
+        static_assert(kNo == 2, "two stages");
+        const uint32_t sb = smem_u32(sm + kSmO + st * kSo);
+        const float *co = reinterpret_cast<const float *>(sm + kSmO + st * kSo + kSoP + kPx);
+        const uint4 *hs = reinterpret_cast<const uint4 *>(sm + kSmH + hb * kHand) + u * 256 + lane;
+        const uint2 *hu = reinterpret_cast<const uint2 *>(sm + kSmH + hb * kHand + 8192 + u * 2048) + lane;
+        if (good) good = wait_both(&bar->fo[st], (uint32_t)((c >> 1) & 1), &bar->fs[hb], (uint32_t)((c >> 1) & 1));
+        float o[4][4] = {};
+#pragma unroll
+        for (int kp = 0; kp < 4; ++kp) {
+            const uint4 w0 = hs[(2 * kp) * 32], w1 = hs[(2 * kp + 1) * 32];
+            const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
+            uint32_t b[4][4];
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr) ldsm4(b[pr], sb + (kp >> 1) * 8192 + (off[pr] ^ ((kp & 1) * 64)));
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr) mma(o[pr], a0, b[pr][0], b[pr][1]);
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr) mma(o[pr], a1, b[pr][2], b[pr][3]);
+        }
+#pragma unroll
+        for (int pr = 0; pr < 4; ++pr) {
+            const float2 x = *reinterpret_cast<const float2 *>(co + 16 * pr + 8 * own(kw, pr) + q2);
+            o[pr][0] *= x.x;
+            o[pr][1] *= x.y;
+            o[pr][2] *= x.x;
+            o[pr][3] *= x.y;
+        }
+        if (good) good = mbar_wait_bounded(&bar->fh[hb], (uint32_t)((c >> 1) & 1), kStSpin);
+#pragma unroll
+        for (int kp = 0; kp < 2; ++kp) {
+            uint32_t b[4][4];
+#pragma unroll
+            for (int pr = 2 * kp; pr < 4; ++pr) ldsm4(b[pr], sb + kSoP + (off[pr] ^ (kp * 64)));
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+                const int ks = 2 * kp + k2;
+                const uint2 w0 = hu[2 * ks * 32], w1 = hu[(2 * ks + 1) * 32];
+                const uint32_t a[4] = {w0.x, w0.y, w1.x, w1.y};
+#pragma unroll
+                for (int pr = ks; pr < 4; ++pr) mma(o[pr], a, b[pr][2 * k2], b[pr][2 * k2 + 1]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bar->eh[hb]);
+            mbar_arrive(&bar->eo[st]);
+        }
+        // 32 tokens x 16 values, staged as rows of 32 bytes
+        const int n = min(kC, pl.len - c * kC);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            stsm2t(smem_u32(stg) + (uint32_t)((8 * j + (lane & 7)) * 32 + ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4)), om[j][0], om[j][1]);
+            stsm2t(smem_u32(stg) + (uint32_t)((8 * j + (lane & 7)) * 32 + ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4)),
+                   pack2(o[j][0], o[j][1]), pack2(o[j][2], o[j][3]));
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int x = lane + 32 * i, r = x >> 1, half = x & 1;  // row r of the staged 32
-            const int t = r < 16 ? 16 * pr0 + r : 16 * pr1 + r - 16;
+            const int r = 16 * i + (lane >> 1), half = lane & 1, pr = r >> 3, t = 16 * pr + 8 * own(kw, pr) + (r & 7);
             const uint4 w = *reinterpret_cast<const uint4 *>(stg + r * 32 + ((half ^ ((r >> 2) & 1)) << 4));
-            if (t < n) {
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.rows.out) +
-                                   ((int64_t)pl.t0 + c * kC + t) * p.rows.out_stride + (size_t)h * kD + v0 + 16 * u + 8 * half;
-                *reinterpret_cast<uint4 *>(o) = w;
-            }
+            if (t < n)
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.rows.out) + ((int64_t)pl.t0 + c * kC + t) * p.rows.out_stride +
+                                           (size_t)h * kD + v0 + 16 * u + 8 * half) = w;
         }
         __syncwarp();
     }
     return good;
 }
 
-template <int VB>
-__global__ void __launch_bounds__(St<VB>::kThreads, 1)
+__global__ void __launch_bounds__(kStThreads, 1)
 gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__ Args p,
                  const unsigned char *__restrict__ blocks, int64_t n_chunks, int box_rows)
 {
-    using L = St<VB>;
     extern __shared__ unsigned char sm_raw[];
     unsigned char *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::kBar), *empty = full + L::kStages;
-    Place *place = reinterpret_cast<Place *>(empty + L::kStages);
+    StBars *bar = reinterpret_cast<StBars *>(sm + kSmBar);
+    Place *place = reinterpret_cast<Place *>(bar + 1);
     int *ok = reinterpret_cast<int *>(place + 1);
+    static_assert(sizeof(StBars) + sizeof(Place) + 8 <= 256, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kVBlocks = kD / VB;
+    constexpr int kVBlocks = kD / kVB;
     const int vb = blockIdx.x % kVBlocks;
     const int h = (blockIdx.x / kVBlocks) % p.H, seq = blockIdx.x / (kVBlocks * p.H);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], L::kWarps);
+        for (int s = 0; s < kNa; ++s) {
+            mbar_init(&bar->fa[s], 1);
+            mbar_init(&bar->ea[s], 4);
+        }
+        for (int s = 0; s < kNo; ++s) {
+            mbar_init(&bar->fo[s], 1);
+            mbar_init(&bar->eo[s], 4);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar->fs[s], 4);
+            mbar_init(&bar->fh[s], 4);
+            mbar_init(&bar->eh[s], 4);
         }
         fence_mbar_init();
     }
-    if (warp == L::kWarps) {
+    if (warp == 8) {
         Place pl;
         const bool good = find_place(p.cu, p.N, p.total_T, n_chunks, 0, seq, pl);
         if (lane == 0) {
@@ -641,60 +809,67 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     }
     const Place pl = *place;
     const int nc = (pl.len + kC - 1) / kC;
-    if (warp == L::kWarps) {
-        if (lane == 0) {
+    // 384 threads x 168 registers at the launch: 128 x (232 + 152 + 56) after this
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 8 && lane == 0) {
             const int hk = h / p.G;
             bool good = true;
-            for (int c = 0; c < nc; ++c) {
-                const int st = c % L::kStages;
-                if (c >= L::kStages && !mbar_wait_bounded(&empty[st], (uint32_t)(((c / L::kStages) - 1) & 1), kStSpin)) {
-                    good = false;
-                    break;
-                }
-                unsigned char *b = sm + st * L::kStage;
-                const int t = pl.t0 + c * kC;
-                mbar_arrive_expect_tx(&full[st], (uint32_t)(box_rows * (4 * 128 + VB * 2) + kBlkBytes));
-                tma_load_2d(b, &maps.k, hk * kD, t, &full[st]);
-                tma_load_2d(b + 8192, &maps.k, hk * kD + 64, t, &full[st]);
-                bulk_g2s(b + L::kBlk, blocks + ((size_t)(pl.first + c) * p.H + h) * kBlkBytes, kBlkBytes, &full[st]);
-                tma_load_2d(b + L::kV, &maps.v, h * kD + vb * VB, t, &full[st]);
-                tma_load_2d(b + L::kQ, &maps.q, hk * kD, t, &full[st]);
-                tma_load_2d(b + L::kQ + 8192, &maps.q, hk * kD + 64, t, &full[st]);
+            for (int c = 0; c < nc && good; ++c) {
+                const int sa = c % kNa, so = c % kNo, t = pl.t0 + c * kC;
+                const unsigned char *blk = blocks + ((size_t)(pl.first + c) * p.H + h) * kBlkBytes;
+                if (c >= kNa) good = mbar_wait_bounded(&bar->ea[sa], (uint32_t)(((c / kNa) - 1) & 1), kStSpin);
+                if (!good) break;
+                unsigned char *b = sm + sa * kSa;
+                mbar_arrive_expect_tx(&bar->fa[sa], (uint32_t)(box_rows * (2 * 128 + kVB * 2) + kPartT));
+                tma_load_2d(b, &maps.k, hk * kD, t, &bar->fa[sa]);
+                tma_load_2d(b + 8192, &maps.k, hk * kD + 64, t, &bar->fa[sa]);
+                bulk_g2s(b + kSaT, blk, kPartT, &bar->fa[sa]);
+                tma_load_2d(b + kSaV, &maps.v, h * kD + vb * kVB, t, &bar->fa[sa]);
+                if (c >= kNo) good = mbar_wait_bounded(&bar->eo[so], (uint32_t)(((c / kNo) - 1) & 1), kStSpin);
+                if (!good) break;
+                b = sm + kSmO + so * kSo;
+                mbar_arrive_expect_tx(&bar->fo[so], (uint32_t)(box_rows * 2 * 128 + kPartP));
+                tma_load_2d(b, &maps.q, hk * kD, t, &bar->fo[so]);
+                tma_load_2d(b + 8192, &maps.q, hk * kD + 64, t, &bar->fo[so]);
+                bulk_g2s(b + kSoP, blk + kPartT, kPartP, &bar->fo[so]);
             }
             if (!good) {
                 if (p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
-                for (int s = 0; s < L::kStages; ++s) mbar_wait_bounded(&full[s], 0, 1u << 16);  // copies in flight land
+                for (int s = 0; s < kNa; ++s) mbar_wait_bounded(&bar->fa[s], 0, 1u << 16);  // copies in flight land
             }
         }
         return;
     }
-    // this warp's part of S^T: value rows g, g + 8 of unit u, key rows 64 kw ..
-    const int u = warp >> 1, kw = warp & 1, g = lane >> 2, q2 = 2 * (lane & 3);
-    const size_t at = (size_t)(64 * kw + q2) * kD + vb * VB + 16 * u + g;
-    float S[8][4];
-    if (src >= 0) {
-        const float *s = p.S + ((size_t)src * p.H + h) * kD * kD + at;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[j][e] = s[(8 * j + (e & 1)) * kD + 8 * (e >> 1)];
+    const int u = (warp >> 1) & 1, kw = warp & 1;
+    bool good;
+    if (warp >= 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
+        good = output_pass(p, sm, bar, u, kw, pl, h, vb * kVB);
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        // this warp's part of S^T: value rows g, g + 8 of unit u, key rows 64 kw ..
+        const int g = lane >> 2, q2 = 2 * (lane & 3);
+        const size_t at = (size_t)(64 * kw + q2) * kD + vb * kVB + 16 * u + g;
+        float2 S[8][2];
+        const float *s = p.S + ((size_t)max(src, 0) * p.H + h) * kD * kD + at;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[j][e] = 0.f;
-    }
-    const bool good = kw == 0 ? state_pass<VB, 0>(p, sm, full, empty, u, pl, h, vb * VB, S)
-                              : state_pass<VB, 1>(p, sm, full, empty, u, pl, h, vb * VB, S);
-    if (!good) {
-        if (lane == 0 && p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
-        return;
-    }
-    float *d = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
+            for (int e = 0; e < 2; ++e)
+                S[j][e] = src >= 0 ? make_float2(s[8 * j * kD + 8 * e], s[(8 * j + 1) * kD + 8 * e]) : make_float2(0.f, 0.f);
+        good = chain_pass(sm, bar, u, kw, pl.len, S);
+        float *d = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
+        if (good)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[(8 * j + (e & 1)) * kD + 8 * (e >> 1)] = S[j][e];
+                for (int e = 0; e < 2; ++e) {
+                    d[8 * j * kD + 8 * e] = S[j][e].x;
+                    d[(8 * j + 1) * kD + 8 * e] = S[j][e].y;
+                }
+    }
+    if (!good && lane == 0 && p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
 }
 
 cudaError_t rows_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t stride, int box_cols, int box_rows)
@@ -712,7 +887,6 @@ cudaError_t rows_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int VB>
 cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_chunks, cudaStream_t stream)
 {
     const int64_t T = p.total_T;
@@ -723,13 +897,12 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
         const int64_t Dk = (int64_t)(p.H / p.G) * kD, Dv = (int64_t)p.H * kD;
         if ((e = rows_map(&m.k, p.rows.k, T, Dk, p.rows.k_stride, 64, box)) != cudaSuccess ||
             (e = rows_map(&m.q, p.rows.q, T, Dk, p.rows.q_stride, 64, box)) != cudaSuccess ||
-            (e = rows_map(&m.v, p.rows.v, T, Dv, p.rows.v_stride, VB, box)) != cudaSuccess)
+            (e = rows_map(&m.v, p.rows.v, T, Dv, p.rows.v_stride, kVB, box)) != cudaSuccess)
             return e;
     }
-    e = cudaFuncSetAttribute(gdr_state_kernel<VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, St<VB>::kSmem);
+    e = cudaFuncSetAttribute(gdr_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem);
     if (e != cudaSuccess) return e;
-    gdr_state_kernel<VB><<<(unsigned)((int64_t)p.N * p.H * (kD / VB)), St<VB>::kThreads, St<VB>::kSmem, stream>>>(
-        m, p, blocks, n_chunks, box);
+    gdr_state_kernel<<<(unsigned)((int64_t)p.N * p.H * (kD / kVB)), kStThreads, kStSmem, stream>>>(m, p, blocks, n_chunks, box);
     return cudaGetLastError();
 }
 
@@ -737,20 +910,19 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
 
 size_t chunked_workspace_bytes(int64_t n_chunks, int32_t H) { return 256 + (size_t)n_chunks * H * kBlkBytes; }
 
-cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int sms, cudaStream_t stream)
+cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, cudaStream_t stream)
 {
     unsigned char *blocks = static_cast<unsigned char *>(ws) +
                             ((128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127);
     cudaError_t e;
     if (n_chunks > 0) {
         const int Hk = p.H / p.G;
-        e = cudaFuncSetAttribute(gdr_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
+        e = cudaFuncSetAttribute(gdr_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem(2));
         if (e != cudaSuccess) return e;
-        gdr_prep_kernel<<<(unsigned)(n_chunks * Hk), kPrepThreads, kPrepSmem, stream>>>(p, blocks, n_chunks, Hk);
+        gdr_prep_kernel<<<(unsigned)(n_chunks * Hk), kPrepThreads, prep_smem(p.G), stream>>>(p, blocks, n_chunks, Hk);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return (int64_t)p.N * p.H * 4 <= 2 * (int64_t)sms ? launch_state<32>(p, blocks, n_chunks, stream)
-                                                      : launch_state<64>(p, blocks, n_chunks, stream);
+    return launch_state(p, blocks, n_chunks, stream);
 }
 
 }  // namespace gdr

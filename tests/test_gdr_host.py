@@ -30,7 +30,7 @@ def test_config(K):
 def test_workspace(K):
     c = K.kda_gdr_config(4, 2)
     one = K.kda_gdr_workspace_bytes(c, [0, 64]) - K.kda_gdr_workspace_bytes(c, [0, 0])
-    assert one == 4 * 25600
+    assert one == 4 * 25856
     for cu, chunks in (([0, 1], 1), ([0, 65], 2), ([0, 0, 64, 64, 129], 3), ([0, 2 ** 31 - 1], 2 ** 25)):
         assert K.kda_gdr_workspace_bytes(c, cu) == K.kda_gdr_workspace_bytes(c, [0, 0]) + chunks * one
     for cu in ([1, 2], [0, 5, 4], [0, -1]):
