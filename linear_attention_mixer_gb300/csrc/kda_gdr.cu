@@ -360,7 +360,10 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
         if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need)
             return gdr::fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed",
                              workspace_bytes, need);
-        e = gdr::launch_chunked(p, nc, workspace, static_cast<cudaStream_t>(stream));
+        int dev = 0, sms = 0;
+        if ((e = cudaGetDevice(&dev)) == cudaSuccess &&
+            (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) == cudaSuccess)
+            e = gdr::launch_chunked(p, nc, workspace, sms, static_cast<cudaStream_t>(stream));
     }
     return e == cudaSuccess ? KDA_OK : gdr::fail(KDA_ERR_CUDA, "kda_gdr_prefill: %s", cudaGetErrorString(e));
 }

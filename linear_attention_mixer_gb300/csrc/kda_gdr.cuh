@@ -57,7 +57,7 @@ __device__ __forceinline__ float log_decay(float a, float dt_bias, float expA)
 cudaError_t launch_recurrent(const Args &p, bool f32, int64_t n_rows, cudaStream_t stream);
 
 size_t chunked_workspace_bytes(int64_t n_chunks, int32_t H);
-cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, cudaStream_t stream);
+cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int sms, cudaStream_t stream);
 
 }  // namespace gdr
 }  // namespace kda

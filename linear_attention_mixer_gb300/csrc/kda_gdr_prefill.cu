@@ -90,29 +90,30 @@ __device__ __forceinline__ float ex2(float x)
 // One warp reads cu_seqlens once: checks it against what the host sized the call for and finds either
 // the sequence of chunk `want` (seq < 0 on entry) or the first chunk of sequence seq. Every lane gets
 // the result; false on a mismatch.
-struct Place { int seq, t0, len; int64_t first; };
-__device__ __forceinline__ bool find_place(const int32_t *cu, int N, int64_t total_T, int64_t n_chunks, int64_t want,
-                                           int seq, Place &out)
+struct Place { int seq, t0, len, first; };
+__device__ __forceinline__ bool find_place(const int32_t *cu, int N, int64_t total_T, int64_t n_chunks, int want, int seq,
+                                           Place &out)
 {
     const int lane = threadIdx.x & 31;
-    int64_t base = 0;
+    int base = 0;  // the host has checked that chunks x heads fit 28 bits; a cu_seqlens that says otherwise is not ok
     bool ok = true, found = false;
-    for (int s0 = 0; s0 < N; s0 += 32) {
+    for (int s0 = 0; s0 < N && ok; s0 += 32) {
         const int s = s0 + lane;
         int b = 0, e = 0;
         if (s < N) {
             b = __ldg(cu + s);
             e = __ldg(cu + s + 1);
-            ok = ok && b >= 0 && e >= b && (s > 0 || b == 0) && (s < N - 1 || e == total_T);
+            ok = b >= 0 && e >= b && e <= total_T && (s > 0 || b == 0) && (s < N - 1 || e == total_T);
         }
-        int nc = e >= b ? (e - b + kC - 1) / kC : 0;
-        const int mine = nc;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        const int mine = ok ? (e - b + kC - 1) / kC : 0;
+        int nc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xFFFFFFFFu, nc, o);
             if (lane >= o) nc += x;
         }
-        const int64_t before = base + nc - mine;
+        const int before = base + nc - mine;
         const bool hit = s < N && (seq >= 0 ? s == seq : (want >= before && want < before + mine));
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
         if (m && !found) {
@@ -125,7 +126,17 @@ __device__ __forceinline__ bool find_place(const int32_t *cu, int N, int64_t tot
         }
         base += __shfl_sync(0xFFFFFFFFu, nc, 31);
     }
-    return __all_sync(0xFFFFFFFFu, ok) && base == n_chunks && found;
+    return ok && base == n_chunks && found;
+}
+
+// (h, l) += (x, y) for sums kept as two FP32, |l| far below |h| (the exact error of the addition by Knuth's
+// two-sum)
+__device__ __forceinline__ void add2(float &h, float &l, float x, float y)
+{
+    const float s = h + x, t = s - h;
+    const float e = (h - (s - t)) + (x - t) + (l + y);
+    h = s + e;
+    l = e - (h - s);
 }
 
 // ---------------------------------------------------------------- prep
@@ -134,16 +145,15 @@ __device__ __forceinline__ bool find_place(const int32_t *cu, int N, int64_t tot
 //   T[w][:] = -D_w sum_{j < w} A[w][j] T[j][:]
 // on the tensor cores with split factors, three barriers deep. (The whole inverse by forward
 // substitution, a column a lane, took 92 us for 4096 (chunk, value head) pairs; see the launch below.)
-// Shared memory: K and Q rows, in whose place the first block is then built; a second block when there
-// is more than one value head a key head; A's diagonal blocks; scalars of up to four value heads.
-constexpr int kPrepThreads = 128;
-constexpr int kPsQ = 16384, kPsB1 = 32768;
+// Shared memory: two buffers of K and Q rows (the next item's are loaded while one is computed; a block is
+// built in the place of the rows that it came from), A's diagonal blocks, scalars of up to four value heads.
+constexpr int kPrepThreads = 128, kPrepPerSm = 3;
+constexpr int kPsQ = 16384, kPsBuf = 32768;
 constexpr int kDp = 20;                               // row pitch of a diagonal block of A^T
-constexpr int kPsDiag = 0, kPsScal = 4 * 16 * kDp * 4;  // relative to the end of the blocks
-constexpr int kScal = 5 * kC;                         // per head: G high, G low, beta, exp G, exp(G_last - G)
-constexpr int kPsNorm = kPsScal + 4 * (kScal + 4) * 4;
-constexpr int kPsPlace = kPsNorm + 2 * kC * 4, kPsTail = kPsPlace + 64;
-constexpr int prep_smem(int G) { return kPsB1 + (G > 1 ? kBlkBytes : 0) + kPsTail; }
+constexpr int kScal = 5 * kC + 4;                     // per head: G high, G low, beta, exp G, exp(G_last - G); exp G_last
+constexpr int kPsDiag = 2 * kPsBuf, kPsScal = kPsDiag + 4 * 16 * kDp * 4, kPsNorm = kPsScal + 4 * kScal * 4;
+constexpr int kPrepSmem = kPsNorm + 2 * kC * 4;
+static_assert(kBlkBytes <= kPsBuf && kPrepPerSm * (kPrepSmem + 1024) <= 228 * 1024, "prep shared memory");
 
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes)
 {
@@ -151,90 +161,115 @@ __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t by
                  : "memory");
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 4)
-gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ blocks, int64_t n_chunks, int Hk)
+__global__ void __launch_bounds__(kPrepThreads, kPrepPerSm)
+gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ blocks, int n_chunks, int Hk)
 {
-    extern __shared__ __align__(1024) unsigned char sm[];
-    unsigned char *tail = sm + kPsB1 + (p.G > 1 ? kBlkBytes : 0);
-    Place *place = reinterpret_cast<Place *>(tail + kPsPlace);
-    int *ok = reinterpret_cast<int *>(place + 1);
+    extern __shared__ __align__(1024) unsigned char sm_all[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q2 = 2 * (lane & 3);
-    const int64_t chunk = blockIdx.x / Hk;
-    const int hk = (int)(blockIdx.x - chunk * Hk);
-    if (warp == 0) {
+    float *sRk = reinterpret_cast<float *>(sm_all + kPsNorm), *sRq = sRk + kC;
+    float *scal = reinterpret_cast<float *>(sm_all + kPsScal);
+    float *diag = reinterpret_cast<float *>(sm_all + kPsDiag) + warp * 16 * kDp;
+    const int n_items = n_chunks * Hk;  // (chunk, key head), key heads fastest
+    struct Item { int chunk, hk, n; int64_t t0; };
+    auto locate = [&](int item, Item &x) {
+        x.chunk = item / Hk;
+        x.hk = item - x.chunk * Hk;
         Place pl;
-        const bool good = find_place(p.cu, p.N, p.total_T, n_chunks, chunk, -1, pl);
-        if (lane == 0) {
-            *place = pl;
-            *ok = good;
-            if (!good) set_err(p.err);
-        }
-    }
-    __syncthreads();
-    if (!*ok) return;
-    const int pos = (int)(chunk - place->first) * kC;
-    const int64_t t0 = (int64_t)place->t0 + pos;
-    const int n = min(kC, place->len - pos);
-    const uint32_t sK = smem_u32(sm), sQ = sK + kPsQ;
-    float *sRk = reinterpret_cast<float *>(tail + kPsNorm), *sRq = sRk + kC;
-    float *scal = reinterpret_cast<float *>(tail + kPsScal);
-    float *diag = reinterpret_cast<float *>(tail + kPsDiag) + warp * 16 * kDp;
-
+        if (!find_place(p.cu, p.N, p.total_T, n_chunks, x.chunk, -1, pl)) return false;
+        const int pos = (x.chunk - pl.first) * kC;
+        x.t0 = (int64_t)pl.t0 + pos;
+        x.n = min(kC, pl.len - pos);
+        return true;
+    };
     // rows n .. 63 read as zeros
-    const __nv_bfloat16 *kg = static_cast<const __nv_bfloat16 *>(p.rows.k) + t0 * p.rows.k_stride + (size_t)hk * kD;
-    const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(p.rows.q) + t0 * p.rows.q_stride + (size_t)hk * kD;
+    auto load_rows = [&](const Item &x, unsigned char *sm) {
+        const __nv_bfloat16 *kg = static_cast<const __nv_bfloat16 *>(p.rows.k) + x.t0 * p.rows.k_stride + (size_t)x.hk * kD;
+        const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(p.rows.q) + x.t0 * p.rows.q_stride + (size_t)x.hk * kD;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int x = tid + i * kPrepThreads, r = x >> 4, c = x & 15;  // 16 pieces of 16 bytes a row
-        const uint32_t off = (uint32_t)(c >> 3) * 8192 + swz(r, c & 7);
-        const int rr = r < n ? r : 0;
-        cp_async16(sm + off, kg + rr * p.rows.k_stride + 8 * c, r < n ? 16 : 0);
-        cp_async16(sm + kPsQ + off, qg + rr * p.rows.q_stride + 8 * c, r < n ? 16 : 0);
-    }
-    // decays of value head j + warp, two tokens a lane. The sums are taken in 64 bits and kept as two FP32,
-    // so that differences of tokens far down a strongly decaying chunk stay exact.
-    auto decays = [&](int j) {
+        for (int i = 0; i < 8; ++i) {
+            const int r = (tid >> 4) + 8 * i, c = tid & 15;  // 16 pieces of 16 bytes a row
+            const uint32_t off = (uint32_t)(c >> 3) * 8192 + swz(r, c & 7);
+            const int rr = r < x.n ? r : 0;
+            cp_async16(sm + off, kg + rr * p.rows.k_stride + 8 * c, r < x.n ? 16 : 0);
+            cp_async16(sm + kPsQ + off, qg + rr * p.rows.q_stride + 8 * c, r < x.n ? 16 : 0);
+        }
+    };
+    // decay and beta logits of value head j + warp, two tokens a lane
+    struct Logits { float a[2], b[2], A_log, dt_bias; };
+    auto load_logits = [&](const Item &x, int j, Logits &l) {
         if (j + warp >= p.G) return;
-        const int h = hk * p.G + j + warp;
-        const float expA = expf(__ldg(p.A_log + h)), dtb = __ldg(p.dt_bias + h);
-        const __nv_bfloat16 *ag = static_cast<const __nv_bfloat16 *>(p.rows.a) + t0 * p.rows.a_stride + h;
-        const __nv_bfloat16 *bg = static_cast<const __nv_bfloat16 *>(p.rows.b) + t0 * p.rows.b_stride + h;
-        float *s = scal + warp * (kScal + 4);
-        double ga[2];
-        float be[2];
+        const int h = x.hk * p.G + j + warp;
+        const __nv_bfloat16 *ag = static_cast<const __nv_bfloat16 *>(p.rows.a) + x.t0 * p.rows.a_stride + h;
+        const __nv_bfloat16 *bg = static_cast<const __nv_bfloat16 *>(p.rows.b) + x.t0 * p.rows.b_stride + h;
+        l.A_log = __ldg(p.A_log + h);
+        l.dt_bias = __ldg(p.dt_bias + h);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int t = 2 * lane + e;
-            ga[e] = 0.0;
-            be[e] = 0.f;
-            if (t < n) {
-                ga[e] = (double)log_decay(__bfloat162float(ag[t * p.rows.a_stride]), dtb, expA) * 1.4426950408889634;
-                be[e] = sigmoidf_(__bfloat162float(bg[t * p.rows.b_stride]));
-            }
+            const int t = min(2 * lane + e, x.n - 1);
+            l.a[e] = __bfloat162float(ag[t * p.rows.a_stride]);
+            l.b[e] = __bfloat162float(bg[t * p.rows.b_stride]);
         }
-        double c = ga[0] + ga[1];
+    };
+    // The sums are kept as two FP32, so that differences of tokens far down a strongly decaying chunk stay exact.
+    auto decays = [&](const Item &x, int j, const Logits &l) {
+        if (j + warp >= p.G) return;
+        const float expA = expf(l.A_log);
+        float *s = scal + warp * kScal;
+        float ga[2], be[2];  // base-2 logarithms
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bool in = 2 * lane + e < x.n;
+            ga[e] = in ? log_decay(l.a[e], l.dt_bias, expA) * 1.4426950408889634f : 0.f;
+            be[e] = in ? sigmoidf_(l.b[e]) : 0.f;
+        }
+        float ch = ga[0], cl = 0.f;
+        add2(ch, cl, ga[1], 0.f);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_up_sync(0xFFFFFFFFu, c, o);
-            if (lane >= o) c += x;
+            const float xh = __shfl_up_sync(0xFFFFFFFFu, ch, o), xl = __shfl_up_sync(0xFFFFFFFFu, cl, o);
+            if (lane >= o) add2(ch, cl, xh, xl);
         }
-        const double last = __shfl_sync(0xFFFFFFFFu, c, 31);
-        const double Gs[2] = {c - ga[1], c};
+        const float lh = __shfl_sync(0xFFFFFFFFu, ch, 31), ll = __shfl_sync(0xFFFFFFFFu, cl, 31);
+        float h0 = ch, l0 = cl;  // of token 2 lane
+        add2(h0, l0, -ga[1], 0.f);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = 2 * lane + e;
-            const float h0 = (float)Gs[e];
-            s[t] = h0;
-            s[kC + t] = (float)(Gs[e] - (double)h0);
+            const float Gh = e ? ch : h0, Gl = e ? cl : l0;
+            s[t] = Gh;
+            s[kC + t] = Gl;
             s[2 * kC + t] = be[e];
-            s[3 * kC + t] = ex2(h0);
-            s[4 * kC + t] = ex2((float)(last - Gs[e]));
+            s[3 * kC + t] = ex2(Gh);
+            s[4 * kC + t] = ex2((lh - Gh) + (ll - Gl));
         }
-        if (lane == 0) s[5 * kC] = ex2((float)last);
+        if (lane == 0) s[5 * kC] = ex2(lh);
     };
-    decays(0);
+
+    int item = blockIdx.x, buf = 0;
+    Item cur, nxt;
+    if (!locate(item, cur)) {  // the same for every thread
+        if (tid == 0) set_err(p.err);
+        return;
+    }
+    Logits lg;
+    load_rows(cur, sm_all);
+    load_logits(cur, 0, lg);
+#pragma unroll 1
+    for (; item < n_items; item += gridDim.x, buf ^= 1, cur = nxt) {
+    unsigned char *sm = sm_all + buf * kPsBuf;
+    const uint32_t sK = smem_u32(sm), sQ = sK + kPsQ;
+    const int64_t chunk = cur.chunk;
+    const int hk = cur.hk;
+    const bool more = item + (int)gridDim.x < n_items;
+    if (more) locate(item + gridDim.x, nxt);
+    decays(cur, 0, lg);
     cp_async_wait_all();
+    if (tid == 0) bulk_wait_read_all();  // the other buffer's block has been read
     __syncthreads();
+    if (more) {
+        load_rows(nxt, sm_all + (buf ^ 1) * kPsBuf);
+        load_logits(nxt, 0, lg);
+    }
     {  // norms: two threads a row of K and of Q
         const int r = tid >> 1, half = tid & 1;
         float kk = 0.f, qq = 0.f;
@@ -284,25 +319,18 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
     const int rowT = (lane & 7) + (((lane >> 3) & 1) << 3), pcT = lane >> 4;  // ldmatrix.trans of B operands
 #pragma unroll 1
     for (int j = 0; j < p.G; ++j) {
-        unsigned char *blk = j & 1 ? sm + kPsB1 : sm;
-        const uint32_t sT = smem_u32(blk);
+        unsigned char *blk = sm;
+        const uint32_t sT = sK;
         if (j && (j & 3) == 0) {
             __syncthreads();  // every warp has read the last four heads' scalars
-            decays(j);
+            Logits l;
+            load_logits(cur, j, l);
+            decays(cur, j, l);
         }
-        if (tid == 0 && j > 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncthreads();  // K, Q are read, the scalars are written, this block's last store has read it
-        const float *s = scal + (j & 3) * (kScal + 4);
-        if (tid < kC) {
-            float *x = reinterpret_cast<float *>(blk + kTx);
-            x[tid] = s[2 * kC + tid] * sRk[tid] * s[3 * kC + tid];
-            x[kC + tid] = s[2 * kC + tid];
-            x[2 * kC + tid] = sRk[tid] * s[4 * kC + tid];
-            if (tid == 0) x[3 * kC] = s[5 * kC];
-            reinterpret_cast<float *>(blk + kPartT + kPx)[tid] = sRq[tid] * s[3 * kC + tid];
-        }
+        if (j == 0 || (j & 3) == 0) __syncthreads();  // scalars and norms are written
+        const float *s = scal + (j & 3) * kScal;
         // A and P from the products: A's blocks left of the diagonal stay in registers as split A operands
-        uint32_t ah[3][4], al[3][4];
+        uint32_t ah[3][4], al[3][4], pk[8][2];
         {
             const int ta = 16 * warp + g;
             float Gh[2], Gl[2], fb[2], fq[2];
@@ -332,7 +360,7 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
                     }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    *reinterpret_cast<uint32_t *>(blk + kPartT + swz(ta + 8 * e, nt) + 2 * q2) = pack2(pv[e][0], pv[e][1]);
+                    pk[nt][e] = pack2(pv[e][0], pv[e][1]);
                     if ((nt >> 1) < warp) {
                         if (nt < 6) split2(av[e][0], av[e][1], ah[(nt >> 1) % 3][2 * (nt & 1) + e], al[(nt >> 1) % 3][2 * (nt & 1) + e]);
                     } else {
@@ -343,26 +371,46 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
             }
         }
         __syncwarp();
-        {  // the diagonal block: column lane & 15; lanes 0..15 store its high part, lanes 16..31 its low part
-            const int jc = lane & 15;
-            float acc[16];
+        const int jc = lane & 15;  // the diagonal block's inverse: column lane & 15
+        float acc[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[r] = r == jc ? 1.f : 0.f;
+        for (int r = 0; r < 16; ++r) acc[r] = r == jc ? 1.f : 0.f;
 #pragma unroll
-            for (int r = 0; r < 15; ++r) {
-                float a[16];
+        for (int r = 0; r < 15; ++r) {
+            float a[16];
 #pragma unroll
-                for (int e = (r + 1) / 4; e < 4; ++e)
-                    *reinterpret_cast<float4 *>(a + 4 * e) = *reinterpret_cast<const float4 *>(diag + r * kDp + 4 * e);
+            for (int e = (r + 1) / 4; e < 4; ++e)
+                *reinterpret_cast<float4 *>(a + 4 * e) = *reinterpret_cast<const float4 *>(diag + r * kDp + 4 * e);
 #pragma unroll
-                for (int r2 = r + 1; r2 < 16; ++r2) acc[r2] = fmaf(-a[r2], acc[r], acc[r2]);
-            }
-            unsigned char *dst = blk + (lane & 16 ? kTl : 0) + 2 * (jc & 7);
+            for (int r2 = r + 1; r2 < 16; ++r2) acc[r2] = fmaf(-a[r2], acc[r], acc[r2]);
+        }
+        if (j) {
+            if (tid == 0) bulk_wait_read_all();  // the previous head's block has been read
+            __syncthreads();
+        }
+        // the block takes the place of K and Q (read before the first head's barrier above)
+        {
+            unsigned char *dst = blk + (lane & 16 ? kTl : 0) + 2 * (jc & 7);  // lanes 0..15 the high part, 16..31 the low
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const __nv_bfloat16 hi = __float2bfloat16_rn(acc[r]);
                 const __nv_bfloat16 lo = __float2bfloat16_rn(acc[r] - __bfloat162float(hi));
                 *reinterpret_cast<__nv_bfloat16 *>(dst + swz(16 * warp + r, 2 * warp + (jc >> 3))) = lane & 16 ? lo : hi;
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                if ((nt >> 1) > warp) break;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<uint32_t *>(blk + kPartT + swz(16 * warp + g + 8 * e, nt) + 2 * q2) = pk[nt][e];
+            }
+            if (tid < kC) {
+                float *x = reinterpret_cast<float *>(blk + kTx);
+                x[tid] = s[2 * kC + tid] * sRk[tid] * s[3 * kC + tid];
+                x[kC + tid] = s[2 * kC + tid];
+                x[2 * kC + tid] = sRk[tid] * s[4 * kC + tid];
+                if (tid == 0) x[3 * kC] = s[5 * kC];
+                reinterpret_cast<float *>(blk + kPartT + kPx)[tid] = sRq[tid] * s[3 * kC + tid];
             }
         }
         float Y[6][4];
@@ -437,6 +485,7 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
             bulk_commit_group();
         }
     }
+    }
     if (tid == 0) bulk_wait_all();
 }
 
@@ -461,7 +510,7 @@ constexpr int kNa = 3, kNo = 2;  // stages of the two rings
 constexpr int kSaT = 16384, kSaV = kSaT + kPartT, kSa = kSaV + kC * kVB * 2;
 constexpr int kSoP = 16384, kSo = 25600;
 constexpr int kSmO = kNa * kSa, kSmX = kSmO + kNo * kSo;  // X: [2 units][2 kw][8 tiles][32 lanes] float4
-constexpr int kSmU = kSmX + 16384, kSmH = kSmU + 8192;    // U: [2][2][4][32] float4; hand-over buffers
+constexpr int kSmU = kSmX + 16384, kSmH = kSmU + 8192;    // U split: [2][2][4][32] uint4; hand-over buffers
 constexpr int kHand = 12288;                              // S [2][8 k steps][32] uint4, U [2][4][32] uint4
 constexpr int kSmSt = kSmH + 2 * kHand, kSmBar = kSmSt + 4096;
 constexpr int kStSmem = kSmBar + 256 + 1024;
@@ -483,7 +532,9 @@ __device__ __forceinline__ int own(int kw, int p) { return (p ^ kw) & 1; }
 __device__ __forceinline__ bool wait_both(uint64_t *x, uint32_t px, uint64_t *y, uint32_t py)
 {
     const bool odd = threadIdx.x & 1;
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odd ? y : x, odd ? py : px, kStSpin));
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odd ? y : x, odd ? py : px, kStSpin));
+    __syncwarp();
+    return ok;
 }
 
 // The two k halves of a fragment of 16 values rows by 16, from FP32 pairs, split
@@ -497,7 +548,7 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
 {
     const int lane = threadIdx.x & 31, q2 = 2 * (lane & 3);
     float4 *xb = reinterpret_cast<float4 *>(sm + kSmX) + u * 512 + lane;
-    float4 *ub = reinterpret_cast<float4 *>(sm + kSmU) + u * 256 + lane;
+    uint4 *ub = reinterpret_cast<uint4 *>(sm + kSmU) + u * 256 + lane;
     const int nc = (len + kC - 1) / kC;
     bool good = true;
     // row and 16-byte piece within an ldmatrix of B operands: two tiles of tokens in rows, or tokens as k
@@ -507,18 +558,22 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
 #pragma unroll
     for (int pr = 0; pr < 4; ++pr) offT[pr] = swz(16 * pr + 8 * own(kw, pr) + (lane & 7), lane >> 3);
     int st = 0, pa = 0;
-#pragma unroll 1
-    for (int c = 0; c < nc; ++c) {
-        const int hb = c & 1;
+    uint32_t b[2][4][4];          // B operands of a k step, fetched a step ahead
+    uint32_t ah[2][4], al[2][4];  // A operand of a k step, split a step ahead
+    // Chunk c's stage has arrived and its hand-over buffer is free. peek asks both barriers once, without using
+    // the answer yet; enter waits if it was no, and fetches the first B operands. (After a wait that gave up the
+    // warp goes on without waiting, so that every barrier is met.)
+    auto peek = [&](int c) {
+        const bool odd = lane & (c >= 2);
+        return mbar_try_wait(odd ? &bar->eh[c & 1] : &bar->fa[st], odd ? (uint32_t)(((c >> 1) - 1) & 1) : (uint32_t)pa);
+    };
+    auto enter = [&](int c, bool ready) {
         unsigned char *base = sm + st * kSa;
-        const uint32_t sb = smem_u32(base), sk = sb + kw * 8192;
-        uint4 *hs = reinterpret_cast<uint4 *>(sm + kSmH + hb * kHand) + u * 256 + kw * 128 + lane;
-        uint2 *hu = reinterpret_cast<uint2 *>(sm + kSmH + hb * kHand + 8192 + u * 2048) + lane;
-        const int n = min(kC, len - c * kC);
-        // after a wait that gave up the warp goes on without waiting, so that every barrier is met
-        if (good)
+        if (!__all_sync(0xFFFFFFFFu, ready) && good)
             good = c < 2 ? mbar_wait_bounded(&bar->fa[st], (uint32_t)pa, kStSpin)
-                         : wait_both(&bar->fa[st], (uint32_t)pa, &bar->eh[hb], (uint32_t)(((c >> 1) - 1) & 1));
+                         : wait_both(&bar->fa[st], (uint32_t)pa, &bar->eh[c & 1], (uint32_t)(((c >> 1) - 1) & 1));
+        __syncwarp();
+        const int n = len - c * kC;
         if (n < kC) {  // the last chunk: what follows the sequence in K and V counts as zero
             for (int x = threadIdx.x; x < (kC - n) * 16; x += 128)
                 *reinterpret_cast<uint4 *>(base + ((x >> 3) & 1) * 8192 + (n + (x >> 4)) * 128 + (x & 7) * 16) =
@@ -527,17 +582,25 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
                 *reinterpret_cast<uint4 *>(base + kSaV + n * kVB * 2 + x * 16) = make_uint4(0, 0, 0, 0);
             named_bar_sync(3, 128);
         }
+        const uint32_t sk = smem_u32(base) + kw * 8192;
+#pragma unroll
+        for (int jp = 0; jp < 4; ++jp) ldsm4(b[0][jp], sk + swz(16 * jp + rowB, pcB));
+    };
+    if (nc > 0) enter(0, false);
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c) {
+        const int hb = c & 1, now = st;
+        unsigned char *base = sm + st * kSa;
+        const uint32_t sb = smem_u32(base), sk = sb + kw * 8192;
+        uint4 *hs = reinterpret_cast<uint4 *>(sm + kSmH + hb * kHand) + u * 256 + kw * 128 + lane;
+        uint2 *hu = reinterpret_cast<uint2 *>(sm + kSmH + hb * kHand + 8192 + u * 2048) + lane;
         const float *sx = reinterpret_cast<const float *>(base + kSaT + kTx);
-        uint32_t b[2][4][4];      // B operands of a k step, fetched a step ahead
-        uint32_t ah[2][4], al[2][4];  // A operand of a k step, split a step ahead
         // X^T over this warp's 64 key rows
         float X[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) X[j][e] = 0.f;
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) ldsm4(b[0][jp], sk + swz(16 * jp + rowB, pcB));
 #pragma unroll
         for (int e = 0; e < 2; ++e) split_tile(S[e][0], S[e][1], ah[0] + 2 * e, al[0] + 2 * e);
 #pragma unroll
@@ -626,45 +689,44 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
         const int pcT = lane >> 4;
 #pragma unroll
         for (int jp = 0; jp < 4; ++jp) ldsm4t(b[0][jp], sk + swz(rowT[0], 2 * jp + pcT));
-        float2 cu[4][2];  // of the own tile of a pair, of the other's
+        float2 cu[4];
 #pragma unroll
-        for (int pr = 0; pr < 4; ++pr) {
-            cu[pr][0] = *reinterpret_cast<const float2 *>(sx + 2 * kC + 16 * pr + 8 * own(kw, pr) + q2);
-            cu[pr][1] = *reinterpret_cast<const float2 *>(sx + 2 * kC + 16 * pr + 8 - 8 * own(kw, pr) + q2);
-        }
+        for (int pr = 0; pr < 4; ++pr) cu[pr] = *reinterpret_cast<const float2 *>(sx + 2 * kC + 16 * pr + 8 * own(kw, pr) + q2);
+        uint32_t uh[4][4], ul[4][4];  // (x U)^T of a pair, own tile first
 #pragma unroll
         for (int pr = 0; pr < 4; ++pr) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) U[pr][e] += W[pr][e];
-            ub[(kw * 4 + pr) * 32] = make_float4(U[pr][0], U[pr][1], U[pr][2], U[pr][3]);
             hu[(2 * pr + own(kw, pr)) * 32] = make_uint2(pack2(U[pr][0], U[pr][1]), pack2(U[pr][2], U[pr][3]));
-        }
-        uint32_t uh[4][4], ul[4][4];  // (x U)^T of a pair, own tile first
-#pragma unroll
-        for (int pr = 0; pr < 4; ++pr)
-            split_tile(f2_mul(cu[pr][0], make_float2(U[pr][0], U[pr][1])), f2_mul(cu[pr][0], make_float2(U[pr][2], U[pr][3])),
+            split_tile(f2_mul(cu[pr], make_float2(U[pr][0], U[pr][1])), f2_mul(cu[pr], make_float2(U[pr][2], U[pr][3])),
                        uh[pr], ul[pr]);
+            ub[(kw * 4 + pr) * 32] = make_uint4(uh[pr][0], uh[pr][1], ul[pr][0], ul[pr][1]);
+        }
         named_bar_sync(1 + u, 64);
         if (lane == 0) mbar_arrive(&bar->fh[hb]);
         // S^T = exp(G_last) S^T + (x U)^T K over this warp's key rows
+        bool ready = true;
         {
-            float4 o[4];
 #pragma unroll
-            for (int pr = 0; pr < 4; ++pr) o[pr] = ub[((1 - kw) * 4 + pr) * 32];
+            for (int pr = 0; pr < 4; ++pr) {
+                const uint4 o = ub[((1 - kw) * 4 + pr) * 32];
+                uh[pr][2] = o.x; uh[pr][3] = o.y; ul[pr][2] = o.z; ul[pr][3] = o.w;
+            }
             float acc[8][4];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 acc[j][0] = S[j][0].x; acc[j][1] = S[j][0].y; acc[j][2] = S[j][1].x; acc[j][3] = S[j][1].y;
             }
-            split_tile(f2_mul(cu[0][1], make_float2(o[0].x, o[0].y)), f2_mul(cu[0][1], make_float2(o[0].z, o[0].w)), uh[0] + 2, ul[0] + 2);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 const int x = ks & 1, y = x ^ 1;
                 if (ks < 3) {
 #pragma unroll
                     for (int jp = 0; jp < 4; ++jp) ldsm4t(b[y][jp], sk + swz(16 * (ks + 1) + rowT[y], 2 * jp + pcT));
-                    split_tile(f2_mul(cu[ks + 1][1], make_float2(o[ks + 1].x, o[ks + 1].y)),
-                               f2_mul(cu[ks + 1][1], make_float2(o[ks + 1].z, o[ks + 1].w)), uh[ks + 1] + 2, ul[ks + 1] + 2);
+                }
+                if (ks == 2 && c + 1 < nc) {
+                    if (++st == kNa) st = 0, pa ^= 1;
+                    ready = peek(c + 1);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) mma(acc[j], uh[ks], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
@@ -678,8 +740,8 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->ea[st]);
-        if (++st == kNa) st = 0, pa ^= 1;
+        if (lane == 0) mbar_arrive(&bar->ea[now]);
+        if (c + 1 < nc) enter(c + 1, ready);
     }
     return good;
 }
@@ -701,42 +763,43 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
         const float *co = reinterpret_cast<const float *>(sm + kSmO + st * kSo + kSoP + kPx);
         const uint4 *hs = reinterpret_cast<const uint4 *>(sm + kSmH + hb * kHand) + u * 256 + lane;
         const uint2 *hu = reinterpret_cast<const uint2 *>(sm + kSmH + hb * kHand + 8192 + u * 2048) + lane;
+        // Q is read once the chain has handed over S0, while it makes little use of shared memory itself
         if (good) good = wait_both(&bar->fo[st], (uint32_t)((c >> 1) & 1), &bar->fs[hb], (uint32_t)((c >> 1) & 1));
+        uint32_t qb[4][4][4];
+#pragma unroll
+        for (int kp = 0; kp < 4; ++kp)
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr) ldsm4(qb[kp][pr], sb + (kp >> 1) * 8192 + (off[pr] ^ ((kp & 1) * 64)));
         float o[4][4] = {};
 #pragma unroll
-        for (int kp = 0; kp < 4; ++kp) {
-            const uint4 w0 = hs[(2 * kp) * 32], w1 = hs[(2 * kp + 1) * 32];
-            const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
-            uint32_t b[4][4];
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint4 w = hs[ks * 32];
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int pr = 0; pr < 4; ++pr) ldsm4(b[pr], sb + (kp >> 1) * 8192 + (off[pr] ^ ((kp & 1) * 64)));
+            for (int pr = 0; pr < 4; ++pr) mma(o[pr], a, qb[ks >> 1][pr][2 * (ks & 1)], qb[ks >> 1][pr][2 * (ks & 1) + 1]);
+        }
+        uint32_t pb[2][4][4];
+        float2 x[4];
 #pragma unroll
-            for (int pr = 0; pr < 4; ++pr) mma(o[pr], a0, b[pr][0], b[pr][1]);
-#pragma unroll
-            for (int pr = 0; pr < 4; ++pr) mma(o[pr], a1, b[pr][2], b[pr][3]);
+        for (int pr = 0; pr < 4; ++pr) {
+            ldsm4(pb[0][pr], sb + kSoP + off[pr]);
+            if (pr >= 2) ldsm4(pb[1][pr], sb + kSoP + (off[pr] ^ 64));
+            x[pr] = *reinterpret_cast<const float2 *>(co + 16 * pr + 8 * own(kw, pr) + q2);
         }
 #pragma unroll
         for (int pr = 0; pr < 4; ++pr) {
-            const float2 x = *reinterpret_cast<const float2 *>(co + 16 * pr + 8 * own(kw, pr) + q2);
-            o[pr][0] *= x.x;
-            o[pr][1] *= x.y;
-            o[pr][2] *= x.x;
-            o[pr][3] *= x.y;
+            o[pr][0] *= x[pr].x;
+            o[pr][1] *= x[pr].y;
+            o[pr][2] *= x[pr].x;
+            o[pr][3] *= x[pr].y;
         }
         if (good) good = mbar_wait_bounded(&bar->fh[hb], (uint32_t)((c >> 1) & 1), kStSpin);
 #pragma unroll
-        for (int kp = 0; kp < 2; ++kp) {
-            uint32_t b[4][4];
+        for (int ks = 0; ks < 4; ++ks) {
+            const uint2 w0 = hu[2 * ks * 32], w1 = hu[(2 * ks + 1) * 32];
+            const uint32_t a[4] = {w0.x, w0.y, w1.x, w1.y};
 #pragma unroll
-            for (int pr = 2 * kp; pr < 4; ++pr) ldsm4(b[pr], sb + kSoP + (off[pr] ^ (kp * 64)));
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-                const int ks = 2 * kp + k2;
-                const uint2 w0 = hu[2 * ks * 32], w1 = hu[(2 * ks + 1) * 32];
-                const uint32_t a[4] = {w0.x, w0.y, w1.x, w1.y};
-#pragma unroll
-                for (int pr = ks; pr < 4; ++pr) mma(o[pr], a, b[pr][2 * k2], b[pr][2 * k2 + 1]);
-            }
+            for (int pr = ks; pr < 4; ++pr) mma(o[pr], a, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
         }
         __syncwarp();
         if (lane == 0) {
@@ -910,16 +973,18 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
 
 size_t chunked_workspace_bytes(int64_t n_chunks, int32_t H) { return 256 + (size_t)n_chunks * H * kBlkBytes; }
 
-cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, cudaStream_t stream)
+cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int sms, cudaStream_t stream)
 {
     unsigned char *blocks = static_cast<unsigned char *>(ws) +
                             ((128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127);
     cudaError_t e;
     if (n_chunks > 0) {
         const int Hk = p.H / p.G;
-        e = cudaFuncSetAttribute(gdr_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem(2));
+        e = cudaFuncSetAttribute(gdr_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
         if (e != cudaSuccess) return e;
-        gdr_prep_kernel<<<(unsigned)(n_chunks * Hk), kPrepThreads, prep_smem(p.G), stream>>>(p, blocks, n_chunks, Hk);
+        const int64_t items = n_chunks * Hk;
+        const unsigned grid = (unsigned)(items < (int64_t)kPrepPerSm * sms ? items : (int64_t)kPrepPerSm * sms);
+        gdr_prep_kernel<<<grid, kPrepThreads, kPrepSmem, stream>>>(p, blocks, (int)n_chunks, Hk);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return launch_state(p, blocks, n_chunks, stream);
