@@ -31,91 +31,123 @@ namespace {
 // ---------------------------------------------------------------- quantiser
 constexpr int kQb = 128;  // columns per scale
 
-// The scale of a group whose largest finite magnitude is amax: 2^e, e the smallest integer with amax <=
+// The scale of a group whose largest finite magnitude has the bits u: 2^e, e the smallest integer with it <=
 // 448 2^e (448 is E4M3's largest number), at least 2^-126; 1 for an empty or all-zero group. x / 2^e is
 // exact (but for what is far below E4M3's smallest step), so q is x rounded once.
-__device__ __forceinline__ void q8_scale(float amax, float &s, float &inv)
+__device__ __forceinline__ void q8_scale(uint32_t u, float &s, float &inv)
 {
-    if (!(amax > 0.f)) {
+    if (u == 0) {
         s = inv = 1.f;
         return;
     }
-    const uint32_t u = __float_as_uint(amax);
     int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);  // 448 = 1.75 x 2^8
     e = max(e, -126);
     s = __uint_as_float((uint32_t)(e + 127) << 23);
     inv = __uint_as_float((uint32_t)(127 - e) << 23);
 }
-__device__ __forceinline__ float q8_mag(float x)
-{
-    const float m = fabsf(x);
-    return m < INFINITY ? m : 0.f;  // NaN and infinity do not set the scale
-}
-// E4M3 codes of two values; what is not finite becomes NaN
-__device__ __forceinline__ uint32_t q8_pair(float x, float y, float inv)
-{
-    x = fabsf(x) < INFINITY ? x * inv : __uint_as_float(0x7FC00000u);
-    y = fabsf(y) < INFINITY ? y * inv : __uint_as_float(0x7FC00000u);
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-}
-
-template <typename T> __device__ __forceinline__ void q8_load8(const T *p, float (&f)[8]);
-template <> __device__ __forceinline__ void q8_load8(const __nv_bfloat16 *p, float (&f)[8])
-{
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 values as they lie in memory
+template <typename T> struct Q8;
+template <> struct Q8<__nv_bfloat16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void bits(uint32_t (&u)[8]) const
+    {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) u[2 * i] = w[i] << 16, u[2 * i + 1] = w[i] & 0xFFFF0000u;
     }
-}
-template <> __device__ __forceinline__ void q8_load8(const float *p, float (&f)[8])
+};
+template <> struct Q8<float> {
+    uint4 r[2];
+    __device__ __forceinline__ void load(const float *p)
+    {
+        r[0] = __ldcs(reinterpret_cast<const uint4 *>(p));
+        r[1] = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { r[0] = r[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void bits(uint32_t (&u)[8]) const
+    {
+        u[0] = r[0].x; u[1] = r[0].y; u[2] = r[0].z; u[3] = r[0].w;
+        u[4] = r[1].x; u[5] = r[1].y; u[6] = r[1].z; u[7] = r[1].w;
+    }
+};
+
+constexpr uint32_t kQInf = 0x7F800000u;  // magnitudes from here on are not finite
+
+// The largest magnitude of 8 values, as bits (whose order is that of the magnitudes).
+template <typename T> __device__ __forceinline__ uint32_t q8_max(const Q8<T> &x)
 {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    uint32_t u[8], m = 0;
+    x.bits(u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, u[i] & 0x7FFFFFFFu);
+    return m;
 }
-__device__ __forceinline__ uint2 q8_eight(const float (&f)[8], float inv)
+// The same over what is finite.
+template <typename T> __device__ __forceinline__ uint32_t q8_max_finite(const Q8<T> &x)
 {
-    return make_uint2(q8_pair(f[0], f[1], inv) | q8_pair(f[2], f[3], inv) << 16,
-                      q8_pair(f[4], f[5], inv) | q8_pair(f[6], f[7], inv) << 16);
+    uint32_t u[8], m = 0;
+    x.bits(u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t a = u[i] & 0x7FFFFFFFu;
+        if (a < kQInf) m = max(m, a);
+    }
+    return m;
+}
+// E4M3 codes. `odd`: some value of the group is not finite; such values become NaN.
+template <typename T> __device__ __forceinline__ uint2 q8_codes(const Q8<T> &x, float inv, bool odd)
+{
+    uint32_t u[8], c[4];
+    x.bits(u);
+    if (odd)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((u[i] & 0x7FFFFFFFu) >= kQInf) u[i] = 0x7FC00000u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(u[2 * i]) * inv, __uint_as_float(u[2 * i + 1]) * inv),
+                                                  __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-// One scale per row and 128 columns: 16 lanes a group, 8 values a lane; kG groups a lane so that as many
+// One scale per row and 128 columns: 16 lanes a group, 8 values a lane, kG groups a lane so that as many
 // loads are in flight.
 template <typename T, int kG>
 __global__ void __launch_bounds__(256)
-q8_rows_kernel(const T *__restrict__ x, int64_t stride, int64_t M, int K, int nkb, unsigned char *__restrict__ q,
+q8_rows_kernel(const T *__restrict__ x, int64_t stride, int groups, int K, int nkb, unsigned char *__restrict__ q,
                float *__restrict__ s)
 {
     const int lane16 = threadIdx.x & 15;
-    const int64_t groups = M * nkb;
-    const int64_t first = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kG;
-    float f[kG][8];
-    int64_t row[kG];
-    int col[kG];
+    const int first = blockIdx.x * (16 * kG) + (threadIdx.x >> 4);  // groups first, first + 16, ..
+    Q8<T> f[kG];
+    int row[kG], col[kG];
 #pragma unroll
     for (int i = 0; i < kG; ++i) {
-        const int64_t g = first + i;
-        row[i] = g / nkb;
-        col[i] = (int)(g - row[i] * nkb) * kQb + 8 * lane16;
-        if (g < groups && col[i] < K) q8_load8<T>(x + row[i] * stride + col[i], f[i]);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+        const int g = first + 16 * i;
+        row[i] = (int)((unsigned)g / (unsigned)nkb);
+        col[i] = (g - row[i] * nkb) * kQb + 8 * lane16;
+        if (g < groups && col[i] < K) f[i].load(x + row[i] * stride + col[i]);
+        else f[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < kG; ++i) {
-        float m = 0.f;
+        uint32_t m = q8_max(f[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, q8_mag(f[i][e]));
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const bool odd = m >= kQInf;
+        if (__any_sync(0xFFFFFFFFu, odd)) {  // both groups of the warp
+            m = q8_max_finite(f[i]);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        }
         float sc, inv;
         q8_scale(m, sc, inv);
-        if (first + i < groups) {
-            if (col[i] < K) *reinterpret_cast<uint2 *>(q + row[i] * K + col[i]) = q8_eight(f[i], inv);
-            if (lane16 == 0) s[first + i] = sc;
+        const int g = first + 16 * i;
+        if (g < groups) {
+            if (col[i] < K) __stcs(reinterpret_cast<uint2 *>(q + (int64_t)row[i] * K + col[i]), q8_codes(f[i], inv, odd));
+            if (lane16 == 0) s[g] = sc;
         }
     }
 }
@@ -123,41 +155,43 @@ q8_rows_kernel(const T *__restrict__ x, int64_t stride, int64_t M, int K, int nk
 // One scale per 128 x 128 block: a thread block each, 64 values a thread in registers.
 template <typename T>
 __global__ void __launch_bounds__(256)
-q8_blocks_kernel(const T *__restrict__ x, int64_t stride, int64_t M, int K, int nkb, unsigned char *__restrict__ q,
+q8_blocks_kernel(const T *__restrict__ x, int64_t stride, int M, int K, int nkb, unsigned char *__restrict__ q,
                  float *__restrict__ s)
 {
-    __shared__ float part[8];
-    const int64_t mb = blockIdx.x / nkb;
-    const int kb = (int)(blockIdx.x - mb * nkb);
-    const int col = kb * kQb + 8 * (threadIdx.x & 15);
-    const int64_t r0 = mb * 128 + (threadIdx.x >> 4);
-    float f[8][8];
-    float m = 0.f;
+    __shared__ uint32_t part[2][8];
+    const int mb = blockIdx.x / nkb, kb = blockIdx.x - mb * nkb;
+    const int col = kb * kQb + 8 * (threadIdx.x & 15), r0 = mb * 128 + (threadIdx.x >> 4);
+    Q8<T> f[8];
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + 16 * i;
-        if (r < M && col < K) q8_load8<T>(x + r * stride + col, f[i]);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+        if (r0 + 16 * i < M && col < K) f[i].load(x + (r0 + 16 * i) * stride + col);
+        else f[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, q8_mag(f[i][e]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    for (int i = 0; i < 8; ++i) m = max(m, q8_max(f[i]));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, part[w]);
+    for (int w = 0; w < 8; ++w) m = max(m, part[0][w]);
+    const bool odd = m >= kQInf;  // the same for every thread
+    if (odd) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, q8_max_finite(f[i]));
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if ((threadIdx.x & 31) == 0) part[1][threadIdx.x >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m = max(m, part[1][w]);
+    }
     float sc, inv;
     q8_scale(m, sc, inv);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + 16 * i;
-        if (r < M && col < K) *reinterpret_cast<uint2 *>(q + r * K + col) = q8_eight(f[i], inv);
-    }
+    for (int i = 0; i < 8; ++i)
+        if (r0 + 16 * i < M && col < K)
+            __stcs(reinterpret_cast<uint2 *>(q + (int64_t)(r0 + 16 * i) * K + col), q8_codes(f[i], inv, odd));
     if (threadIdx.x == 0) s[blockIdx.x] = sc;
 }
 
@@ -558,18 +592,19 @@ extern "C" kda_status kda_quant_fp8(int64_t M, int32_t K, const void *x, int64_t
         (M > 1 && (x_stride * es) % 16))
         return f8_fail(KDA_ERR_INVALID, "x and q must be 16-byte aligned, x_stride a multiple of 16 bytes, s 4-byte aligned");
     const int nkb = (K + kQb - 1) / kQb;
-    if (M * nkb > INT_MAX) return f8_fail(KDA_ERR_INVALID, "M * K is too large");
+    if (M * nkb > INT_MAX - 128) return f8_fail(KDA_ERR_INVALID, "M * K is too large");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char *qp = static_cast<unsigned char *>(q);
     if (block_rows == 1) {
         constexpr int kG = 4;
-        const unsigned grid = (unsigned)((M * nkb + 16 * kG - 1) / (16 * kG));
-        if (es == 2) q8_rows_kernel<__nv_bfloat16, kG><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16 *>(x), x_stride, M, K, nkb, qp, s);
-        else q8_rows_kernel<float, kG><<<grid, 256, 0, st>>>(static_cast<const float *>(x), x_stride, M, K, nkb, qp, s);
+        const int groups = (int)(M * nkb);
+        const unsigned grid = (unsigned)((groups + 16 * kG - 1) / (16 * kG));
+        if (es == 2) q8_rows_kernel<__nv_bfloat16, kG><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16 *>(x), x_stride, groups, K, nkb, qp, s);
+        else q8_rows_kernel<float, kG><<<grid, 256, 0, st>>>(static_cast<const float *>(x), x_stride, groups, K, nkb, qp, s);
     } else {
         const unsigned grid = (unsigned)((M + 127) / 128 * nkb);
-        if (es == 2) q8_blocks_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16 *>(x), x_stride, M, K, nkb, qp, s);
-        else q8_blocks_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float *>(x), x_stride, M, K, nkb, qp, s);
+        if (es == 2) q8_blocks_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16 *>(x), x_stride, (int)M, K, nkb, qp, s);
+        else q8_blocks_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float *>(x), x_stride, (int)M, K, nkb, qp, s);
     }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? KDA_OK : f8_fail(KDA_ERR_CUDA, "kda_quant_fp8: %s", cudaGetErrorString(e));
