@@ -265,6 +265,7 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
     uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    if (sh.split > 1) launch_dependents();  // the kernel that adds the splits
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -466,6 +467,7 @@ f8_reduce_kernel(const float *__restrict__ part, const __nv_bfloat16 *__restrict
 {
     const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
     const int64_t plane = (int64_t)M * N;
+    wait_for_previous();  // the partial sums
     if (e >= plane) return;
     const int64_t m = e / N;
     const int n = (int)(e - m * N);
@@ -678,9 +680,9 @@ extern "C" kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void
     if (e != cudaSuccess) return f8_fail(KDA_ERR_CUDA, "kda_linear_fp8: %s", cudaGetErrorString(e));
     if (sh.split > 1) {
         const int64_t total8 = (int64_t)M * N / 8;
-        f8_reduce_kernel<<<(unsigned)((total8 + 255) / 256), 256, 0, s>>>(part, static_cast<const __nv_bfloat16 *>(r),
-                                                                          static_cast<__nv_bfloat16 *>(y), M, N, sh.split, ysplit);
-        if ((e = cudaGetLastError()) != cudaSuccess) return f8_fail(KDA_ERR_CUDA, "kda_linear_fp8: %s", cudaGetErrorString(e));
+        e = launch_after(f8_reduce_kernel, dim3((unsigned)((total8 + 255) / 256)), dim3(256), 0, s, (const float *)part,
+                         static_cast<const __nv_bfloat16 *>(r), static_cast<__nv_bfloat16 *>(y), M, N, sh.split, ysplit);
+        if (e != cudaSuccess) return f8_fail(KDA_ERR_CUDA, "kda_linear_fp8: %s", cudaGetErrorString(e));
     }
     return KDA_OK;
 }

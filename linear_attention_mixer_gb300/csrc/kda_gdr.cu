@@ -66,9 +66,72 @@ struct Token {
     float v, a, b;
 };
 
+// Sums of p = S^T k and r = S^T q over the rows of all lanes, for the column 4 cg + (rg & 3) of this lane:
+// halving exchanges over rg; lane bit 4 keeps p (0) or r (1), bits 3 and 2 pick the column.
+__device__ __forceinline__ void column_sums(float2 p01, float2 p23, float2 r01, float2 r23, int lane, float &ps, float &rs)
+{
+    const bool hi = lane & 16, b3 = lane & 8, b2 = lane & 4;
+    float x0 = hi ? r01.x : p01.x, x1 = hi ? r01.y : p01.y, x2 = hi ? r23.x : p23.x, x3 = hi ? r23.y : p23.y;
+    x0 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p01.x : r01.x, 16);
+    x1 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p01.y : r01.y, 16);
+    x2 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p23.x : r23.x, 16);
+    x3 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p23.y : r23.y, 16);
+    float y0 = b3 ? x2 : x0, y1 = b3 ? x3 : x1;
+    y0 += __shfl_xor_sync(0xFFFFFFFFu, b3 ? x0 : x2, 8);
+    y1 += __shfl_xor_sync(0xFFFFFFFFu, b3 ? x1 : x3, 8);
+    float z = b2 ? y1 : y0;
+    z += __shfl_xor_sync(0xFFFFFFFFu, b2 ? y0 : y1, 4);
+    const float z2 = __shfl_xor_sync(0xFFFFFFFFu, z, 16);
+    ps = hi ? z2 : z;
+    rs = hi ? z : z2;
+}
+// this lane's 16 rows of its 4 columns: p += S^T k, r += S^T q
+__device__ __forceinline__ void column_partials(const float4 (&s)[16], const float (&k)[16], const float (&q)[16], float2 &p01,
+                                                float2 &p23, float2 &r01, float2 &r23)
+{
+    p01 = p23 = r01 = r23 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 k2 = make_float2(k[i], k[i]), q2 = make_float2(q[i], q[i]);
+        const float2 s01 = make_float2(s[i].x, s[i].y), s23 = make_float2(s[i].z, s[i].w);
+        p01 = f2_fma(k2, s01, p01);
+        p23 = f2_fma(k2, s23, p23);
+        r01 = f2_fma(q2, s01, r01);
+        r23 = f2_fma(q2, s23, r23);
+    }
+}
+// S = alpha S + k w^T; w is of column c = rg & 3 of every lane's own cg
+__device__ __forceinline__ void column_update(float4 (&s)[16], const float (&k)[16], float alpha, float w, int cg)
+{
+    const float w0 = __shfl_sync(0xFFFFFFFFu, w, cg), w1 = __shfl_sync(0xFFFFFFFFu, w, cg + 4);
+    const float w2 = __shfl_sync(0xFFFFFFFFu, w, cg + 8), w3 = __shfl_sync(0xFFFFFFFFu, w, cg + 12);
+    const float2 w01 = make_float2(w0, w1), w23 = make_float2(w2, w3), al = make_float2(alpha, alpha);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 k2 = make_float2(k[i], k[i]);
+        const float2 s01 = f2_fma(k2, w01, f2_mul(al, make_float2(s[i].x, s[i].y)));
+        const float2 s23 = f2_fma(k2, w23, f2_mul(al, make_float2(s[i].z, s[i].w)));
+        s[i] = make_float4(s01.x, s01.y, s23.x, s23.y);
+    }
+}
+__device__ __forceinline__ void load_state(float4 (&s)[16], const Args &p, int src, int h, size_t at)
+{
+    const float *S = p.S + ((size_t)max(src, 0) * p.H + h) * kD * kD + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        s[i] = src >= 0 ? ld_stream(reinterpret_cast<const float4 *>(S + i * kD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+__device__ __forceinline__ void store_state(const float4 (&s)[16], const Args &p, int dst, int h, size_t at)
+{
+    float *S = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st_stream(reinterpret_cast<float4 *>(S + i * kD), s[i]);
+}
+
+// Decode: n tokens for each row, the next token's row fetched while one is computed.
 template <typename T>
 __global__ void __launch_bounds__(32 * kRecWarps)
-gdr_recurrent_kernel(const __grid_constant__ Args p, int64_t n_units)
+gdr_decode_kernel(const __grid_constant__ Args p, int64_t n_units)
 {
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kRecWarps + (threadIdx.x >> 5);  // (row, head, 16 columns)
@@ -82,25 +145,10 @@ gdr_recurrent_kernel(const __grid_constant__ Args p, int64_t n_units)
         if (lane == 0) set_err(p.err);
         return;
     }
-    int64_t t0 = (int64_t)row * p.n, t1 = t0 + p.n;
-    if (p.cu) {
-        t0 = __ldg(p.cu + row);
-        t1 = __ldg(p.cu + row + 1);
-        if (t0 < 0 || t1 < t0 || t1 > p.total_T) {
-            if (lane == 0) set_err(p.err);
-            return;
-        }
-    }
+    const int64_t t0 = (int64_t)row * p.n, t1 = t0 + p.n;
     const size_t at = (size_t)(16 * rg) * kD + 16 * cb + 4 * cg;
     float4 s[16];
-    if (src >= 0) {
-        const float *S = p.S + ((size_t)src * p.H + h) * kD * kD + at;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = ld_stream(reinterpret_cast<const float4 *>(S + i * kD));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    load_state(s, p, src, h, at);
     const int hk = h / p.G, col = 16 * cb + 4 * cg + c;
     const float expA = expf(__ldg(p.A_log + h)), dt_bias = __ldg(p.dt_bias + h);
     const T *kp = static_cast<const T *>(p.rows.k) + (size_t)hk * kD + 16 * rg;
@@ -117,7 +165,7 @@ gdr_recurrent_kernel(const __grid_constant__ Args p, int64_t n_units)
         x.b = IO<T>::ld(bp + t * p.rows.b_stride);
     };
     Token<T> next;
-    if (t0 < t1) load(t0, next);
+    load(t0, next);
 #pragma unroll 1
     for (int64_t t = t0; t < t1; ++t) {
         float k[16], q[16];
@@ -144,48 +192,138 @@ gdr_recurrent_kernel(const __grid_constant__ Args p, int64_t n_units)
         }
         const float rk = p.l2norm ? rsqrtf(kk + p.l2_eps) : 1.f;
         const float rq = p.l2norm ? p.q_scale * rsqrtf(qq + p.l2_eps) : p.q_scale;
-        float2 p01 = make_float2(0.f, 0.f), p23 = p01, r01 = p01, r23 = p01;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 k2 = make_float2(k[i], k[i]), q2 = make_float2(q[i], q[i]);
-            const float2 s01 = make_float2(s[i].x, s[i].y), s23 = make_float2(s[i].z, s[i].w);
-            p01 = f2_fma(k2, s01, p01);
-            p23 = f2_fma(k2, s23, p23);
-            r01 = f2_fma(q2, s01, r01);
-            r23 = f2_fma(q2, s23, r23);
-        }
-        // halving exchanges over rg: lane bit 4 keeps p (0) or r (1), bits 3 and 2 pick the column c = rg & 3
-        const bool hi = lane & 16, b3 = lane & 8, b2 = lane & 4;
-        float x0 = hi ? r01.x : p01.x, x1 = hi ? r01.y : p01.y, x2 = hi ? r23.x : p23.x, x3 = hi ? r23.y : p23.y;
-        x0 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p01.x : r01.x, 16);
-        x1 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p01.y : r01.y, 16);
-        x2 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p23.x : r23.x, 16);
-        x3 += __shfl_xor_sync(0xFFFFFFFFu, hi ? p23.y : r23.y, 16);
-        float y0 = b3 ? x2 : x0, y1 = b3 ? x3 : x1;
-        y0 += __shfl_xor_sync(0xFFFFFFFFu, b3 ? x0 : x2, 8);
-        y1 += __shfl_xor_sync(0xFFFFFFFFu, b3 ? x1 : x3, 8);
-        float z = b2 ? y1 : y0;
-        z += __shfl_xor_sync(0xFFFFFFFFu, b2 ? y0 : y1, 4);
-        const float z2 = __shfl_xor_sync(0xFFFFFFFFu, z, 16);
-        const float ps = hi ? z2 : z, rs = hi ? z : z2;
+        float2 p01, p23, r01, r23;
+        column_partials(s, k, q, p01, p23, r01, r23);
+        float ps, rs;
+        column_sums(p01, p23, r01, r23, lane, ps, rs);
         const float u = beta * fmaf(-alpha * rk, ps, v);
         const float o = rq * fmaf(rk * kq, u, alpha * rs);
-        if (!hi) IO<T>::st(op + t * p.rows.out_stride, o);
-        const float w = rk * u;  // of column c; this lane updates its columns 0 .. 3
-        const float w0 = __shfl_sync(0xFFFFFFFFu, w, cg), w1 = __shfl_sync(0xFFFFFFFFu, w, cg + 4);
-        const float w2 = __shfl_sync(0xFFFFFFFFu, w, cg + 8), w3 = __shfl_sync(0xFFFFFFFFu, w, cg + 12);
-        const float2 w01 = make_float2(w0, w1), w23 = make_float2(w2, w3), al = make_float2(alpha, alpha);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 k2 = make_float2(k[i], k[i]);
-            const float2 s01 = f2_fma(k2, w01, f2_mul(al, make_float2(s[i].x, s[i].y)));
-            const float2 s23 = f2_fma(k2, w23, f2_mul(al, make_float2(s[i].z, s[i].w)));
-            s[i] = make_float4(s01.x, s01.y, s23.x, s23.y);
-        }
+        if (!(lane & 16)) IO<T>::st(op + t * p.rows.out_stride, o);
+        column_update(s, k, alpha, rk * u, cg);
     }
-    float *D = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
+    store_state(s, p, dst, h, at);
+}
+
+// FP32 prefill: the same walk over whole sequences. A block has half of a (sequence, head); its rows come by
+// eight tokens through a ring of three stages in shared memory, two ahead. What is the same for every column
+// of a token (the gates, the norms, k . q) each warp works out for eight tokens at once, four lanes a token.
+// Bound by the latency of a token's chain (two sums over the rows, an exchange, the update).
+constexpr int kStep = 8, kSeqStages = 3;
+constexpr int kSqK = 0, kSqQ = kStep * 512, kSqV = 2 * kStep * 512, kSqA = kSqV + kStep * 256, kSqB = kSqA + kStep * 4;
+constexpr int kSqStage = kSqB + kStep * 4;
+
+__global__ void __launch_bounds__(128)
+gdr_sequence_kernel(const __grid_constant__ Args p)
+{
+    __shared__ __align__(16) unsigned char ring[kSeqStages][kSqStage];
+    __shared__ __align__(16) float scal[4][kStep][8];  // per warp and token: alpha, beta, -beta alpha rk, rq alpha, rq rk k.q, rk
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int half = blockIdx.x & 1;
+    const int h = (int)((blockIdx.x >> 1) % (unsigned)p.H), row = (int)((blockIdx.x >> 1) / (unsigned)p.H);
+    const int rg = lane >> 2, cg = lane & 3, hk = h / p.G;
+    int src, dst;
+    const int64_t t0 = __ldg(p.cu + row), t1 = __ldg(p.cu + row + 1);
+    if (!slots_ok(p, row, src, dst) || t0 < 0 || t1 < t0 || t1 > p.total_T) {  // the same for every thread
+        if (tid == 0) set_err(p.err);
+        return;
+    }
+    const int n = (int)(t1 - t0), steps = (n + kStep - 1) / kStep;
+    const float *kg = static_cast<const float *>(p.rows.k) + (size_t)hk * kD + t0 * p.rows.k_stride;
+    const float *qg = static_cast<const float *>(p.rows.q) + (size_t)hk * kD + t0 * p.rows.q_stride;
+    const float *vg = static_cast<const float *>(p.rows.v) + (size_t)h * kD + 64 * half + t0 * p.rows.v_stride;
+    const float *ag = static_cast<const float *>(p.rows.a) + h + t0 * p.rows.a_stride;
+    const float *bg = static_cast<const float *>(p.rows.b) + h + t0 * p.rows.b_stride;
+    auto fetch = [&](int st) {
+        if (st < steps) {
+            unsigned char *d = ring[st % kSeqStages];
+            const int t = st * kStep, left = n - t;  // tokens past the end read the last one, and are not used
 #pragma unroll
-    for (int i = 0; i < 16; ++i) st_stream(reinterpret_cast<float4 *>(D + i * kD), s[i]);
+            for (int i = 0; i < 2; ++i) {
+                const int x = tid + 128 * i, r = x >> 5, c = x & 31, rr = t + min(r, left - 1);
+                cp_async16(d + kSqK + r * 512 + c * 16, kg + rr * p.rows.k_stride + 4 * c, 16);
+                cp_async16(d + kSqQ + r * 512 + c * 16, qg + rr * p.rows.q_stride + 4 * c, 16);
+            }
+            const int r = tid >> 4, rr = t + min(r, left - 1);
+            cp_async16(d + kSqV + r * 256 + (tid & 15) * 16, vg + rr * p.rows.v_stride + 4 * (tid & 15), 16);
+            if (tid < 2 * kStep) {
+                const int r2 = tid & (kStep - 1), r3 = t + min(r2, left - 1);
+                const float *g = tid < kStep ? ag + r3 * p.rows.a_stride : bg + r3 * p.rows.b_stride;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(d + (tid < kStep ? kSqA : kSqB) + 4 * r2)), "l"(g) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(0);
+    fetch(1);
+    const int col = 16 * warp + 4 * cg + (rg & 3);  // of this block's 64
+    const size_t at = (size_t)(16 * rg) * kD + 64 * half + 16 * warp + 4 * cg;
+    float4 s[16];
+    load_state(s, p, src, h, at);
+    const float expA = expf(__ldg(p.A_log + h)), dt_bias = __ldg(p.dt_bias + h);
+    float *op = static_cast<float *>(p.rows.out) + (size_t)h * kD + 64 * half + col + t0 * p.rows.out_stride;
+#pragma unroll 1
+    for (int st = 0; st < steps; ++st) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();  // this stage has arrived; the one before it has been read
+        fetch(st + 2);
+        const unsigned char *d = ring[st % kSeqStages];
+        const float *ks = reinterpret_cast<const float *>(d + kSqK), *qs = reinterpret_cast<const float *>(d + kSqQ);
+        const float *vs = reinterpret_cast<const float *>(d + kSqV);
+        {  // lane / 4: token, lane % 4: 32 of its elements (in an order that spreads the lanes over the banks)
+            float kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int x = rg * 128 + cg * 32 + 4 * ((i + lane) & 7);
+                const float4 a = *reinterpret_cast<const float4 *>(ks + x), b = *reinterpret_cast<const float4 *>(qs + x);
+                kk = fmaf(a.x, a.x, fmaf(a.y, a.y, fmaf(a.z, a.z, fmaf(a.w, a.w, kk))));
+                qq = fmaf(b.x, b.x, fmaf(b.y, b.y, fmaf(b.z, b.z, fmaf(b.w, b.w, qq))));
+                kq = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, kq))));
+            }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+                kk += __shfl_xor_sync(0xFFFFFFFFu, kk, o);
+                qq += __shfl_xor_sync(0xFFFFFFFFu, qq, o);
+                kq += __shfl_xor_sync(0xFFFFFFFFu, kq, o);
+            }
+            const float rk = p.l2norm ? rsqrtf(kk + p.l2_eps) : 1.f;
+            const float rq = p.l2norm ? p.q_scale * rsqrtf(qq + p.l2_eps) : p.q_scale;
+            const float alpha = expf(log_decay(reinterpret_cast<const float *>(d + kSqA)[rg], dt_bias, expA));
+            const float beta = sigmoidf_(reinterpret_cast<const float *>(d + kSqB)[rg]);
+            if (cg == 0) {
+                *reinterpret_cast<float4 *>(scal[warp][rg]) = make_float4(alpha, beta, -beta * alpha * rk, rq * alpha);
+                *reinterpret_cast<float2 *>(scal[warp][rg] + 4) = make_float2(rq * rk * kq, rk);
+            }
+            __syncwarp();
+        }
+        const int tn = min(kStep, n - st * kStep);
+        float k[16], q[16];
+        auto load = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 a = *reinterpret_cast<const float4 *>(ks + t * 128 + 16 * rg + 4 * i);
+                const float4 b = *reinterpret_cast<const float4 *>(qs + t * 128 + 16 * rg + 4 * i);
+                k[4 * i] = a.x; k[4 * i + 1] = a.y; k[4 * i + 2] = a.z; k[4 * i + 3] = a.w;
+                q[4 * i] = b.x; q[4 * i + 1] = b.y; q[4 * i + 2] = b.z; q[4 * i + 3] = b.w;
+            }
+        };
+#pragma unroll 2
+        for (int t = 0; t < tn; ++t) {
+            load(t);
+            const float4 c0 = *reinterpret_cast<const float4 *>(scal[warp][t]);
+            const float2 c1 = *reinterpret_cast<const float2 *>(scal[warp][t] + 4);
+            const float v = vs[t * 64 + col];
+            float2 p01, p23, r01, r23;
+            column_partials(s, k, q, p01, p23, r01, r23);
+            float ps, rs;
+            column_sums(p01, p23, r01, r23, lane, ps, rs);
+            const float u = fmaf(c0.z, ps, c0.y * v);
+            if (!(lane & 16)) op[(int64_t)(st * kStep + t) * p.rows.out_stride] = fmaf(c1.x, u, c0.w * rs);
+            column_update(s, k, c0.x, c1.y * u, cg);
+        }
+        __syncwarp();  // the scalars have been read
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    store_state(s, p, dst, h, at);
 }
 
 thread_local char g_msg[256];
@@ -274,12 +412,18 @@ int64_t count_chunks(const int32_t *cu, int32_t N)
 
 }  // namespace
 
-cudaError_t launch_recurrent(const Args &p, bool f32, int64_t n_rows, cudaStream_t stream)
+cudaError_t launch_decode_rows(const Args &p, bool f32, cudaStream_t stream)
 {
-    const int64_t units = n_rows * p.H * (kD / 16);
+    const int64_t units = (int64_t)p.N * p.H * (kD / 16);
     const unsigned grid = (unsigned)((units + kRecWarps - 1) / kRecWarps);
-    if (f32) gdr_recurrent_kernel<float><<<grid, 32 * kRecWarps, 0, stream>>>(p, units);
-    else gdr_recurrent_kernel<__nv_bfloat16><<<grid, 32 * kRecWarps, 0, stream>>>(p, units);
+    if (f32) gdr_decode_kernel<float><<<grid, 32 * kRecWarps, 0, stream>>>(p, units);
+    else gdr_decode_kernel<__nv_bfloat16><<<grid, 32 * kRecWarps, 0, stream>>>(p, units);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_sequences(const Args &p, cudaStream_t stream)
+{
+    gdr_sequence_kernel<<<(unsigned)((int64_t)p.N * p.H * 2), 128, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -321,7 +465,7 @@ kda_status kda_gdr_decode(const kda_gdr_config_t *cfg, const kda_gdr_params *par
     gdr::Args p = gdr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, B, rows, err);
     p.n = n;
     p.total_T = (int64_t)B * n;
-    const cudaError_t e = gdr::launch_recurrent(p, cfg->io_dtype == KDA_F32, B, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = gdr::launch_decode_rows(p, cfg->io_dtype == KDA_F32, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KDA_OK : gdr::fail(KDA_ERR_CUDA, "kda_gdr_decode: %s", cudaGetErrorString(e));
 }
 
@@ -354,7 +498,7 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
     p.total_T = T;
     cudaError_t e;
     if (cfg->io_dtype == KDA_F32) {
-        e = gdr::launch_recurrent(p, true, N, static_cast<cudaStream_t>(stream));
+        e = gdr::launch_sequences(p, static_cast<cudaStream_t>(stream));
     } else {
         const size_t need = gdr::chunked_workspace_bytes(nc, cfg->num_heads);
         if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need)

@@ -21,7 +21,7 @@ struct Args {
     int32_t max_slots;
     const int32_t *src, *dst;
     int32_t *err;          // may be null
-    const int32_t *cu;     // [N + 1], or null: n tokens a row
+    const int32_t *cu;     // prefill: [N + 1]; decode: n tokens a row
     int32_t N, n;
     int64_t total_T;
     int32_t H, G;          // value heads, value heads per key head
@@ -54,7 +54,8 @@ __device__ __forceinline__ float log_decay(float a, float dt_bias, float expA)
     return g < -1e4f ? -1e4f : g;
 }
 
-cudaError_t launch_recurrent(const Args &p, bool f32, int64_t n_rows, cudaStream_t stream);
+cudaError_t launch_decode_rows(const Args &p, bool f32, cudaStream_t stream);  // N rows of n tokens
+cudaError_t launch_sequences(const Args &p, cudaStream_t stream);               // FP32 rows, N sequences
 
 size_t chunked_workspace_bytes(int64_t n_chunks, int32_t H);
 cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int sms, cudaStream_t stream);

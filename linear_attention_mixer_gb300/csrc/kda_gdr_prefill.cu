@@ -245,6 +245,7 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
         if (lane == 0) s[5 * kC] = ex2(lh);
     };
 
+    launch_dependents();
     int item = blockIdx.x, buf = 0;
     Item cur, nxt;
     if (!locate(item, cur)) {  // the same for every thread
@@ -878,6 +879,7 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
         if (warp == 8 && lane == 0) {
             const int hk = h / p.G;
             bool good = true;
+            wait_for_previous();  // the blocks; everything else that is read here is older than the prep kernel
             for (int c = 0; c < nc && good; ++c) {
                 const int sa = c % kNa, so = c % kNo, t = pl.t0 + c * kC;
                 const unsigned char *blk = blocks + ((size_t)(pl.first + c) * p.H + h) * kBlkBytes;
@@ -965,7 +967,10 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
     }
     e = cudaFuncSetAttribute(gdr_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem);
     if (e != cudaSuccess) return e;
-    gdr_state_kernel<<<(unsigned)((int64_t)p.N * p.H * (kD / kVB)), kStThreads, kStSmem, stream>>>(m, p, blocks, n_chunks, box);
+    const unsigned grid = (unsigned)((int64_t)p.N * p.H * (kD / kVB));
+    if (n_chunks > 0) return launch_after(gdr_state_kernel, dim3(grid), dim3(kStThreads), kStSmem, stream, m, p, blocks, n_chunks, box);
+    // no prep kernel before it: whatever the stream holds may still be writing the states
+    gdr_state_kernel<<<grid, kStThreads, kStSmem, stream>>>(m, p, blocks, n_chunks, box);
     return cudaGetLastError();
 }
 
