@@ -22,6 +22,7 @@
 #include <cstring>
 
 #include "kda_internal.cuh"
+#include "kda_launch.cuh"
 #include "kda_ptx.cuh"
 #include "kda_tc.cuh"
 

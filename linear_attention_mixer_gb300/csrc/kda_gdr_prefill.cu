@@ -24,6 +24,7 @@
 #include <cudaTypedefs.h>
 
 #include "kda_gdr.cuh"
+#include "kda_launch.cuh"
 #include "kda_tc.cuh"
 
 namespace kda {

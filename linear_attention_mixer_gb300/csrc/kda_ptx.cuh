@@ -137,11 +137,6 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// Programmatic dependent launch: the next kernel of the stream, if it was launched for it, may start; and in
-// that kernel, wait until the one before has finished and its writes are visible.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // 16-bit read-only global load whose result is not needed until later (no conversion here).
 __device__ __forceinline__ unsigned short ld_nc_u16(const void *p)
 {

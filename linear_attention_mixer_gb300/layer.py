@@ -1,4 +1,4 @@
-"""A whole KDA layer and a stack of them, on the library's kernels only.
+"""Whole layers - a KDA layer and a gated delta rule layer - on the library's kernels only.
 
 Per token of each sequence (kimi_k3.c header comment, block "KDA per-head
 recurrence"; struct Kda: W q, k, v, o, g, fa, fb, bp):
@@ -14,6 +14,15 @@ The residual add stands in for the model's residual stream (the pages' attention
 residuals and the MoE/MLP blocks between KDA layers are other components). This module
 only sequences library calls and owns their buffers; every product and every step of the
 mixer runs in libkda's kernels.
+
+The gated delta rule layer has the same frame around the recurrence with one decay per head:
+
+    q, k, v, a, b = columns of W_in x              one product; its columns go on as they lie
+    o             = kda_gdr_decode / kda_gdr_prefill
+    x'            = x + W_o o
+
+The dense products of either layer run in BF16 (kda_linear) or, for weights given as
+Fp8Weight, in FP8 (kda_quant_fp8 of the activations, kda_linear_fp8).
 """
 from __future__ import annotations
 
@@ -25,8 +34,60 @@ from . import kda as K
 
 
 @dataclass
+class Fp8Weight:
+    """A weight matrix [N, K] in E4M3 with one FP32 scale per 128 x 128 block."""
+    q: torch.Tensor   # [N, K] float8_e4m3fn
+    s: torch.Tensor   # [ceil(N / 128), ceil(K / 128)]
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+
+def fp8_weight(w: torch.Tensor, stream=None) -> Fp8Weight:
+    """w [N, K] (BF16 or FP32) quantised by kda_quant_fp8."""
+    N, Kw = w.shape
+    q = torch.empty(N, Kw, dtype=torch.float8_e4m3fn, device=w.device)
+    s = torch.empty(-(-N // 128), -(-Kw // 128), dtype=torch.float32, device=w.device)
+    K.kda_quant_fp8(w, q, s, block_rows=128, stream=stream)
+    return Fp8Weight(q, s)
+
+
+class Products:
+    """The buffers of y = x W^T (+ r) for up to `rows` rows of x and the (N, K) of `shapes`."""
+
+    def __init__(self, shapes, rows: int, device, fp8: bool):
+        self.fp8 = fp8
+        if fp8:
+            # the k split (and so the workspace) depends on the number of rows: the largest need of all of them
+            ws = max(K.kda_linear_fp8_workspace_bytes(m, N, Kw) for N, Kw in shapes for m in range(1, rows + 1))
+            Kmax = max(Kw for _, Kw in shapes)
+            self.xq = torch.empty(rows * Kmax, dtype=torch.float8_e4m3fn, device=device)
+            self.xs = torch.empty(rows * -(-Kmax // 128), dtype=torch.float32, device=device)
+            self.ws = torch.zeros(ws, dtype=torch.uint8, device=device)  # the error word starts at 0
+        else:
+            # the same, by 256-row blocks
+            ws = 256
+            for mb in range(1, (rows + 255) // 256 + 1):
+                ws = max(ws, *(K.kda_linear_workspace_bytes(min(rows, 256 * mb), N, Kw) for N, Kw in shapes))
+            self.ws = torch.empty(ws, dtype=torch.uint8, device=device)
+
+    def __call__(self, x: torch.Tensor, w, y: torch.Tensor, r=None, ysplit: int = 0, stream=None) -> None:
+        if isinstance(w, Fp8Weight) != self.fp8:
+            raise TypeError("an FP8 runner takes Fp8Weight products, a BF16 runner BF16 tensors")
+        if not self.fp8:
+            K.kda_linear(x, w, y, self.ws, r=r, ysplit=ysplit, stream=stream)
+            return
+        n, Kx = x.shape
+        xq, xs = self.xq[:n * Kx].view(n, Kx), self.xs[:n * -(-Kx // 128)].view(n, -(-Kx // 128))
+        K.kda_quant_fp8(x, xq, xs, stream=stream)
+        K.kda_linear_fp8(xq, xs, w.q, w.s, y, self.ws, r=r, ysplit=ysplit, stream=stream)
+
+
+@dataclass
 class KdaLayerWeights:
-    """Device weights of one KDA layer (BF16 products, FP32 mixer parameters)."""
+    """Device weights of one KDA layer (BF16 products, FP32 mixer parameters); w_qkvg and w_o may
+    be Fp8Weight."""
     w_qkvg: torch.Tensor   # [4 H d, hidden]: rows of W_q, W_k, W_v, W_g in that order
     w_fa: torch.Tensor     # [d, hidden]
     w_fb: torch.Tensor     # [H d, d]
@@ -54,9 +115,10 @@ def random_layer_weights(H: int, d: int, hidden: int, gen: torch.Generator, devi
 
 
 class KdaLayerRunner:
-    """Buffers for running KDA layers on a batch of up to `rows` tokens at a time."""
+    """Buffers for running KDA layers on a batch of up to `rows` tokens at a time; fp8: with the
+    stacked projection and W_o in FP8."""
 
-    def __init__(self, cfg: K.kda_config_t, hidden: int, rows: int, device):
+    def __init__(self, cfg: K.kda_config_t, hidden: int, rows: int, device, fp8: bool = False):
         self.cfg = cfg
         self.hidden = hidden
         H, d = cfg.num_heads, cfg.head_dim
@@ -67,20 +129,15 @@ class KdaLayerRunner:
         self.z = torch.empty(rows, D, dtype=bf, device=device)
         self.b = torch.empty(rows, H, dtype=bf, device=device)
         self.o = torch.empty(rows, D, dtype=bf, device=device)
-        # the k split (and so the workspace) depends on the number of 256-row blocks: take the
-        # largest need over every row count up to `rows`
-        ws = 256
-        for mb in range(1, (rows + 255) // 256 + 1):
-            m = min(rows, 256 * mb)
-            ws = max(ws, K.kda_linear_workspace_bytes(m, 4 * D, hidden), K.kda_linear_workspace_bytes(m, hidden, D))
-        self.ws_lin = torch.empty(ws, dtype=torch.uint8, device=device)
+        self.products = Products([(4 * D, hidden), (hidden, D)], rows, device, fp8)
+        self.ws_lin = self.products.ws
         self.ws_gp = torch.empty(K.kda_gate_proj_workspace_bytes(cfg, hidden, rows), dtype=torch.uint8, device=device)
 
     def _inputs(self, lw: KdaLayerWeights, x: torch.Tensor, stream):
         n = x.shape[0]
         D = self.o.shape[1]
         qkvg = self.qkvg.view(-1)[:4 * n * D].view(4, n, D)  # four contiguous [n, D] matrices
-        K.kda_linear(x, lw.w_qkvg, qkvg, self.ws_lin, ysplit=self.o.shape[1], stream=stream)
+        self.products(x, lw.w_qkvg, qkvg, ysplit=self.o.shape[1], stream=stream)
         z, b = self.z[:n], self.b[:n]
         K.kda_gate_proj(self.cfg, x, lw.w_fa, lw.w_fb, lw.w_b, z, b, self.ws_gp, stream)
         return qkvg, z, b
@@ -92,7 +149,7 @@ class KdaLayerRunner:
         qkvg, z, b = self._inputs(lw, x, stream)
         o = self.o[:n]
         K.kda_decode_token(self.cfg, lw.params, st, slots, qkvg[0], qkvg[1], qkvg[2], z, b, qkvg[3], o, stream)
-        K.kda_linear(o, lw.w_o, x_out, self.ws_lin, r=x, stream=stream)
+        self.products(o, lw.w_o, x_out, r=x, stream=stream)
 
     def prefill(self, lw: KdaLayerWeights, st, slots: torch.Tensor, cu_seqlens: torch.Tensor, cu_seqlens_host,
                 x: torch.Tensor, x_out: torch.Tensor, stream=None) -> None:
@@ -102,4 +159,61 @@ class KdaLayerRunner:
         o = self.o[:n]
         K.kda_prefill(self.cfg, lw.params, st, slots, cu_seqlens, cu_seqlens_host, qkvg[0], qkvg[1], qkvg[2], z, b,
                       qkvg[3], o, stream)
-        K.kda_linear(o, lw.w_o, x_out, self.ws_lin, r=x, stream=stream)
+        self.products(o, lw.w_o, x_out, r=x, stream=stream)
+
+
+@dataclass
+class GdrLayerWeights:
+    """Device weights of one gated delta rule layer; w_in and w_o BF16 or Fp8Weight."""
+    w_in: torch.Tensor     # [gdr_width(cfg), hidden]: rows of W_q, W_k [Hk d], W_v [H d], W_a, W_b [H], then padding
+    w_o: torch.Tensor      # [hidden, H d]
+    params: K.kda_gdr_params  # A_log, dt_bias (FP32)
+
+
+def gdr_width(cfg: K.kda_gdr_config_t) -> int:
+    """Rows of w_in: q, k, v, a and b side by side, up to a multiple of 128 (what the BF16 product takes)."""
+    n = (2 * cfg.num_qk_heads + cfg.num_heads) * cfg.head_dim + 2 * cfg.num_heads
+    return -(-n // 128) * 128
+
+
+class GdrLayerRunner:
+    """Buffers for running gated delta rule layers on a batch of up to `rows` tokens at a time
+    (num_heads a multiple of 8: the columns of the projection then start on 16 bytes)."""
+
+    def __init__(self, cfg: K.kda_gdr_config_t, hidden: int, rows: int, device, fp8: bool = False):
+        if cfg.io_dtype != K.KDA_BF16:
+            raise ValueError("the layer's products are BF16")
+        self.cfg, self.hidden, self.rows = cfg, hidden, rows
+        D, W = cfg.num_heads * cfg.head_dim, gdr_width(cfg)
+        self.proj = torch.empty(rows, W, dtype=torch.bfloat16, device=device)
+        self.o = torch.empty(rows, D, dtype=torch.bfloat16, device=device)
+        self.products = Products([(W, hidden), (hidden, D)], rows, device, fp8)
+        self.ws = torch.empty(0, dtype=torch.uint8, device=device)
+
+    def _inputs(self, lw: GdrLayerWeights, x: torch.Tensor, stream):
+        n = x.shape[0]
+        if n > self.rows:
+            raise ValueError(f"{n} rows, the runner was made for {self.rows}")
+        proj = self.proj[:n]
+        self.products(x, lw.w_in, proj, stream=stream)
+        H, Hk, d = self.cfg.num_heads, self.cfg.num_qk_heads, self.cfg.head_dim
+        return (*torch.split(proj[:, :(2 * Hk + H) * d + 2 * H], [Hk * d, Hk * d, H * d, H, H], dim=1), self.o[:n])
+
+    def decode(self, lw: GdrLayerWeights, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor, n: int,
+               x: torch.Tensor, x_out: torch.Tensor, err=None, stream=None) -> None:
+        """n tokens for each of src_slots.numel() sequences, rows r n + t of x: x_out = x + W_o o."""
+        rows = self._inputs(lw, x, stream)
+        K.kda_gdr_decode(self.cfg, lw.params, S, src_slots, dst_slots, n, *rows, err=err, stream=stream)
+        self.products(rows[-1], lw.w_o, x_out, r=x, stream=stream)
+
+    def prefill(self, lw: GdrLayerWeights, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor,
+                cu_seqlens: torch.Tensor, cu_seqlens_host, x: torch.Tensor, x_out: torch.Tensor, err=None, stream=None) -> None:
+        """Packed variable-length prefill of x.shape[0] tokens: x_out = x + W_o o. Grows its workspace
+        (an allocation) when a batch needs more chunks than any before."""
+        need = K.kda_gdr_workspace_bytes(self.cfg, cu_seqlens_host)
+        if self.ws.numel() < need:
+            self.ws = torch.empty(need, dtype=torch.uint8, device=self.proj.device)
+        rows = self._inputs(lw, x, stream)
+        K.kda_gdr_prefill(self.cfg, lw.params, S, src_slots, dst_slots, cu_seqlens, cu_seqlens_host, *rows, self.ws,
+                          err=err, stream=stream)
+        self.products(rows[-1], lw.w_o, x_out, r=x, stream=stream)
