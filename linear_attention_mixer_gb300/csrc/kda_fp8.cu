@@ -557,19 +557,15 @@ bool f8_shape_ok(int M, int N, int K)
     return true;
 }
 
-size_t f8_workspace(int M, int N, int nkb, int sms)
-{
-    if (M == 0) return 256;
-    const F8Plan p = f8_plan(M, N, nkb, sms);
-    return 256 + (p.split > 1 ? (size_t)p.split * M * N * 4 : 0);
-}
+size_t f8_workspace(int M, int N, const F8Plan &p) { return 256 + (p.split > 1 ? (size_t)p.split * M * N * 4 : 0); }
 
 template <int BN>
 cudaError_t f8_launch(const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &ty, const CUtensorMap &tp,
-                      const float *xs, const float *ws, const __nv_bfloat16 *r, const F8Shape &sh, int32_t *err, int sms,
-                      cudaStream_t s)
+                      const float *xs, const float *ws, const __nv_bfloat16 *r, const F8Shape &sh, int32_t *err, int dev,
+                      int sms, cudaStream_t s)
 {
-    const cudaError_t e = cudaFuncSetAttribute(f8_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, F8<BN>::kSmem);
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = raise_smem_on(done, dev, f8_kernel<BN>, F8<BN>::kSmem);
     if (e != cudaSuccess) return e;
     f8_kernel<BN><<<sh.n_units < sms ? sh.n_units : sms, F8<BN>::kThreads, F8<BN>::kSmem, s>>>(tx, tw, ty, tp, xs, ws, r, sh, err);
     return cudaGetLastError();
@@ -616,12 +612,13 @@ extern "C" kda_status kda_quant_fp8(int64_t M, int32_t K, const void *x, int64_t
 extern "C" size_t kda_linear_fp8_workspace_bytes(int32_t M, int32_t N, int32_t K)
 {
     if (!f8_shape_ok(M, N, K)) return 0;
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    if (M == 0) return 256;
+    int dev = 0, sms = 0;
+    if (current_sms(&dev, &sms) != cudaSuccess) {
         cudaGetLastError();
         sms = 148;
     }
-    return f8_workspace(M, N, (K + kF8K - 1) / kF8K, sms);
+    return f8_workspace(M, N, f8_plan(M, N, (K + kF8K - 1) / kF8K, sms));
 }
 
 extern "C" kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void *xq, const float *xs, const void *wq,
@@ -641,15 +638,14 @@ extern "C" kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void
     if ((al & 15u) || (al4 & 3u))
         return f8_fail(KDA_ERR_INVALID, "xq, wq, r, y and workspace must be 16-byte aligned, xs and ws 4-byte aligned");
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = current_sms(&dev, &sms);
     if (e != cudaSuccess) return f8_fail(KDA_ERR_CUDA, "%s", cudaGetErrorString(e));
     F8Shape sh;
     sh.M = M; sh.N = N; sh.nkb = (K + kF8K - 1) / kF8K; sh.ysplit = ysplit;
-    const size_t need = f8_workspace(M, N, sh.nkb, sms);
+    const F8Plan plan = f8_plan(M, N, sh.nkb, sms);
+    const size_t need = f8_workspace(M, N, plan);
     if (workspace_bytes < need)
         return f8_fail(KDA_ERR_INVALID, "workspace holds %zu bytes, %zu needed", workspace_bytes, need);
-    const F8Plan plan = f8_plan(M, N, sh.nkb, sms);
     sh.split = plan.split;
     sh.kb_per_split = (sh.nkb + sh.split - 1) / sh.split;
     sh.n_mblk = (M + kF8M - 1) / kF8M;
@@ -676,8 +672,8 @@ extern "C" kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const __nv_bfloat16 *rr = sh.split == 1 ? static_cast<const __nv_bfloat16 *>(r) : nullptr;
-    e = plan.bn == 256 ? f8_launch<256>(tx, tw, ty, tp, xs, ws, rr, sh, err, sms, s)
-                       : f8_launch<128>(tx, tw, ty, tp, xs, ws, rr, sh, err, sms, s);
+    e = plan.bn == 256 ? f8_launch<256>(tx, tw, ty, tp, xs, ws, rr, sh, err, dev, sms, s)
+                       : f8_launch<128>(tx, tw, ty, tp, xs, ws, rr, sh, err, dev, sms, s);
     if (e != cudaSuccess) return f8_fail(KDA_ERR_CUDA, "kda_linear_fp8: %s", cudaGetErrorString(e));
     if (sh.split > 1) {
         const int64_t total8 = (int64_t)M * N / 8;

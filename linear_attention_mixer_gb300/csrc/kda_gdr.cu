@@ -15,6 +15,7 @@
 #include <cstdio>
 
 #include "kda_gdr.cuh"
+#include "kda_launch.cuh"
 
 namespace kda {
 namespace gdr {
@@ -505,9 +506,8 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
             return gdr::fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed",
                              workspace_bytes, need);
         int dev = 0, sms = 0;
-        if ((e = cudaGetDevice(&dev)) == cudaSuccess &&
-            (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) == cudaSuccess)
-            e = gdr::launch_chunked(p, nc, workspace, sms, static_cast<cudaStream_t>(stream));
+        if ((e = current_sms(&dev, &sms)) == cudaSuccess)
+            e = gdr::launch_chunked(p, nc, workspace, dev, sms, static_cast<cudaStream_t>(stream));
     }
     return e == cudaSuccess ? KDA_OK : gdr::fail(KDA_ERR_CUDA, "kda_gdr_prefill: %s", cudaGetErrorString(e));
 }

@@ -19,7 +19,8 @@
 // state is kept to about 16 bits: S, beta (V - ..), T and U go into the products as a BF16 high part and a
 // BF16 low part (x - high), products of two such factors as hi hi + lo hi + hi lo, and sums are FP32.
 // With single BF16 operands the state would be off by 2^-9 a chunk. The output, which is rounded to
-// BF16 itself, takes the high parts of S and U and P in one BF16.
+// BF16 itself, takes the high part of S and P in one BF16 (and U in two: with one it was 1.7 times as far
+// from the exact result as the rounding alone, so it is 1.4 times).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -501,7 +502,7 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
 //              memory. Of each pair of 8-token tiles a warp has one, in turn the first and the second, so
 //              that both halves of the triangular product are equal.
 //   warps 4-7  the output, one chunk behind the chain at most: unit and token tiles as above, O^T from the
-//              high parts of S0 and U that the chain hands over (two buffers)
+//              high part of S0 and from U, which the chain hands over (two buffers)
 //   warp 8     (of a third warpgroup, which leaves its registers to the first) copies: a ring of K, T and V for the chain, one of Q and P for the output
 // What bounds it is the chain of a chunk, 158 MMAs a warp (m16n8k16, 8 cycles each on its quarter of the
 // SM) with the exchanges between them. Tcgen05 would run the same products in tiles of 64 or 128 rows at
@@ -513,7 +514,7 @@ constexpr int kSaT = 16384, kSaV = kSaT + kPartT, kSa = kSaV + kC * kVB * 2;
 constexpr int kSoP = 16384, kSo = 25600;
 constexpr int kSmO = kNa * kSa, kSmX = kSmO + kNo * kSo;  // X: [2 units][2 kw][8 tiles][32 lanes] float4
 constexpr int kSmU = kSmX + 16384, kSmH = kSmU + 8192;    // U split: [2][2][4][32] uint4; hand-over buffers
-constexpr int kHand = 12288;                              // S [2][8 k steps][32] uint4, U [2][4][32] uint4
+constexpr int kHand = 16384;                              // S [2][8 k steps][32] uint4, U split [2][8 tiles][32] uint4
 constexpr int kSmSt = kSmH + 2 * kHand, kSmBar = kSmSt + 4096;
 constexpr int kStSmem = kSmBar + 256 + 1024;
 static_assert(kSa % 1024 == 0 && kSo % 1024 == 0 && kSaV % 512 == 0 && kSoP + kPartP <= kSo, "stages");
@@ -595,7 +596,7 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
         unsigned char *base = sm + st * kSa;
         const uint32_t sb = smem_u32(base), sk = sb + kw * 8192;
         uint4 *hs = reinterpret_cast<uint4 *>(sm + kSmH + hb * kHand) + u * 256 + kw * 128 + lane;
-        uint2 *hu = reinterpret_cast<uint2 *>(sm + kSmH + hb * kHand + 8192 + u * 2048) + lane;
+        uint4 *hu = reinterpret_cast<uint4 *>(sm + kSmH + hb * kHand + 8192 + u * 4096) + lane;
         const float *sx = reinterpret_cast<const float *>(base + kSaT + kTx);
         // X^T over this warp's 64 key rows
         float X[8][4];
@@ -699,7 +700,9 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
         for (int pr = 0; pr < 4; ++pr) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) U[pr][e] += W[pr][e];
-            hu[(2 * pr + own(kw, pr)) * 32] = make_uint2(pack2(U[pr][0], U[pr][1]), pack2(U[pr][2], U[pr][3]));
+            uint32_t h[2], l[2];
+            split_tile(make_float2(U[pr][0], U[pr][1]), make_float2(U[pr][2], U[pr][3]), h, l);
+            hu[(2 * pr + own(kw, pr)) * 32] = make_uint4(h[0], h[1], l[0], l[1]);
             split_tile(f2_mul(cu[pr], make_float2(U[pr][0], U[pr][1])), f2_mul(cu[pr], make_float2(U[pr][2], U[pr][3])),
                        uh[pr], ul[pr]);
             ub[(kw * 4 + pr) * 32] = make_uint4(uh[pr][0], uh[pr][1], ul[pr][0], ul[pr][1]);
@@ -764,7 +767,7 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
         const uint32_t sb = smem_u32(sm + kSmO + st * kSo);
         const float *co = reinterpret_cast<const float *>(sm + kSmO + st * kSo + kSoP + kPx);
         const uint4 *hs = reinterpret_cast<const uint4 *>(sm + kSmH + hb * kHand) + u * 256 + lane;
-        const uint2 *hu = reinterpret_cast<const uint2 *>(sm + kSmH + hb * kHand + 8192 + u * 2048) + lane;
+        const uint4 *hu = reinterpret_cast<const uint4 *>(sm + kSmH + hb * kHand + 8192 + u * 4096) + lane;
         // Q is read once the chain has handed over S0, while it makes little use of shared memory itself
         if (good) good = wait_both(&bar->fo[st], (uint32_t)((c >> 1) & 1), &bar->fs[hb], (uint32_t)((c >> 1) & 1));
         uint32_t qb[4][4][4];
@@ -798,10 +801,12 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
         if (good) good = mbar_wait_bounded(&bar->fh[hb], (uint32_t)((c >> 1) & 1), kStSpin);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            const uint2 w0 = hu[2 * ks * 32], w1 = hu[(2 * ks + 1) * 32];
-            const uint32_t a[4] = {w0.x, w0.y, w1.x, w1.y};
+            const uint4 w0 = hu[2 * ks * 32], w1 = hu[(2 * ks + 1) * 32];
+            const uint32_t a[4] = {w0.x, w0.y, w1.x, w1.y}, al[4] = {w0.z, w0.w, w1.z, w1.w};
 #pragma unroll
             for (int pr = ks; pr < 4; ++pr) mma(o[pr], a, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
+#pragma unroll
+            for (int pr = ks; pr < 4; ++pr) mma(o[pr], al, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
         }
         __syncwarp();
         if (lane == 0) {
@@ -953,7 +958,7 @@ cudaError_t rows_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_chunks, cudaStream_t stream)
+cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_chunks, int dev, cudaStream_t stream)
 {
     const int64_t T = p.total_T;
     const int box = T < kC ? (T > 0 ? (int)T : 1) : kC;
@@ -966,7 +971,8 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
             (e = rows_map(&m.v, p.rows.v, T, Dv, p.rows.v_stride, kVB, box)) != cudaSuccess)
             return e;
     }
-    e = cudaFuncSetAttribute(gdr_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem);
+    static std::atomic<uint64_t> done;
+    e = raise_smem_on(done, dev, gdr_state_kernel, kStSmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((int64_t)p.N * p.H * (kD / kVB));
     if (n_chunks > 0) return launch_after(gdr_state_kernel, dim3(grid), dim3(kStThreads), kStSmem, stream, m, p, blocks, n_chunks, box);
@@ -979,21 +985,22 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
 
 size_t chunked_workspace_bytes(int64_t n_chunks, int32_t H) { return 256 + (size_t)n_chunks * H * kBlkBytes; }
 
-cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int sms, cudaStream_t stream)
+cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int dev, int sms, cudaStream_t stream)
 {
     unsigned char *blocks = static_cast<unsigned char *>(ws) +
                             ((128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127);
     cudaError_t e;
     if (n_chunks > 0) {
         const int Hk = p.H / p.G;
-        e = cudaFuncSetAttribute(gdr_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
+        static std::atomic<uint64_t> done;
+        e = raise_smem_on(done, dev, gdr_prep_kernel, kPrepSmem);
         if (e != cudaSuccess) return e;
         const int64_t items = n_chunks * Hk;
         const unsigned grid = (unsigned)(items < (int64_t)kPrepPerSm * sms ? items : (int64_t)kPrepPerSm * sms);
         gdr_prep_kernel<<<grid, kPrepThreads, kPrepSmem, stream>>>(p, blocks, (int)n_chunks, Hk);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return launch_state(p, blocks, n_chunks, stream);
+    return launch_state(p, blocks, n_chunks, dev, stream);
 }
 
 }  // namespace gdr

@@ -1,12 +1,38 @@
-// kda_launch.cuh - programmatic dependent launch: a kernel is set up while the one before it in the stream
-// is still running, and waits for it on the device.
+// kda_launch.cuh - host side of a launch: what is asked of a device once, and programmatic dependent launch
+// (a kernel is set up while the one before it in the stream is still running, and waits for it on the device).
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 namespace kda {
+
+// The current device and its SM count (asked once per device).
+inline cudaError_t current_sms(int *dev, int *sms)
+{
+    static std::atomic<int> known[64];
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return e;
+    const bool slot = *dev >= 0 && *dev < 64;
+    if (slot && (*sms = known[*dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e == cudaSuccess && slot) known[*dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
+// Raise a kernel's dynamic shared-memory limit, once per device: `done` is a bit per device, static at the call.
+template <typename Fn>
+inline cudaError_t raise_smem_on(std::atomic<uint64_t> &done, int dev, Fn *kernel, int bytes)
+{
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // In the first kernel: the next one, if it was launched by launch_after, may start.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 KDA_OK, KDA_ERR_INVALID, KDA_ERR_OOM, KDA_ERR_CUDA, KDA_ERR_BLOB, KDA_ERR_TIMEOUT, KDA_ERR_DEVICE, KDA_ERR_IO = range(8)
@@ -110,7 +111,7 @@ SIGNATURES = [
                               _I32, _I32, ctypes.POINTER(kda_gdr_rows), _VP, _VP]),
     ("kda_gdr_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(kda_gdr_config_t), _PI32, _I32]),
     ("kda_gdr_prefill", _I32, [ctypes.POINTER(kda_gdr_config_t), ctypes.POINTER(kda_gdr_params), _VP, _I32, _VP, _VP,
-                               _VP, _PI32, _I32, ctypes.POINTER(kda_gdr_rows), _VP, ctypes.c_size_t, _VP, _VP]),
+                               _VP, _VP, _I32, ctypes.POINTER(kda_gdr_rows), _VP, ctypes.c_size_t, _VP, _VP]),
     ("kda_photo_store_create", _I32, [_I32, ctypes.c_char_p, ctypes.POINTER(_VP)]),
     ("kda_photo_store_free", _I32, [_VP]),
     ("kda_photo_count", _I32, [_VP]),
@@ -153,6 +154,18 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return _VP(stream.cuda_stream)
     return _VP(int(stream))
+
+
+# A call's host time is most of what a small one costs, so the entry points from here on ask torch's C layer
+# for the current device and stream.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        return _current_raw_stream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _torch_io_dtype(cfg: kda_config_t):
@@ -398,30 +411,51 @@ def kda_linear(x, w, y, workspace: torch.Tensor, r=None, ysplit: int = 0, stream
                             _stream(stream)))
 
 
-def _same_device(*tensors) -> None:
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on {t.device}")
+def _bad_tensor(name: str, t, dtype, dev: int, shape=None) -> None:
+    """Why a tensor was not taken: not of dtype (None: any), contiguous, on CUDA device dev and (if given) of shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(name: str, t, dtype, dev: int, shape=None) -> int:
+    """The address of a tensor that passes (the tests in the order of their cost)."""
+    try:
+        if (dtype is None or t.dtype is dtype) and t.get_device() == dev and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _bad_tensor(name, t, dtype, dev, shape)
+
+
+_BF16, _F32, _F8, _I32T = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
 
 
 def kda_quant_fp8(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, block_rows: int = 1, stream=None) -> None:
     """q [M, K] (float8_e4m3fn) and s [ceil(M / block_rows), ceil(K / 128)] (FP32) from x [M, K] (BF16 or
     FP32, contiguous within a row): one power-of-two scale for each 1 x 128 or 128 x 128 block."""
-    if x.dim() != 2 or not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float32):
+    dev = _current_device()
+    dt = x.dtype
+    if x.dim() != 2 or not x.is_cuda or not (dt is _BF16 or dt is _F32):
         raise TypeError("x must be a CUDA tensor [M, K] of bfloat16 or float32")
-    M, K = int(x.shape[0]), int(x.shape[1])
+    M, K = x.shape
+    if block_rows < 1:
+        raise ValueError("block_rows must be 1 or 128")
     if M > 0 and K > 1 and x.stride(1) != 1:
         raise ValueError("x must be contiguous within a row")
-    rows = int(block_rows)
-    if rows < 1:
-        raise ValueError("block_rows must be 1 or 128")
-    if tuple(q.shape) != (M, K) or tuple(s.shape) != (-(-M // rows), -(-K // 128)):
-        raise ValueError(f"q must be [{M}, {K}] and s [{-(-M // rows)}, {-(-K // 128)}], got {tuple(q.shape)}, {tuple(s.shape)}")
-    _same_device(x, q, s)
-    _check(lib().kda_quant_fp8(M, K, _VP(x.data_ptr()), x.stride(0) if M > 1 else K,
-                               KDA_BF16 if x.dtype == torch.bfloat16 else KDA_F32, rows, _dev(q, torch.float8_e4m3fn, "q"),
-                               _dev(s, torch.float32, "s"), _stream(stream)))
+    if x.get_device() != dev:
+        raise ValueError(f"x is on {x.device}, the current device is cuda:{dev}")
+    st = lib().kda_quant_fp8(M, K, x.data_ptr(), x.stride(0) if M > 1 else K, KDA_BF16 if dt is _BF16 else KDA_F32, block_rows,
+                             _ptr("q", q, _F8, dev, (M, K)), _ptr("s", s, _F32, dev, (-(-M // block_rows), -(-K // 128))),
+                             _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def kda_linear_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -434,21 +468,20 @@ def kda_linear_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
 def kda_linear_fp8(xq, xs, wq, ws, y, workspace: torch.Tensor, r=None, ysplit: int = 0, stream=None) -> None:
     """y = x w^T (+ r) in BF16 from E4M3 xq [M, K], wq [N, K] and their scales xs [M, ceil(K / 128)],
     ws [ceil(N / 128), ceil(K / 128)]; y [M, N] (or [N / ysplit, M, ysplit] with ysplit)."""
-    f8, bf = torch.float8_e4m3fn, torch.bfloat16
+    dev = _current_device()
     if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
         raise ValueError("xq must be [M, K] and wq [N, K]")
-    M, K = int(xq.shape[0]), int(xq.shape[1])
-    N = int(wq.shape[0])
-    if tuple(xs.shape) != (M, -(-K // 128)) or tuple(ws.shape) != (-(-N // 128), -(-K // 128)):
-        raise ValueError(f"xs must be [{M}, {-(-K // 128)}] and ws [{-(-N // 128)}, {-(-K // 128)}], "
-                         f"got {tuple(xs.shape)}, {tuple(ws.shape)}")
+    M, K = xq.shape
+    N = wq.shape[0]
+    nk = -(-K // 128)
     if y.numel() != M * N or (r is not None and r.numel() != M * N):
         raise ValueError(f"y and r must hold {M} x {N} elements")
-    _same_device(xq, xs, wq, ws, y, r, workspace)
-    _check(lib().kda_linear_fp8(M, N, K, _dev(xq, f8, "xq"), _dev(xs, torch.float32, "xs"), _dev(wq, f8, "wq"),
-                                _dev(ws, torch.float32, "ws"), _VP(None) if r is None else _dev(r, bf, "r"),
-                                _dev(y, bf, "y"), int(ysplit), _dev(workspace, None, "workspace"),
-                                workspace.numel() * workspace.element_size(), _stream(stream)))
+    st = lib().kda_linear_fp8(M, N, K, _ptr("xq", xq, _F8, dev), _ptr("xs", xs, _F32, dev, (M, nk)), _ptr("wq", wq, _F8, dev),
+                              _ptr("ws", ws, _F32, dev, (-(-N // 128), nk)), None if r is None else _ptr("r", r, _BF16, dev),
+                              _ptr("y", y, _BF16, dev), ysplit, _ptr("workspace", workspace, None, dev), workspace.nbytes,
+                              _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def kda_gdr_config(num_heads: int, num_qk_heads: int | None = None, head_dim: int = 128,
@@ -463,44 +496,64 @@ def kda_gdr_params_from(A_log: torch.Tensor, dt_bias: torch.Tensor) -> kda_gdr_p
     if A_log.shape != dt_bias.shape or A_log.dim() != 1:
         raise ValueError("A_log and dt_bias must both be [H]")
     p = kda_gdr_params(_dev(A_log, torch.float32, "A_log"), _dev(dt_bias, torch.float32, "dt_bias"))
+    if A_log.device != dt_bias.device:
+        raise ValueError("A_log and dt_bias must be on one device")
     p._keep = (A_log, dt_bias)
+    p.heads, p.device = A_log.numel(), A_log.device.index
     return p
 
 
-def _gdr_args(cfg, params, S, src_slots, dst_slots, T, q, k, v, a, b, out, err):
-    """Checked rows, slots and states of a gated delta rule call, and T, the tokens of each row tensor."""
-    H, Hk, d = cfg.num_heads, cfg.num_qk_heads, cfg.head_dim
-    dt = _torch_io_dtype(cfg)
-    if S.dim() != 4 or tuple(S.shape[1:]) != (H, d, d):
-        raise ValueError(f"S must be [max_slots, {H}, {d}, {d}], got {tuple(S.shape)}")
-    if params._keep[0].numel() != H:
-        raise ValueError(f"A_log and dt_bias must hold {H} elements")
+def _bad_row(name, t, T, width, dt, dev) -> None:
+    """Why a row tensor was not taken."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dt:
+        raise TypeError(f"{name} must be a CUDA tensor of {dt}")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if tuple(t.shape) != (T, width):
+        raise ValueError(f"{name} must be [{T}, {width}], got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous within a token")
+
+
+def _gdr_call(cfg, params, S, src_slots, dst_slots, T, q, k, v, a, b, out, err, dev):
+    """The checked pointers of a gated delta rule call over T tokens, the current device being dev: S, src,
+    dst, rows, err."""
+    H, d = cfg.num_heads, cfg.head_dim
+    wk, wv = cfg.num_qk_heads * d, H * d
+    dt = _BF16 if cfg.io_dtype == KDA_BF16 else _F32
+    if S.shape[1:] != (H, d, d):
+        raise ValueError(f"S must be [max_slots, {H}, {d}, {d}], got {list(S.shape)}")
+    if params.heads != H or params.device != dev:
+        raise ValueError(f"A_log and dt_bias must hold {H} elements on cuda:{dev}, got {params.heads} on cuda:{params.device}")
     if src_slots.numel() != dst_slots.numel():
         raise ValueError("src_slots and dst_slots must have the same length")
-    r = kda_gdr_rows()
-    for name, t, width in (("q", q, Hk * d), ("k", k, Hk * d), ("v", v, H * d), ("a", a, H), ("b", b, H),
-                           ("out", out, H * d)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dt:
-            raise TypeError(f"{name} must be a CUDA tensor of {dt}")
-        if tuple(t.shape) != (T, width):
-            raise ValueError(f"{name} must be [{T}, {width}], got {tuple(t.shape)}")
-        if T > 0 and t.stride(1) != 1 and width > 1:
-            raise ValueError(f"{name} must be contiguous within a token")
-        setattr(r, name, t.data_ptr())
-        setattr(r, name + "_stride", t.stride(0) if T > 1 else width)
-    _same_device(S, src_slots, dst_slots, q, k, v, a, b, out, err, *params._keep)
-    return (_dev(S, torch.float32, "S"), int(S.shape[0]), _dev(src_slots, torch.int32, "src_slots"),
-            _dev(dst_slots, torch.int32, "dst_slots"), r, _VP(None) if err is None else _dev(err, torch.int32, "err"))
+    qk, vo, ab = (T, wk), (T, wv), (T, H)
+    rows = ((q, qk), (k, qk), (v, vo), (a, ab), (b, ab), (out, vo))
+    ptrs, strides = [], []
+    for t, shape in rows:
+        if t.dtype is not dt or t.shape != shape or t.get_device() != dev:
+            break
+        s0, s1 = t.stride()
+        if s1 != 1 and shape[1] > 1 and T > 0:
+            break
+        ptrs.append(t.data_ptr())
+        strides.append(s0 if T > 1 else shape[1])
+    else:
+        return (_ptr("S", S, _F32, dev), _ptr("src_slots", src_slots, _I32T, dev), _ptr("dst_slots", dst_slots, _I32T, dev),
+                kda_gdr_rows(*ptrs, *strides), None if err is None else _ptr("err", err, _I32T, dev))
+    i = len(ptrs)
+    _bad_row(("q", "k", "v", "a", "b", "out")[i], rows[i][0], *rows[i][1], dt, dev)
 
 
 def kda_gdr_decode(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tensor, src_slots: torch.Tensor,
                    dst_slots: torch.Tensor, n: int, q, k, v, a, b, out, err=None, stream=None) -> None:
     """n tokens for each row: q, k [B n, Hk d], v, out [B n, H d], a, b [B n, H], contiguous within a
     token; S FP32 [max_slots, H, d, d], read at src_slots (-1: zeros) and written at dst_slots."""
-    B = int(src_slots.numel())
-    Sp, slots, sp, dp, r, ep = _gdr_args(cfg, params, S, src_slots, dst_slots, B * int(n), q, k, v, a, b, out, err)
-    _check(lib().kda_gdr_decode(ctypes.byref(cfg), ctypes.byref(params), Sp, slots, sp, dp, B, int(n), ctypes.byref(r),
-                                ep, _stream(stream)))
+    dev = _current_device()
+    B = src_slots.numel()
+    Sp, sp, dp, r, ep = _gdr_call(cfg, params, S, src_slots, dst_slots, B * n, q, k, v, a, b, out, err, dev)
+    st = lib().kda_gdr_decode(cfg, params, Sp, S.shape[0], sp, dp, B, n, r, ep, _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def kda_gdr_workspace_bytes(cfg: kda_gdr_config_t, cu_seqlens_host) -> int:
@@ -516,16 +569,17 @@ def kda_gdr_prefill(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tens
                     workspace: torch.Tensor, err=None, stream=None) -> None:
     """Packed sequences, rows as in kda_gdr_decode with T = cu_seqlens[-1]; workspace of at least
     kda_gdr_workspace_bytes(cfg, cu_seqlens_host) bytes."""
-    N = int(src_slots.numel())
-    cu_h, cu_p = _host_i32(cu_seqlens_host)
-    if len(cu_h) != N + 1 or cu_seqlens.numel() != N + 1:
-        raise ValueError("cu_seqlens must hold N + 1 entries")
-    Sp, slots, sp, dp, r, ep = _gdr_args(cfg, params, S, src_slots, dst_slots, int(cu_h[-1]), q, k, v, a, b, out, err)
-    _same_device(cu_seqlens, workspace)
-    _check(lib().kda_gdr_prefill(ctypes.byref(cfg), ctypes.byref(params), Sp, slots, sp, dp,
-                                 _dev(cu_seqlens, torch.int32, "cu_seqlens"), cu_p, N, ctypes.byref(r),
-                                 _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size(), ep,
-                                 _stream(stream)))
+    dev = _current_device()
+    N = src_slots.numel()
+    cu_h = np.ascontiguousarray(cu_seqlens_host, dtype=np.int32)
+    if cu_h.shape != (N + 1,):
+        raise ValueError("cu_seqlens_host must hold N + 1 entries")
+    Sp, sp, dp, r, ep = _gdr_call(cfg, params, S, src_slots, dst_slots, int(cu_h[N]), q, k, v, a, b, out, err, dev)
+    st = lib().kda_gdr_prefill(cfg, params, Sp, S.shape[0], sp, dp, _ptr("cu_seqlens", cu_seqlens, _I32T, dev, (N + 1,)),
+                               cu_h.ctypes.data, N, r, _ptr("workspace", workspace, None, dev), workspace.nbytes, ep,
+                               _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def _layers(layers):
