@@ -503,15 +503,16 @@ def kda_gdr_params_from(A_log: torch.Tensor, dt_bias: torch.Tensor) -> kda_gdr_p
     return p
 
 
-def _bad_row(name, t, T, width, dt, dev) -> None:
-    """Why a row tensor was not taken."""
+def _check_row(name, t, T, width, dt, dev) -> None:
+    """Raise for a row tensor that a call cannot take."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dt:
         raise TypeError(f"{name} must be a CUDA tensor of {dt}")
     if t.device.index != dev:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     if tuple(t.shape) != (T, width):
         raise ValueError(f"{name} must be [{T}, {width}], got {list(t.shape)}")
-    raise ValueError(f"{name} must be contiguous within a token")
+    if T > 0 and width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous within a token")
 
 
 def _gdr_call(cfg, params, S, src_slots, dst_slots, T, q, k, v, a, b, out, err, dev):
@@ -527,21 +528,18 @@ def _gdr_call(cfg, params, S, src_slots, dst_slots, T, q, k, v, a, b, out, err, 
     if src_slots.numel() != dst_slots.numel():
         raise ValueError("src_slots and dst_slots must have the same length")
     qk, vo, ab = (T, wk), (T, wv), (T, H)
-    rows = ((q, qk), (k, qk), (v, vo), (a, ab), (b, ab), (out, vo))
-    ptrs, strides = [], []
-    for t, shape in rows:
-        if t.dtype is not dt or t.shape != shape or t.get_device() != dev:
-            break
-        s0, s1 = t.stride()
-        if s1 != 1 and shape[1] > 1 and T > 0:
-            break
-        ptrs.append(t.data_ptr())
-        strides.append(s0 if T > 1 else shape[1])
-    else:
+    if (q.dtype is dt and k.dtype is dt and v.dtype is dt and a.dtype is dt and b.dtype is dt and out.dtype is dt
+            and q.shape == qk and k.shape == qk and v.shape == vo and out.shape == vo and a.shape == ab and b.shape == ab
+            and q.get_device() == k.get_device() == v.get_device() == a.get_device() == b.get_device() == out.get_device() == dev
+            and (T == 0 or (q.stride(1) == k.stride(1) == v.stride(1) == out.stride(1) == 1
+                            and (H == 1 or a.stride(1) == b.stride(1) == 1)))):
+        r = kda_gdr_rows(q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), out.data_ptr(),
+                         *((q.stride(0), k.stride(0), v.stride(0), a.stride(0), b.stride(0), out.stride(0)) if T > 1 else
+                           (wk, wk, wv, H, H, wv)))
         return (_ptr("S", S, _F32, dev), _ptr("src_slots", src_slots, _I32T, dev), _ptr("dst_slots", dst_slots, _I32T, dev),
-                kda_gdr_rows(*ptrs, *strides), None if err is None else _ptr("err", err, _I32T, dev))
-    i = len(ptrs)
-    _bad_row(("q", "k", "v", "a", "b", "out")[i], rows[i][0], *rows[i][1], dt, dev)
+                r, None if err is None else _ptr("err", err, _I32T, dev))
+    for name, t, width in (("q", q, wk), ("k", k, wk), ("v", v, wv), ("a", a, H), ("b", b, H), ("out", out, wv)):
+        _check_row(name, t, T, width, dt, dev)
 
 
 def kda_gdr_decode(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tensor, src_slots: torch.Tensor,
