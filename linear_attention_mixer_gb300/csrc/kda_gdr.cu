@@ -399,14 +399,16 @@ Args make_args(const kda_gdr_config_t *c, const kda_gdr_params *prm, float *S, i
     return p;
 }
 
-// host cu_seqlens: total chunks (or -1 with the error set)
-int64_t count_chunks(const int32_t *cu, int32_t N)
+// host cu_seqlens: total chunks (or -1 with the error set), and those of the longest sequence
+int64_t count_chunks(const int32_t *cu, int32_t N, int64_t *longest = nullptr)
 {
     if (cu[0] != 0) return fail(KDA_ERR_INVALID, "cu_seqlens[0] must be 0 (got %d)", cu[0]), -1;
     int64_t n = 0;
     for (int32_t i = 0; i < N; ++i) {
         if (cu[i + 1] < cu[i]) return fail(KDA_ERR_INVALID, "cu_seqlens decreases at %d", i + 1), -1;
-        n += ((int64_t)cu[i + 1] - cu[i] + kC - 1) / kC;
+        const int64_t c = ((int64_t)cu[i + 1] - cu[i] + kC - 1) / kC;
+        n += c;
+        if (longest && c > *longest) *longest = c;
     }
     return n;
 }
@@ -489,7 +491,8 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
     if (N == 0) return KDA_OK;
     if (!cu_seqlens || !cu_seqlens_host) return gdr::fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL");
     if ((int64_t)N * cfg->num_heads > INT_MAX / 8) return gdr::fail(KDA_ERR_INVALID, "N * num_heads is too large");
-    const int64_t nc = gdr::count_chunks(cu_seqlens_host, N);
+    int64_t longest = 0;
+    const int64_t nc = gdr::count_chunks(cu_seqlens_host, N, &longest);
     if (nc < 0) return KDA_ERR_INVALID;
     if (nc * cfg->num_heads > INT_MAX / 8) return gdr::fail(KDA_ERR_INVALID, "chunks * num_heads is too large");
     const int64_t T = cu_seqlens_host[N];
@@ -507,7 +510,7 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
                              workspace_bytes, need);
         int dev = 0, sms = 0;
         if ((e = current_sms(&dev, &sms)) == cudaSuccess)
-            e = gdr::launch_chunked(p, nc, workspace, dev, sms, static_cast<cudaStream_t>(stream));
+            e = gdr::launch_chunked(p, nc, longest, workspace, dev, sms, static_cast<cudaStream_t>(stream));
     }
     return e == cudaSuccess ? KDA_OK : gdr::fail(KDA_ERR_CUDA, "kda_gdr_prefill: %s", cudaGetErrorString(e));
 }

@@ -58,7 +58,7 @@ cudaError_t launch_decode_rows(const Args &p, bool f32, cudaStream_t stream);  /
 cudaError_t launch_sequences(const Args &p, cudaStream_t stream);               // FP32 rows, N sequences
 
 size_t chunked_workspace_bytes(int64_t n_chunks, int32_t H);
-cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int dev, int sms, cudaStream_t stream);
+cudaError_t launch_chunked(const Args &p, int64_t n_chunks, int64_t longest, void *ws, int dev, int sms, cudaStream_t stream);
 
 }  // namespace gdr
 }  // namespace kda

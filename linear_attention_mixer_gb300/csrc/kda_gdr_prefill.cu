@@ -493,40 +493,56 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
 }
 
 // ---------------------------------------------------------------- state
-// A block takes 32 value columns of one (sequence, head) through its chunks. Everything is held
-// transposed, with 16 value columns (a unit) as the 16 rows of the MMA: the FP32 accumulators of S^T, X^T
-// = S0^T K^T and U^T then have the register layout of the next product's A operand, and the operands in
-// shared memory are only read.
+// A block takes 32 MT value columns of one (sequence, head) through its chunks. Everything is held transposed,
+// with the 16 MT value columns of a unit as MT times the 16 rows of the MMA: the FP32 accumulators of S^T, X^T
+// = S0^T K^T and U^T then have the register layout of the next product's A operand, and the operands in shared
+// memory are only read.
 //   warps 0-3  the chain: warp 2 u + kw has unit u and the key rows 64 kw .. 64 kw + 63 of S. Its partial
 //              sums of X, then half of the token tiles of U, go to the unit's other warp through shared
 //              memory. Of each pair of 8-token tiles a warp has one, in turn the first and the second, so
 //              that both halves of the triangular product are equal.
 //   warps 4-7  the output, one chunk behind the chain at most: unit and token tiles as above, O^T from the
-//              high part of S0 and from U, which the chain hands over (two buffers)
-//   warp 8     (of a third warpgroup, which leaves its registers to the first) copies: a ring of K, T and V for the chain, one of Q and P for the output
-// What bounds it is the chain of a chunk, 158 MMAs a warp (m16n8k16, 8 cycles each on its quarter of the
-// SM) with the exchanges between them. Tcgen05 would run the same products in tiles of 64 or 128 rows at
-// four times that rate, but the four dependent products of a chunk (64 x 128 x 32 and smaller) would each
-// pay for the way through tensor memory and back into shared memory.
-constexpr int kVB = 32, kStThreads = 384;
-constexpr int kNa = 3, kNo = 2;  // stages of the two rings
-constexpr int kSaT = 16384, kSaV = kSaT + kPartT, kSa = kSaV + kC * kVB * 2;
-constexpr int kSoP = 16384, kSo = 25600;
-constexpr int kSmO = kNa * kSa, kSmX = kSmO + kNo * kSo;  // X: [2 units][2 kw][8 tiles][32 lanes] float4
-constexpr int kSmU = kSmX + 16384, kSmH = kSmU + 8192;    // U split: [2][2][4][32] uint4; hand-over buffers
-constexpr int kHand = 16384;                              // S [2][8 k steps][32] uint4, U split [2][8 tiles][32] uint4
-constexpr int kSmSt = kSmH + 2 * kHand, kSmBar = kSmSt + 4096;
-constexpr int kStSmem = kSmBar + 256 + 1024;
-static_assert(kSa % 1024 == 0 && kSo % 1024 == 0 && kSaV % 512 == 0 && kSoP + kPartP <= kSo, "stages");
-static_assert(kStSmem <= 232448, "state kernel shared memory");
+//              high part of S0 and from U, which the chain hands over
+//   warp 8     (of a third warpgroup, which leaves its registers to the first) copies: a ring of K, T and V
+//              for the chain, one of Q and P for the output
+// With MT = 1 what bounds it is the chain of a chunk: 158 MMAs a warp (m16n8k16, 8 cycles each on its quarter
+// of the SM) with the exchanges between them, and shared memory, which delivers operands for 16 rows at a
+// time: 2400 wavefronts and 520 of arriving copies in the 3250 cycles of a chunk. With MT = 2 an operand
+// fetched serves 32 rows. A chunk of it takes longer, two columns' worth of it less; see the rule at the launch.
+// Tcgen05 would run the same products in tiles of 64 or 128 rows at four times the MMA rate, but the four
+// dependent products of a chunk (64 x 128 x 32 and smaller) would each pay for the way through tensor memory
+// and back into shared memory.
+constexpr int kStThreads = 384;
+template <int MT> struct St {
+    static constexpr int kVB = 32 * MT;
+    static constexpr int kNa = MT == 1 ? 3 : 2, kNo = 2, kNh = MT == 1 ? 2 : 1;  // stages of the rings, hand-over buffers
+    static constexpr int kT = 16384, kV = kT + kPartT, kSa = kV + kC * kVB * 2;
+    static constexpr int kP = 16384, kSo = 25600;
+    static constexpr int kO = kNa * kSa, kX = kO + kNo * kSo;         // X: [2 units][2 kw][8 tiles][MT][32 lanes] float4
+    static constexpr int kU = kX + 16384 * MT, kH = kU + 8192 * MT;   // U split: [2][2][4][MT][32] uint4
+    static constexpr int kHu = 8192 * MT, kHand = 2 * kHu;            // S [2][8 k steps][MT][32], U split [2][8 tiles][MT][32] uint4
+    static constexpr int kStg = kH + kNh * kHand, kBar = kStg + 4096 * MT;
+    static constexpr int kSmem = kBar + 256 + 1024;
+};
+static_assert(St<1>::kSa % 1024 == 0 && St<2>::kSa % 1024 == 0 && St<1>::kSo % 1024 == 0 && St<1>::kV % 1024 == 0 &&
+              St<1>::kP + kPartP <= St<1>::kSo, "stages");
+static_assert(St<1>::kSmem <= 232448 && St<2>::kSmem <= 232448, "state kernel shared memory");
 constexpr uint32_t kStSpin = 1u << 26;
 
 struct StateMaps { CUtensorMap k, q, v; };
 // full and empty of the two rings; S0 handed over, U handed over, both read
-struct StBars { uint64_t fa[kNa], ea[kNa], fo[kNo], eo[kNo], fs[2], fh[2], eh[2]; };
+struct StBars { uint64_t fa[3], ea[3], fo[2], eo[2], fs[2], fh[2], eh[2]; };
 
-// byte offset of 16-byte piece c of row r of the V tile (rows of 64 bytes, TMA's 64-byte swizzle)
-__device__ __forceinline__ uint32_t v_off(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+// byte offset of 16-byte piece c of row r of the V tile (rows of 64 or 128 bytes, TMA's swizzle of that width)
+template <int MT> __device__ __forceinline__ uint32_t v_off(int r, int c)
+{
+    return MT == 2 ? swz(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+// and of piece c of row r of the staged output (rows of 32 or 64 bytes)
+template <int MT> __device__ __forceinline__ uint32_t o_off(int r, int c)
+{
+    return MT == 2 ? (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)) : (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+}
 
 // Token tiles (8 tokens) of the unit's warp kw: one of each pair, 2 p + own(p).
 __device__ __forceinline__ int own(int kw, int p) { return (p ^ kw) & 1; }
@@ -547,11 +563,13 @@ __device__ __forceinline__ void split_tile(float2 x, float2 y, uint32_t *h, uint
     split2(y.x, y.y, h[1], l[1]);
 }
 
-__device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u, int kw, int len, float2 (&S)[8][2])
+template <int MT>
+__device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u, int kw, int len, float2 (&S)[MT][8][2])
 {
+    using L = St<MT>;
     const int lane = threadIdx.x & 31, q2 = 2 * (lane & 3);
-    float4 *xb = reinterpret_cast<float4 *>(sm + kSmX) + u * 512 + lane;
-    uint4 *ub = reinterpret_cast<uint4 *>(sm + kSmU) + u * 256 + lane;
+    float4 *xb = reinterpret_cast<float4 *>(sm + L::kX) + u * (512 * MT) + lane;
+    uint4 *ub = reinterpret_cast<uint4 *>(sm + L::kU) + u * (256 * MT) + lane;
     const int nc = (len + kC - 1) / kC;
     bool good = true;
     // row and 16-byte piece within an ldmatrix of B operands: two tiles of tokens in rows, or tokens as k
@@ -562,27 +580,26 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
     for (int pr = 0; pr < 4; ++pr) offT[pr] = swz(16 * pr + 8 * own(kw, pr) + (lane & 7), lane >> 3);
     int st = 0, pa = 0;
     uint32_t b[2][4][4];          // B operands of a k step, fetched a step ahead
-    uint32_t ah[2][4], al[2][4];  // A operand of a k step, split a step ahead
     // Chunk c's stage has arrived and its hand-over buffer is free. peek asks both barriers once, without using
     // the answer yet; enter waits if it was no, and fetches the first B operands. (After a wait that gave up the
     // warp goes on without waiting, so that every barrier is met.)
     auto peek = [&](int c) {
-        const bool odd = lane & (c >= 2);
-        return mbar_try_wait(odd ? &bar->eh[c & 1] : &bar->fa[st], odd ? (uint32_t)(((c >> 1) - 1) & 1) : (uint32_t)pa);
+        const bool odd = lane & (c >= L::kNh);
+        return mbar_try_wait(odd ? &bar->eh[c % L::kNh] : &bar->fa[st], odd ? (uint32_t)(((c / L::kNh) - 1) & 1) : (uint32_t)pa);
     };
     auto enter = [&](int c, bool ready) {
-        unsigned char *base = sm + st * kSa;
+        unsigned char *base = sm + st * L::kSa;
         if (!__all_sync(0xFFFFFFFFu, ready) && good)
-            good = c < 2 ? mbar_wait_bounded(&bar->fa[st], (uint32_t)pa, kStSpin)
-                         : wait_both(&bar->fa[st], (uint32_t)pa, &bar->eh[c & 1], (uint32_t)(((c >> 1) - 1) & 1));
+            good = c < L::kNh ? mbar_wait_bounded(&bar->fa[st], (uint32_t)pa, kStSpin)
+                              : wait_both(&bar->fa[st], (uint32_t)pa, &bar->eh[c % L::kNh], (uint32_t)(((c / L::kNh) - 1) & 1));
         __syncwarp();
         const int n = len - c * kC;
         if (n < kC) {  // the last chunk: what follows the sequence in K and V counts as zero
             for (int x = threadIdx.x; x < (kC - n) * 16; x += 128)
                 *reinterpret_cast<uint4 *>(base + ((x >> 3) & 1) * 8192 + (n + (x >> 4)) * 128 + (x & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
-            for (int x = threadIdx.x; x < (kC - n) * (kVB / 8); x += 128)
-                *reinterpret_cast<uint4 *>(base + kSaV + n * kVB * 2 + x * 16) = make_uint4(0, 0, 0, 0);
+            for (int x = threadIdx.x; x < (kC - n) * (L::kVB / 8); x += 128)
+                *reinterpret_cast<uint4 *>(base + L::kV + n * L::kVB * 2 + x * 16) = make_uint4(0, 0, 0, 0);
             named_bar_sync(3, 128);
         }
         const uint32_t sk = smem_u32(base) + kw * 8192;
@@ -592,120 +609,165 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
     if (nc > 0) enter(0, false);
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
-        const int hb = c & 1, now = st;
-        unsigned char *base = sm + st * kSa;
+        const int hb = c % L::kNh, now = st;
+        unsigned char *base = sm + st * L::kSa;
         const uint32_t sb = smem_u32(base), sk = sb + kw * 8192;
-        uint4 *hs = reinterpret_cast<uint4 *>(sm + kSmH + hb * kHand) + u * 256 + kw * 128 + lane;
-        uint4 *hu = reinterpret_cast<uint4 *>(sm + kSmH + hb * kHand + 8192 + u * 4096) + lane;
-        const float *sx = reinterpret_cast<const float *>(base + kSaT + kTx);
+        uint4 *hs = reinterpret_cast<uint4 *>(sm + L::kH + hb * L::kHand) + (u * 8 + kw * 4) * (32 * MT) + lane;
+        uint4 *hu = reinterpret_cast<uint4 *>(sm + L::kH + hb * L::kHand + L::kHu) + u * (256 * MT) + lane;
+        const float *sx = reinterpret_cast<const float *>(base + L::kT + kTx);
         // X^T over this warp's 64 key rows
-        float X[8][4];
+        float X[MT][8][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) X[j][e] = 0.f;
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) split_tile(S[e][0], S[e][1], ah[0] + 2 * e, al[0] + 2 * e);
+                for (int e = 0; e < 4; ++e) X[m][j][e] = 0.f;
+        {
+            uint32_t ah[2][MT][4], al[2][MT][4];  // A operand of a k step, split a step ahead
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const int x = ks & 1, y = x ^ 1;
-            hs[ks * 32] = make_uint4(ah[x][0], ah[x][1], ah[x][2], ah[x][3]);
-            if (ks < 3) {
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int jp = 0; jp < 4; ++jp) ldsm4(b[y][jp], sk + swz(16 * jp + rowB, 2 * (ks + 1) + pcB));
+                for (int e = 0; e < 2; ++e) split_tile(S[m][e][0], S[m][e][1], ah[0][m] + 2 * e, al[0][m] + 2 * e);
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    split_tile(S[2 * ks + 2 + e][0], S[2 * ks + 2 + e][1], ah[y] + 2 * e, al[y] + 2 * e);
+            for (int ks = 0; ks < 4; ++ks) {
+                const int x = ks & 1, y = x ^ 1;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) hs[(ks * MT + m) * 32] = make_uint4(ah[x][m][0], ah[x][m][1], ah[x][m][2], ah[x][m][3]);
+                if (ks < 3) {
+#pragma unroll
+                    for (int jp = 0; jp < 4; ++jp) ldsm4(b[y][jp], sk + swz(16 * jp + rowB, 2 * (ks + 1) + pcB));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            split_tile(S[m][2 * ks + 2 + e][0], S[m][2 * ks + 2 + e][1], ah[y][m] + 2 * e, al[y][m] + 2 * e);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mma(X[m][j], ah[x][m], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mma(X[m][j], al[x][m], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mma(X[j], ah[x], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mma(X[j], al[x], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
         }
-        // fetched while the products drain: V^T (value rows g and g + 8 of a tile), the scalars, T
-        uint32_t vv[4][4], th[2][4][4], tl[2][4][4];
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) ldsm4t(vv[ks], sb + kSaV + v_off(16 * ks + rowB, 2 * u + pcB));
+        // fetched while the products drain (as far as the registers go): V^T (value rows g and g + 8 of a tile),
+        // the scalars, T
+        uint32_t vv[MT][4][4], th[2][4][4], tl[2][4][4];
         float2 cx[8], be[8];
+        auto fetch_right = [&](int ks) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            cx[j] = *reinterpret_cast<const float2 *>(sx + 8 * j + q2);
-            be[j] = *reinterpret_cast<const float2 *>(sx + kC + 8 * j + q2);
+            for (int m = 0; m < MT; ++m) ldsm4t(vv[m][ks], sb + L::kV + v_off<MT>(16 * ks + rowB, 2 * (MT * u + m) + pcB));
+#pragma unroll
+            for (int j = 2 * ks; j < 2 * ks + 2; ++j) {
+                cx[j] = *reinterpret_cast<const float2 *>(sx + 8 * j + q2);
+                be[j] = *reinterpret_cast<const float2 *>(sx + kC + 8 * j + q2);
+            }
+        };
+        auto fetch_T = [&](int kp) {
+#pragma unroll
+            for (int pr = 2 * kp; pr < 4; ++pr) {
+                ldsm4(th[kp][pr], sb + L::kT + (offT[pr] ^ (kp * 64)));
+                ldsm4(tl[kp][pr], sb + L::kT + kTl + (offT[pr] ^ (kp * 64)));
+            }
+        };
+        if (MT == 1) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) fetch_right(ks);
+            fetch_T(0);
         }
         const float gl = sx[3 * kC];
 #pragma unroll
-        for (int pr = 0; pr < 4; ++pr) {
-            ldsm4(th[0][pr], sb + kSaT + offT[pr]);
-            ldsm4(tl[0][pr], sb + kSaT + kTl + offT[pr]);
-        }
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xb[(kw * 8 + j) * 32] = make_float4(X[j][0], X[j][1], X[j][2], X[j][3]);
+            for (int m = 0; m < MT; ++m)
+                xb[((kw * 8 + j) * MT + m) * 32] = make_float4(X[m][j][0], X[m][j][1], X[m][j][2], X[m][j][3]);
         named_bar_sync(1 + u, 64);
         if (lane == 0) mbar_arrive(&bar->fs[hb]);
         // right side beta V - x X, split; token tiles 2 ks, 2 ks + 1 are k step ks of the next product
-        uint32_t rh[4][4], rl[4][4];
-        {
-            float4 o[8];
+        uint32_t rh[MT][4][4], rl[MT][4][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = xb[((1 - kw) * 8 + j) * 32];
+        for (int ks = 0; ks < 4; ++ks) {
+            if (MT > 1) fetch_right(ks);
+            float4 o[2][MT];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int ks = j >> 1, e = j & 1;
-                const float2 m = make_float2(-cx[j].x, -cx[j].y);
-                const float2 v0 = make_float2(lo_f(vv[ks][2 * e]), hi_f(vv[ks][2 * e]));
-                const float2 v1 = make_float2(lo_f(vv[ks][2 * e + 1]), hi_f(vv[ks][2 * e + 1]));
-                const float2 x0 = f2_add(make_float2(X[j][0], X[j][1]), make_float2(o[j].x, o[j].y));
-                const float2 x1 = f2_add(make_float2(X[j][2], X[j][3]), make_float2(o[j].z, o[j].w));
-                split_tile(f2_fma(m, x0, f2_mul(be[j], v0)), f2_fma(m, x1, f2_mul(be[j], v1)), rh[ks] + 2 * e, rl[ks] + 2 * e);
-            }
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) o[e][m] = xb[(((1 - kw) * 8 + 2 * ks + e) * MT + m) * 32];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int j = 2 * ks + e;
+                    const float2 x = make_float2(-cx[j].x, -cx[j].y);
+                    const uint32_t w0 = vv[m][ks][2 * e], w1 = vv[m][ks][2 * e + 1];
+                    const float2 v0 = make_float2(lo_f(w0), hi_f(w0)), v1 = make_float2(lo_f(w1), hi_f(w1));
+                    const float2 x0 = f2_add(make_float2(X[m][j][0], X[m][j][1]), make_float2(o[e][m].x, o[e][m].y));
+                    const float2 x1 = f2_add(make_float2(X[m][j][2], X[m][j][3]), make_float2(o[e][m].z, o[e][m].w));
+                    split_tile(f2_fma(x, x0, f2_mul(be[j], v0)), f2_fma(x, x1, f2_mul(be[j], v1)), rh[m][ks] + 2 * e, rl[m][ks] + 2 * e);
+                }
         }
-        // U^T of this warp's tiles, the high products and the mixed ones apart (shorter chains of MMAs)
-        float U[4][4], W[4][4];
+        // U^T of this warp's tiles; with MT = 1 the high products and the mixed ones apart (shorter chains of MMAs)
+        float U[MT][4][4], W[4][4];
 #pragma unroll
         for (int pr = 0; pr < 4; ++pr)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) U[pr][e] = W[pr][e] = 0.f;
+            for (int e = 0; e < 4; ++e) {
+                W[pr][e] = 0.f;
 #pragma unroll
-        for (int pr = 2; pr < 4; ++pr) {
-            ldsm4(th[1][pr], sb + kSaT + (offT[pr] ^ 64));
-            ldsm4(tl[1][pr], sb + kSaT + kTl + (offT[pr] ^ 64));
-        }
+                for (int m = 0; m < MT; ++m) U[m][pr][e] = 0.f;
+            }
+        if (MT > 1) fetch_T(0);
+        if (MT == 1) fetch_T(1);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             const int kp = ks >> 1, k2 = 2 * (ks & 1);
+            if (MT > 1 && ks == 2) fetch_T(1);
 #pragma unroll
-            for (int pr = ks; pr < 4; ++pr) mma(U[pr], rh[ks], th[kp][pr][k2], th[kp][pr][k2 + 1]);
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int pr = ks; pr < 4; ++pr) mma(W[pr], rl[ks], th[kp][pr][k2], th[kp][pr][k2 + 1]);
+                for (int pr = ks; pr < 4; ++pr) mma(U[m][pr], rh[m][ks], th[kp][pr][k2], th[kp][pr][k2 + 1]);
 #pragma unroll
-            for (int pr = ks; pr < 4; ++pr) mma(W[pr], rh[ks], tl[kp][pr][k2], tl[kp][pr][k2 + 1]);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int pr = ks; pr < 4; ++pr) mma(MT == 1 ? W[pr] : U[m][pr], rl[m][ks], th[kp][pr][k2], th[kp][pr][k2 + 1]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int pr = ks; pr < 4; ++pr) mma(MT == 1 ? W[pr] : U[m][pr], rh[m][ks], tl[kp][pr][k2], tl[kp][pr][k2 + 1]);
         }
         // while they run: the state's decay, K as the next B operand, the scalars of U
         const float2 gl2 = make_float2(gl, gl);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            S[j][0] = f2_mul(S[j][0], gl2);
-            S[j][1] = f2_mul(S[j][1], gl2);
-        }
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                S[m][j][0] = f2_mul(S[m][j][0], gl2);
+                S[m][j][1] = f2_mul(S[m][j][1], gl2);
+            }
         const uint32_t rowT[2] = {(uint32_t)((lane & 7) + ((((lane >> 3) & 1) ^ own(kw, 0)) << 3)),
                                   (uint32_t)((lane & 7) + ((((lane >> 3) & 1) ^ own(kw, 1)) << 3))};
         const int pcT = lane >> 4;
 #pragma unroll
         for (int jp = 0; jp < 4; ++jp) ldsm4t(b[0][jp], sk + swz(rowT[0], 2 * jp + pcT));
-        float2 cu[4];
-#pragma unroll
-        for (int pr = 0; pr < 4; ++pr) cu[pr] = *reinterpret_cast<const float2 *>(sx + 2 * kC + 16 * pr + 8 * own(kw, pr) + q2);
-        uint32_t uh[4][4], ul[4][4];  // (x U)^T of a pair, own tile first
+        uint32_t uh[MT][4][4], ul[MT][4][4];  // (x U)^T of a pair, own tile first
 #pragma unroll
         for (int pr = 0; pr < 4; ++pr) {
+            const float2 cu = *reinterpret_cast<const float2 *>(sx + 2 * kC + 16 * pr + 8 * own(kw, pr) + q2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) U[pr][e] += W[pr][e];
-            uint32_t h[2], l[2];
-            split_tile(make_float2(U[pr][0], U[pr][1]), make_float2(U[pr][2], U[pr][3]), h, l);
-            hu[(2 * pr + own(kw, pr)) * 32] = make_uint4(h[0], h[1], l[0], l[1]);
-            split_tile(f2_mul(cu[pr], make_float2(U[pr][0], U[pr][1])), f2_mul(cu[pr], make_float2(U[pr][2], U[pr][3])),
-                       uh[pr], ul[pr]);
-            ub[(kw * 4 + pr) * 32] = make_uint4(uh[pr][0], uh[pr][1], ul[pr][0], ul[pr][1]);
+            for (int m = 0; m < MT; ++m) {
+                if (MT == 1)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) U[m][pr][e] += W[pr][e];
+                const float2 u0 = make_float2(U[m][pr][0], U[m][pr][1]), u1 = make_float2(U[m][pr][2], U[m][pr][3]);
+                uint32_t h[2], l[2];
+                split_tile(u0, u1, h, l);
+                hu[((2 * pr + own(kw, pr)) * MT + m) * 32] = make_uint4(h[0], h[1], l[0], l[1]);
+                split_tile(f2_mul(cu, u0), f2_mul(cu, u1), uh[m][pr], ul[m][pr]);
+                ub[((kw * 4 + pr) * MT + m) * 32] = make_uint4(uh[m][pr][0], uh[m][pr][1], ul[m][pr][0], ul[m][pr][1]);
+            }
         }
         named_bar_sync(1 + u, 64);
         if (lane == 0) mbar_arrive(&bar->fh[hb]);
@@ -713,15 +775,20 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
         bool ready = true;
         {
 #pragma unroll
-            for (int pr = 0; pr < 4; ++pr) {
-                const uint4 o = ub[((1 - kw) * 4 + pr) * 32];
-                uh[pr][2] = o.x; uh[pr][3] = o.y; ul[pr][2] = o.z; ul[pr][3] = o.w;
-            }
-            float acc[8][4];
+            for (int pr = 0; pr < 4; ++pr)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc[j][0] = S[j][0].x; acc[j][1] = S[j][0].y; acc[j][2] = S[j][1].x; acc[j][3] = S[j][1].y;
-            }
+                for (int m = 0; m < MT; ++m) {
+                    const uint4 o = ub[(((1 - kw) * 4 + pr) * MT + m) * 32];
+                    uh[m][pr][2] = o.x; uh[m][pr][3] = o.y; ul[m][pr][2] = o.z; ul[m][pr][3] = o.w;
+                }
+            float acc[MT][8][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc[m][j][0] = S[m][j][0].x; acc[m][j][1] = S[m][j][0].y;
+                    acc[m][j][2] = S[m][j][1].x; acc[m][j][3] = S[m][j][1].y;
+                }
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 const int x = ks & 1, y = x ^ 1;
@@ -730,19 +797,25 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
                     for (int jp = 0; jp < 4; ++jp) ldsm4t(b[y][jp], sk + swz(16 * (ks + 1) + rowT[y], 2 * jp + pcT));
                 }
                 if (ks == 2 && c + 1 < nc) {
-                    if (++st == kNa) st = 0, pa ^= 1;
+                    if (++st == L::kNa) st = 0, pa ^= 1;
                     ready = peek(c + 1);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mma(acc[j], uh[ks], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mma(acc[j], ul[ks], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
+                    for (int j = 0; j < 8; ++j) mma(acc[m][j], uh[m][ks], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mma(acc[m][j], ul[m][ks], b[x][j >> 1][2 * (j & 1)], b[x][j >> 1][2 * (j & 1) + 1]);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                S[j][0] = make_float2(acc[j][0], acc[j][1]);
-                S[j][1] = make_float2(acc[j][2], acc[j][3]);
-            }
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    S[m][j][0] = make_float2(acc[m][j][0], acc[m][j][1]);
+                    S[m][j][1] = make_float2(acc[m][j][2], acc[m][j][3]);
+                }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->ea[now]);
@@ -751,10 +824,12 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
     return good;
 }
 
+template <int MT>
 __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, StBars *bar, int u, int kw, const Place &pl, int h, int v0)
 {
+    using L = St<MT>;
     const int lane = threadIdx.x & 31, q2 = 2 * (lane & 3);
-    unsigned char *stg = sm + kSmSt + (2 * u + kw) * 1024;
+    unsigned char *stg = sm + L::kStg + (2 * u + kw) * (1024 * MT);
     const int nc = (pl.len + kC - 1) / kC;
     uint32_t off[4];  // rows of this warp's tile of pair p, pieces 0..3 (4..7: ^ 64)
 #pragma unroll
@@ -762,101 +837,111 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
     bool good = true;
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
-        const int st = c & 1, hb = c & 1;
-        static_assert(kNo == 2, "two stages");
-        const uint32_t sb = smem_u32(sm + kSmO + st * kSo);
-        const float *co = reinterpret_cast<const float *>(sm + kSmO + st * kSo + kSoP + kPx);
-        const uint4 *hs = reinterpret_cast<const uint4 *>(sm + kSmH + hb * kHand) + u * 256 + lane;
-        const uint4 *hu = reinterpret_cast<const uint4 *>(sm + kSmH + hb * kHand + 8192 + u * 4096) + lane;
+        const int st = c & 1, hb = c % L::kNh;
+        static_assert(L::kNo == 2, "two stages");
+        const uint32_t sb = smem_u32(sm + L::kO + st * L::kSo), ph = (uint32_t)((c / L::kNh) & 1);
+        const float *co = reinterpret_cast<const float *>(sm + L::kO + st * L::kSo + L::kP + kPx);
+        const uint4 *hs = reinterpret_cast<const uint4 *>(sm + L::kH + hb * L::kHand) + u * (256 * MT) + lane;
+        const uint4 *hu = reinterpret_cast<const uint4 *>(sm + L::kH + hb * L::kHand + L::kHu) + u * (256 * MT) + lane;
         // Q is read once the chain has handed over S0, while it makes little use of shared memory itself
-        if (good) good = wait_both(&bar->fo[st], (uint32_t)((c >> 1) & 1), &bar->fs[hb], (uint32_t)((c >> 1) & 1));
+        if (good) good = wait_both(&bar->fo[st], (uint32_t)((c >> 1) & 1), &bar->fs[hb], ph);
         uint32_t qb[4][4][4];
 #pragma unroll
         for (int kp = 0; kp < 4; ++kp)
 #pragma unroll
             for (int pr = 0; pr < 4; ++pr) ldsm4(qb[kp][pr], sb + (kp >> 1) * 8192 + (off[pr] ^ ((kp & 1) * 64)));
-        float o[4][4] = {};
+        float o[MT][4][4] = {};
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            const uint4 w = hs[ks * 32];
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+        for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-            for (int pr = 0; pr < 4; ++pr) mma(o[pr], a, qb[ks >> 1][pr][2 * (ks & 1)], qb[ks >> 1][pr][2 * (ks & 1) + 1]);
-        }
+            for (int m = 0; m < MT; ++m) {
+                const uint4 w = hs[(ks * MT + m) * 32];
+                const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int pr = 0; pr < 4; ++pr) mma(o[m][pr], a, qb[ks >> 1][pr][2 * (ks & 1)], qb[ks >> 1][pr][2 * (ks & 1) + 1]);
+            }
         uint32_t pb[2][4][4];
         float2 x[4];
 #pragma unroll
         for (int pr = 0; pr < 4; ++pr) {
-            ldsm4(pb[0][pr], sb + kSoP + off[pr]);
-            if (pr >= 2) ldsm4(pb[1][pr], sb + kSoP + (off[pr] ^ 64));
+            ldsm4(pb[0][pr], sb + L::kP + off[pr]);
+            if (pr >= 2) ldsm4(pb[1][pr], sb + L::kP + (off[pr] ^ 64));
             x[pr] = *reinterpret_cast<const float2 *>(co + 16 * pr + 8 * own(kw, pr) + q2);
         }
 #pragma unroll
-        for (int pr = 0; pr < 4; ++pr) {
-            o[pr][0] *= x[pr].x;
-            o[pr][1] *= x[pr].y;
-            o[pr][2] *= x[pr].x;
-            o[pr][3] *= x[pr].y;
-        }
-        if (good) good = mbar_wait_bounded(&bar->fh[hb], (uint32_t)((c >> 1) & 1), kStSpin);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const uint4 w0 = hu[2 * ks * 32], w1 = hu[(2 * ks + 1) * 32];
-            const uint32_t a[4] = {w0.x, w0.y, w1.x, w1.y}, al[4] = {w0.z, w0.w, w1.z, w1.w};
+            for (int pr = 0; pr < 4; ++pr) {
+                o[m][pr][0] *= x[pr].x;
+                o[m][pr][1] *= x[pr].y;
+                o[m][pr][2] *= x[pr].x;
+                o[m][pr][3] *= x[pr].y;
+            }
+        if (good) good = mbar_wait_bounded(&bar->fh[hb], ph, kStSpin);
 #pragma unroll
-            for (int pr = ks; pr < 4; ++pr) mma(o[pr], a, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-            for (int pr = ks; pr < 4; ++pr) mma(o[pr], al, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
-        }
+            for (int m = 0; m < MT; ++m) {
+                const uint4 w0 = hu[(2 * ks * MT + m) * 32], w1 = hu[((2 * ks + 1) * MT + m) * 32];
+                const uint32_t a[4] = {w0.x, w0.y, w1.x, w1.y}, al[4] = {w0.z, w0.w, w1.z, w1.w};
+#pragma unroll
+                for (int pr = ks; pr < 4; ++pr) mma(o[m][pr], a, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
+#pragma unroll
+                for (int pr = ks; pr < 4; ++pr) mma(o[m][pr], al, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
+            }
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&bar->eh[hb]);
             mbar_arrive(&bar->eo[st]);
         }
-        // 32 tokens x 16 values, staged as rows of 32 bytes
+        // 32 tokens x 16 MT values, staged as rows
         const int n = min(kC, pl.len - c * kC);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            stsm2t(smem_u32(stg) + (uint32_t)((8 * j + (lane & 7)) * 32 + ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4)),
-                   pack2(o[j][0], o[j][1]), pack2(o[j][2], o[j][3]));
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                stsm2t(smem_u32(stg) + o_off<MT>(8 * j + (lane & 7), 2 * m + ((lane >> 3) & 1)), pack2(o[m][j][0], o[m][j][1]),
+                       pack2(o[m][j][2], o[m][j][3]));
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 16 * i + (lane >> 1), half = lane & 1, pr = r >> 3, t = 16 * pr + 8 * own(kw, pr) + (r & 7);
-            const uint4 w = *reinterpret_cast<const uint4 *>(stg + r * 32 + ((half ^ ((r >> 2) & 1)) << 4));
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int e = 32 * i + lane, r = e / (2 * MT), pc = e % (2 * MT), pr = r >> 3, t = 16 * pr + 8 * own(kw, pr) + (r & 7);
+            const uint4 w = *reinterpret_cast<const uint4 *>(stg + o_off<MT>(r, pc));
             if (t < n)
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.rows.out) + ((int64_t)pl.t0 + c * kC + t) * p.rows.out_stride +
-                                           (size_t)h * kD + v0 + 16 * u + 8 * half) = w;
+                                           (size_t)h * kD + v0 + 16 * MT * u + 8 * pc) = w;
         }
         __syncwarp();
     }
     return good;
 }
 
+template <int MT>
 __global__ void __launch_bounds__(kStThreads, 1)
 gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__ Args p,
                  const unsigned char *__restrict__ blocks, int64_t n_chunks, int box_rows)
 {
+    using L = St<MT>;
     extern __shared__ unsigned char sm_raw[];
     unsigned char *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-    StBars *bar = reinterpret_cast<StBars *>(sm + kSmBar);
+    StBars *bar = reinterpret_cast<StBars *>(sm + L::kBar);
     Place *place = reinterpret_cast<Place *>(bar + 1);
     int *ok = reinterpret_cast<int *>(place + 1);
     static_assert(sizeof(StBars) + sizeof(Place) + 8 <= 256, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kVBlocks = kD / kVB;
+    constexpr int kVBlocks = kD / L::kVB;
     const int vb = blockIdx.x % kVBlocks;
     const int h = (blockIdx.x / kVBlocks) % p.H, seq = blockIdx.x / (kVBlocks * p.H);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kNa; ++s) {
+        for (int s = 0; s < L::kNa; ++s) {
             mbar_init(&bar->fa[s], 1);
             mbar_init(&bar->ea[s], 4);
         }
-        for (int s = 0; s < kNo; ++s) {
+        for (int s = 0; s < L::kNo; ++s) {
             mbar_init(&bar->fo[s], 1);
             mbar_init(&bar->eo[s], 4);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < L::kNh; ++s) {
             mbar_init(&bar->fs[s], 4);
             mbar_init(&bar->fh[s], 4);
             mbar_init(&bar->eh[s], 4);
@@ -887,27 +972,27 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
             bool good = true;
             wait_for_previous();  // the blocks; everything else that is read here is older than the prep kernel
             for (int c = 0; c < nc && good; ++c) {
-                const int sa = c % kNa, so = c % kNo, t = pl.t0 + c * kC;
+                const int sa = c % L::kNa, so = c % L::kNo, t = pl.t0 + c * kC;
                 const unsigned char *blk = blocks + ((size_t)(pl.first + c) * p.H + h) * kBlkBytes;
-                if (c >= kNa) good = mbar_wait_bounded(&bar->ea[sa], (uint32_t)(((c / kNa) - 1) & 1), kStSpin);
+                if (c >= L::kNa) good = mbar_wait_bounded(&bar->ea[sa], (uint32_t)(((c / L::kNa) - 1) & 1), kStSpin);
                 if (!good) break;
-                unsigned char *b = sm + sa * kSa;
-                mbar_arrive_expect_tx(&bar->fa[sa], (uint32_t)(box_rows * (2 * 128 + kVB * 2) + kPartT));
+                unsigned char *b = sm + sa * L::kSa;
+                mbar_arrive_expect_tx(&bar->fa[sa], (uint32_t)(box_rows * (2 * 128 + L::kVB * 2) + kPartT));
                 tma_load_2d(b, &maps.k, hk * kD, t, &bar->fa[sa]);
                 tma_load_2d(b + 8192, &maps.k, hk * kD + 64, t, &bar->fa[sa]);
-                bulk_g2s(b + kSaT, blk, kPartT, &bar->fa[sa]);
-                tma_load_2d(b + kSaV, &maps.v, h * kD + vb * kVB, t, &bar->fa[sa]);
-                if (c >= kNo) good = mbar_wait_bounded(&bar->eo[so], (uint32_t)(((c / kNo) - 1) & 1), kStSpin);
+                bulk_g2s(b + L::kT, blk, kPartT, &bar->fa[sa]);
+                tma_load_2d(b + L::kV, &maps.v, h * kD + vb * L::kVB, t, &bar->fa[sa]);
+                if (c >= L::kNo) good = mbar_wait_bounded(&bar->eo[so], (uint32_t)(((c / L::kNo) - 1) & 1), kStSpin);
                 if (!good) break;
-                b = sm + kSmO + so * kSo;
+                b = sm + L::kO + so * L::kSo;
                 mbar_arrive_expect_tx(&bar->fo[so], (uint32_t)(box_rows * 2 * 128 + kPartP));
                 tma_load_2d(b, &maps.q, hk * kD, t, &bar->fo[so]);
                 tma_load_2d(b + 8192, &maps.q, hk * kD + 64, t, &bar->fo[so]);
-                bulk_g2s(b + kSoP, blk + kPartT, kPartP, &bar->fo[so]);
+                bulk_g2s(b + L::kP, blk + kPartT, kPartP, &bar->fo[so]);
             }
             if (!good) {
                 if (p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
-                for (int s = 0; s < kNa; ++s) mbar_wait_bounded(&bar->fa[s], 0, 1u << 16);  // copies in flight land
+                for (int s = 0; s < L::kNa; ++s) mbar_wait_bounded(&bar->fa[s], 0, 1u << 16);  // copies in flight land
             }
         }
         return;
@@ -916,29 +1001,35 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     bool good;
     if (warp >= 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
-        good = output_pass(p, sm, bar, u, kw, pl, h, vb * kVB);
+        good = output_pass<MT>(p, sm, bar, u, kw, pl, h, vb * L::kVB);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        // this warp's part of S^T: value rows g, g + 8 of unit u, key rows 64 kw ..
-        const int g = lane >> 2, q2 = 2 * (lane & 3);
-        const size_t at = (size_t)(64 * kw + q2) * kD + vb * kVB + 16 * u + g;
-        float2 S[8][2];
+        // this warp's part of S^T: value rows g, g + 8 of the unit's tiles, key rows 64 kw ..
+        const size_t at = (size_t)(64 * kw + 2 * (lane & 3)) * kD + vb * L::kVB + 16 * MT * u + (lane >> 2);
+        float2 S[MT][8][2];
         const float *s = p.S + ((size_t)max(src, 0) * p.H + h) * kD * kD + at;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                S[j][e] = src >= 0 ? make_float2(s[8 * j * kD + 8 * e], s[(8 * j + 1) * kD + 8 * e]) : make_float2(0.f, 0.f);
-        good = chain_pass(sm, bar, u, kw, pl.len, S);
-        float *d = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
-        if (good)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    d[8 * j * kD + 8 * e] = S[j][e].x;
-                    d[(8 * j + 1) * kD + 8 * e] = S[j][e].y;
+                    const int i = 8 * j * kD + 16 * m + 8 * e;
+                    S[m][j][e] = src >= 0 ? make_float2(s[i], s[i + kD]) : make_float2(0.f, 0.f);
                 }
+        good = chain_pass<MT>(sm, bar, u, kw, pl.len, S);
+        float *d = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
+        if (good)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = 8 * j * kD + 16 * m + 8 * e;
+                        d[i] = S[m][j][e].x;
+                        d[i + kD] = S[m][j][e].y;
+                    }
     }
     if (!good && lane == 0 && p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
 }
@@ -958,6 +1049,7 @@ cudaError_t rows_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+template <int MT>
 cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_chunks, int dev, cudaStream_t stream)
 {
     const int64_t T = p.total_T;
@@ -968,16 +1060,16 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
         const int64_t Dk = (int64_t)(p.H / p.G) * kD, Dv = (int64_t)p.H * kD;
         if ((e = rows_map(&m.k, p.rows.k, T, Dk, p.rows.k_stride, 64, box)) != cudaSuccess ||
             (e = rows_map(&m.q, p.rows.q, T, Dk, p.rows.q_stride, 64, box)) != cudaSuccess ||
-            (e = rows_map(&m.v, p.rows.v, T, Dv, p.rows.v_stride, kVB, box)) != cudaSuccess)
+            (e = rows_map(&m.v, p.rows.v, T, Dv, p.rows.v_stride, St<MT>::kVB, box)) != cudaSuccess)
             return e;
     }
     static std::atomic<uint64_t> done;
-    e = raise_smem_on(done, dev, gdr_state_kernel, kStSmem);
+    e = raise_smem_on(done, dev, gdr_state_kernel<MT>, St<MT>::kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((int64_t)p.N * p.H * (kD / kVB));
-    if (n_chunks > 0) return launch_after(gdr_state_kernel, dim3(grid), dim3(kStThreads), kStSmem, stream, m, p, blocks, n_chunks, box);
+    const unsigned grid = (unsigned)((int64_t)p.N * p.H * (kD / St<MT>::kVB));
+    if (n_chunks > 0) return launch_after(gdr_state_kernel<MT>, dim3(grid), dim3(kStThreads), St<MT>::kSmem, stream, m, p, blocks, n_chunks, box);
     // no prep kernel before it: whatever the stream holds may still be writing the states
-    gdr_state_kernel<<<grid, kStThreads, kStSmem, stream>>>(m, p, blocks, n_chunks, box);
+    gdr_state_kernel<MT><<<grid, kStThreads, St<MT>::kSmem, stream>>>(m, p, blocks, n_chunks, box);
     return cudaGetLastError();
 }
 
@@ -985,7 +1077,7 @@ cudaError_t launch_state(const Args &p, const unsigned char *blocks, int64_t n_c
 
 size_t chunked_workspace_bytes(int64_t n_chunks, int32_t H) { return 256 + (size_t)n_chunks * H * kBlkBytes; }
 
-cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int dev, int sms, cudaStream_t stream)
+cudaError_t launch_chunked(const Args &p, int64_t n_chunks, int64_t longest, void *ws, int dev, int sms, cudaStream_t stream)
 {
     unsigned char *blocks = static_cast<unsigned char *>(ws) +
                             ((128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127);
@@ -1000,7 +1092,16 @@ cudaError_t launch_chunked(const Args &p, int64_t n_chunks, void *ws, int dev, i
         gdr_prep_kernel<<<grid, kPrepThreads, kPrepSmem, stream>>>(p, blocks, (int)n_chunks, Hk);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return launch_state(p, blocks, n_chunks, dev, stream);
+    // 32 or 64 value columns a block, by the time that either is estimated to take: the longest sequence, or all
+    // of the work over the SMs, at 1.65 us a chunk of 32 columns, 3.2 us a chunk of 64 and 3.5 us to start a
+    // block. One sequence of 8192 tokens and 32 heads: 288 us with 32 columns, 482 us with 64; ten sequences of
+    // 2 .. 467 tokens and 64 heads: 176 and 156 us.
+    auto estimate = [&](int mt, double chunk) {
+        const double work = (n_chunks * chunk + p.N * 3.5) * p.H * (4 / mt) / sms, chain = longest * chunk + 3.5;
+        return work > chain ? work : chain;
+    };
+    return estimate(1, 1.65) <= estimate(2, 3.2) ? launch_state<1>(p, blocks, n_chunks, dev, stream)
+                                                 : launch_state<2>(p, blocks, n_chunks, dev, stream);
 }
 
 }  // namespace gdr
