@@ -409,8 +409,9 @@ kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void *xq, const
  * distinct, and no row's dst may be another row's src.
  *   src_slots, dst_slots  device int32. A row with an id out of range is skipped (its out rows
  *                         and slots keep their contents) and KDA_ERR_DEVICE is recorded.
- *   err     device int32 word or NULL. Receives KDA_ERR_DEVICE (a bad slot id, or a cu_seqlens
- *           that disagrees with cu_seqlens_host; the call then leaves out and S as they are) or
+ *   err     device int32 word or NULL. Receives KDA_ERR_DEVICE (a bad slot id; or a cu_seqlens that
+ *           does not rise from 0 to cu_seqlens_host[N], or for BF16 rows has another number of
+ *           64-token chunks than the host's: the call then leaves out and S as they are) or
  *           KDA_ERR_TIMEOUT (a bounded wait gave up). Never cleared by the library.
  */
 typedef struct {

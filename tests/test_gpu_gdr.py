@@ -145,7 +145,8 @@ def test_decode(n, B, H, Hk, bf16, packed):
 
 
 @pytest.mark.parametrize("lens", [[1], [63], [64], [65], [128], [200], [0, 1, 0, 130, 64, 2, 0]])
-@pytest.mark.parametrize("H,Hk,bf16,packed", [(2, 1, True, True), (3, 3, True, False), (4, 1, True, True), (4, 2, False, True)])
+@pytest.mark.parametrize("H,Hk,bf16,packed", [(2, 1, True, True), (3, 3, True, False), (4, 1, True, True), (9, 1, True, False),
+                                               (4, 2, False, True)])
 def test_prefill(lens, H, Hk, bf16, packed):
     p = Problem(lens, H, Hk, bf16, seed=2, packed=packed)
     S, src, dst = p.slots()
@@ -296,6 +297,29 @@ def test_bad_slots_and_lengths_are_recorded():
     p.decode(S, src, dst, 1, err=err)
     assert err.item() == K.KDA_ERR_DEVICE and bool((p.out[0] == -7.0).all())
     near_state(S[3], p.ref(1)[1], False)
+
+
+def test_fp32_sequences_refuse_a_cu_seqlens_that_is_wrong_anywhere():
+    p = Problem([6] * 40, 2, 2, False, seed=16)  # more sequences than a warp has lanes
+    ws = torch.empty(K.kda_gdr_workspace_bytes(p.cfg, p.cu), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for at, value in ((0, 1), (40, 239), (7, 30), (36, 217), (39, 1 << 30), (20, -1)):
+        wrong = p.cu.copy()
+        wrong[at] = value
+        S, src, dst = p.slots()
+        keep = S.clone()
+        p.out.fill_(-7.0)
+        err.zero_()
+        K.kda_gdr_prefill(p.cfg, p.params, S, src, dst, torch.from_numpy(wrong).cuda(), p.cu, *p.rows(), ws, err=err)
+        torch.cuda.synchronize()
+        if (at, value) == (36, 217):  # .. 210, 217, 222 ..: it rises from 0 to 240, another split of the same tokens
+            assert err.item() == 0
+            p.cu, p.lens = wrong, [int(n) for n in np.diff(wrong)]
+            check(p, S, src, dst, p.S0, False)
+            p.cu, p.lens = np.arange(0, 241, 6, dtype=np.int32), [6] * 40
+            continue
+        assert err.item() == K.KDA_ERR_DEVICE, (at, value)
+        assert bool((p.out == -7.0).all()) and torch.equal(S, keep), (at, value)
 
 
 def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph():
