@@ -145,8 +145,9 @@ __device__ __forceinline__ void add2(float &h, float &l, float x, float y)
 // 128 threads; warp w has the rows t = 16 w .. 16 w + 15. T by blocks of 16 rows: the diagonal blocks
 // D_w = (I + A_ww)^-1 by forward substitution in FP32, a warp each, one column a lane; below them
 //   T[w][:] = -D_w sum_{j < w} A[w][j] T[j][:]
-// on the tensor cores with split factors, three barriers deep. (The whole inverse by forward
-// substitution, a column a lane, took 92 us for 4096 (chunk, value head) pairs; see the launch below.)
+// on the tensor cores with split factors, three barriers deep. 66 us for 4096 (chunk, value head) pairs of
+// two value heads a key head (92 us with the whole inverse by forward substitution, a column a lane); bound
+// by the latency of its phases, 12 warps an SM, with DRAM at 22% and issue slots at 32%.
 // Shared memory: two buffers of K and Q rows (the next item's are loaded while one is computed; a block is
 // built in the place of the rows that it came from), A's diagonal blocks, scalars of up to four value heads.
 constexpr int kPrepThreads = 128, kPrepPerSm = 3;
@@ -259,235 +260,235 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
     load_logits(cur, 0, lg);
 #pragma unroll 1
     for (; item < n_items; item += gridDim.x, buf ^= 1, cur = nxt) {
-    unsigned char *sm = sm_all + buf * kPsBuf;
-    const uint32_t sK = smem_u32(sm), sQ = sK + kPsQ;
-    const int64_t chunk = cur.chunk;
-    const int hk = cur.hk;
-    const bool more = item + (int)gridDim.x < n_items;
-    if (more) locate(item + gridDim.x, nxt);
-    decays(cur, 0, lg);
-    cp_async_wait_all();
-    if (tid == 0) bulk_wait_read_all();  // the other buffer's block has been read
-    __syncthreads();
-    if (more) {
-        load_rows(nxt, sm_all + (buf ^ 1) * kPsBuf);
-        load_logits(nxt, 0, lg);
-    }
-    {  // norms: two threads a row of K and of Q
-        const int r = tid >> 1, half = tid & 1;
-        float kk = 0.f, qq = 0.f;
+        unsigned char *sm = sm_all + buf * kPsBuf;
+        const uint32_t sK = smem_u32(sm), sQ = sK + kPsQ;
+        const int64_t chunk = cur.chunk;
+        const int hk = cur.hk;
+        const bool more = item + (int)gridDim.x < n_items;
+        if (more) locate(item + gridDim.x, nxt);
+        decays(cur, 0, lg);
+        cp_async_wait_all();
+        if (tid == 0) bulk_wait_read_all();  // the other buffer's block has been read
+        __syncthreads();
+        if (more) {
+            load_rows(nxt, sm_all + (buf ^ 1) * kPsBuf);
+            load_logits(nxt, 0, lg);
+        }
+        {  // norms: two threads a row of K and of Q
+            const int r = tid >> 1, half = tid & 1;
+            float kk = 0.f, qq = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const uint32_t off = (uint32_t)half * 8192 + swz(r, c);
-            const uint4 a = *reinterpret_cast<const uint4 *>(sm + off);
-            const uint4 b = *reinterpret_cast<const uint4 *>(sm + kPsQ + off);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t off = (uint32_t)half * 8192 + swz(r, c);
+                const uint4 a = *reinterpret_cast<const uint4 *>(sm + off);
+                const uint4 b = *reinterpret_cast<const uint4 *>(sm + kPsQ + off);
+                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                kk = fmaf(lo_f(aw[e]), lo_f(aw[e]), fmaf(hi_f(aw[e]), hi_f(aw[e]), kk));
-                qq = fmaf(lo_f(bw[e]), lo_f(bw[e]), fmaf(hi_f(bw[e]), hi_f(bw[e]), qq));
+                for (int e = 0; e < 4; ++e) {
+                    kk = fmaf(lo_f(aw[e]), lo_f(aw[e]), fmaf(hi_f(aw[e]), hi_f(aw[e]), kk));
+                    qq = fmaf(lo_f(bw[e]), lo_f(bw[e]), fmaf(hi_f(bw[e]), hi_f(bw[e]), qq));
+                }
+            }
+            kk += __shfl_xor_sync(0xFFFFFFFFu, kk, 1);
+            qq += __shfl_xor_sync(0xFFFFFFFFu, qq, 1);
+            if (half == 0) {
+                sRk[r] = p.l2norm ? rsqrtf(kk + p.l2_eps) : 1.f;
+                sRq[r] = p.l2norm ? p.q_scale * rsqrtf(qq + p.l2_eps) : p.q_scale;
             }
         }
-        kk += __shfl_xor_sync(0xFFFFFFFFu, kk, 1);
-        qq += __shfl_xor_sync(0xFFFFFFFFu, qq, 1);
-        if (half == 0) {
-            sRk[r] = p.l2norm ? rsqrtf(kk + p.l2_eps) : 1.f;
-            sRq[r] = p.l2norm ? p.q_scale * rsqrtf(qq + p.l2_eps) : p.q_scale;
+        // K K^T and Q K^T: rows t of this warp, columns i <= 16 w + 15
+        float kk[8][4], qk[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t half = (uint32_t)(ks >> 2) * 8192;
+            uint32_t ak[4], aq[4];
+            const uint32_t oa = half + swz(16 * warp + (lane & 15), 2 * (ks & 3) + (lane >> 4));
+            ldsm4(ak, sK + oa);
+            ldsm4(aq, sQ + oa);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) {
+                if (jp > warp) break;
+                uint32_t b[4];
+                ldsm4(b, sK + half + swz(16 * jp + (lane & 7) + ((lane >> 4) << 3), 2 * (ks & 3) + ((lane >> 3) & 1)));
+                mma(kk[2 * jp], ak, b[0], b[1]);
+                mma(kk[2 * jp + 1], ak, b[2], b[3]);
+                mma(qk[2 * jp], aq, b[0], b[1]);
+                mma(qk[2 * jp + 1], aq, b[2], b[3]);
+            }
         }
-    }
-    // K K^T and Q K^T: rows t of this warp, columns i <= 16 w + 15
-    float kk[8][4], qk[8][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t half = (uint32_t)(ks >> 2) * 8192;
-        uint32_t ak[4], aq[4];
-        const uint32_t oa = half + swz(16 * warp + (lane & 15), 2 * (ks & 3) + (lane >> 4));
-        ldsm4(ak, sK + oa);
-        ldsm4(aq, sQ + oa);
-#pragma unroll
-        for (int jp = 0; jp < 4; ++jp) {
-            if (jp > warp) break;
-            uint32_t b[4];
-            ldsm4(b, sK + half + swz(16 * jp + (lane & 7) + ((lane >> 4) << 3), 2 * (ks & 3) + ((lane >> 3) & 1)));
-            mma(kk[2 * jp], ak, b[0], b[1]);
-            mma(kk[2 * jp + 1], ak, b[2], b[3]);
-            mma(qk[2 * jp], aq, b[0], b[1]);
-            mma(qk[2 * jp + 1], aq, b[2], b[3]);
-        }
-    }
-    const int rowT = (lane & 7) + (((lane >> 3) & 1) << 3), pcT = lane >> 4;  // ldmatrix.trans of B operands
+        const int rowT = (lane & 7) + (((lane >> 3) & 1) << 3), pcT = lane >> 4;  // ldmatrix.trans of B operands
 #pragma unroll 1
-    for (int j = 0; j < p.G; ++j) {
-        unsigned char *blk = sm;
-        const uint32_t sT = sK;
-        if (j && (j & 3) == 0) {
-            __syncthreads();  // every warp has read the last four heads' scalars
-            Logits l;
-            load_logits(cur, j, l);
-            decays(cur, j, l);
-        }
-        if (j == 0 || (j & 3) == 0) __syncthreads();  // scalars and norms are written
-        const float *s = scal + (j & 3) * kScal;
-        // A and P from the products: A's blocks left of the diagonal stay in registers as split A operands
-        uint32_t ah[3][4], al[3][4], pk[8][2];
-        {
-            const int ta = 16 * warp + g;
-            float Gh[2], Gl[2], fb[2], fq[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = ta + 8 * e;
-                Gh[e] = s[t];
-                Gl[e] = s[kC + t];
-                fb[e] = s[2 * kC + t] * sRk[t];
-                fq[e] = sRq[t];
+        for (int j = 0; j < p.G; ++j) {
+            unsigned char *blk = sm;
+            const uint32_t sT = sK;
+            if (j && (j & 3) == 0) {
+                __syncthreads();  // every warp has read the last four heads' scalars
+                Logits l;
+                load_logits(cur, j, l);
+                decays(cur, j, l);
             }
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                if ((nt >> 1) > warp) break;
-                const int i = 8 * nt + q2;
-                const float2 gh = *reinterpret_cast<const float2 *>(s + i), gl = *reinterpret_cast<const float2 *>(s + kC + i);
-                const float2 rk = *reinterpret_cast<const float2 *>(sRk + i);
-                float av[2][2], pv[2][2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const float x = (Gh[e] - (f ? gh.y : gh.x)) + (Gl[e] - (f ? gl.y : gl.x));
-                        const float d = ex2(x) * (f ? rk.y : rk.x);
-                        av[e][f] = i + f < ta + 8 * e ? fb[e] * d * kk[nt][2 * e + f] : 0.f;
-                        pv[e][f] = i + f <= ta + 8 * e ? fq[e] * d * qk[nt][2 * e + f] : 0.f;
-                    }
+            if (j == 0 || (j & 3) == 0) __syncthreads();  // scalars and norms are written
+            const float *s = scal + (j & 3) * kScal;
+            // A and P from the products: A's blocks left of the diagonal stay in registers as split A operands
+            uint32_t ah[3][4], al[3][4], pk[8][2];
+            {
+                const int ta = 16 * warp + g;
+                float Gh[2], Gl[2], fb[2], fq[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    pk[nt][e] = pack2(pv[e][0], pv[e][1]);
-                    if ((nt >> 1) < warp) {
-                        if (nt < 6) split2(av[e][0], av[e][1], ah[(nt >> 1) % 3][2 * (nt & 1) + e], al[(nt >> 1) % 3][2 * (nt & 1) + e]);
-                    } else {
+                    const int t = ta + 8 * e;
+                    Gh[e] = s[t];
+                    Gl[e] = s[kC + t];
+                    fb[e] = s[2 * kC + t] * sRk[t];
+                    fq[e] = sRq[t];
+                }
 #pragma unroll
-                        for (int f = 0; f < 2; ++f) diag[(8 * (nt & 1) + q2 + f) * kDp + g + 8 * e] = av[e][f];
+                for (int nt = 0; nt < 8; ++nt) {
+                    if ((nt >> 1) > warp) break;
+                    const int i = 8 * nt + q2;
+                    const float2 gh = *reinterpret_cast<const float2 *>(s + i), gl = *reinterpret_cast<const float2 *>(s + kC + i);
+                    const float2 rk = *reinterpret_cast<const float2 *>(sRk + i);
+                    float av[2][2], pv[2][2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const float x = (Gh[e] - (f ? gh.y : gh.x)) + (Gl[e] - (f ? gl.y : gl.x));
+                            const float d = ex2(x) * (f ? rk.y : rk.x);
+                            av[e][f] = i + f < ta + 8 * e ? fb[e] * d * kk[nt][2 * e + f] : 0.f;
+                            pv[e][f] = i + f <= ta + 8 * e ? fq[e] * d * qk[nt][2 * e + f] : 0.f;
+                        }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        pk[nt][e] = pack2(pv[e][0], pv[e][1]);
+                        if ((nt >> 1) < warp) {
+                            if (nt < 6) split2(av[e][0], av[e][1], ah[(nt >> 1) % 3][2 * (nt & 1) + e], al[(nt >> 1) % 3][2 * (nt & 1) + e]);
+                        } else {
+#pragma unroll
+                            for (int f = 0; f < 2; ++f) diag[(8 * (nt & 1) + q2 + f) * kDp + g + 8 * e] = av[e][f];
+                        }
                     }
                 }
             }
-        }
-        __syncwarp();
-        const int jc = lane & 15;  // the diagonal block's inverse: column lane & 15
-        float acc[16];
+            __syncwarp();
+            const int jc = lane & 15;  // the diagonal block's inverse: column lane & 15
+            float acc[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[r] = r == jc ? 1.f : 0.f;
+            for (int r = 0; r < 16; ++r) acc[r] = r == jc ? 1.f : 0.f;
 #pragma unroll
-        for (int r = 0; r < 15; ++r) {
-            float a[16];
+            for (int r = 0; r < 15; ++r) {
+                float a[16];
 #pragma unroll
-            for (int e = (r + 1) / 4; e < 4; ++e)
-                *reinterpret_cast<float4 *>(a + 4 * e) = *reinterpret_cast<const float4 *>(diag + r * kDp + 4 * e);
+                for (int e = (r + 1) / 4; e < 4; ++e)
+                    *reinterpret_cast<float4 *>(a + 4 * e) = *reinterpret_cast<const float4 *>(diag + r * kDp + 4 * e);
 #pragma unroll
-            for (int r2 = r + 1; r2 < 16; ++r2) acc[r2] = fmaf(-a[r2], acc[r], acc[r2]);
-        }
-        if (j) {
-            if (tid == 0) bulk_wait_read_all();  // the previous head's block has been read
-            __syncthreads();
-        }
-        // the block takes the place of K and Q (read before the first head's barrier above)
-        {
-            unsigned char *dst = blk + (lane & 16 ? kTl : 0) + 2 * (jc & 7);  // lanes 0..15 the high part, 16..31 the low
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(acc[r]);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(acc[r] - __bfloat162float(hi));
-                *reinterpret_cast<__nv_bfloat16 *>(dst + swz(16 * warp + r, 2 * warp + (jc >> 3))) = lane & 16 ? lo : hi;
+                for (int r2 = r + 1; r2 < 16; ++r2) acc[r2] = fmaf(-a[r2], acc[r], acc[r2]);
             }
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                if ((nt >> 1) > warp) break;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<uint32_t *>(blk + kPartT + swz(16 * warp + g + 8 * e, nt) + 2 * q2) = pk[nt][e];
+            if (j) {
+                if (tid == 0) bulk_wait_read_all();  // the previous head's block has been read
+                __syncthreads();
             }
-            if (tid < kC) {
-                float *x = reinterpret_cast<float *>(blk + kTx);
-                x[tid] = s[2 * kC + tid] * sRk[tid] * s[3 * kC + tid];
-                x[kC + tid] = s[2 * kC + tid];
-                x[2 * kC + tid] = sRk[tid] * s[4 * kC + tid];
-                if (tid == 0) x[3 * kC] = s[5 * kC];
-                reinterpret_cast<float *>(blk + kPartT + kPx)[tid] = sRq[tid] * s[3 * kC + tid];
+            // the block takes the place of K and Q (read before the first head's barrier above)
+            {
+                unsigned char *dst = blk + (lane & 16 ? kTl : 0) + 2 * (jc & 7);  // lanes 0..15 the high part, 16..31 the low
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(acc[r]);
+                    const __nv_bfloat16 lo = __float2bfloat16_rn(acc[r] - __bfloat162float(hi));
+                    *reinterpret_cast<__nv_bfloat16 *>(dst + swz(16 * warp + r, 2 * warp + (jc >> 3))) = lane & 16 ? lo : hi;
+                }
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    if ((nt >> 1) > warp) break;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint32_t *>(blk + kPartT + swz(16 * warp + g + 8 * e, nt) + 2 * q2) = pk[nt][e];
+                }
+                if (tid < kC) {
+                    float *x = reinterpret_cast<float *>(blk + kTx);
+                    x[tid] = s[2 * kC + tid] * sRk[tid] * s[3 * kC + tid];
+                    x[kC + tid] = s[2 * kC + tid];
+                    x[2 * kC + tid] = sRk[tid] * s[4 * kC + tid];
+                    if (tid == 0) x[3 * kC] = s[5 * kC];
+                    reinterpret_cast<float *>(blk + kPartT + kPx)[tid] = sRq[tid] * s[3 * kC + tid];
+                }
             }
-        }
-        float Y[6][4];
+            float Y[6][4];
 #pragma unroll
-        for (int i = 0; i < 6; ++i)
+            for (int i = 0; i < 6; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) Y[i][e] = 0.f;
+                for (int e = 0; e < 4; ++e) Y[i][e] = 0.f;
 #pragma unroll
-        for (int jb = 0; jb < 3; ++jb) {
-            __syncthreads();  // block row jb of T is complete
-            if (warp <= jb) continue;
-#pragma unroll
-            for (int np = 0; np <= jb; ++np) {
-                uint32_t bh[4], bl[4];
-                const uint32_t off = swz(16 * jb + rowT, 2 * np + pcT);
-                ldsm4t(bh, sT + off);
-                ldsm4t(bl, sT + kTl + off);
-                mma(Y[2 * np], ah[jb], bh[0], bh[1]);
-                mma(Y[2 * np + 1], ah[jb], bh[2], bh[3]);
-                mma(Y[2 * np], al[jb], bh[0], bh[1]);
-                mma(Y[2 * np + 1], al[jb], bh[2], bh[3]);
-                mma(Y[2 * np], ah[jb], bl[0], bl[1]);
-                mma(Y[2 * np + 1], ah[jb], bl[2], bl[3]);
-            }
-            if (warp == jb + 1) {  // T[w][:] = -D Y: Y goes to its own place in T first, to be read as a B operand
-                uint32_t dh[4], dl[4];
-                const uint32_t od = swz(16 * warp + (lane & 15), 2 * warp + (lane >> 4));
-                ldsm4(dh, sT + od);
-                ldsm4(dl, sT + kTl + od);
-#pragma unroll
-                for (int nt = 0; nt < 2 * jb + 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t h, l;
-                        split2(-Y[nt][2 * e], -Y[nt][2 * e + 1], h, l);
-                        unsigned char *dst = blk + swz(16 * warp + g + 8 * e, nt) + 2 * q2;
-                        *reinterpret_cast<uint32_t *>(dst) = h;
-                        *reinterpret_cast<uint32_t *>(dst + kTl) = l;
-                    }
-                __syncwarp();
+            for (int jb = 0; jb < 3; ++jb) {
+                __syncthreads();  // block row jb of T is complete
+                if (warp <= jb) continue;
 #pragma unroll
                 for (int np = 0; np <= jb; ++np) {
                     uint32_t bh[4], bl[4];
-                    const uint32_t off = swz(16 * warp + rowT, 2 * np + pcT);
+                    const uint32_t off = swz(16 * jb + rowT, 2 * np + pcT);
                     ldsm4t(bh, sT + off);
                     ldsm4t(bl, sT + kTl + off);
-                    __syncwarp();
-                    float z[2][4] = {};
-                    mma(z[0], dh, bh[0], bh[1]);
-                    mma(z[1], dh, bh[2], bh[3]);
-                    mma(z[0], dl, bh[0], bh[1]);
-                    mma(z[1], dl, bh[2], bh[3]);
-                    mma(z[0], dh, bl[0], bl[1]);
-                    mma(z[1], dh, bl[2], bl[3]);
+                    mma(Y[2 * np], ah[jb], bh[0], bh[1]);
+                    mma(Y[2 * np + 1], ah[jb], bh[2], bh[3]);
+                    mma(Y[2 * np], al[jb], bh[0], bh[1]);
+                    mma(Y[2 * np + 1], al[jb], bh[2], bh[3]);
+                    mma(Y[2 * np], ah[jb], bl[0], bl[1]);
+                    mma(Y[2 * np + 1], ah[jb], bl[2], bl[3]);
+                }
+                if (warp == jb + 1) {  // T[w][:] = -D Y: Y goes to its own place in T first, to be read as a B operand
+                    uint32_t dh[4], dl[4];
+                    const uint32_t od = swz(16 * warp + (lane & 15), 2 * warp + (lane >> 4));
+                    ldsm4(dh, sT + od);
+                    ldsm4(dl, sT + kTl + od);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
+                    for (int nt = 0; nt < 2 * jb + 2; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             uint32_t h, l;
-                            split2(z[x][2 * e], z[x][2 * e + 1], h, l);
-                            unsigned char *dst = blk + swz(16 * warp + g + 8 * e, 2 * np + x) + 2 * q2;
+                            split2(-Y[nt][2 * e], -Y[nt][2 * e + 1], h, l);
+                            unsigned char *dst = blk + swz(16 * warp + g + 8 * e, nt) + 2 * q2;
                             *reinterpret_cast<uint32_t *>(dst) = h;
                             *reinterpret_cast<uint32_t *>(dst + kTl) = l;
                         }
+                    __syncwarp();
+#pragma unroll
+                    for (int np = 0; np <= jb; ++np) {
+                        uint32_t bh[4], bl[4];
+                        const uint32_t off = swz(16 * warp + rowT, 2 * np + pcT);
+                        ldsm4t(bh, sT + off);
+                        ldsm4t(bl, sT + kTl + off);
+                        __syncwarp();
+                        float z[2][4] = {};
+                        mma(z[0], dh, bh[0], bh[1]);
+                        mma(z[1], dh, bh[2], bh[3]);
+                        mma(z[0], dl, bh[0], bh[1]);
+                        mma(z[1], dl, bh[2], bh[3]);
+                        mma(z[0], dh, bl[0], bl[1]);
+                        mma(z[1], dh, bl[2], bl[3]);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t h, l;
+                                split2(z[x][2 * e], z[x][2 * e + 1], h, l);
+                                unsigned char *dst = blk + swz(16 * warp + g + 8 * e, 2 * np + x) + 2 * q2;
+                                *reinterpret_cast<uint32_t *>(dst) = h;
+                                *reinterpret_cast<uint32_t *>(dst + kTl) = l;
+                            }
+                    }
                 }
             }
+            tc::fence_smem_to_async();
+            __syncthreads();
+            if (tid == 0) {
+                bulk_s2g(blocks + ((size_t)chunk * p.H + hk * p.G + j) * kBlkBytes, blk, kBlkBytes);
+                bulk_commit_group();
+            }
         }
-        tc::fence_smem_to_async();
-        __syncthreads();
-        if (tid == 0) {
-            bulk_s2g(blocks + ((size_t)chunk * p.H + hk * p.G + j) * kBlkBytes, blk, kBlkBytes);
-            bulk_commit_group();
-        }
-    }
     }
     if (tid == 0) bulk_wait_all();
 }
@@ -511,7 +512,7 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
 // fetched serves 32 rows. A chunk of it takes longer, two columns' worth of it less; see the rule at the launch.
 // Tcgen05 would run the same products in tiles of 64 or 128 rows at four times the MMA rate, but the four
 // dependent products of a chunk (64 x 128 x 32 and smaller) would each pay for the way through tensor memory
-// and back into shared memory.
+// and back into shared memory. 219 us for 32 heads of 8192 tokens (1.7 us a chunk), the tensor pipe 52% busy.
 constexpr int kStThreads = 384;
 template <int MT> struct St {
     static constexpr int kVB = 32 * MT;
