@@ -13,13 +13,12 @@
 // With a k split the FP32 partial sums go to the workspace and a second kernel adds them in split
 // order, so the result does not depend on timing.
 //
-// 8192 x 12288 x 7168: 543 us (2.66 PFLOP/s), the tensor pipe 64% busy. Without the sums' multiplications and
-// additions the same loads and MMAs take 447 us, without any of the epilogue's work 400 to 450: what bounds it
-// is an epilogue warp's turn a block, about 930 cycles for 128 columns (the wait, four loads from tensor
-// memory, 64 paired FMAs and the release), where the block's MMAs take 512. A form in which two CTAs share a
-// unit of 256 x 256 (cta_group::2; its operands alone: 400 us) had the same turn and was no faster (560 us), and
-// 16 epilogue warps of half the columns were slower (734 us: their registers spill).
-// 16 x 7168 x 12288: 25 us, 20 of it in this kernel at 4.4 TB/s and the rest in adding five splits.
+// 8192 x 12288 x 7168: 525 to 545 us (2.7 PFLOP/s), the tensor pipe 64% busy. The epilogue is well hidden: with
+// neither its reads of tensor memory nor its sums the kernel took 504 us where it took 527. The rest is operands and
+// MMAs: 48 KB a block of 128 of K and SM are about 17 TB/s out of L2, the likely bound. Forms in which two CTAs
+// share a unit of 256 x 256 (cta_group::2, a third fewer bytes) were no faster (560 us, the epilogue's hand-over
+// being their bound), nor were they with 16 epilogue warps of half the columns (734 us).
+// 16 x 7168 x 12288: 25 us, 19 to 21 of it in this kernel, about 4.4 TB/s, and the rest in adding the splits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>

@@ -54,6 +54,7 @@ class kda_gdr_config_t(ctypes.Structure):
 
 class kda_gdr_params(ctypes.Structure):
     _fields_ = [("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+    heads, device = 0, None  # set by kda_gdr_params_from; without them a call refuses the parameters
 
 
 class kda_gdr_rows(ctypes.Structure):
