@@ -961,6 +961,9 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     int src, dst;
     if (!slots_ok(p, seq, src, dst) || !*ok) {  // the same for every thread
         if (threadIdx.x == 0) set_err(p.err);
+        // Every block waits for the prep kernel, those without work too: were all of a call's rows skipped, what
+        // follows in the stream could otherwise start (and take the workspace) while it still writes its blocks.
+        wait_for_previous();
         return;
     }
     const Place pl = *place;

@@ -322,6 +322,23 @@ def test_fp32_sequences_refuse_a_cu_seqlens_that_is_wrong_anywhere():
         assert bool((p.out == -7.0).all()) and torch.equal(S, keep), (at, value)
 
 
+def test_a_call_whose_rows_are_all_skipped_keeps_its_place_in_the_stream():
+    """The workspace is taken for something else right behind a call that has nothing to do but its first
+    kernel's part: what is written there later stays."""
+    p = Problem([4096], 16, 4, True, seed=18)
+    S, src, dst = p.slots()
+    keep = S.clone()
+    dst[0] = -1
+    cu = torch.from_numpy(p.cu).cuda()
+    ws = torch.empty(K.kda_gdr_workspace_bytes(p.cfg, p.cu), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for i in range(20):
+        K.kda_gdr_prefill(p.cfg, p.params, S, src, dst, cu, p.cu, *p.rows(), ws, err=err)
+        ws.fill_(i)
+        assert bool((ws == i).all()), i
+    assert err.item() == K.KDA_ERR_DEVICE and torch.equal(S, keep) and bool((p.out == -7.0).all())
+
+
 def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph():
     p = Problem([130, 64, 1], 4, 2, True, seed=15)
     S, src, dst = p.slots()
