@@ -593,12 +593,13 @@ extern "C" kda_status kda_quant_fp8(int64_t M, int32_t K, const void *x, int64_t
     if (M == 0) return KDA_OK;
     if (!x || !q || !s) return f8_fail(KDA_ERR_INVALID, "x, q or s is NULL");
     const int es = x_dtype == KDA_BF16 ? 2 : 4;
-    if (M > 1 && x_stride < K) return f8_fail(KDA_ERR_INVALID, "x_stride must be >= K (got %lld)", (long long)x_stride);
+    if (M > 1 && (x_stride < K || x_stride > ((int64_t)1 << 38)))
+        return f8_fail(KDA_ERR_INVALID, "x_stride must be >= K and at most 2^38 (got %lld)", (long long)x_stride);
     if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(q)) & 15u) || (reinterpret_cast<uintptr_t>(s) & 3u) ||
         (M > 1 && (x_stride * es) % 16))
         return f8_fail(KDA_ERR_INVALID, "x and q must be 16-byte aligned, x_stride a multiple of 16 bytes, s 4-byte aligned");
     const int nkb = (K + kQb - 1) / kQb;
-    if (M * nkb > INT_MAX - 128) return f8_fail(KDA_ERR_INVALID, "M * K is too large");
+    if (M > (INT_MAX - 128) / nkb) return f8_fail(KDA_ERR_INVALID, "M * K is too large");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char *qp = static_cast<unsigned char *>(q);
     if (block_rows == 1) {

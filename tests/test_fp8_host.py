@@ -38,7 +38,7 @@ def test_quantiser_refusals(K):
         return K.lib().kda_quant_fp8(x["M"], x["K"], x["x"], x["st"], x["dt"], x["rows"], x["q"], x["s"], None)
 
     for e in ({"M": -1}, {"K": 0}, {"K": 24}, {"x": None}, {"x": P + 8}, {"st": 255}, {"st": 260}, {"dt": 2}, {"rows": 64},
-              {"q": None}, {"q": P + 4}, {"s": None}, {"s": P + 2}, {"M": 1 << 40}, {"dt": K.KDA_F32, "st": 258}):
+              {"q": None}, {"q": P + 4}, {"s": None}, {"s": P + 2}, {"M": 1 << 40}, {"M": 1 << 62}, {"M": (1 << 63) - 1}, {"st": 1 << 62}, {"dt": K.KDA_F32, "st": 258}):
         assert call(**e) == K.KDA_ERR_INVALID, e
         assert K.kda_last_error()
     assert call(M=0) == K.KDA_OK
