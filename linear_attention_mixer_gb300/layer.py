@@ -189,6 +189,7 @@ class GdrLayerRunner:
         self.o = torch.empty(rows, D, dtype=torch.bfloat16, device=device)
         self.products = Products([(W, hidden), (hidden, D)], rows, device, fp8)
         self.ws = torch.empty(0, dtype=torch.uint8, device=device)
+        self._captured = []  # workspaces that a captured prefill writes to
 
     def _inputs(self, lw: GdrLayerWeights, x: torch.Tensor, stream):
         n = x.shape[0]
@@ -208,11 +209,19 @@ class GdrLayerRunner:
 
     def prefill(self, lw: GdrLayerWeights, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor,
                 cu_seqlens: torch.Tensor, cu_seqlens_host, x: torch.Tensor, x_out: torch.Tensor, err=None, stream=None) -> None:
-        """Packed variable-length prefill of x.shape[0] tokens: x_out = x + W_o o. Grows its workspace
-        (an allocation) when a batch needs more chunks than any before."""
+        """Packed variable-length prefill of x.shape[0] tokens: x_out = x + W_o o. When a batch needs more
+        chunks than any before, the workspace grows, which waits for the device; not while a graph is
+        captured (run a prefill of that size first)."""
         need = K.kda_gdr_workspace_bytes(self.cfg, cu_seqlens_host)
+        capturing = torch.cuda.is_current_stream_capturing()
         if self.ws.numel() < need:
+            if capturing:
+                raise RuntimeError(f"the workspace must grow to {need} bytes: run a prefill of this size before one is captured")
+            torch.cuda.synchronize(self.proj.device)  # calls on other streams may be using the old one
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.proj.device)
+            torch.cuda.synchronize(self.proj.device)  # and the new one's memory may have had another use
+        if capturing and not any(w is self.ws for w in self._captured):
+            self._captured.append(self.ws)  # a graph keeps writing to it
         rows = self._inputs(lw, x, stream)
         K.kda_gdr_prefill(self.cfg, lw.params, S, src_slots, dst_slots, cu_seqlens, cu_seqlens_host, *rows, self.ws,
                           err=err, stream=stream)

@@ -126,6 +126,54 @@ def test_captured_decode_step():
     assert torch.equal(y, want) and torch.equal(S, S1)
 
 
+def test_a_captured_prefill_outlives_a_larger_one():
+    cfg, lw, _, _, rng = gdr_layer(2, 1, 256, False, 4)
+    run = L.GdrLayerRunner(cfg, 256, 1000, "cuda")
+    S, slot = torch.zeros(2, 2, D, D, device="cuda"), torch.arange(1, dtype=torch.int32, device="cuda")
+    fresh = slot - 1
+    bufs = {n: (dev(rng.standard_normal((n, 256))), torch.empty(n, 256, dtype=torch.bfloat16, device="cuda"),
+                torch.tensor([0, n], dtype=torch.int32, device="cuda")) for n in (100, 1000)}
+
+    def prefill(n):
+        x, y, cu = bufs[n]
+        run.prefill(lw, S, fresh, slot, cu, [0, n], x, y)
+
+    g = torch.cuda.CUDAGraph()
+    prefill(100)
+    torch.cuda.synchronize()
+    want, S1 = bufs[100][1].clone(), S.clone()
+    with torch.cuda.graph(g):
+        prefill(100)
+    old = run.ws
+    address, size = old.data_ptr(), old.numel()
+    del old
+    prefill(1000)
+    assert run.ws.data_ptr() != address
+    # what is allocated now does not get the memory that the graph writes to
+    other = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    bufs[100][1].zero_()
+    S.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bufs[100][1], want) and torch.equal(S, S1)
+    assert all(bool((t == 7).all()) for t in other)
+
+
+def test_a_prefill_whose_workspace_must_grow_is_not_captured():
+    cfg, lw, _, _, rng = gdr_layer(2, 1, 256, False, 5)
+    run = L.GdrLayerRunner(cfg, 256, 100, "cuda")
+    S, slot = torch.zeros(1, 2, D, D, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, y = dev(rng.standard_normal((100, 256))), torch.empty(100, 256, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(RuntimeError):
+            run.prefill(lw, S, slot, slot, cu, [0, 100], x, y)
+    run.prefill(lw, S, slot, slot, cu, [0, 100], x, y)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(y.float()).all())
+
+
 def test_kda_layer_with_fp8_projections(oracle_mod):
     """The stacked projection and W_o of a KDA layer in FP8, decode and prefill; the mixer between them is
     the one that test_gpu_linear.py checks."""
