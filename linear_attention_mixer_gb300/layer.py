@@ -177,8 +177,8 @@ def gdr_width(cfg: K.kda_gdr_config_t) -> int:
 
 
 class GdrLayerRunner:
-    """Buffers for running gated delta rule layers on a batch of up to `rows` tokens at a time
-    (num_heads a multiple of 8: the columns of the projection then start on 16 bytes)."""
+    """Buffers for running gated delta rule layers on a batch of up to `rows` tokens at a time, made on
+    the current stream."""
 
     def __init__(self, cfg: K.kda_gdr_config_t, hidden: int, rows: int, device, fp8: bool = False):
         if cfg.io_dtype != K.KDA_BF16:

@@ -107,6 +107,26 @@ def test_prefill_then_decode(fp8):
         x = y
 
 
+@pytest.mark.parametrize("H,Hk", [(3, 1), (5, 5)])
+def test_heads_that_are_no_multiple_of_8(H, Hk):
+    cfg, lw, A_log, dt_bias, rng = gdr_layer(H, Hk, 128, True, 6)
+    run = L.GdrLayerRunner(cfg, 128, 70, "cuda", True)
+    S = torch.zeros(1, H, D, D, device="cuda")
+    slot = torch.zeros(1, dtype=torch.int32, device="cuda")
+    S0 = np.zeros((H, D, D))
+    for n in (70, 2):
+        x, y = dev(rng.standard_normal((n, 128))), torch.empty(n, 128, dtype=torch.bfloat16, device="cuda")
+        if n == 70:
+            run.prefill(lw, S, slot, slot, torch.tensor([0, n], dtype=torch.int32, device="cuda"), [0, n], x, y)
+        else:
+            run.decode(lw, S, slot, slot, n, x, y)
+        torch.cuda.synchronize()
+        check_product(x, lw.w_in, run.proj[:n])
+        check_mixer(cfg, run, slice(0, n), S0, A_log, dt_bias, S[0], n == 70)
+        check_product(run.o[:n], lw.w_o, y, x)
+        S0 = host(S[0])
+
+
 def test_captured_decode_step():
     cfg, lw, A_log, dt_bias, rng = gdr_layer(8, 8, 256, True, 2)
     B = 5
