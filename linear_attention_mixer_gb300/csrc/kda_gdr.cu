@@ -228,13 +228,17 @@ gdr_sequence_kernel(const __grid_constant__ Args p)
     const int h = (int)((blockIdx.x >> 1) % (unsigned)p.H), row = (int)((blockIdx.x >> 1) / (unsigned)p.H);
     const int rg = lane >> 2, cg = lane & 3, hk = h / p.G;
     int src, dst;
-    // every warp looks at the whole cu_seqlens, so that one that is wrong anywhere leaves every sequence alone
-    bool ok = true;
-    for (int s0 = 0; s0 < p.N; s0 += 32) {
-        const int s = min(s0 + lane, p.N - 1), b = __ldg(p.cu + s), e = __ldg(p.cu + s + 1);
-        ok = ok && b >= 0 && e >= b && e <= p.total_T && (s > 0 || b == 0) && (s < p.N - 1 || e == p.total_T);
+    // Every block looks at the whole cu_seqlens, so that one that is wrong anywhere leaves every sequence alone. (A
+    // vote over the block in place of the shared word costs the walk below 32 registers, and a block an SM.)
+    __shared__ int bad;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    for (int s = tid; s < p.N; s += 128) {
+        const int b = __ldg(p.cu + s), e = __ldg(p.cu + s + 1);
+        if (!(b >= 0 && e >= b && e <= p.total_T && (s > 0 || b == 0) && (s < p.N - 1 || e == p.total_T))) bad = 1;
     }
-    ok = __all_sync(0xFFFFFFFFu, ok);
+    __syncthreads();
+    const bool ok = bad == 0;
     const int64_t t0 = __ldg(p.cu + row), t1 = __ldg(p.cu + row + 1);
     if (!ok || !slots_ok(p, row, src, dst)) {  // the same for every thread
         if (tid == 0) set_err(p.err);

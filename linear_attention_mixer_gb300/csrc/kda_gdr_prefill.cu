@@ -89,26 +89,38 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// One warp reads cu_seqlens once: checks it against what the host sized the call for and finds either
-// the sequence of chunk `want` (seq < 0 on entry) or the first chunk of sequence seq. Every lane gets
-// the result; false on a mismatch.
+// A sequence: its rows t0 .. t0 + len - 1 and its first chunk.
 struct Place { int seq, t0, len, first; };
-__device__ __forceinline__ bool find_place(const int32_t *cu, int N, int64_t total_T, int64_t n_chunks, int want, int seq,
-                                           Place &out)
+
+// What threads first, first + step, .. of a block read of cu_seqlens: whether it is one of total_T tokens, the
+// chunks before sequence seq and all chunks (which cannot wrap in one that is right: the host has checked that
+// chunks x heads fit 28 bits). The sums are over the warp.
+struct Scan { int ok; uint32_t before, all; };
+__device__ __forceinline__ Scan scan_cu(const Args &p, int first, int step, int seq)
+{
+    bool ok = true;
+    uint32_t before = 0, all = 0;
+#pragma unroll 4
+    for (int s = first; s < p.N; s += step) {
+        const int b = __ldg(p.cu + s), e = __ldg(p.cu + s + 1);
+        ok = ok && b >= 0 && e >= b && e <= p.total_T && (s > 0 || b == 0) && (s < p.N - 1 || e == p.total_T);
+        const uint32_t c = ((uint32_t)e - (uint32_t)b + kC - 1) / kC;
+        all += c;
+        before += s < seq ? c : 0u;
+    }
+    return {__all_sync(0xFFFFFFFFu, ok), __reduce_add_sync(0xFFFFFFFFu, before), __reduce_add_sync(0xFFFFFFFFu, all)};
+}
+
+// One warp: the sequence that has chunk `want`, from the place `out` of an earlier chunk on (or of sequence 0). For a
+// cu_seqlens that is right; false when there is none.
+__device__ __forceinline__ bool find_chunk(const Args &p, int want, Place &out)
 {
     const int lane = threadIdx.x & 31;
-    int base = 0;  // the host has checked that chunks x heads fit 28 bits; a cu_seqlens that says otherwise is not ok
-    bool ok = true, found = false;
-    for (int s0 = 0; s0 < N && ok; s0 += 32) {
+    int base = out.first;
+    for (int s0 = out.seq; s0 < p.N; s0 += 32) {
         const int s = s0 + lane;
-        int b = 0, e = 0;
-        if (s < N) {
-            b = __ldg(cu + s);
-            e = __ldg(cu + s + 1);
-            ok = b >= 0 && e >= b && e <= total_T && (s > 0 || b == 0) && (s < N - 1 || e == total_T);
-        }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        const int mine = ok ? (e - b + kC - 1) / kC : 0;
+        const int b = s < p.N ? __ldg(p.cu + s) : 0, e = s < p.N ? __ldg(p.cu + s + 1) : 0;
+        const int mine = (e - b + kC - 1) / kC;
         int nc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -116,19 +128,18 @@ __device__ __forceinline__ bool find_place(const int32_t *cu, int N, int64_t tot
             if (lane >= o) nc += x;
         }
         const int before = base + nc - mine;
-        const bool hit = s < N && (seq >= 0 ? s == seq : (want >= before && want < before + mine));
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
-        if (m && !found) {
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, want >= before && want < before + mine);
+        if (m) {
             const int l = __ffs(m) - 1;
             out.seq = s0 + l;
             out.t0 = __shfl_sync(0xFFFFFFFFu, b, l);
             out.len = __shfl_sync(0xFFFFFFFFu, e, l) - out.t0;
             out.first = __shfl_sync(0xFFFFFFFFu, before, l);
-            found = true;
+            return true;
         }
         base += __shfl_sync(0xFFFFFFFFu, nc, 31);
     }
-    return ok && base == n_chunks && found;
+    return false;
 }
 
 // (h, l) += (x, y) for sums kept as two FP32, |l| far below |h| (the exact error of the addition by Knuth's
@@ -174,11 +185,11 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
     float *diag = reinterpret_cast<float *>(sm_all + kPsDiag) + warp * 16 * kDp;
     const int n_items = n_chunks * Hk;  // (chunk, key head), key heads fastest
     struct Item { int chunk, hk, n; int64_t t0; };
+    Place pl = {0, 0, 0, 0};  // of the last chunk that was located; items only go up
     auto locate = [&](int item, Item &x) {
         x.chunk = item / Hk;
         x.hk = item - x.chunk * Hk;
-        Place pl;
-        if (!find_place(p.cu, p.N, p.total_T, n_chunks, x.chunk, -1, pl)) return false;
+        if (!find_chunk(p, x.chunk, pl)) return false;
         const int pos = (x.chunk - pl.first) * kC;
         x.t0 = (int64_t)pl.t0 + pos;
         x.n = min(kC, pl.len - pos);
@@ -251,7 +262,8 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
     launch_dependents();
     int item = blockIdx.x, buf = 0;
     Item cur, nxt;
-    if (!locate(item, cur)) {  // the same for every thread
+    const Scan cu = scan_cu(p, lane, 32, 0);  // a warp each: the same for every thread
+    if (!cu.ok || cu.all != (uint32_t)n_chunks || !locate(item, cur)) {
         if (tid == 0) set_err(p.err);
         return;
     }
@@ -523,7 +535,7 @@ template <int MT> struct St {
     static constexpr int kU = kX + 16384 * MT, kH = kU + 8192 * MT;   // U split: [2][2][4][MT][32] uint4
     static constexpr int kHu = 8192 * MT, kHand = 2 * kHu;            // S [2][8 k steps][MT][32], U split [2][8 tiles][MT][32] uint4
     static constexpr int kStg = kH + kNh * kHand, kBar = kStg + 4096 * MT;
-    static constexpr int kSmem = kBar + 256 + 1024;
+    static constexpr int kSmem = kBar + 384 + 1024;
 };
 static_assert(St<1>::kSa % 1024 == 0 && St<2>::kSa % 1024 == 0 && St<1>::kSo % 1024 == 0 && St<1>::kV % 1024 == 0 &&
               St<1>::kP + kPartP <= St<1>::kSo, "stages");
@@ -926,9 +938,8 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     extern __shared__ unsigned char sm_raw[];
     unsigned char *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
     StBars *bar = reinterpret_cast<StBars *>(sm + L::kBar);
-    Place *place = reinterpret_cast<Place *>(bar + 1);
-    int *ok = reinterpret_cast<int *>(place + 1);
-    static_assert(sizeof(StBars) + sizeof(Place) + 8 <= 256, "barriers");
+    Scan *scans = reinterpret_cast<Scan *>(bar + 1);
+    static_assert(sizeof(StBars) + kStThreads / 32 * sizeof(Scan) <= 384, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kVBlocks = kD / L::kVB;
     const int vb = blockIdx.x % kVBlocks;
@@ -949,24 +960,26 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
         }
         fence_mbar_init();
     }
-    if (warp == 8) {
-        Place pl;
-        const bool good = find_place(p.cu, p.N, p.total_T, n_chunks, 0, seq, pl);
-        if (lane == 0) {
-            *place = pl;
-            *ok = good;
-        }
-    }
+    const Scan part = scan_cu(p, threadIdx.x, kStThreads, seq);
+    if (lane == 0) scans[warp] = part;
     __syncthreads();
+    Scan cu = {1, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kStThreads / 32; ++w) {
+        cu.ok &= scans[w].ok;
+        cu.before += scans[w].before;
+        cu.all += scans[w].all;
+    }
     int src, dst;
-    if (!slots_ok(p, seq, src, dst) || !*ok) {  // the same for every thread
+    if (!slots_ok(p, seq, src, dst) || !cu.ok || cu.all != (uint64_t)n_chunks) {  // the same for every thread
         if (threadIdx.x == 0) set_err(p.err);
         // Every block waits for the prep kernel, those without work too: were all of a call's rows skipped, what
         // follows in the stream could otherwise start (and take the workspace) while it still writes its blocks.
         wait_for_previous();
         return;
     }
-    const Place pl = *place;
+    const int t0 = __ldg(p.cu + seq);
+    const Place pl = {seq, t0, __ldg(p.cu + seq + 1) - t0, (int)cu.before};
     const int nc = (pl.len + kC - 1) / kC;
     // 384 threads x 168 registers at the launch: 128 x (232 + 152 + 56) after this
     if (warp >= 8) {

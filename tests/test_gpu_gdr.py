@@ -168,6 +168,15 @@ def test_many_heads(lens, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+def test_many_sequences(bf16):
+    """More sequences than a block has threads, empty ones and ones of several chunks among them."""
+    p = Problem([(0, 1, 3, 0, 2)[i % 5] for i in range(400)] + [0] * 70 + [130, 1, 0, 65] + [1, 0] * 20, 2, 1, bf16, seed=19)
+    S, src, dst = p.slots()
+    p.prefill(S, src, dst)
+    check(p, S, src, dst, p.S0, bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 def test_fresh_in_place_and_forked_rows(bf16):
     """src -1 starts from zeros without reading a slot, src == dst updates in place, one src may serve two rows."""
     p = Problem([70, 20, 65, 65], 2, 2, bf16, seed=4)
