@@ -94,7 +94,9 @@ struct Place { int seq, t0, len, first; };
 
 // What threads first, first + step, .. of a block read of cu_seqlens: whether it is one of total_T tokens, the
 // chunks before sequence seq and all chunks (which cannot wrap in one that is right: the host has checked that
-// chunks x heads fit 28 bits). The sums are over the warp.
+// chunks x heads fit 28 bits). The sums are over the warp. Shared by all of a state block's warps, and in the
+// prep only the first item's: 4096 sequences of 1 to 16 tokens and 8 heads 3.8 ms (25.5 ms with one warp's scan
+// for each block and item), 256 of them 215 us (281).
 struct Scan { int ok; uint32_t before, all; };
 __device__ __forceinline__ Scan scan_cu(const Args &p, int first, int step, int seq)
 {
