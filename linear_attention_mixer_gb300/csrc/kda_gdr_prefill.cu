@@ -160,7 +160,7 @@ __device__ __forceinline__ void add2(float &h, float &l, float x, float y)
 //   T[w][:] = -D_w sum_{j < w} A[w][j] T[j][:]
 // on the tensor cores with split factors, three barriers deep. 66 us for 4096 (chunk, value head) pairs of
 // two value heads a key head (92 us with the whole inverse by forward substitution, a column a lane); bound
-// by the latency of its phases, 12 warps an SM, with DRAM at 22% and issue slots at 32%.
+// by the latency of its phases, 12 warps an SM, with DRAM at 22% and compute throughput at 32%.
 // Shared memory: two buffers of K and Q rows (the next item's are loaded while one is computed; a block is
 // built in the place of the rows that it came from), A's diagonal blocks, scalars of up to four value heads.
 constexpr int kPrepThreads = 128, kPrepPerSm = 3;

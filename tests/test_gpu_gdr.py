@@ -419,6 +419,14 @@ def test_no_rows():
     torch.cuda.synchronize()
 
 
+def test_parameters_made_by_hand_are_refused():
+    p = Problem([1], 2, 1, True, seed=20)
+    S, src, dst = p.slots()
+    p.params = K.kda_gdr_params(p.params.A_log, p.params.dt_bias)  # no count and no device to check
+    with pytest.raises(ValueError):
+        p.decode(S, src, dst, 1)
+
+
 def test_binding_refusals():
     p = Problem([4], 2, 1, True, seed=20)
     S, src, dst = p.slots()
