@@ -412,7 +412,8 @@ kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void *xq, const
  *   err     device int32 word or NULL. Receives KDA_ERR_DEVICE (a bad slot id; or a cu_seqlens that
  *           does not rise from 0 to cu_seqlens_host[N], or for BF16 rows has another number of
  *           64-token chunks than the host's: the call then leaves out and S as they are) or
- *           KDA_ERR_TIMEOUT (a bounded wait gave up). Never cleared by the library.
+ *           KDA_ERR_TIMEOUT (a bounded wait gave up: what the call was to write is undefined). Never
+ *           cleared by the library.
  */
 typedef struct {
     int32_t num_heads;     /* H value heads, a multiple of num_qk_heads, <= 65536 */

@@ -542,7 +542,13 @@ template <int MT> struct St {
 static_assert(St<1>::kSa % 1024 == 0 && St<2>::kSa % 1024 == 0 && St<1>::kSo % 1024 == 0 && St<1>::kV % 1024 == 0 &&
               St<1>::kP + kPartP <= St<1>::kSo, "stages");
 static_assert(St<1>::kSmem <= 232448 && St<2>::kSmem <= 232448, "state kernel shared memory");
-constexpr uint32_t kStSpin = 1u << 26;
+// Polls before a wait gives up (a test builds this file with limits that run out). A warp that gave up goes on
+// without waiting, so that every named barrier is met, but releases no stage of the rings and writes nothing to
+// the output or the states: a stage is filled again only when all its readers have seen the last copies land.
+#ifndef KDA_GDR_WAIT_LIMIT
+#define KDA_GDR_WAIT_LIMIT (1u << 26)
+#endif
+constexpr uint32_t kLandSpin = 1u << 26;  // for copies that are on their way when a block ends
 
 struct StateMaps { CUtensorMap k, q, v; };
 // full and empty of the two rings; S0 handed over, U handed over, both read
@@ -566,7 +572,7 @@ __device__ __forceinline__ int own(int kw, int p) { return (p ^ kw) & 1; }
 __device__ __forceinline__ bool wait_both(uint64_t *x, uint32_t px, uint64_t *y, uint32_t py)
 {
     const bool odd = threadIdx.x & 1;
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odd ? y : x, odd ? py : px, kStSpin));
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odd ? y : x, odd ? py : px, KDA_GDR_WAIT_LIMIT));
     __syncwarp();
     return ok;
 }
@@ -586,7 +592,7 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
     float4 *xb = reinterpret_cast<float4 *>(sm + L::kX) + u * (512 * MT) + lane;
     uint4 *ub = reinterpret_cast<uint4 *>(sm + L::kU) + u * (256 * MT) + lane;
     const int nc = (len + kC - 1) / kC;
-    bool good = true;
+    bool good = true;  // the same in every lane
     // row and 16-byte piece within an ldmatrix of B operands: two tiles of tokens in rows, or tokens as k
     // (transposed; own tile first), or one tile of tokens with two k steps
     const int rowB = (lane & 7) + ((lane >> 4) << 3), pcB = (lane >> 3) & 1;
@@ -596,8 +602,7 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
     int st = 0, pa = 0;
     uint32_t b[2][4][4];          // B operands of a k step, fetched a step ahead
     // Chunk c's stage has arrived and its hand-over buffer is free. peek asks both barriers once, without using
-    // the answer yet; enter waits if it was no, and fetches the first B operands. (After a wait that gave up the
-    // warp goes on without waiting, so that every barrier is met.)
+    // the answer yet; enter waits if it was no, and fetches the first B operands.
     auto peek = [&](int c) {
         const bool odd = lane & (c >= L::kNh);
         return mbar_try_wait(odd ? &bar->eh[c % L::kNh] : &bar->fa[st], odd ? (uint32_t)(((c / L::kNh) - 1) & 1) : (uint32_t)pa);
@@ -605,7 +610,7 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
     auto enter = [&](int c, bool ready) {
         unsigned char *base = sm + st * L::kSa;
         if (!__all_sync(0xFFFFFFFFu, ready) && good)
-            good = c < L::kNh ? mbar_wait_bounded(&bar->fa[st], (uint32_t)pa, kStSpin)
+            good = c < L::kNh ? mbar_wait_warp(&bar->fa[st], (uint32_t)pa, KDA_GDR_WAIT_LIMIT)
                               : wait_both(&bar->fa[st], (uint32_t)pa, &bar->eh[c % L::kNh], (uint32_t)(((c / L::kNh) - 1) & 1));
         __syncwarp();
         const int n = len - c * kC;
@@ -833,7 +838,7 @@ __device__ __forceinline__ bool chain_pass(unsigned char *sm, StBars *bar, int u
                 }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->ea[now]);
+        if (lane == 0 && good) mbar_arrive(&bar->ea[now]);
         if (c + 1 < nc) enter(c + 1, ready);
     }
     return good;
@@ -892,7 +897,7 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
                 o[m][pr][2] *= x[pr].x;
                 o[m][pr][3] *= x[pr].y;
             }
-        if (good) good = mbar_wait_bounded(&bar->fh[hb], ph, kStSpin);
+        if (good) good = mbar_wait_warp(&bar->fh[hb], ph, KDA_GDR_WAIT_LIMIT);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
@@ -907,7 +912,7 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&bar->eh[hb]);
-            mbar_arrive(&bar->eo[st]);
+            if (good) mbar_arrive(&bar->eo[st]);
         }
         // 32 tokens x 16 MT values, staged as rows
         const int n = min(kC, pl.len - c * kC);
@@ -922,7 +927,7 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
         for (int i = 0; i < 2 * MT; ++i) {
             const int e = 32 * i + lane, r = e / (2 * MT), pc = e % (2 * MT), pr = r >> 3, t = 16 * pr + 8 * own(kw, pr) + (r & 7);
             const uint4 w = *reinterpret_cast<const uint4 *>(stg + o_off<MT>(r, pc));
-            if (t < n)
+            if (t < n && good)
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.rows.out) + ((int64_t)pl.t0 + c * kC + t) * p.rows.out_stride +
                                            (size_t)h * kD + v0 + 16 * MT * u + 8 * pc) = w;
         }
@@ -989,30 +994,36 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
         if (warp == 8 && lane == 0) {
             const int hk = h / p.G;
             bool good = true;
+            int na = 0, no = 0;   // copies into either ring
             wait_for_previous();  // the blocks; everything else that is read here is older than the prep kernel
             for (int c = 0; c < nc && good; ++c) {
                 const int sa = c % L::kNa, so = c % L::kNo, t = pl.t0 + c * kC;
                 const unsigned char *blk = blocks + ((size_t)(pl.first + c) * p.H + h) * kBlkBytes;
-                if (c >= L::kNa) good = mbar_wait_bounded(&bar->ea[sa], (uint32_t)(((c / L::kNa) - 1) & 1), kStSpin);
+                if (c >= L::kNa) good = mbar_wait_bounded(&bar->ea[sa], (uint32_t)(((c / L::kNa) - 1) & 1), KDA_GDR_WAIT_LIMIT);
                 if (!good) break;
+                ++na;
                 unsigned char *b = sm + sa * L::kSa;
                 mbar_arrive_expect_tx(&bar->fa[sa], (uint32_t)(box_rows * (2 * 128 + L::kVB * 2) + kPartT));
                 tma_load_2d(b, &maps.k, hk * kD, t, &bar->fa[sa]);
                 tma_load_2d(b + 8192, &maps.k, hk * kD + 64, t, &bar->fa[sa]);
                 bulk_g2s(b + L::kT, blk, kPartT, &bar->fa[sa]);
                 tma_load_2d(b + L::kV, &maps.v, h * kD + vb * L::kVB, t, &bar->fa[sa]);
-                if (c >= L::kNo) good = mbar_wait_bounded(&bar->eo[so], (uint32_t)(((c / L::kNo) - 1) & 1), kStSpin);
+                if (c >= L::kNo) good = mbar_wait_bounded(&bar->eo[so], (uint32_t)(((c / L::kNo) - 1) & 1), KDA_GDR_WAIT_LIMIT);
                 if (!good) break;
+                ++no;
                 b = sm + L::kO + so * L::kSo;
                 mbar_arrive_expect_tx(&bar->fo[so], (uint32_t)(box_rows * 2 * 128 + kPartP));
                 tma_load_2d(b, &maps.q, hk * kD, t, &bar->fo[so]);
                 tma_load_2d(b + 8192, &maps.q, hk * kD + 64, t, &bar->fo[so]);
                 bulk_g2s(b + L::kP, blk + kPartT, kPartP, &bar->fo[so]);
             }
-            if (!good) {
-                if (p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
-                for (int s = 0; s < L::kNa; ++s) mbar_wait_bounded(&bar->fa[s], 0, 1u << 16);  // copies in flight land
-            }
+            // The last copies into every stage land before the block ends and its shared memory is another's,
+            // whether the other warps have waited for them or gave up.
+            for (int c = max(na - L::kNa, 0); c < na; ++c)
+                if (!mbar_wait_bounded(&bar->fa[c % L::kNa], (uint32_t)((c / L::kNa) & 1), kLandSpin)) good = false;
+            for (int c = max(no - L::kNo, 0); c < no; ++c)
+                if (!mbar_wait_bounded(&bar->fo[c % L::kNo], (uint32_t)((c / L::kNo) & 1), kLandSpin)) good = false;
+            if (!good && p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
         }
         return;
     }

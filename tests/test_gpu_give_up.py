@@ -1,0 +1,87 @@
+"""Waits that give up, in kernels whose warps wait for one another. The kernel files are built once more with
+limits that run out at once in chosen warps and lanes (tests/cuda/wait_limits.cuh): the call has to end by
+itself, record KDA_ERR_TIMEOUT, leave alone what it does not own, and leave the library usable.
+
+Lanes apart matter: a limit may run out in one lane of a warp and not in the next."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+from linear_attention_mixer_gb300 import kda as K
+from tests.test_gpu_gdr import Problem, check
+
+pytestmark = pytest.mark.gpu
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "linear_attention_mixer_gb300", "csrc")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from linear_attention_mixer_gb300 import build
+    build.build()
+    torch.cuda.set_device(0)
+
+
+def compiled(tmp, name, source, macro, others=()):
+    """A library of `source` with its wait limit replaced, and the other sources as they are; what else it calls
+    comes from libkda.so, which is loaded first so that its own calls stay in it."""
+    K.lib()
+    nvcc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
+    flags = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
+    jobs, objs = [], []
+    for s in (source, *others):
+        objs.append(str(tmp / (s + ".o")))
+        edit = ["-include", os.path.join(HERE, "cuda", "wait_limits.cuh"), f"-D{macro}=(wl_limit())"] if s == source else []
+        jobs.append(subprocess.Popen([nvcc, *flags, *edit, "-c", os.path.join(CSRC, s), "-o", objs[-1]]))
+    assert all(j.wait() == 0 for j in jobs)
+    out = tmp / f"lib{name}.so"
+    subprocess.run([nvcc, "-shared", *objs, K.LIB_PATH, "-Xlinker", "-Bsymbolic", "-Xlinker", "-rpath=" + os.path.dirname(K.LIB_PATH), "-o", str(out)],
+                   check=True)
+    L = ctypes.CDLL(str(out))
+    for fn, res, args in K.SIGNATURES:
+        f = getattr(L, fn)  # its own, or libkda's behind it
+        f.restype, f.argtypes = res, args
+    L.wl_set.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
+    return L
+
+
+@pytest.fixture(scope="module")
+def gdr_lib(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("gdr"), "gdr_give_up", "kda_gdr_prefill.cu", "KDA_GDR_WAIT_LIMIT", ["kda_gdr.cu"])
+
+
+EVERY, ODD, EVEN = 0xFFFFFFFF, 0xAAAAAAAA, 0x55555555
+# warps 0-3 carry the state, 4-7 form the output, lane 0 of warp 8 copies
+GDR = [(1 << 0, EVERY), (1 << 0, ODD), (1 << 3, EVEN), (0xF, 1 << 31), (1 << 4, EVERY), (1 << 5, ODD), (0xF0, EVEN),
+       (1 << 8, EVERY), (0x1FF, EVERY), (0xFF, ODD)]
+
+
+@pytest.mark.parametrize("lens,H", [([650], 2), ([330] * 8, 32)])  # 32 and 64 value columns a block
+def test_prefill(gdr_lib, monkeypatch, lens, H):
+    p = Problem(lens, H, H // 2, True, seed=30)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    N = len(lens)
+    with monkeypatch.context() as m:
+        m.setattr(K, "lib", lambda: gdr_lib)
+        for warps, lanes in [(0, 0)] + GDR:
+            assert gdr_lib.wl_set(warps, lanes) == 0
+            S, src, dst = p.slots()
+            keep = S.clone()
+            p.out.fill_(-7.0)
+            err.zero_()
+            p.prefill(S, src, dst, err=err)
+            assert err.item() == (K.KDA_ERR_TIMEOUT if warps else K.KDA_OK), (hex(warps), hex(lanes))
+            assert torch.equal(S[:N], keep[:N]) and torch.equal(S[2 * N:], keep[2 * N:])
+            assert bool((p.out[p.T:] == -7.0).all())
+            if not warps:
+                check(p, S, src, dst, p.S0, True)
+            if warps == 0x1FF:  # no warp saw its rows
+                assert torch.equal(S, keep) and bool((p.out == -7.0).all())
+    S, src, dst = p.slots()
+    err.zero_()
+    p.prefill(S, src, dst, err=err)
+    assert err.item() == K.KDA_OK
+    check(p, S, src, dst, p.S0, True)
