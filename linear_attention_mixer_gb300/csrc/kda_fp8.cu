@@ -206,7 +206,11 @@ q8_blocks_kernel(const T *__restrict__ x, int64_t stride, int M, int K, int nkb,
 // ---------------------------------------------------------------- product
 constexpr int kF8M = 128;          // rows a unit (MMA M)
 constexpr int kF8K = 128;          // K per stage: one scale block, one 128-byte row
-constexpr uint32_t kF8Spin = 1u << 26;
+// Polls before a wait gives up (a test builds this file with limits that run out).
+#ifndef KDA_F8_WAIT_LIMIT
+#define KDA_F8_WAIT_LIMIT (1u << 26)
+#endif
+constexpr uint32_t kF8Land = 1u << 26;  // for copies and products that are on their way when a block ends
 constexpr int kF8MaxSplit = 16;
 
 template <int BN> struct F8 {
@@ -312,7 +316,7 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                 unit(u, mb, nb, k0, k1, ks);
                 for (int kb = k0; kb < k1; ++kb, ++step) {
                     const int s = step % L::kStages;
-                    if (step >= L::kStages && !mbar_wait_bounded(&empty[s], ((step / L::kStages) - 1) & 1, kF8Spin)) {
+                    if (step >= L::kStages && !mbar_wait_bounded(&empty[s], ((step / L::kStages) - 1) & 1, KDA_F8_WAIT_LIMIT)) {
                         ok = false;
                         break;
                     }
@@ -322,6 +326,9 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                     tma_load_2d(st + L::kA, &tm_w, kb * kF8K, nb * BN, &full[s]);
                 }
             }
+            // the last copy into every stage lands before the block ends, whether its products run or not
+            for (int i = max(step - L::kStages, 0); i < step; ++i)
+                if (!mbar_wait_bounded(&full[i % L::kStages], (i / L::kStages) & 1, kF8Land)) ok = false;
             if (!ok) atomicExch(err, KDA_ERR_TIMEOUT);
         } else if (warp == L::kEpi + 1 && lane == 0) {  // MMA issuer
             bool ok = true;
@@ -332,8 +339,8 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                 unit(u, mb, nb, k0, k1, ks);
                 for (int kb = k0; kb < k1; ++kb, ++step) {
                     const int s = step % L::kStages, a = step & 1;
-                    if ((step >= 2 && !mbar_wait_bounded(&accempty[a], ((step >> 1) - 1) & 1, kF8Spin)) ||
-                        !mbar_wait_bounded(&full[s], (step / L::kStages) & 1, kF8Spin)) {
+                    if ((step >= 2 && !mbar_wait_bounded(&accempty[a], ((step >> 1) - 1) & 1, KDA_F8_WAIT_LIMIT)) ||
+                        !mbar_wait_bounded(&full[s], (step / L::kStages) & 1, KDA_F8_WAIT_LIMIT)) {
                         ok = false;
                         break;
                     }
@@ -348,14 +355,14 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                 }
             }
             tc::mma_commit(fin);
-            if (!mbar_wait_bounded(fin, 0, kF8Spin)) ok = false;
+            if (!mbar_wait_bounded(fin, 0, kF8Land)) ok = false;
             if (!ok) atomicExch(err, KDA_ERR_TIMEOUT);
         }
         __syncwarp();
     } else {
         if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int q = warp & 3, half = warp >> 2;
-        bool ok = true;
+        bool ok = true;  // the same in every lane
         int step = 0;
         unsigned char *box = stg + warp * L::kStg;
         for (int u = blockIdx.x; u < sh.n_units && ok; u += gridDim.x) {
@@ -379,7 +386,7 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                     sx = __ldg(xp + kb + 1);
                     sw = __ldg(wp + kb + 1);
                 }
-                if (!mbar_wait_bounded(&accfull[a], (step >> 1) & 1, kF8Spin)) {
+                if (!mbar_wait_warp(&accfull[a], (step >> 1) & 1, KDA_F8_WAIT_LIMIT)) {
                     ok = false;
                     break;
                 }

@@ -7,10 +7,13 @@ import ctypes
 import os
 import subprocess
 
+import numpy as np
 import pytest
 import torch
 
 from linear_attention_mixer_gb300 import kda as K
+from oracle import fp8 as O8
+from tests import test_gpu_fp8 as F8
 from tests.test_gpu_gdr import Problem, check
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +88,46 @@ def test_prefill(gdr_lib, monkeypatch, lens, H):
     p.prefill(S, src, dst, err=err)
     assert err.item() == K.KDA_OK
     check(p, S, src, dst, p.S0, True)
+
+
+@pytest.fixture(scope="module")
+def fp8_lib(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("fp8"), "fp8_give_up", "kda_fp8.cu", "KDA_F8_WAIT_LIMIT")
+
+
+def modes(epi):
+    """Epilogue warps 0 .. epi - 1, then lane 0 of the copying warp and of the one that issues the products."""
+    return [(1, EVERY), (1, ODD), (1 << (epi - 1), EVEN), ((1 << epi) - 1, 1 << 31), (1 << epi, EVERY), (2 << epi, EVERY),
+            ((4 << epi) - 1, EVERY), ((1 << epi) - 1, ODD)]
+
+
+# one k range and several, 128 and 256 columns a tile
+@pytest.mark.parametrize("M,N,Kd", [(130, 264, 2064), (16, 1024, 4096), (1200, 4104, 1040)])
+def test_fp8_product(fp8_lib, monkeypatch, M, N, Kd):
+    ops = F8.operands(M, N, Kd, 4)
+    args = [F8.dev8(ops[0]), torch.from_numpy(ops[1]).cuda(), F8.dev8(ops[2]), torch.from_numpy(ops[3]).cuda()]
+    y = torch.empty(M * N + 64, dtype=torch.bfloat16, device="cuda")
+    work = torch.zeros(K.kda_linear_fp8_workspace_bytes(M, N, Kd), dtype=torch.uint8, device="cuda")
+
+    def call():
+        y.fill_(-7.0)
+        work.zero_()
+        K.kda_linear_fp8(*args, y[:M * N], work)
+        torch.cuda.synchronize()
+        assert bool((y[M * N:] == -7.0).all())
+        return int(work[:4].view(torch.int32).item())
+
+    assert call() == K.KDA_OK
+    want = y.clone()
+    F8.near(want[:M * N].float().cpu().numpy().astype(np.float64).reshape(M, N), *O8.linear(*ops))
+    with monkeypatch.context() as m:
+        m.setattr(K, "lib", lambda: fp8_lib)
+        for epi in (4, 8):  # whichever the tile's width is: other numbers of warps are covered by the masks too
+            for warps, lanes in [(0, 0)] + modes(epi):
+                assert fp8_lib.wl_set(warps, lanes) == 0
+                got = call()
+                if warps == 0:
+                    assert got == K.KDA_OK and torch.equal(y, want)
+                elif warps & 1:  # the first epilogue warp always waits for a product
+                    assert got == K.KDA_ERR_TIMEOUT, (hex(warps), hex(lanes))
+    assert call() == K.KDA_OK and torch.equal(y, want)
