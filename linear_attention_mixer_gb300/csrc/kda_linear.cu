@@ -49,7 +49,11 @@ constexpr int kLnEpiWarps = 4;
 constexpr int kLnThreads = 32 * (kLnEpiWarps + 2);
 constexpr int kLnAlign = 1024;
 constexpr int kLnSmem = kLnStages * kLnStage + kLnEpiWarps * 2 * kLnStg + 256 + kLnAlign;
-constexpr uint32_t kLnSpin = 1u << 26;
+// Polls before a wait gives up (a test builds this file with limits that run out).
+#ifndef KDA_LN_WAIT_LIMIT
+#define KDA_LN_WAIT_LIMIT (1u << 26)
+#endif
+constexpr uint32_t kLnLand = 1u << 26;  // for copies and products that are on their way when a block ends
 constexpr int kLnMaxSplit = 8;
 static_assert(kLnSmem <= 232448, "kda_linear shared memory");
 
@@ -148,7 +152,7 @@ ln_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                 const uint32_t bytes = (uint32_t)(n_a * a_rows + kLnBN) * kLnAtom;
                 for (int kb = k0; kb < k1; ++kb, ++step) {
                     const int s = step % kLnStages;
-                    if (step >= kLnStages && !mbar_wait_bounded(&empty[s], ((step / kLnStages) - 1) & 1, kLnSpin)) {
+                    if (step >= kLnStages && !mbar_wait_bounded(&empty[s], ((step / kLnStages) - 1) & 1, KDA_LN_WAIT_LIMIT)) {
                         ok = false;
                         break;
                     }
@@ -159,6 +163,9 @@ ln_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                     tma_load_2d(st + kLnMT * kLnABytes, &tm_w, kb * kLnBK, nb * kLnBN, &full[s]);
                 }
             }
+            // the last copies into every stage land before the block ends, whether their products run or not
+            for (int i = max(step - kLnStages, 0); i < step; ++i)
+                if (!mbar_wait_bounded(&full[i % kLnStages], (i / kLnStages) & 1, kLnLand)) ok = false;
             if (!ok) atomicExch(err, KDA_ERR_TIMEOUT);
         }
         __syncwarp();
@@ -173,14 +180,14 @@ ln_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                 kb_range(ks, k0, k1);
                 const int n_a = min(kLnMT, (sh.M - mb * kLnMT * kLnBM + kLnBM - 1) / kLnBM);
                 const int a = it & 1;
-                if (it >= 2 && !mbar_wait_bounded(&accempty[a], ((it >> 1) - 1) & 1, kLnSpin)) {
+                if (it >= 2 && !mbar_wait_bounded(&accempty[a], ((it >> 1) - 1) & 1, KDA_LN_WAIT_LIMIT)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
                 for (int kb = k0; kb < k1; ++kb, ++step) {
                     const int s = step % kLnStages;
-                    if (!mbar_wait_bounded(&full[s], (step / kLnStages) & 1, kLnSpin)) {
+                    if (!mbar_wait_bounded(&full[s], (step / kLnStages) & 1, KDA_LN_WAIT_LIMIT)) {
                         ok = false;
                         break;
                     }
@@ -198,19 +205,19 @@ ln_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                 if (ok) tc::mma_commit(&accfull[a]);
             }
             tc::mma_commit(fin);
-            if (!mbar_wait_bounded(fin, 0, kLnSpin)) ok = false;
+            if (!mbar_wait_bounded(fin, 0, kLnLand)) ok = false;
             if (!ok) atomicExch(err, KDA_ERR_TIMEOUT);
         }
         __syncwarp();
     } else {  // epilogue: warp q owns TMEM lanes 32q .. 32q + 31
-        bool ok = true;
+        bool ok = true;  // the same in every lane
         int it = 0, nbuf = 0;
         unsigned char *my = stg + warp * 2 * kLnStg;
         for (int u = blockIdx.x; u < sh.n_units; u += gridDim.x, ++it) {
             int mb, ks, nb;
             unit_coords(u, mb, ks, nb);
             const int a = it & 1;
-            ok = mbar_wait_bounded(&accfull[a], (it >> 1) & 1, kLnSpin);
+            ok = mbar_wait_warp(&accfull[a], (it >> 1) & 1, KDA_LN_WAIT_LIMIT);
             if (!ok) break;
             tc::fence_after_sync();
             const int m0 = mb * kLnMT * kLnBM;

@@ -131,3 +131,35 @@ def test_fp8_product(fp8_lib, monkeypatch, M, N, Kd):
                 elif warps & 1:  # the first epilogue warp always waits for a product
                     assert got == K.KDA_ERR_TIMEOUT, (hex(warps), hex(lanes))
     assert call() == K.KDA_OK and torch.equal(y, want)
+
+
+@pytest.fixture(scope="module")
+def linear_lib(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("lin"), "linear_give_up", "kda_linear.cu", "KDA_LN_WAIT_LIMIT")
+
+
+@pytest.mark.parametrize("M,N,Kd", [(300, 384, 1024), (16, 256, 8192)])
+def test_product(linear_lib, monkeypatch, M, N, Kd):
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(M, Kd, generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(N, Kd, generator=gen, device="cuda") * Kd ** -0.5).to(torch.bfloat16)
+    y = torch.empty(M * N + 64, dtype=torch.bfloat16, device="cuda")
+    work = torch.zeros(K.kda_linear_workspace_bytes(M, N, Kd), dtype=torch.uint8, device="cuda")
+
+    def call():
+        y.fill_(-7.0)
+        work.zero_()
+        K.kda_linear(x, w, y[:M * N].view(M, N), work)
+        torch.cuda.synchronize()
+        assert bool((y[M * N:] == -7.0).all())
+        return int(work[:4].view(torch.int32).item())
+
+    assert call() == K.KDA_OK
+    want = y.clone()
+    with monkeypatch.context() as m:
+        m.setattr(K, "lib", lambda: linear_lib)
+        for warps, lanes in [(0, 0)] + modes(4):
+            assert linear_lib.wl_set(warps, lanes) == 0
+            got = call()
+            assert (got == K.KDA_OK and torch.equal(y, want)) if warps == 0 else got == K.KDA_ERR_TIMEOUT or not warps & 1
+    assert call() == K.KDA_OK and torch.equal(y, want)
