@@ -366,14 +366,15 @@ kda_status kda_linear(int32_t M, int32_t N, int32_t K, const void *x, const void
  * kda_quant_fp8: the operands from BF16 or FP32. Per group s = 2^e with e the smallest integer (>= -126)
  * for which every finite |x| <= 448 s (s = 1 when all are 0), q = x / s rounded to the nearest E4M3
  * (ties to even; x / s is exact, so one rounding). NaN and infinities become NaN and do not set s.
- *   M, K      rows and columns; M >= 0 (0 is a no-op), K a multiple of 16 (a last group may be short)
+ *   M, K      rows and columns; M >= 0 (0 is a no-op), K a multiple of 16 (a last group may be short) and at
+ *             most 2^31 - 128
  *   x         device x_dtype [M], rows x_stride elements apart, 16-byte aligned, x_stride a multiple of
  *             16 bytes and >= K (not used when M == 1)
  *   q         device E4M3 [M][K], 16-byte aligned      out
  *   s         device FP32 [ceil(M / block_rows)][ceil(K / 128)]      out
  * kda_linear_fp8: y = x W^T (+ r) in BF16, each block's product accumulated in FP32 on the tensor cores,
  * scaled by xs * ws and added in FP32, in the blocks' order. The scales may be any FP32 numbers.
- *   M, N, K   as for kda_linear, with N a multiple of 8 and K a multiple of 16
+ *   M, N, K   as for kda_linear, with N a multiple of 8 and K a multiple of 16, at most 2^31 - 128
  *   xq, xs    device E4M3 [M][K], FP32 [M][ceil(K / 128)]
  *   wq, ws    device E4M3 [N][K], FP32 [ceil(N / 128)][ceil(K / 128)]
  *   r, y, ysplit   as for kda_linear (a ysplit other than 0 and N: a multiple of 128 that divides N)

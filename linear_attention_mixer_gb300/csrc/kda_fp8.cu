@@ -38,6 +38,7 @@ namespace {
 
 // ---------------------------------------------------------------- quantiser
 constexpr int kQb = 128;  // columns per scale
+constexpr int kMaxK = INT_MAX - 127;  // so that K's blocks of 128 and their columns are counted in 32 bits
 
 // The scale of a group whose largest finite magnitude has the bits u: 2^e, e the smallest integer with it <=
 // 448 2^e (448 is E4M3's largest number), at least 2^-126; 1 for an empty or all-zero group. x / 2^e is
@@ -567,6 +568,7 @@ bool f8_shape_ok(int M, int N, int K)
     if (M < 0 || N <= 0 || K <= 0) return f8_fail(KDA_ERR_INVALID, "M must be >= 0 and N, K > 0 (got %d, %d, %d)", M, N, K), false;
     if (N % 8 != 0) return f8_fail(KDA_ERR_INVALID, "N must be a multiple of 8 (got %d)", N), false;
     if (K % 16 != 0) return f8_fail(KDA_ERR_INVALID, "K must be a multiple of 16 (got %d)", K), false;
+    if (K > kMaxK) return f8_fail(KDA_ERR_INVALID, "K must be at most %d (got %d)", kMaxK, K), false;
     if ((int64_t)M * N > INT_MAX / 2) return f8_fail(KDA_ERR_INVALID, "M * N is too large"), false;
     return true;
 }
@@ -595,6 +597,7 @@ extern "C" kda_status kda_quant_fp8(int64_t M, int32_t K, const void *x, int64_t
 {
     if (M < 0 || K <= 0) return f8_fail(KDA_ERR_INVALID, "M must be >= 0 and K > 0 (got %lld, %d)", (long long)M, K);
     if (K % 16 != 0) return f8_fail(KDA_ERR_INVALID, "K must be a multiple of 16 (got %d)", K);
+    if (K > kMaxK) return f8_fail(KDA_ERR_INVALID, "K must be at most %d (got %d)", kMaxK, K);
     if (x_dtype != KDA_F32 && x_dtype != KDA_BF16) return f8_fail(KDA_ERR_INVALID, "x_dtype must be KDA_F32 or KDA_BF16");
     if (block_rows != 1 && block_rows != 128) return f8_fail(KDA_ERR_INVALID, "block_rows must be 1 or 128 (got %d)", block_rows);
     if (M == 0) return KDA_OK;

@@ -62,3 +62,19 @@ def test_product_refusals(K):
         with pytest.raises(K.KdaError):
             K.kda_linear_fp8_workspace_bytes(*bad)
     assert K.kda_linear_fp8_workspace_bytes(0, 256, 256) == 256
+
+
+def test_a_k_whose_blocks_are_not_counted_in_32_bits(K):
+    """K + 127 passes 2^31: refused by name, by the product, its query and the quantiser; the largest K is taken."""
+    top = 2 ** 31 - 128
+    assert K.kda_linear_fp8_workspace_bytes(2, 8, top) > 256  # k splits: partial sums
+    for k in (top + 16, 2 ** 31 - 16):
+        with pytest.raises(K.KdaError) as e:
+            K.kda_linear_fp8_workspace_bytes(2, 8, k)
+        assert str(top) in e.value.message
+        for M in (0, 2):
+            assert K.lib().kda_linear_fp8(M, 8, k, P, P, P, P, None, P, 0, P, 1 << 30, None) == K.KDA_ERR_INVALID
+            assert str(top) in K.kda_last_error()
+            for rows in (1, 128):
+                assert K.lib().kda_quant_fp8(M, k, P, k, K.KDA_BF16, rows, P, P, None) == K.KDA_ERR_INVALID
+                assert str(top) in K.kda_last_error()
