@@ -23,6 +23,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
+#include <cfloat>
 #include <climits>
 #include <cstdarg>
 #include <cstdio>
@@ -382,7 +383,14 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
 #pragma unroll 1
             for (int kb = k0; kb < k1; ++kb, ++step) {
                 const int a = step & 1;
-                const float2 sc = make_float2(sx * sw, sx * sw);
+                // Where the product of the scales is no normal number its product with a block's sum may be one: the
+                // sum (0, or 2^-18 .. 2^25 of magnitude) is then multiplied by the larger scale first, which cannot
+                // overflow unless the result does. (Lanes are rows; each has its own scale.)
+                const float s = sx * sw;
+                const bool apart = !(fabsf(s) >= FLT_MIN && fabsf(s) <= FLT_MAX) && sx != 0.f && sw != 0.f;
+                const bool larger = fabsf(sx) >= fabsf(sw), odd = __any_sync(0xFFFFFFFFu, apart);
+                const float h = apart ? (larger ? sx : sw) : s, l = apart ? (larger ? sw : sx) : 1.f;
+                const float2 sc = make_float2(s, s), hi = make_float2(h, h), lo = make_float2(l, l);
                 if (kb + 1 < k1) {
                     sx = __ldg(xp + kb + 1);
                     sw = __ldg(wp + kb + 1);
@@ -398,10 +406,17 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                         uint32_t v[32];
                         tc::tmem_ld32_nowait(tb + (uint32_t)(a * BN + 32 * c), v);
                         tc::tmem_wait_ld();
+                        if (odd) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[16 * c + i] = f2_fma(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                                     sc, acc[16 * c + i]);
+                            for (int i = 0; i < 16; ++i)
+                                acc[16 * c + i] = f2_fma(f2_mul(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                                                hi), lo, acc[16 * c + i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                acc[16 * c + i] = f2_fma(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                                         sc, acc[16 * c + i]);
+                        }
                     }
                 }
                 tc::fence_before_sync();

@@ -124,6 +124,46 @@ def test_product_split_outputs(M, N, Kd, ysplit):
     near(product(ops, None, ysplit), *O8.linear(*ops))
 
 
+@pytest.mark.parametrize("M,N,Kd", [(5, 136, 400), (150, 264, 4096), (1200, 4104, 272)])
+@pytest.mark.parametrize("ex,ew", [(70, 60), (-76, -76), (-70, -70), (-126, 20), (100, -126), (120, -20), (-10, 127)])
+def test_scales_at_both_ends(M, N, Kd, ex, ew):
+    """Scales whose product overflows or underflows where the result does not, in some rows and blocks, among
+    ordinary ones; the blocks with a product past 2^127 hold zeros and the smallest codes alone. Beyond the bound
+    of `near`: half a step of BF16's smallest numbers, 2^-134."""
+    xq, xs, wq, ws = operands(M, N, Kd, 6)
+    rng = np.random.default_rng([M, N, Kd, 7])
+    rows, blocks = rng.random(M) < 0.4, rng.random(xs.shape[1]) < 0.6
+    rows[0] = blocks[0] = True
+    if ex + ew > 100:  # E4M3's smallest code is 2^-9, so that a sum is k 2^-18: results of up to 2^126
+        small = 2.0 ** -9 * (rng.random((M, Kd)) < 0.02)
+        xq = np.where(np.repeat(blocks, 128)[None, :Kd], np.where(rng.random((M, 1)) < 0.5, small, 0), xq)
+        wq = np.where(np.repeat(blocks, 128)[None, :Kd], 2.0 ** -9 * rng.integers(-1, 2, (N, Kd)), wq)
+    xs = np.where(rows[:, None] & blocks[None], np.ldexp(rng.uniform(1, 2, xs.shape), ex), xs).astype(np.float32)
+    ws = np.where(blocks[None], np.ldexp(rng.uniform(1, 2, ws.shape), ew), ws).astype(np.float32)
+    if ex + ew < -120:  # rows of scales of that size alone, so that ordinary ones do not hide them
+        xs[0], ws[0] = np.ldexp(1.5, ex), np.ldexp(1.25, ew)
+    got = product((xq, xs, wq, ws))
+    ref, mag = O8.linear(xq, xs, wq, ws)
+    assert np.isfinite(ref).all() and np.abs(ref).max() < 3e38
+    bad = ~(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mag + 2.0 ** -134)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], ref[bad][:4])
+    if ex + ew < -120:
+        assert (got[0, :128] != 0).any() == (np.abs(ref[0, :128]) > 2.0 ** -134).any()
+
+
+def test_scales_far_apart_in_neighbouring_rows():
+    """Rows whose product of scales is ordinary, though one of the two is huge, beside rows whose product underflows."""
+    M, N, Kd = 64, 136, 272
+    xq, xs, wq, ws = operands(M, N, Kd, 8)
+    xs = np.ldexp(xs, np.where(np.arange(M) % 2, 115, -115)[:, None]).astype(np.float32)
+    ws = np.ldexp(ws, -20).astype(np.float32)
+    got = product((xq, xs, wq, ws))
+    ref, mag = O8.linear(xq, xs, wq, ws)
+    assert np.isfinite(ref).all()
+    bad = ~(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mag + 2.0 ** -134)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], ref[bad][:4])
+
+
 def test_not_finite_codes_stay_in_their_rows():
     ops = operands(140, 264, 272, 2)
     ops[0][3, 5] = np.nan
