@@ -176,6 +176,14 @@ def gdr_width(cfg: K.kda_gdr_config_t) -> int:
     return -(-n // 128) * 128
 
 
+def _capturing(stream) -> bool:
+    """Whether the stream a call is given (a torch stream or its handle; None: the current one) is being captured."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class GdrLayerRunner:
     """Buffers for running gated delta rule layers on a batch of up to `rows` tokens at a time, made on
     the current stream."""
@@ -213,9 +221,9 @@ class GdrLayerRunner:
         chunks than any before, the workspace grows, which waits for the device; not while a graph is
         captured (run a prefill of that size first)."""
         need = K.kda_gdr_workspace_bytes(self.cfg, cu_seqlens_host)
-        capturing = torch.cuda.is_current_stream_capturing()
+        capturing = _capturing(stream)
         if self.ws.numel() < need:
-            if capturing:
+            if capturing or torch.cuda.is_current_stream_capturing():  # neither capture would survive the waits below
                 raise RuntimeError(f"the workspace must grow to {need} bytes: run a prefill of this size before one is captured")
             torch.cuda.synchronize(self.proj.device)  # calls on other streams may be using the old one
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.proj.device)

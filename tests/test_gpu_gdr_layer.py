@@ -194,6 +194,51 @@ def test_a_prefill_whose_workspace_must_grow_is_not_captured():
     assert bool(torch.isfinite(y.float()).all())
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_prefill_captured_on_another_stream_than_the_current_one(handle):
+    """The stream that the call is given decides: a captured workspace is kept when it is replaced, and does not grow
+    during the capture."""
+    cfg, lw, _, _, rng = gdr_layer(2, 1, 256, False, 7)
+    run = L.GdrLayerRunner(cfg, 256, 1000, "cuda")
+    S, slot = torch.zeros(2, 2, D, D, device="cuda"), torch.arange(1, dtype=torch.int32, device="cuda")
+    fresh = slot - 1
+    bufs = {n: (dev(rng.standard_normal((n, 256))), torch.empty(n, 256, dtype=torch.bfloat16, device="cuda"),
+                torch.tensor([0, n], dtype=torch.int32, device="cuda")) for n in (100, 1000)}
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if handle else side
+
+    def prefill(n, **kw):
+        x, y, cu = bufs[n]
+        run.prefill(lw, S, fresh, slot, cu, [0, n], x, y, **kw)
+
+    prefill(100)
+    torch.cuda.synchronize()
+    want, S1 = bufs[100][1].clone(), S.clone()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        g.capture_begin()
+    assert torch.cuda.current_stream() != side
+    prefill(100, stream=given)
+    with pytest.raises(RuntimeError, match="must grow"):
+        prefill(1000, stream=given)
+    with torch.cuda.stream(side):
+        with pytest.raises(RuntimeError, match="must grow"):  # nor does a call beside the capture end it
+            prefill(1000, stream=torch.cuda.default_stream())
+        g.capture_end()
+    address, size = run.ws.data_ptr(), run.ws.numel()
+    prefill(1000)
+    assert run.ws.data_ptr() != address
+    other = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    bufs[100][1].zero_()
+    S.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bufs[100][1], want) and torch.equal(S, S1)
+    assert all(bool((t == 7).all()) for t in other)
+
+
 def test_kda_layer_with_fp8_projections(oracle_mod):
     """The stacked projection and W_o of a KDA layer in FP8, decode and prefill; the mixer between them is
     the one that test_gpu_linear.py checks."""
