@@ -58,18 +58,15 @@ class Products:
 
     def __init__(self, shapes, rows: int, device, fp8: bool):
         self.fp8 = fp8
+        # the k split (and so the workspace) depends on the number of rows, up and down: the largest need of all of them
+        query = K.kda_linear_fp8_workspace_bytes if fp8 else K.kda_linear_workspace_bytes
+        ws = max(query(m, N, Kw) for N, Kw in shapes for m in range(1, rows + 1)) if rows else 256
         if fp8:
-            # the k split (and so the workspace) depends on the number of rows: the largest need of all of them
-            ws = max(K.kda_linear_fp8_workspace_bytes(m, N, Kw) for N, Kw in shapes for m in range(1, rows + 1))
             Kmax = max(Kw for _, Kw in shapes)
             self.xq = torch.empty(rows * Kmax, dtype=torch.float8_e4m3fn, device=device)
             self.xs = torch.empty(rows * -(-Kmax // 128), dtype=torch.float32, device=device)
             self.ws = torch.zeros(ws, dtype=torch.uint8, device=device)  # the error word starts at 0
         else:
-            # the same, by 256-row blocks
-            ws = 256
-            for mb in range(1, (rows + 255) // 256 + 1):
-                ws = max(ws, *(K.kda_linear_workspace_bytes(min(rows, 256 * mb), N, Kw) for N, Kw in shapes))
             self.ws = torch.empty(ws, dtype=torch.uint8, device=device)
 
     def __call__(self, x: torch.Tensor, w, y: torch.Tensor, r=None, ysplit: int = 0, stream=None) -> None:

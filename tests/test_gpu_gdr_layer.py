@@ -127,6 +127,23 @@ def test_heads_that_are_no_multiple_of_8(H, Hk):
         S0 = host(S[0])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_fewer_rows_than_the_runner_was_made_for(fp8):
+    """Row counts whose products are split along K, in a runner for a number of rows whose products are not."""
+    cfg, lw, A_log, dt_bias, rng = gdr_layer(8, 4, 512, fp8, 8)
+    run = L.GdrLayerRunner(cfg, 512, 256, "cuda", fp8)
+    for B in (1, 17, 60, 129, 256):
+        S = torch.zeros(B, 8, D, D, device="cuda")
+        slot = torch.arange(B, dtype=torch.int32, device="cuda")
+        x, y = dev(rng.standard_normal((B, 512))), torch.empty(B, 512, dtype=torch.bfloat16, device="cuda")
+        run.decode(lw, S, slot, slot, 1, x, y)
+        torch.cuda.synchronize()
+        check_product(x, lw.w_in, run.proj[:B])
+        for s in (0, B - 1):
+            check_mixer(cfg, run, slice(s, s + 1), np.zeros((8, D, D)), A_log, dt_bias, S[s], False)
+        check_product(run.o[:B], lw.w_o, y, x)
+
+
 def test_captured_decode_step():
     cfg, lw, A_log, dt_bias, rng = gdr_layer(8, 8, 256, True, 2)
     B = 5
