@@ -24,6 +24,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
+
 #include "kda_gdr.cuh"
 #include "kda_launch.cuh"
 #include "kda_tc.cuh"
@@ -946,12 +948,14 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     unsigned char *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
     StBars *bar = reinterpret_cast<StBars *>(sm + L::kBar);
     Scan *scans = reinterpret_cast<Scan *>(bar + 1);
-    static_assert(sizeof(StBars) + kStThreads / 32 * sizeof(Scan) <= 384, "barriers");
+    uint32_t *odd = reinterpret_cast<uint32_t *>(scans + kStThreads / 32);
+    static_assert(sizeof(StBars) + kStThreads / 32 * sizeof(Scan) + sizeof(*odd) <= 384, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kVBlocks = kD / L::kVB;
     const int vb = blockIdx.x % kVBlocks;
     const int h = (blockIdx.x / kVBlocks) % p.H, seq = blockIdx.x / (kVBlocks * p.H);
     if (threadIdx.x == 0) {
+        *odd = 0;
         for (int s = 0; s < L::kNa; ++s) {
             mbar_init(&bar->fa[s], 1);
             mbar_init(&bar->ea[s], 4);
@@ -1032,6 +1036,7 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     if (warp >= 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
         good = output_pass<MT>(p, sm, bar, u, kw, pl, h, vb * L::kVB);
+        named_bar_arrive(4, 256);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // this warp's part of S^T: value rows g, g + 8 of the unit's tiles, key rows 64 kw ..
@@ -1048,10 +1053,25 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
                     S[m][j][e] = src >= 0 ? make_float2(s[i], s[i + kD]) : make_float2(0.f, 0.f);
                 }
         good = chain_pass<MT>(sm, bar, u, kw, pl.len, S);
-        float *d = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
-        if (good)
+        // A value that is not finite spreads inside its chunk through the zeros above the diagonals of T and P, to
+        // tokens before its own. It always stays in its column of S as well (S is only ever scaled and added to), so
+        // that columns whose S is finite are right; 16 columns with one that is not are taken token by token.
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) {
+            bool ok = true;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) ok = ok && fabsf(S[m][j][e].x) <= FLT_MAX && fabsf(S[m][j][e].y) <= FLT_MAX;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok && nc > 0 && lane == 0) atomicOr(odd, 1u << (MT * u + m));
+        }
+        named_bar_sync(3, 128);
+        const uint32_t again = *const_cast<volatile uint32_t *>(odd);
+        float *d = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            if (good && !(again >> (MT * u + m) & 1u))
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -1060,6 +1080,8 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
                         d[i] = S[m][j][e].x;
                         d[i + kD] = S[m][j][e].y;
                     }
+        named_bar_sync(4, 256);  // the output of the chunks is written
+        if (good && again >> warp & 1u) walk_tokens<__nv_bfloat16>(p, src, dst, h, vb * (L::kVB / 16) + warp, pl.t0, pl.t0 + pl.len);
     }
     if (!good && lane == 0 && p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
 }

@@ -146,6 +146,12 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// Arrive at such a barrier without waiting for it; what this thread wrote before is seen by those who wait.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // 16-bit read-only global load whose result is not needed until later (no conversion here).
 __device__ __forceinline__ unsigned short ld_nc_u16(const void *p)
 {
