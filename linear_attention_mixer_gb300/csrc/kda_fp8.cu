@@ -400,23 +400,27 @@ f8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUte
                     break;
                 }
                 tc::fence_after_sync();
-                if (work) {
+                if (work && !odd) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t v[32];
                         tc::tmem_ld32_nowait(tb + (uint32_t)(a * BN + 32 * c), v);
                         tc::tmem_wait_ld();
-                        if (odd) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                acc[16 * c + i] = f2_fma(f2_mul(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                                                hi), lo, acc[16 * c + i]);
-                        } else {
+                        for (int i = 0; i < 16; ++i)
+                            acc[16 * c + i] = f2_fma(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                                     sc, acc[16 * c + i]);
+                    }
+                } else if (work) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                acc[16 * c + i] = f2_fma(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                                         sc, acc[16 * c + i]);
-                        }
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tc::tmem_ld32_nowait(tb + (uint32_t)(a * BN + 32 * c), v);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[16 * c + i] = f2_fma(f2_mul(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), hi),
+                                                     lo, acc[16 * c + i]);
                     }
                 }
                 tc::fence_before_sync();
