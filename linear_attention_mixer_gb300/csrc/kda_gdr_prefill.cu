@@ -19,8 +19,10 @@
 // state is kept to about 16 bits: S, beta (V - ..), T and U go into the products as a BF16 high part and a
 // BF16 low part (x - high), products of two such factors as hi hi + lo hi + hi lo, and sums are FP32.
 // With single BF16 operands the state would be off by 2^-9 a chunk. The output, which is rounded to
-// BF16 itself, takes the high part of S and P in one BF16 (and U in two: with one it was 1.7 times as far
-// from the exact result as the rounding alone, so it is 1.4 times).
+// BF16 itself, takes the high part of S alone, and P and U in two parts: with P in one it was 1.4 times as far
+// from the exact result as that rounding for keys that have nothing in common, and 3 to 8 times where they are
+// all positive or nearly equal, since Q S0 and P U then cancel. So it is 1.0 times, and 1.4 at the most measured.
+// Keeping P's low part costs 3% (8192 tokens, 32 heads: 287 -> 295 us) to 6%.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -38,12 +40,18 @@ namespace {
 // Tiles: BF16, 64 rows t of 64 columns i (128 bytes), 16-byte piece c of row t at c ^ (t & 7); only the
 // 16 x 16 blocks on and below the diagonal are meaningful.
 //   T high | T low | FP32 scalars: beta rk exp G [64], beta [64], rk exp(G_last - G) [64], exp G_last
-//   P | rq exp G [64]
+//   P high | rq exp G [64]
+// P's low part lies where the tiles are not used: that of a 16 x 16 block below the diagonal in the block's mirror
+// image in P's tile (not itself mirrored); of the diagonal blocks the lower left 8 x 8 in the upper right one, and the
+// two 8 x 8 on the diagonal in columns 16 .. 63 of T high's rows 0 .. 15 (pd_off), which go to P's ring as well.
 constexpr int kTl = 8192, kTx = 16384, kPartT = kTx + 1024;
-constexpr int kPx = 8192, kPartP = kPx + 256;
+constexpr int kPx = 8192, kPartP = kPx + 256, kPd = 2048;
 constexpr int kBlkBytes = kPartT + kPartP;
 
 __device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
+// Row r of P's low part in the j-th 8 x 8 on the diagonal, in T high's tile. (As swz(8 + r, j - 4) for the last two,
+// nvcc 13.0.88 addressed piece 0 of every row.)
+__device__ __forceinline__ uint32_t pd_off(int j, int r) { return (j < 6 ? 0 : 1024) + swz(r, j < 6 ? 2 + j : j - 4); }
 
 // Shared memory read as matrix operands. Volatile keeps these behind the barrier that the data came with;
 // what this thread's warp wrote itself is followed by __syncwarp.
@@ -160,9 +168,10 @@ __device__ __forceinline__ void add2(float &h, float &l, float x, float y)
 // 128 threads; warp w has the rows t = 16 w .. 16 w + 15. T by blocks of 16 rows: the diagonal blocks
 // D_w = (I + A_ww)^-1 by forward substitution in FP32, a warp each, one column a lane; below them
 //   T[w][:] = -D_w sum_{j < w} A[w][j] T[j][:]
-// on the tensor cores with split factors, three barriers deep. 66 us for 4096 (chunk, value head) pairs of
-// two value heads a key head (92 us with the whole inverse by forward substitution, a column a lane); bound
-// by the latency of its phases, 12 warps an SM, with DRAM at 22% and compute throughput at 32%.
+// on the tensor cores with split factors, three barriers deep. 61 to 64 us for 4096 (chunk, value head) pairs of
+// two value heads a key head (92 us with the whole inverse by forward substitution, a column a lane; P is written
+// before the inverse is formed, as its registers would spill otherwise); bound by the latency of its phases, 12
+// warps an SM, with DRAM at 22% and compute throughput at 34%.
 // Shared memory: two buffers of K and Q rows (the next item's are loaded while one is computed; a block is
 // built in the place of the rows that it came from), A's diagonal blocks, scalars of up to four value heads.
 constexpr int kPrepThreads = 128, kPrepPerSm = 3;
@@ -349,8 +358,13 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
             }
             if (j == 0 || (j & 3) == 0) __syncthreads();  // scalars and norms are written
             const float *s = scal + (j & 3) * kScal;
-            // A and P from the products: A's blocks left of the diagonal stay in registers as split A operands
-            uint32_t ah[3][4], al[3][4], pk[8][2];
+            if (j) {
+                if (tid == 0) bulk_wait_read_all();  // the previous head's block has been read
+                __syncthreads();
+            }
+            // A and P from the products: A's blocks left of the diagonal stay in registers as split A operands, P goes
+            // to the block, which takes the place of K and Q (read before the first head's barrier above)
+            uint32_t ah[3][4], al[3][4];
             {
                 const int ta = 16 * warp + g;
                 float Gh[2], Gl[2], fb[2], fq[2];
@@ -380,7 +394,16 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
                         }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        pk[nt][e] = pack2(pv[e][0], pv[e][1]);
+                        const bool diag8 = nt == 2 * warp + e;  // 8 x 8 on the diagonal
+                        if (nt <= 2 * warp + e) {               // or below it
+                            uint32_t ph, pl;
+                            split2(pv[e][0], pv[e][1], ph, pl);
+                            *reinterpret_cast<uint32_t *>(blk + kPartT + swz(16 * warp + g + 8 * e, nt) + 2 * q2) = ph;
+                            unsigned char *low = diag8                ? blk + pd_off(nt, g)
+                                                 : (nt >> 1) == warp ? blk + kPartT + swz(16 * warp + g, nt + 1)
+                                                                     : blk + kPartT + swz(16 * (nt >> 1) + g + 8 * e, 2 * warp + (nt & 1));
+                            *reinterpret_cast<uint32_t *>(low + 2 * q2) = pl;
+                        }
                         if ((nt >> 1) < warp) {
                             if (nt < 6) split2(av[e][0], av[e][1], ah[(nt >> 1) % 3][2 * (nt & 1) + e], al[(nt >> 1) % 3][2 * (nt & 1) + e]);
                         } else {
@@ -404,11 +427,6 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
 #pragma unroll
                 for (int r2 = r + 1; r2 < 16; ++r2) acc[r2] = fmaf(-a[r2], acc[r], acc[r2]);
             }
-            if (j) {
-                if (tid == 0) bulk_wait_read_all();  // the previous head's block has been read
-                __syncthreads();
-            }
-            // the block takes the place of K and Q (read before the first head's barrier above)
             {
                 unsigned char *dst = blk + (lane & 16 ? kTl : 0) + 2 * (jc & 7);  // lanes 0..15 the high part, 16..31 the low
 #pragma unroll
@@ -416,13 +434,6 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
                     const __nv_bfloat16 hi = __float2bfloat16_rn(acc[r]);
                     const __nv_bfloat16 lo = __float2bfloat16_rn(acc[r] - __bfloat162float(hi));
                     *reinterpret_cast<__nv_bfloat16 *>(dst + swz(16 * warp + r, 2 * warp + (jc >> 3))) = lane & 16 ? lo : hi;
-                }
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                    if ((nt >> 1) > warp) break;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<uint32_t *>(blk + kPartT + swz(16 * warp + g + 8 * e, nt) + 2 * q2) = pk[nt][e];
                 }
                 if (tid < kC) {
                     float *x = reinterpret_cast<float *>(blk + kTx);
@@ -524,17 +535,18 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
 //              for the chain, one of Q and P for the output
 // With MT = 1 what bounds it is the chain of a chunk: 158 MMAs a warp (m16n8k16, 8 cycles each on its quarter
 // of the SM) with the exchanges between them, and shared memory, which delivers operands for 16 rows at a
-// time: 2400 wavefronts and 520 of arriving copies in the 3250 cycles of a chunk. With MT = 2 an operand
+// time: 2370 wavefronts and 540 of arriving copies in the 3400 cycles of a chunk. With MT = 2 an operand
 // fetched serves 32 rows. A chunk of it takes longer, two columns' worth of it less; see the rule at the launch.
 // Tcgen05 would run the same products in tiles of 64 or 128 rows at four times the MMA rate, but the four
 // dependent products of a chunk (64 x 128 x 32 and smaller) would each pay for the way through tensor memory
-// and back into shared memory. 219 us for 32 heads of 8192 tokens (1.7 us a chunk), the tensor pipe 52% busy.
+// and back into shared memory. 229 us for 32 heads of 8192 tokens (1.8 us a chunk), the tensor pipe 50% busy
+// on the 128 SMs that have a block.
 constexpr int kStThreads = 384;
 template <int MT> struct St {
     static constexpr int kVB = 32 * MT;
     static constexpr int kNa = MT == 1 ? 3 : 2, kNo = 2, kNh = MT == 1 ? 2 : 1;  // stages of the rings, hand-over buffers
     static constexpr int kT = 16384, kV = kT + kPartT, kSa = kV + kC * kVB * 2;
-    static constexpr int kP = 16384, kSo = 25600;
+    static constexpr int kP = 16384, kDiag = kP + kPartP, kSo = 27648;
     static constexpr int kO = kNa * kSa, kX = kO + kNo * kSo;         // X: [2 units][2 kw][8 tiles][MT][32 lanes] float4
     static constexpr int kU = kX + 16384 * MT, kH = kU + 8192 * MT;   // U split: [2][2][4][MT][32] uint4
     static constexpr int kHu = 8192 * MT, kHand = 2 * kHu;            // S [2][8 k steps][MT][32], U split [2][8 tiles][MT][32] uint4
@@ -542,7 +554,7 @@ template <int MT> struct St {
     static constexpr int kSmem = kBar + 384 + 1024;
 };
 static_assert(St<1>::kSa % 1024 == 0 && St<2>::kSa % 1024 == 0 && St<1>::kSo % 1024 == 0 && St<1>::kV % 1024 == 0 &&
-              St<1>::kP + kPartP <= St<1>::kSo, "stages");
+              St<1>::kDiag + kPd <= St<1>::kSo, "stages");
 static_assert(St<1>::kSmem <= 232448 && St<2>::kSmem <= 232448, "state kernel shared memory");
 // Polls before a wait gives up (a test builds this file with limits that run out). A warp that gave up goes on
 // without waiting, so that every named barrier is met, but releases no stage of the rings and writes nothing to
@@ -856,6 +868,22 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
     uint32_t off[4];  // rows of this warp's tile of pair p, pieces 0..3 (4..7: ^ 64)
 #pragma unroll
     for (int pr = 0; pr < 4; ++pr) off[pr] = swz(16 * pr + 8 * own(kw, pr) + (lane & 7), lane >> 3);
+    // P's low part, five fetches of four 8 x 8: of pair 0's and 2's diagonal; of pair 1 (k step 0, the diagonal); of
+    // pair 2 (k steps 0, 1); of pair 3 (k steps 0, 1; 2 and the diagonal)
+    uint32_t lo[5];
+    {
+        const int i = lane >> 3, r = lane & 7;
+        auto diag = [&](int pr) {  // tile own 0: its triangle, twice (the second is not used); 1: the full 8 x 8, its triangle
+            const int w = own(kw, pr);
+            return w && !(i & 1) ? (uint32_t)L::kP + swz(16 * pr + r, 2 * pr + 1) : (uint32_t)L::kDiag + pd_off(2 * pr + w, r);
+        };
+        auto low = [&](int pr, int ks) { return (uint32_t)L::kP + swz(16 * ks + 8 * own(kw, pr) + r, 2 * pr + (i & 1)); };
+        lo[0] = diag(i < 2 ? 0 : 2);
+        lo[1] = i < 2 ? low(1, 0) : diag(1);
+        lo[2] = low(2, i >> 1);
+        lo[3] = low(3, i >> 1);
+        lo[4] = i < 2 ? low(3, 2) : diag(3);
+    }
     bool good = true;
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
@@ -890,6 +918,26 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
             if (pr >= 2) ldsm4(pb[1][pr], sb + L::kP + (off[pr] ^ 64));
             x[pr] = *reinterpret_cast<const float2 *>(co + 16 * pr + 8 * own(kw, pr) + q2);
         }
+        uint32_t plo[4][4][2];  // P's low part: pair, k step
+        {
+            uint32_t d[4], e[4], f[4], w[4], y[4];
+            ldsm4(d, sb + lo[0]);
+            ldsm4(e, sb + lo[1]);
+            ldsm4(f, sb + lo[2]);
+            ldsm4(w, sb + lo[3]);
+            ldsm4(y, sb + lo[4]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                plo[0][0][i] = d[i]; plo[2][2][i] = d[2 + i];
+                plo[1][0][i] = e[i]; plo[1][1][i] = e[2 + i];
+                plo[2][0][i] = f[i]; plo[2][1][i] = f[2 + i];
+                plo[3][0][i] = w[i]; plo[3][1][i] = w[2 + i];
+                plo[3][2][i] = y[i]; plo[3][3][i] = y[2 + i];
+            }
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr)  // what lies above the diagonal: zeros
+                if (!own(kw, pr)) plo[pr][pr][1] = pb[pr >> 1][pr][2 * (pr & 1) + 1] = 0;
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -910,6 +958,8 @@ __device__ __forceinline__ bool output_pass(const Args &p, unsigned char *sm, St
                 for (int pr = ks; pr < 4; ++pr) mma(o[m][pr], a, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
 #pragma unroll
                 for (int pr = ks; pr < 4; ++pr) mma(o[m][pr], al, pb[ks >> 1][pr][2 * (ks & 1)], pb[ks >> 1][pr][2 * (ks & 1) + 1]);
+#pragma unroll
+                for (int pr = ks; pr < 4; ++pr) mma(o[m][pr], a, plo[pr][ks][0], plo[pr][ks][1]);
             }
         __syncwarp();
         if (lane == 0) {
@@ -1016,10 +1066,11 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
                 if (!good) break;
                 ++no;
                 b = sm + L::kO + so * L::kSo;
-                mbar_arrive_expect_tx(&bar->fo[so], (uint32_t)(box_rows * 2 * 128 + kPartP));
+                mbar_arrive_expect_tx(&bar->fo[so], (uint32_t)(box_rows * 2 * 128 + kPartP + kPd));
                 tma_load_2d(b, &maps.q, hk * kD, t, &bar->fo[so]);
                 tma_load_2d(b + 8192, &maps.q, hk * kD + 64, t, &bar->fo[so]);
                 bulk_g2s(b + L::kP, blk + kPartT, kPartP, &bar->fo[so]);
+                bulk_g2s(b + L::kDiag, blk, kPd, &bar->fo[so]);
             }
             // The last copies into every stage land before the block ends and its shared memory is another's,
             // whether the other warps have waited for them or gave up.
@@ -1146,8 +1197,10 @@ cudaError_t launch_chunked(const Args &p, int64_t n_chunks, int64_t longest, voi
     }
     // 32 or 64 value columns a block, by the time that either is estimated to take: the longest sequence, or all
     // of the work over the SMs, at 1.65 us a chunk of 32 columns, 3.2 us a chunk of 64 and 3.5 us to start a
-    // block. One sequence of 8192 tokens and 32 heads: 288 us with 32 columns, 482 us with 64; ten sequences of
-    // 2 .. 467 tokens and 64 heads: 176 and 156 us.
+    // block. One sequence of 8192 tokens and 32 heads: 299 us with 32 columns, 482 us with 64; ten sequences of
+    // up to 322 tokens and 64 heads: 212 and 187 us. It took the faster form in ten of twelve shapes; in the others
+    // whole waves of blocks, which it does not count, decide (8192 tokens, 64 heads: 570 us for 543; 4071 + 3798
+    // tokens, 40 heads: 463 for 406).
     auto estimate = [&](int mt, double chunk) {
         const double work = (n_chunks * chunk + p.N * 3.5) * p.H * (4 / mt) / sms, chain = longest * chunk + 3.5;
         return work > chain ? work : chain;
