@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import numpy as np
 import torch
@@ -183,9 +184,27 @@ def _dev(t: torch.Tensor, dtype=None, name: str = "tensor"):
     return _VP(t.data_ptr())
 
 
+def _i32_array(x) -> np.ndarray:
+    """x as a contiguous int32 array; refused where that would change a number."""
+    if isinstance(x, (list, tuple)):
+        try:
+            return np.frombuffer(array("i", x), dtype=np.int32) if x else np.zeros(0, np.int32)
+        except OverflowError:
+            raise ValueError("slots and lengths must be 32-bit whole numbers") from None
+        except TypeError:  # other numbers than Python's own
+            pass
+    a = np.asarray(x)
+    if a.dtype != np.int32:
+        with np.errstate(invalid="ignore"):
+            b = a.astype(np.int32)
+        if (a != b).any():
+            raise ValueError("slots and lengths must be 32-bit whole numbers")
+        a = b
+    return np.ascontiguousarray(a)
+
+
 def _host_i32(x):
-    import numpy as np
-    a = np.ascontiguousarray(np.asarray(x, dtype=np.int32))
+    a = _i32_array(x)
     return a, a.ctypes.data_as(_PI32)
 
 
@@ -570,7 +589,7 @@ def kda_gdr_prefill(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tens
     kda_gdr_workspace_bytes(cfg, cu_seqlens_host) bytes."""
     dev = _current_device()
     N = src_slots.numel()
-    cu_h = np.ascontiguousarray(cu_seqlens_host, dtype=np.int32)
+    cu_h = _i32_array(cu_seqlens_host)
     if cu_h.shape != (N + 1,):
         raise ValueError("cu_seqlens_host must hold N + 1 entries")
     Sp, sp, dp, r, ep = _gdr_call(cfg, params, S, src_slots, dst_slots, int(cu_h[N]), q, k, v, a, b, out, err, dev)

@@ -39,6 +39,17 @@ def test_workspace(K):
     assert K.lib().kda_gdr_workspace_bytes(None, None, 0) == 0
 
 
+@pytest.mark.parametrize("cu", [np.array([0, 2 ** 32 + 64]), np.array([2 ** 32, 64]), np.array([0, 2 ** 63], dtype=np.uint64), [0, 64.5],
+                                np.array([0.0, np.inf])])
+def test_lengths_that_are_no_32_bit_numbers(K, cu):
+    """Refused, and not taken modulo 2^32 or cut: their queries would answer for other lengths."""
+    c = K.kda_gdr_config(4, 2)
+    with pytest.raises(ValueError):
+        K.kda_gdr_workspace_bytes(c, cu)
+    for same in (np.array([0, 64]), np.array([0, 64], dtype=np.uint8), [0, 64], (0, 64.0), np.array([0, 1, 64], dtype=np.int32)[::2]):
+        assert K.kda_gdr_workspace_bytes(c, same) == K.kda_gdr_workspace_bytes(c, np.array([0, 64], dtype=np.int32))
+
+
 P = 1 << 20  # an aligned address
 
 
