@@ -33,6 +33,7 @@
 #include "kda_launch.cuh"
 #include "kda_ptx.cuh"
 #include "kda_tc.cuh"
+#include "kda_wait.cuh"
 
 namespace kda {
 namespace {

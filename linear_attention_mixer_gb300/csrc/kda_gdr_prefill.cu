@@ -31,6 +31,7 @@
 #include "kda_gdr.cuh"
 #include "kda_launch.cuh"
 #include "kda_tc.cuh"
+#include "kda_wait.cuh"
 
 namespace kda {
 namespace gdr {

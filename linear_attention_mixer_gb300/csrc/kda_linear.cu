@@ -32,6 +32,7 @@
 #include "kda_internal.cuh"
 #include "kda_ptx.cuh"
 #include "kda_tc.cuh"
+#include "kda_wait.cuh"
 
 namespace kda {
 namespace {

@@ -53,15 +53,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     return false;
 }
 
-// The same by a whole warp: true in every lane or in none, so that the warp goes on as one (the limit may run
-// out in one lane just before the phase completes for another).
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, uint32_t limit)
-{
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, limit));
-    __syncwarp();
-    return ok;
-}
-
 __device__ __forceinline__ uint64_t policy_evict_first()
 {
     uint64_t pol;
@@ -144,12 +135,6 @@ __device__ __forceinline__ void prefetch_l2_bulk(const void *src, uint32_t bytes
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
-// Arrive at such a barrier without waiting for it; what this thread wrote before is seen by those who wait.
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
-{
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 // 16-bit read-only global load whose result is not needed until later (no conversion here).
