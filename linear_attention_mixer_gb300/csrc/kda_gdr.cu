@@ -43,8 +43,7 @@ gdr_decode_kernel(const __grid_constant__ Args p, int64_t n_units)
         if (lane == 0) set_err(p.err);
         return;
     }
-    const int64_t t0 = (int64_t)row * p.n;
-    walk_tokens<T>(p, src, dst, h, cb, t0, t0 + p.n);
+    walk_tokens<T>(p, src, dst, h, cb, (int64_t)row * p.n, p.n);
 }
 
 // FP32 prefill: the same walk over whole sequences. A block has half of a (sequence, head); its rows come by

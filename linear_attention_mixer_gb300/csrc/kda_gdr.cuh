@@ -163,10 +163,10 @@ __device__ __forceinline__ void store_state(const float4 (&s)[16], const Args &p
     for (int i = 0; i < 16; ++i) st_stream(reinterpret_cast<float4 *>(S + i * kD), s[i]);
 }
 
-// One warp: columns 16 cb .. of head h through tokens t0 .. t1 - 1, from slot src (-1: zeros) to slot dst; the next
+// One warp: columns 16 cb .. of head h through n tokens from row t0 on, from slot src (-1: zeros) to slot dst; the next
 // token's row is fetched while one is computed.
 template <typename T>
-__device__ __forceinline__ void walk_tokens(const Args &p, int src, int dst, int h, int cb, int64_t t0, int64_t t1)
+__device__ __forceinline__ void walk_tokens(const Args &p, int src, int dst, int h, int cb, int64_t t0, int n)
 {
     const int lane = threadIdx.x & 31, rg = lane >> 2, cg = lane & 3, c = rg & 3;
     const size_t at = (size_t)(16 * rg) * kD + 16 * cb + 4 * cg;
@@ -190,13 +190,14 @@ __device__ __forceinline__ void walk_tokens(const Args &p, int src, int dst, int
     Token<T> next;
     load(t0, next);
 #pragma unroll 1
-    for (int64_t t = t0; t < t1; ++t) {
+    for (int i = 0; i < n; ++i) {
+        const int64_t t = t0 + i;
         float k[16], q[16];
         next.k.get(k);
         next.q.get(q);
         const float v = next.v;
         const float alpha = expf(log_decay(next.a, dt_bias, expA)), beta = sigmoidf_(next.b);
-        if (t + 1 < t1) load(t + 1, next);
+        if (i + 1 < n) load(t + 1, next);
         // |k|^2, |q|^2, k.q: the 16 rows of this lane, then over rg (lane bits 2..4)
         float2 kk2 = make_float2(0.f, 0.f), qq2 = kk2, kq2 = kk2;
 #pragma unroll

@@ -1133,7 +1133,7 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
                         d[i + kD] = S[m][j][e].y;
                     }
         named_bar_sync(4, 256);  // the output of the chunks is written
-        if (good && again >> warp & 1u) walk_tokens<__nv_bfloat16>(p, src, dst, h, vb * (L::kVB / 16) + warp, pl.t0, pl.t0 + pl.len);
+        if (good && again >> warp & 1u) walk_tokens<__nv_bfloat16>(p, src, dst, h, vb * (L::kVB / 16) + warp, pl.t0, pl.len);
     }
     if (!good && lane == 0 && p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
 }
