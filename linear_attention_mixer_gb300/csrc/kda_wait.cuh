@@ -18,6 +18,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, u
 // who wait.
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
 {
+    __threadfence_block();
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
