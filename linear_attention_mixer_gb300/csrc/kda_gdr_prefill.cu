@@ -26,8 +26,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <cfloat>
-
 #include "kda_gdr.cuh"
 #include "kda_launch.cuh"
 #include "kda_tc.cuh"
@@ -540,8 +538,10 @@ gdr_prep_kernel(const __grid_constant__ Args p, unsigned char *__restrict__ bloc
 // fetched serves 32 rows. A chunk of it takes longer, two columns' worth of it less; see the rule at the launch.
 // Tcgen05 would run the same products in tiles of 64 or 128 rows at four times the MMA rate, but the four
 // dependent products of a chunk (64 x 128 x 32 and smaller) would each pay for the way through tensor memory
-// and back into shared memory. 229 us for 32 heads of 8192 tokens (1.8 us a chunk), the tensor pipe 50% busy
-// on the 128 SMs that have a block.
+// and back into shared memory, which lengthens the chain of one sequence. That is no reason for a batch with more
+// (sequence, head) pairs than SMs: there 128 columns of a chunk cost 6.5 to 7.2 us of an SM here, and the KDA state
+// pass, on tcgen05, takes 2.75. Such a form has not been built.
+// 229 us for 32 heads of 8192 tokens (1.8 us a chunk), the tensor pipe 51% busy on the 128 SMs that have a block.
 constexpr int kStThreads = 384;
 template <int MT> struct St {
     static constexpr int kVB = 32 * MT;
@@ -566,8 +566,8 @@ static_assert(St<1>::kSmem <= 232448 && St<2>::kSmem <= 232448, "state kernel sh
 constexpr uint32_t kLandSpin = 1u << 26;  // for copies that are on their way when a block ends
 
 struct StateMaps { CUtensorMap k, q, v; };
-// full and empty of the two rings; S0 handed over, U handed over, both read
-struct StBars { uint64_t fa[3], ea[3], fo[2], eo[2], fs[2], fh[2], eh[2]; };
+// full and empty of the two rings; S0 handed over, U handed over, both read; the output is written
+struct StBars { uint64_t fa[3], ea[3], fo[2], eo[2], fs[2], fh[2], eh[2], done; };
 
 // byte offset of 16-byte piece c of row r of the V tile (rows of 64 or 128 bytes, TMA's swizzle of that width)
 template <int MT> __device__ __forceinline__ uint32_t v_off(int r, int c)
@@ -1000,13 +1000,12 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     StBars *bar = reinterpret_cast<StBars *>(sm + L::kBar);
     Scan *scans = reinterpret_cast<Scan *>(bar + 1);
     uint32_t *odd = reinterpret_cast<uint32_t *>(scans + kStThreads / 32);
-    static_assert(sizeof(StBars) + kStThreads / 32 * sizeof(Scan) + sizeof(*odd) <= 384, "barriers");
+    static_assert(sizeof(StBars) + kStThreads / 32 * sizeof(Scan) + 4 * sizeof(*odd) <= 384, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kVBlocks = kD / L::kVB;
     const int vb = blockIdx.x % kVBlocks;
     const int h = (blockIdx.x / kVBlocks) % p.H, seq = blockIdx.x / (kVBlocks * p.H);
     if (threadIdx.x == 0) {
-        *odd = 0;
         for (int s = 0; s < L::kNa; ++s) {
             mbar_init(&bar->fa[s], 1);
             mbar_init(&bar->ea[s], 4);
@@ -1020,6 +1019,7 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
             mbar_init(&bar->fh[s], 4);
             mbar_init(&bar->eh[s], 4);
         }
+        mbar_init(&bar->done, 4);
         fence_mbar_init();
     }
     const Scan part = scan_cu(p, threadIdx.x, kStThreads, seq);
@@ -1088,7 +1088,8 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
     if (warp >= 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
         good = output_pass<MT>(p, sm, bar, u, kw, pl, h, vb * L::kVB);
-        named_bar_arrive(4, 256);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->done);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // this warp's part of S^T: value rows g, g + 8 of the unit's tiles, key rows 64 kw ..
@@ -1108,18 +1109,22 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
         // A value that is not finite spreads inside its chunk through the zeros above the diagonals of T and P, to
         // tokens before its own. It always stays in its column of S as well (S is only ever scaled and added to), so
         // that columns whose S is finite are right; 16 columns with one that is not are taken token by token.
+        uint32_t again = 0;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            bool ok = true;
+            float2 z[4] = {};  // 0 as long as all is finite
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) ok = ok && fabsf(S[m][j][e].x) <= FLT_MAX && fabsf(S[m][j][e].y) <= FLT_MAX;
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok && nc > 0 && lane == 0) atomicOr(odd, 1u << (MT * u + m));
+                for (int e = 0; e < 2; ++e) z[2 * (j & 1) + e] = f2_fma(S[m][j][e], make_float2(0.f, 0.f), z[2 * (j & 1) + e]);
+            const float2 y = f2_add(f2_add(z[0], z[1]), f2_add(z[2], z[3]));
+            if (__any_sync(0xFFFFFFFFu, y.x + y.y != 0.f)) again |= 1u << (MT * u + m);
         }
-        named_bar_sync(3, 128);
-        const uint32_t again = *const_cast<volatile uint32_t *>(odd);
+        if (nc == 0) again = 0;
+        volatile uint32_t *flags = odd;
+        if (lane == 0) flags[warp] = again;
+        named_bar_sync(1 + u, 64);
+        again |= flags[warp ^ 1];  // the other half of these columns' key rows
         float *d = p.S + ((size_t)dst * p.H + h) * kD * kD + at;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -1132,7 +1137,9 @@ gdr_state_kernel(const __grid_constant__ StateMaps maps, const __grid_constant__
                         d[i] = S[m][j][e].x;
                         d[i + kD] = S[m][j][e].y;
                     }
-        named_bar_sync(4, 256);  // the output of the chunks is written
+        named_bar_sync(3, 128);
+        again = flags[0] | flags[1] | flags[2] | flags[3];
+        if (again && !mbar_wait_warp(&bar->done, 0, kLandSpin)) good = false;
         if (good && again >> warp & 1u) walk_tokens<__nv_bfloat16>(p, src, dst, h, vb * (L::kVB / 16) + warp, pl.t0, pl.len);
     }
     if (!good && lane == 0 && p.err) atomicExch(p.err, KDA_ERR_TIMEOUT);
