@@ -373,7 +373,8 @@ kda_status kda_linear(int32_t M, int32_t N, int32_t K, const void *x, const void
  *   q         device E4M3 [M][K], 16-byte aligned      out
  *   s         device FP32 [ceil(M / block_rows)][ceil(K / 128)]      out
  * kda_linear_fp8: y = x W^T (+ r) in BF16, each block's product accumulated in FP32 on the tensor cores,
- * scaled by xs * ws and added in FP32, in the blocks' order. The scales may be any FP32 numbers.
+ * scaled by xs and ws and added in FP32, in the blocks' order. The scales may be any FP32 numbers:
+ * xs * ws may overflow or underflow where the scaled product does not.
  *   M, N, K   as for kda_linear, with N a multiple of 8 and K a multiple of 16, at most 2^31 - 128
  *   xq, xs    device E4M3 [M][K], FP32 [M][ceil(K / 128)]
  *   wq, ws    device E4M3 [N][K], FP32 [ceil(N / 128)][ceil(K / 128)]
@@ -400,7 +401,8 @@ kda_status kda_linear_fp8(int32_t M, int32_t N, int32_t K, const void *xq, const
  *   k^ = k / sqrt(|k|^2 + l2_eps),  q^ = q_scale q / sqrt(|q|^2 + l2_eps)
  *                                   (qk_l2norm == 0: k^ = k, q^ = q_scale q)
  *   S = alpha S;  u = beta (v - S^T k^);  S = S + k^ u^T;  out = S^T q^
- * -inf and very negative decay logits are allowed (alpha = 1), as are those that make alpha 0.
+ * -inf and very negative decay logits are allowed (alpha = 1), as are those that make alpha 0;
+ * exp(A_log) must be finite in FP32.
  *
  * States are caller-owned: S device FP32 [max_slots][H][d][d], 16-byte aligned (the S part of a
  * kda_state's slots, without the conv history). A call reads row r's state from slot
@@ -460,10 +462,16 @@ kda_status kda_gdr_decode(const kda_gdr_config_t *cfg, const kda_gdr_params *par
 
 /*
  * N sequences packed along the token axis; cu_seqlens (device int32 [N+1]) and cu_seqlens_host as
- * for kda_prefill. An empty sequence copies its src state (or zeros) to its dst. With BF16 rows
- * the tokens are taken in chunks of 64 on the tensor cores, with the state, its updates and all
- * sums held in FP32; with FP32 rows they are taken one by one in FP32. Nothing outside the rows
- * [0, cu[N]) of out is written.
+ * for kda_prefill. An empty sequence copies its src state (or zeros) to its dst. Nothing outside
+ * the rows [0, cu[N]) of out is written. With FP32 rows the tokens are taken one by one in FP32
+ * (state within 1.3e-7 of FP64 in the 2-norm). With BF16 rows they are taken in chunks of 64 on
+ * the tensor cores. The state and all sums are held in FP32 there too, but what enters a product
+ * beside the rows themselves is rounded to two BF16 parts, about 16 bits, and to one where the
+ * output reads the state: the state was 3.5e-6 from FP64 (3e-5 for keys that are nearly equal,
+ * without decay), the output 1.7e-3 (2.3e-3), of which 1.7e-3 is its own rounding to BF16.
+ * What is not finite in a row reaches no earlier token and no other sequence, as in the recurrence;
+ * in BF16 the 16 value columns of a state that it reaches are taken one token at a time, which is
+ * slower.
  *   workspace  device scratch of at least kda_gdr_workspace_bytes(cfg, cu_seqlens_host, N) bytes,
  *              16-byte aligned, caller-owned (25,856 bytes per chunk and value head; with FP32 rows it is
  *              not touched). Calls that share one must be ordered, captured graphs that are replayed

@@ -13,12 +13,11 @@
 // With a k split the FP32 partial sums go to the workspace and a second kernel adds them in split
 // order, so the result does not depend on timing.
 //
-// 8192 x 12288 x 7168: 541 to 549 us alone (2.65 PFLOP/s, the tensor pipe 62% busy), 616 us called again and again,
-// under the power cap (2.34 PFLOP/s). The epilogue is well hidden: with
-// neither its reads of tensor memory nor its sums the kernel took 504 us where it took 527 (before it looked at the
-// scales' product, which costs 1 to 2%). The rest is operands and
-// MMAs: 48 KB a block of 128 of K and SM, 8.5 GB, are 15.5 TB/s out of L2, the likely bound. Forms in which two CTAs
-// share a unit of 256 x 256 (cta_group::2, a third fewer bytes) were no faster (560 us, the epilogue's hand-over
+// 8192 x 12288 x 7168: 541 to 549 us alone (2.65 PFLOP/s, the tensor pipe 62% busy), 606 to 617 us called again and
+// again, under the power cap (2.36 PFLOP/s). The epilogue is well hidden: with neither its reads of tensor memory nor
+// its sums the kernel took 504 us where it took 527 (before it looked at the scales' product, which costs 1 to 2%).
+// The rest is operands and MMAs: 48 KB a block of 128 of K and SM, 8.5 GB, are 15.5 TB/s out of L2, the likely bound.
+// Forms in which two CTAs share a unit of 256 x 256 (cta_group::2, a third fewer bytes) were no faster (560 us, the epilogue's hand-over
 // being their bound), nor were they with 16 epilogue warps of half the columns (734 us).
 // 16 x 7168 x 12288: 25 us, 19 to 21 of it in this kernel, about 4.4 TB/s, and the rest in adding the splits.
 #include <cuda.h>

@@ -22,7 +22,7 @@
 // BF16 itself, takes the high part of S alone, and P and U in two parts: with P in one it was 1.4 times as far
 // from the exact result as that rounding for keys that have nothing in common, and 3 to 8 times where they are
 // all positive or nearly equal, since Q S0 and P U then cancel. So it is 1.0 times, and 1.4 at the most measured.
-// Keeping P's low part costs 3% (8192 tokens, 32 heads: 287 -> 295 us) to 6%.
+// Keeping P's low part costs 1 to 5% (8192 tokens, 32 heads: 287 -> 295 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -104,8 +104,8 @@ struct Place { int seq, t0, len, first; };
 // What threads first, first + step, .. of a block read of cu_seqlens: whether it is one of total_T tokens, the
 // chunks before sequence seq and all chunks (which cannot wrap in one that is right: the host has checked that
 // chunks x heads fit 28 bits). The sums are over the warp. Shared by all of a state block's warps, and in the
-// prep only the first item's: 4096 sequences of 1 to 16 tokens and 8 heads 3.8 ms (25.5 ms with one warp's scan
-// for each block and item), 256 of them 215 us (281).
+// prep only the first item's: 4096 sequences of 1 to 16 tokens and 8 heads 3.9 ms (25.5 ms with one warp's scan
+// for each block and item), 256 of them 221 us (281).
 struct Scan { int ok; uint32_t before, all; };
 __device__ __forceinline__ Scan scan_cu(const Args &p, int first, int step, int seq)
 {

@@ -21,6 +21,10 @@ The gated delta rule layer has the same frame around the recurrence with one dec
     o             = kda_gdr_decode / kda_gdr_prefill
     x'            = x + W_o o
 
+It is the recurrence between two products and no published model's layer: there is no short convolution, no
+SiLU, no output norm and no gate around the recurrence. A model that has them applies them to the columns
+and to o itself, between the library's calls.
+
 The dense products of either layer run in BF16 (kda_linear) or, for weights given as
 Fp8Weight, in FP8 (kda_quant_fp8 of the activations, kda_linear_fp8).
 """
