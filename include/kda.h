@@ -486,6 +486,159 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
                            size_t workspace_bytes, int32_t *err, void *stream);
 
 /*
+ * The gated linear recurrence: a state of one number per channel, with a decay and an input gate of its own per
+ * channel and token (the pages have no counterpart; a KDA layer's state is a matrix per head). Per channel of dim,
+ * the state h in FP32:
+ *   gk = -exp(A_log) sigmoid(a + a_bias),  alpha = exp(gk),  beta = sigmoid(b + b_bias)
+ *   h = alpha h + sqrt(1 - alpha^2) beta x,  out = h, or with an output gate h silu(g)
+ * a = -inf keeps the state as it is (alpha = 1), b = -inf lets nothing in; exp(A_log) must be finite in FP32. What is
+ * not finite in a row reaches no earlier token, no other channel and no other sequence.
+ *
+ * States are caller-owned, device FP32 [max_slots][dim], 16-byte aligned, read and written by slots as the gated delta
+ * rule's are (src_slots, dst_slots, err; KDA_ERR_DEVICE also where a sequence's bounds in cu_seqlens do not rise within
+ * [0, cu_seqlens_host[N]], from 0 for the first and to the end for the last: that sequence is left alone, and what the
+ * call writes for sequences that overlap it is undefined).
+ */
+#define KDA_GLR_MAX_DIM 1048576
+typedef struct {
+    int32_t dim;       /* channels: a multiple of 8 with BF16 rows, of 4 with FP32 rows, <= KDA_GLR_MAX_DIM */
+    int32_t io_dtype;  /* kda_dtype of x, a, b, g, out and of their gradients */
+} kda_glr_config_t;
+
+/* Per-layer parameters, device FP32 [dim] each, 16-byte aligned, caller-owned. */
+typedef struct {
+    const float *A_log, *a_bias, *b_bias;
+} kda_glr_params;
+
+/*
+ * The per-token rows, device io_dtype [.][dim], 16-byte aligned, with the distance between tokens in elements, a multiple
+ * of 16 bytes and >= dim (not used with one token), so that they may be columns of one projection's output. g may be
+ * NULL: no output gate. out must not overlap an input.
+ */
+typedef struct {
+    const void *x, *a, *b, *g;
+    void *out;
+    int64_t x_stride, a_stride, b_stride, g_stride, out_stride;
+} kda_glr_rows;
+
+/* The rows of a backward pass, as above: dx, da, db and dg (NULL exactly where g is) are written and overlap nothing. */
+typedef struct {
+    const void *x, *a, *b, *g, *dout;
+    void *dx, *da, *db, *dg;
+    int64_t x_stride, a_stride, b_stride, g_stride, dout_stride, dx_stride, da_stride, db_stride, dg_stride;
+} kda_glr_grad_rows;
+
+/* Fill *cfg. KDA_ERR_INVALID (cfg untouched) for cfg == NULL or unsupported values. */
+kda_status kda_glr_config(kda_glr_config_t *cfg, int32_t dim, int32_t io_dtype);
+
+/*
+ * n consecutive tokens (1 .. KDA_DECODE_MAX_TOKENS) for each of B sequences; token t of sequence r is row r*n + t.
+ * B == 0 is a no-op. Errors: KDA_ERR_INVALID, KDA_ERR_CUDA.
+ */
+kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *params, float *S, int32_t max_slots,
+                          const int32_t *src_slots, const int32_t *dst_slots, int32_t B, int32_t n,
+                          const kda_glr_rows *rows, int32_t *err, void *stream);
+
+/*
+ * N sequences packed along the token axis; cu_seqlens (device int32 [N+1]) and cu_seqlens_host as for kda_prefill. An
+ * empty sequence copies its src state (or zeros) to its dst. Nothing outside the rows [0, cu[N]) of out is written. All
+ * arithmetic is FP32, and results do not depend on timing.
+ *   starts     device FP32 [kda_glr_chunks(cu_seqlens_host, N)][dim], 16-byte aligned, or NULL. Receives states that
+ *              kda_glr_backward starts from (one for each 16 tokens of a sequence; the layout is the library's).
+ *   workspace  device scratch of at least kda_glr_workspace_bytes(cfg, cu_seqlens_host, N) bytes, 16-byte aligned,
+ *              caller-owned, the same for prefill and backward. Calls that share one must be ordered, captured graphs
+ *              that are replayed at the same time need one each. The query returns 0 for invalid arguments and does
+ *              not touch the device; kda_glr_chunks returns -1.
+ * Errors: KDA_ERR_INVALID, KDA_ERR_CUDA.
+ */
+size_t kda_glr_workspace_bytes(const kda_glr_config_t *cfg, const int32_t *cu_seqlens_host, int32_t N);
+int64_t kda_glr_chunks(const int32_t *cu_seqlens_host, int32_t N);
+kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *params, float *S, int32_t max_slots,
+                           const int32_t *src_slots, const int32_t *dst_slots, const int32_t *cu_seqlens,
+                           const int32_t *cu_seqlens_host, int32_t N, const kda_glr_rows *rows, float *starts,
+                           void *workspace, size_t workspace_bytes, int32_t *err, void *stream);
+
+/*
+ * The gradients of a kda_glr_prefill of the same cu_seqlens, parameters and rows, which was given `starts`:
+ *   rows.dout  the gradient of out          dS_last   device FP32 [N][dim], that of the final states, or NULL: zeros
+ *   rows.dx, .da, .db, .dg  io_dtype        dS_first  device FP32 [N][dim], that of the states at the start, or NULL
+ *   dA_log, da_bias, db_bias  device FP32 [dim], sums over all tokens, each or NULL; overwritten (zeros for N == 0)
+ * dS_last, dS_first and the three sums 16-byte aligned. Sums are FP32, and results do not depend on timing. A sequence
+ * whose bounds are wrong is left alone, as in the prefill, and adds nothing to the sums. Errors: KDA_ERR_INVALID,
+ * KDA_ERR_CUDA.
+ */
+kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *params, const int32_t *cu_seqlens,
+                            const int32_t *cu_seqlens_host, int32_t N, const float *starts, const kda_glr_grad_rows *rows,
+                            const float *dS_last, float *dS_first, float *dA_log, float *da_bias, float *db_bias,
+                            void *workspace, size_t workspace_bytes, int32_t *err, void *stream);
+
+/*
+ * The norms around a block of a stack, fused with the block's gate, its residual scale and the residual add (the pages
+ * keep their residual stream elsewhere). For M rows of dim channels, x the stream and y the block's output:
+ *   x' = x + scale sigmoid(g) post_w y / rms(y),  h = pre_w x' / rms(x'),  rms(z) = sqrt(mean(z^2) + eps)
+ * in FP32, each output rounded once (h from x' before its rounding). The sums of squares must be finite in FP32.
+ */
+#define KDA_BLOCK_NORM_MAX_DIM 16384
+typedef struct {
+    int32_t dim;       /* a multiple of 8 with BF16 rows, of 4 with FP32 rows, <= KDA_BLOCK_NORM_MAX_DIM */
+    int32_t io_dtype;  /* kda_dtype of the rows */
+    float eps;         /* default 1e-6, inside the square root */
+} kda_block_norm_config_t;
+
+/* Device FP32 [dim] each, 16-byte aligned, caller-owned: post_w and scale are read where there is a y, pre_w for an h. */
+typedef struct {
+    const float *post_w, *scale, *pre_w;
+} kda_block_norm_params;
+
+/*
+ * Rows, device [M][dim], 16-byte aligned, with the distance between them in elements, a multiple of 16 bytes and >= dim
+ * (not used with one row).
+ *   x, y, g   io_dtype. g NULL: no gate. y NULL (then g and x_out too): only h, of x itself, as before a first block
+ *   x_out     io_dtype, x'; may be x with the same stride. Otherwise outputs overlap nothing
+ *   h, hs     hs NULL: h in io_dtype. Otherwise h is E4M3 and hs device FP32 [M][ceil(dim / 128)], the operands of
+ *             kda_linear_fp8 as kda_quant_fp8 would make them of h in FP32; dim a multiple of 16, h 8-byte aligned, its
+ *             stride a multiple of 8. h NULL (then hs too): only x', as after a last block
+ */
+typedef struct {
+    const void *x, *y, *g;
+    void *x_out, *h;
+    float *hs;
+    int64_t x_stride, y_stride, g_stride, x_out_stride, h_stride;
+} kda_block_norm_rows;
+
+/*
+ * Rows of the backward pass, in io_dtype, as above. x_out is what the forward wrote (x itself where it had no y).
+ *   dx1  the gradient of x_out from elsewhere, or NULL: zeros       dh   that of h, or NULL: h was not used
+ *   dx, dy, dg  out; dy and dg NULL exactly where y and g are. dx may be dx1 with the same stride
+ */
+typedef struct {
+    const void *x_out, *dh, *dx1, *y, *g;
+    void *dx, *dy, *dg;
+    int64_t x_out_stride, dh_stride, dx1_stride, y_stride, g_stride, dx_stride, dy_stride, dg_stride;
+} kda_block_norm_grad_rows;
+
+/* Fill *cfg with the defaults. KDA_ERR_INVALID (cfg untouched) for cfg == NULL or unsupported values. */
+kda_status kda_block_norm_config(kda_block_norm_config_t *cfg, int32_t dim, int32_t io_dtype);
+
+/* M in 0 .. 2^31 - 1 (0 is a no-op). Errors: KDA_ERR_INVALID, KDA_ERR_CUDA. */
+kda_status kda_block_norm(const kda_block_norm_config_t *cfg, const kda_block_norm_params *params, int64_t M,
+                          const kda_block_norm_rows *rows, void *stream);
+
+/*
+ * Gradients of kda_block_norm with h in io_dtype (through E4M3's rounding they are those of h before it).
+ *   dpost_w, dscale, dpre_w  device FP32 [dim], 16-byte aligned, sums over the rows, each or NULL; overwritten (zeros
+ *              where M is 0, or the rows they come from are NULL)
+ *   workspace  device scratch of at least kda_block_norm_workspace_bytes(cfg, M) bytes, 16-byte aligned. Calls that
+ *              share one must be ordered, captured graphs that are replayed at the same time need one each. The query
+ *              returns 0 for invalid arguments and does not touch the device.
+ * Sums are FP32; results do not depend on timing. Errors: KDA_ERR_INVALID, KDA_ERR_CUDA.
+ */
+size_t kda_block_norm_workspace_bytes(const kda_block_norm_config_t *cfg, int64_t M);
+kda_status kda_block_norm_backward(const kda_block_norm_config_t *cfg, const kda_block_norm_params *params, int64_t M,
+                                   const kda_block_norm_grad_rows *rows, float *dpost_w, float *dscale, float *dpre_w,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Recurrent-state photos (kimi_k3.c header, the COLI_K3_CKPT and
  * COLI_K3_CKPT_DIR serve options). A store keeps up to `capacity` photos of
  * one sequence slot across a stack of KDA layers (one kda_state per layer),

@@ -1,0 +1,379 @@
+// kda_glr.cu - the gated linear recurrence: token by token (decode), packed sequences (prefill), its gradients, and the
+// host side of its entry points.
+#include <climits>
+#include <cstdarg>
+#include <cstdio>
+
+#include "kda_colsum.cuh"
+#include "kda_glr.cuh"
+#include "kda_launch.cuh"
+
+namespace kda {
+namespace glr {
+namespace {
+
+// One thread, two channels of one row, through n tokens from row t0 on.
+template <typename T, bool G>
+__device__ __forceinline__ void walk(const Args &p, int src, int dst, int c, int64_t t0, int n, float *starts)
+{
+    Chan ch;
+    ch.load(p.A_log, p.a_bias, p.b_bias, c);
+    const T *xp = static_cast<const T *>(p.rows.x) + c, *ap = static_cast<const T *>(p.rows.a) + c;
+    const T *bp = static_cast<const T *>(p.rows.b) + c, *gp = static_cast<const T *>(p.rows.g) + c;
+    T *op = static_cast<T *>(p.rows.out) + c;
+    float2 h = src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
+    for (int i = 0; i < n; ++i) {
+        const int64_t t = t0 + i;
+        if (starts && i % kChunk == 0) *reinterpret_cast<float2 *>(starts + (size_t)(i / kChunk) * p.D + c) = h;
+        float2 e, u;
+        gates(ch, Pair<T>::get(ld_pair(xp + t * p.rows.x_stride)), Pair<T>::get(ld_pair(ap + t * p.rows.a_stride)),
+              Pair<T>::get(ld_pair(bp + t * p.rows.b_stride)), e, u);
+        h = step(h, e, u);
+        float2 o = h;
+        if (G) o = f2_mul(o, silu2(Pair<T>::get(ld_pair(gp + t * p.rows.g_stride))));
+        st_pair(op + t * p.rows.out_stride, o);
+    }
+    *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = h;
+}
+
+template <typename T, bool G>
+__global__ void __launch_bounds__(128) glr_decode_kernel(const __grid_constant__ Args p)
+{
+    const int half = p.D / 2, unit = blockIdx.x * 128 + threadIdx.x;
+    const int row = unit / half, c = 2 * (unit - row * half);
+    if (row >= p.N) return;
+    int src, dst;
+    if (!slots_ok(p, row, src, dst)) {
+        if (c == 0) set_err(p.err);
+        return;
+    }
+    walk<T, G>(p, src, dst, c, (int64_t)row * p.n, p.n, nullptr);
+}
+
+template <typename T, bool G>
+__global__ void __launch_bounds__(32) glr_sequence_kernel(const __grid_constant__ Args p)
+{
+    const int slabs = (p.D + kSlab - 1) / kSlab;
+    const int row = blockIdx.x / slabs, c = (blockIdx.x % slabs) * kSlab + 2 * threadIdx.x;
+    int src, dst, t0, t1;
+    if (!bounds_ok(p.cu, row, p.N, p.total_T, t0, t1) || !slots_ok(p, row, src, dst)) {
+        if (threadIdx.x == 0) set_err(p.err);
+        return;
+    }
+    if (c >= p.D) return;
+    walk<T, G>(p, src, dst, c, t0, t1 - t0, p.starts ? p.starts + first_chunk(t0, row) * p.D : nullptr);
+}
+
+// Gradients. From the last token to the first, with c the gradient of the state after the token:
+//   lam = dh + c,  dx = lam m beta,  db = dx x (1 - beta),  c = alpha lam
+//   d gk = lam alpha (h_before - beta x alpha / m),  d A_log = d gk gk,  da = d gk gk (1 - sigmoid(a + a_bias))
+// The states before the tokens are walked again from those that the forward kept every 16 tokens.
+template <typename T, bool G>
+__global__ void __launch_bounds__(32) glr_backward_kernel(const __grid_constant__ BackArgs p)
+{
+    const int slabs = (p.D + kSlab - 1) / kSlab;
+    const int row = blockIdx.x / slabs, c = (blockIdx.x % slabs) * kSlab + 2 * threadIdx.x;
+    if (c >= p.D) return;
+    float2 sA = f2(0.f), sa = sA, sb = sA;
+    int t0, t1;
+    if (!bounds_ok(p.cu, row, p.N, p.total_T, t0, t1)) {
+        set_err(p.err);
+        t1 = t0 = -1;
+    }
+    if (t0 >= 0) {
+        Chan ch;
+        ch.load(p.A_log, p.a_bias, p.b_bias, c);
+        const T *xp = static_cast<const T *>(p.rows.x) + c, *ap = static_cast<const T *>(p.rows.a) + c;
+        const T *bp = static_cast<const T *>(p.rows.b) + c, *gp = static_cast<const T *>(p.rows.g) + c;
+        const T *dp = static_cast<const T *>(p.rows.dout) + c;
+        const float *st = p.starts + first_chunk(t0, row) * p.D + c;
+        const int n = t1 - t0;
+        float2 lc = p.dS_last ? *reinterpret_cast<const float2 *>(p.dS_last + (size_t)row * p.D + c) : f2(0.f);
+        for (int k = (n + kChunk - 1) / kChunk - 1; k >= 0; --k) {
+            const int len = min(kChunk, n - k * kChunk);
+            float2 hb[kChunk];
+            float2 h = *reinterpret_cast<const float2 *>(st + (size_t)k * p.D);
+            for (int i = 0; i < len; ++i) {
+                const int64_t t = t0 + k * kChunk + i;
+                float2 e, u;
+                gates(ch, Pair<T>::get(ld_pair(xp + t * p.rows.x_stride)), Pair<T>::get(ld_pair(ap + t * p.rows.a_stride)),
+                      Pair<T>::get(ld_pair(bp + t * p.rows.b_stride)), e, u);
+                hb[i] = h;
+                h = step(h, e, u);
+            }
+            for (int i = len - 1; i >= 0; --i) {
+                const int64_t t = t0 + k * kChunk + i;
+                const float2 x = Pair<T>::get(ld_pair(xp + t * p.rows.x_stride));
+                Back bk;
+                bk.gates(ch, x, Pair<T>::get(ld_pair(ap + t * p.rows.a_stride)), Pair<T>::get(ld_pair(bp + t * p.rows.b_stride)));
+                float2 dh = Pair<T>::get(ld_pair(dp + t * p.rows.dout_stride));
+                if (G) {
+                    const float2 g = Pair<T>::get(ld_pair(gp + t * p.rows.g_stride));
+                    const float2 E = neg_exp(g, f2(0.f)), s = rcp2(f2_add(E, f2(1.f)));
+                    const float2 ns = make_float2(fminf(E.x, kHuge) * s.x, fminf(E.y, kHuge) * s.y);  // 1 - s
+                    const float2 after = step(hb[i], bk.e, bk.u);
+                    st_pair(static_cast<T *>(p.rows.dg) + c + t * p.rows.dg_stride, f2_mul(f2_mul(dh, after), f2_mul(s, f2_fma(g, ns, f2(1.f)))));
+                    dh = f2_mul(dh, f2_mul(g, s));
+                }
+                float2 dx, da, db, dA;
+                lc = bk.token(f2_add(dh, lc), x, hb[i], dx, da, db, dA);
+                st_pair(static_cast<T *>(p.rows.dx) + c + t * p.rows.dx_stride, dx);
+                st_pair(static_cast<T *>(p.rows.da) + c + t * p.rows.da_stride, da);
+                st_pair(static_cast<T *>(p.rows.db) + c + t * p.rows.db_stride, db);
+                sA = f2_add(sA, dA);
+                sa = f2_add(sa, da);
+                sb = f2_add(sb, db);
+            }
+        }
+        if (p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = lc;
+    }
+    float *part = p.part + (size_t)row * 3 * p.D + c;
+    *reinterpret_cast<float2 *>(part) = sA;
+    *reinterpret_cast<float2 *>(part + p.D) = sa;
+    *reinterpret_cast<float2 *>(part + 2 * (size_t)p.D) = sb;
+}
+
+__global__ void __launch_bounds__(kSumCols *kSumGroups) glr_param_sums_kernel(const float *part, int rows, int D, float *dA_log, float *da_bias, float *db_bias)
+{
+    __shared__ float sh[kSumGroups][kSumCols];
+    float *out = blockIdx.y == 0 ? dA_log : blockIdx.y == 1 ? da_bias : db_bias;
+    if (!out) return;
+    const float s = column_sum(part + (size_t)blockIdx.y * D, rows, 3 * (int64_t)D, blockIdx.x * kSumCols, D, sh);
+    const int c = blockIdx.x * kSumCols + threadIdx.x;
+    if (threadIdx.y == 0 && c < D) out[c] = s;
+}
+
+// ---------------------------------------------------------------- host side
+thread_local char g_msg[256];
+
+kda_status fail(kda_status s, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+    va_end(ap);
+    return record_error(s, g_msg);
+}
+
+bool cfg_ok(const kda_glr_config_t *c)
+{
+    if (!c) return fail(KDA_ERR_INVALID, "config is NULL"), false;
+    if (c->io_dtype != KDA_F32 && c->io_dtype != KDA_BF16) return fail(KDA_ERR_INVALID, "io_dtype must be KDA_F32 or KDA_BF16"), false;
+    const int unit = c->io_dtype == KDA_BF16 ? 8 : 4;
+    if (c->dim < unit || c->dim % unit || c->dim > KDA_GLR_MAX_DIM)
+        return fail(KDA_ERR_INVALID, "dim must be a positive multiple of %d up to %d (got %d)", unit, KDA_GLR_MAX_DIM, c->dim), false;
+    return true;
+}
+
+bool row_ok(const char *name, const void *ptr, int64_t stride, int64_t T, const kda_glr_config_t *c)
+{
+    const int e = c->io_dtype == KDA_BF16 ? 2 : 4;
+    if (!ptr) return fail(KDA_ERR_INVALID, "%s is NULL", name), false;
+    if (T > 1 && stride < c->dim)
+        return fail(KDA_ERR_INVALID, "%s_stride must be >= %d (got %lld)", name, c->dim, (long long)stride), false;
+    if (stride < 0 || stride > ((int64_t)1 << 38)) return fail(KDA_ERR_INVALID, "%s_stride out of range (%lld)", name, (long long)stride), false;
+    if (reinterpret_cast<uintptr_t>(ptr) % 16) return fail(KDA_ERR_INVALID, "%s must be 16-byte aligned", name), false;
+    if ((stride * e) % 16) return fail(KDA_ERR_INVALID, "%s_stride must be a multiple of %d elements (got %lld)", name, 16 / e, (long long)stride), false;
+    return true;
+}
+
+bool f32_ok(const char *name, const void *ptr)
+{
+    if (!ptr || (reinterpret_cast<uintptr_t>(ptr) & 15u)) return fail(KDA_ERR_INVALID, "%s is NULL or not 16-byte aligned", name), false;
+    return true;
+}
+bool f32_or_null_ok(const char *name, const void *ptr) { return !ptr || f32_ok(name, ptr); }
+
+bool params_ok(const kda_glr_params *p)
+{
+    if (!p) return fail(KDA_ERR_INVALID, "params is NULL"), false;
+    return f32_ok("A_log", p->A_log) && f32_ok("a_bias", p->a_bias) && f32_ok("b_bias", p->b_bias);
+}
+
+bool call_ok(const kda_glr_config_t *c, const kda_glr_params *prm, const float *S, int32_t max_slots, const int32_t *src,
+             const int32_t *dst, const kda_glr_rows *r, int64_t T)
+{
+    if (!params_ok(prm) || !f32_ok("S", S)) return false;
+    if (max_slots < 1) return fail(KDA_ERR_INVALID, "max_slots must be >= 1 (got %d)", max_slots), false;
+    if (!src || !dst) return fail(KDA_ERR_INVALID, "src_slots or dst_slots is NULL"), false;
+    if (!r) return fail(KDA_ERR_INVALID, "rows is NULL"), false;
+    if (T == 0) return true;
+    return row_ok("x", r->x, r->x_stride, T, c) && row_ok("a", r->a, r->a_stride, T, c) && row_ok("b", r->b, r->b_stride, T, c) &&
+           (!r->g || row_ok("g", r->g, r->g_stride, T, c)) && row_ok("out", r->out, r->out_stride, T, c);
+}
+
+Args make_args(const kda_glr_config_t *c, const kda_glr_params *prm, float *S, int32_t max_slots, const int32_t *src, const int32_t *dst,
+               int32_t N, const kda_glr_rows *r, int32_t *err)
+{
+    Args p = {};
+    p.S = S; p.max_slots = max_slots; p.src = src; p.dst = dst; p.err = err; p.N = N; p.D = c->dim;
+    p.A_log = prm->A_log; p.a_bias = prm->a_bias; p.b_bias = prm->b_bias;
+    p.rows = *r;
+    return p;
+}
+
+// Checks the host's cu_seqlens; the longest sequence.
+bool lengths_ok(const int32_t *cu, int32_t N, int32_t *longest)
+{
+    *longest = 0;
+    if (N < 0) return fail(KDA_ERR_INVALID, "N must be >= 0 (got %d)", N), false;
+    if (N == 0) return true;
+    if (!cu) return fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL"), false;
+    if (cu[0] != 0) return fail(KDA_ERR_INVALID, "cu_seqlens[0] must be 0 (got %d)", cu[0]), false;
+    for (int32_t i = 0; i < N; ++i) {
+        if (cu[i + 1] < cu[i]) return fail(KDA_ERR_INVALID, "cu_seqlens decreases at %d", i + 1), false;
+        if (cu[i + 1] - cu[i] > *longest) *longest = cu[i + 1] - cu[i];
+    }
+    return true;
+}
+
+int64_t slabs_of(int32_t D) { return (D + kSlab - 1) / kSlab; }
+
+bool workspace_ok(const void *ws, size_t bytes, size_t need)
+{
+    if (ws && !(reinterpret_cast<uintptr_t>(ws) & 15u) && bytes >= need) return true;
+    return fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed", bytes, need), false;
+}
+
+size_t back_bytes(int32_t D, int32_t N) { return (size_t)N * 3 * D * sizeof(float); }
+
+}  // namespace
+}  // namespace glr
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+kda_status kda_glr_config(kda_glr_config_t *cfg, int32_t dim, int32_t io_dtype)
+{
+    if (!cfg) return glr::fail(KDA_ERR_INVALID, "cfg is NULL");
+    const kda_glr_config_t c = {dim, io_dtype};
+    if (!glr::cfg_ok(&c)) return KDA_ERR_INVALID;
+    *cfg = c;
+    return KDA_OK;
+}
+
+kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *params, float *S, int32_t max_slots, const int32_t *src_slots,
+                          const int32_t *dst_slots, int32_t B, int32_t n, const kda_glr_rows *rows, int32_t *err, void *stream)
+{
+    if (!glr::cfg_ok(cfg)) return KDA_ERR_INVALID;
+    if (B < 0) return glr::fail(KDA_ERR_INVALID, "B must be >= 0 (got %d)", B);
+    if (n < 1 || n > KDA_DECODE_MAX_TOKENS) return glr::fail(KDA_ERR_INVALID, "n must be in 1 .. %d (got %d)", KDA_DECODE_MAX_TOKENS, n);
+    if (B == 0) return KDA_OK;
+    if (!glr::call_ok(cfg, params, S, max_slots, src_slots, dst_slots, rows, (int64_t)B * n)) return KDA_ERR_INVALID;
+    glr::Args p = glr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, B, rows, err);
+    p.n = n;
+    p.total_T = (int64_t)B * n;
+    if ((int64_t)B * (cfg->dim / 2) > INT_MAX - 128) return glr::fail(KDA_ERR_INVALID, "B * dim is too large");
+    const int64_t blocks = ((int64_t)B * (cfg->dim / 2) + 127) / 128;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f32 = cfg->io_dtype == KDA_F32;
+    if (rows->g) {
+        if (f32) glr::glr_decode_kernel<float, true><<<(unsigned)blocks, 128, 0, s>>>(p);
+        else glr::glr_decode_kernel<__nv_bfloat16, true><<<(unsigned)blocks, 128, 0, s>>>(p);
+    } else {
+        if (f32) glr::glr_decode_kernel<float, false><<<(unsigned)blocks, 128, 0, s>>>(p);
+        else glr::glr_decode_kernel<__nv_bfloat16, false><<<(unsigned)blocks, 128, 0, s>>>(p);
+    }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_decode: %s", cudaGetErrorString(e));
+}
+
+size_t kda_glr_workspace_bytes(const kda_glr_config_t *cfg, const int32_t *cu_seqlens_host, int32_t N)
+{
+    int32_t longest;
+    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N, &longest)) return 0;
+    return 256 + glr::back_bytes(cfg->dim, N);
+}
+
+int64_t kda_glr_chunks(const int32_t *cu_seqlens_host, int32_t N)
+{
+    int32_t longest;
+    if (!glr::lengths_ok(cu_seqlens_host, N, &longest)) return -1;
+    return N == 0 ? 0 : (int64_t)(cu_seqlens_host[N] / glr::kChunk) + N;
+}
+
+kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *params, float *S, int32_t max_slots, const int32_t *src_slots,
+                           const int32_t *dst_slots, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int32_t N,
+                           const kda_glr_rows *rows, float *starts, void *workspace, size_t workspace_bytes, int32_t *err, void *stream)
+{
+    int32_t longest;
+    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N, &longest)) return KDA_ERR_INVALID;
+    if (N == 0) return KDA_OK;
+    if (!cu_seqlens) return glr::fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL");
+    const int64_t T = cu_seqlens_host[N];
+    if (!glr::call_ok(cfg, params, S, max_slots, src_slots, dst_slots, rows, T) || !glr::f32_or_null_ok("starts", starts)) return KDA_ERR_INVALID;
+    if (N * glr::slabs_of(cfg->dim) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
+    if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(cfg->dim, N))) return KDA_ERR_INVALID;
+    glr::Args p = glr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, N, rows, err);
+    p.cu = cu_seqlens;
+    p.total_T = T;
+    p.starts = starts;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)(N * glr::slabs_of(cfg->dim));
+    const bool f32 = cfg->io_dtype == KDA_F32;
+    if (rows->g) {
+        if (f32) glr::glr_sequence_kernel<float, true><<<grid, 32, 0, s>>>(p);
+        else glr::glr_sequence_kernel<__nv_bfloat16, true><<<grid, 32, 0, s>>>(p);
+    } else {
+        if (f32) glr::glr_sequence_kernel<float, false><<<grid, 32, 0, s>>>(p);
+        else glr::glr_sequence_kernel<__nv_bfloat16, false><<<grid, 32, 0, s>>>(p);
+    }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_prefill: %s", cudaGetErrorString(e));
+}
+
+kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *params, const int32_t *cu_seqlens,
+                            const int32_t *cu_seqlens_host, int32_t N, const float *starts, const kda_glr_grad_rows *rows,
+                            const float *dS_last, float *dS_first, float *dA_log, float *da_bias, float *db_bias, void *workspace,
+                            size_t workspace_bytes, int32_t *err, void *stream)
+{
+    int32_t longest;
+    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N, &longest)) return KDA_ERR_INVALID;
+    if (!glr::f32_or_null_ok("dA_log", dA_log) || !glr::f32_or_null_ok("da_bias", da_bias) || !glr::f32_or_null_ok("db_bias", db_bias)) return KDA_ERR_INVALID;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int32_t D = cfg->dim;
+    cudaError_t e = cudaSuccess;
+    if (N > 0) {
+        if (!cu_seqlens) return glr::fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL");
+        if (!rows) return glr::fail(KDA_ERR_INVALID, "rows is NULL");
+        if (!glr::params_ok(params) || !glr::f32_ok("starts", starts) || !glr::f32_or_null_ok("dS_last", dS_last) ||
+            !glr::f32_or_null_ok("dS_first", dS_first)) return KDA_ERR_INVALID;
+        const int64_t T = cu_seqlens_host[N];
+        const kda_glr_grad_rows *r = rows;
+        if (T > 0) {
+            if (!glr::row_ok("x", r->x, r->x_stride, T, cfg) || !glr::row_ok("a", r->a, r->a_stride, T, cfg) ||
+                !glr::row_ok("b", r->b, r->b_stride, T, cfg) || !glr::row_ok("dout", r->dout, r->dout_stride, T, cfg) ||
+                !glr::row_ok("dx", r->dx, r->dx_stride, T, cfg) || !glr::row_ok("da", r->da, r->da_stride, T, cfg) ||
+                !glr::row_ok("db", r->db, r->db_stride, T, cfg)) return KDA_ERR_INVALID;
+            if (!r->g != !r->dg) return glr::fail(KDA_ERR_INVALID, "g and dg must both be given or both be NULL");
+            if (r->g && (!glr::row_ok("g", r->g, r->g_stride, T, cfg) || !glr::row_ok("dg", r->dg, r->dg_stride, T, cfg))) return KDA_ERR_INVALID;
+        }
+        if (N * glr::slabs_of(D) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
+        if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(D, N))) return KDA_ERR_INVALID;
+        glr::BackArgs p = {};
+        p.err = err; p.cu = cu_seqlens; p.N = N; p.total_T = T; p.D = D;
+        p.A_log = params->A_log; p.a_bias = params->a_bias; p.b_bias = params->b_bias;
+        p.starts = starts; p.rows = *rows; p.dS_last = dS_last; p.dS_first = dS_first;
+        p.part = static_cast<float *>(workspace);
+        const unsigned grid = (unsigned)(N * glr::slabs_of(D));
+        const bool f32 = cfg->io_dtype == KDA_F32;
+        if (rows->g) {
+            if (f32) glr::glr_backward_kernel<float, true><<<grid, 32, 0, s>>>(p);
+            else glr::glr_backward_kernel<__nv_bfloat16, true><<<grid, 32, 0, s>>>(p);
+        } else {
+            if (f32) glr::glr_backward_kernel<float, false><<<grid, 32, 0, s>>>(p);
+            else glr::glr_backward_kernel<__nv_bfloat16, false><<<grid, 32, 0, s>>>(p);
+        }
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && (dA_log || da_bias || db_bias)) {  // without sequences: zeros
+        glr::glr_param_sums_kernel<<<dim3((D + kSumCols - 1) / kSumCols, 3), dim3(kSumCols, kSumGroups), 0, s>>>(
+            static_cast<const float *>(workspace), N, D, dA_log, da_bias, db_bias);
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_backward: %s", cudaGetErrorString(e));
+}
+
+}  // extern "C"

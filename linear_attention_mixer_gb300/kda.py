@@ -63,6 +63,47 @@ class kda_gdr_rows(ctypes.Structure):
         [(n + "_stride", ctypes.c_int64) for n in ("q", "k", "v", "a", "b", "out")]
 
 
+class kda_glr_config_t(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+
+
+class kda_glr_params(ctypes.Structure):
+    _fields_ = [("A_log", ctypes.c_void_p), ("a_bias", ctypes.c_void_p), ("b_bias", ctypes.c_void_p)]
+    dim, device = 0, None  # set by kda_glr_params_from; without them a call refuses the parameters
+
+
+_GLR_ROWS, _GLR_GRADS = ("x", "a", "b", "g", "out"), ("x", "a", "b", "g", "dout", "dx", "da", "db", "dg")
+
+
+class kda_glr_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _GLR_ROWS] + [(n + "_stride", ctypes.c_int64) for n in _GLR_ROWS]
+
+
+class kda_glr_grad_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _GLR_GRADS] + [(n + "_stride", ctypes.c_int64) for n in _GLR_GRADS]
+
+
+class kda_block_norm_config_t(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class kda_block_norm_params(ctypes.Structure):
+    _fields_ = [("post_w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("pre_w", ctypes.c_void_p)]
+    dim, device = 0, None  # set by kda_block_norm_params_from; without them a call refuses the parameters
+
+
+class kda_block_norm_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "y", "g", "x_out", "h", "hs")] + \
+        [(n + "_stride", ctypes.c_int64) for n in ("x", "y", "g", "x_out", "h")]
+
+
+_NORM_GRADS = ("x_out", "dh", "dx1", "y", "g", "dx", "dy", "dg")
+
+
+class kda_block_norm_grad_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _NORM_GRADS] + [(n + "_stride", ctypes.c_int64) for n in _NORM_GRADS]
+
+
 class kda_blob_header(ctypes.Structure):
     _fields_ = [("magic", ctypes.c_uint32), ("version", ctypes.c_uint32),
                 ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
@@ -114,6 +155,21 @@ SIGNATURES = [
     ("kda_gdr_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(kda_gdr_config_t), _PI32, _I32]),
     ("kda_gdr_prefill", _I32, [ctypes.POINTER(kda_gdr_config_t), ctypes.POINTER(kda_gdr_params), _VP, _I32, _VP, _VP,
                                _VP, _VP, _I32, ctypes.POINTER(kda_gdr_rows), _VP, ctypes.c_size_t, _VP, _VP]),
+    ("kda_glr_config", _I32, [ctypes.POINTER(kda_glr_config_t), _I32, _I32]),
+    ("kda_glr_decode", _I32, [ctypes.POINTER(kda_glr_config_t), ctypes.POINTER(kda_glr_params), _VP, _I32, _VP, _VP, _I32, _I32,
+                              ctypes.POINTER(kda_glr_rows), _VP, _VP]),
+    ("kda_glr_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(kda_glr_config_t), _PI32, _I32]),
+    ("kda_glr_chunks", ctypes.c_int64, [_PI32, _I32]),
+    ("kda_glr_prefill", _I32, [ctypes.POINTER(kda_glr_config_t), ctypes.POINTER(kda_glr_params), _VP, _I32, _VP, _VP, _VP, _VP, _I32,
+                               ctypes.POINTER(kda_glr_rows), _VP, _VP, ctypes.c_size_t, _VP, _VP]),
+    ("kda_glr_backward", _I32, [ctypes.POINTER(kda_glr_config_t), ctypes.POINTER(kda_glr_params), _VP, _VP, _I32, _VP,
+                                ctypes.POINTER(kda_glr_grad_rows), _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP]),
+    ("kda_block_norm_config", _I32, [ctypes.POINTER(kda_block_norm_config_t), _I32, _I32]),
+    ("kda_block_norm", _I32, [ctypes.POINTER(kda_block_norm_config_t), ctypes.POINTER(kda_block_norm_params), ctypes.c_int64,
+                              ctypes.POINTER(kda_block_norm_rows), _VP]),
+    ("kda_block_norm_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(kda_block_norm_config_t), ctypes.c_int64]),
+    ("kda_block_norm_backward", _I32, [ctypes.POINTER(kda_block_norm_config_t), ctypes.POINTER(kda_block_norm_params), ctypes.c_int64,
+                                       ctypes.POINTER(kda_block_norm_grad_rows), _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     ("kda_photo_store_create", _I32, [_I32, ctypes.c_char_p, ctypes.POINTER(_VP)]),
     ("kda_photo_store_free", _I32, [_VP]),
     ("kda_photo_count", _I32, [_VP]),
@@ -596,6 +652,214 @@ def kda_gdr_prefill(cfg: kda_gdr_config_t, params: kda_gdr_params, S: torch.Tens
     st = lib().kda_gdr_prefill(cfg, params, Sp, S.shape[0], sp, dp, _ptr("cu_seqlens", cu_seqlens, _I32T, dev, (N + 1,)),
                                cu_h.ctypes.data, N, r, _ptr("workspace", workspace, None, dev), workspace.nbytes, ep,
                                _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def kda_glr_config(dim: int, io_dtype: int = KDA_BF16) -> kda_glr_config_t:
+    cfg = kda_glr_config_t()
+    _check(lib().kda_glr_config(ctypes.byref(cfg), dim, io_dtype))
+    return cfg
+
+
+def _vectors(p, device, **tensors) -> None:
+    """Keep a layer's FP32 vectors, all of one length and on one device, in its parameters p."""
+    shape = next(iter(tensors.values())).shape
+    for name, t in tensors.items():
+        if t.dim() != 1 or t.shape != shape or t.device != device:
+            raise ValueError(f"{' and '.join(tensors)} must be vectors of one length on one device")
+        setattr(p, name, _dev(t, torch.float32, name))
+    p._keep = tuple(tensors.values())
+    p.dim, p.device = shape[0], device.index
+
+
+def kda_glr_params_from(A_log: torch.Tensor, a_bias: torch.Tensor, b_bias: torch.Tensor) -> kda_glr_params:
+    p = kda_glr_params()
+    _vectors(p, A_log.device, A_log=A_log, a_bias=a_bias, b_bias=b_bias)
+    return p
+
+
+def _row_args(struct, names, tensors, T, width, dt, dev):
+    """The checked row struct: [T, width] tensors of dt on device dev, contiguous within a token (None: not given)."""
+    shape = (T, width)
+    ptrs, strides = [], []
+    for name, t in zip(names, tensors):
+        if t is None:
+            ptrs.append(None)
+            strides.append(0)
+            continue
+        if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.get_device() == dev and (T == 0 or t.stride(1) == 1)):
+            _check_row(name, t, T, width, dt, dev)
+        ptrs.append(t.data_ptr())
+        strides.append(t.stride(0) if T > 1 else width)
+    return struct(*ptrs, *strides)
+
+
+def _f32(name, t, dev, shape):
+    return None if t is None else _ptr(name, t, _F32, dev, shape)
+
+
+def _glr_params_ok(cfg, params, dev) -> None:
+    if params.dim != cfg.dim or params.device != dev:
+        raise ValueError(f"the parameters must hold {cfg.dim} elements on cuda:{dev}, got {params.dim} on cuda:{params.device}")
+
+
+def _glr_call(cfg, params, S, src_slots, dst_slots, T, rows, err, dev):
+    """The checked pointers of a call over T tokens: S, src, dst, rows, err."""
+    _glr_params_ok(cfg, params, dev)
+    if S.dim() != 2 or S.shape[1] != cfg.dim:
+        raise ValueError(f"S must be [max_slots, {cfg.dim}], got {list(S.shape)}")
+    if src_slots.numel() != dst_slots.numel():
+        raise ValueError("src_slots and dst_slots must have the same length")
+    r = _row_args(kda_glr_rows, _GLR_ROWS, rows, T, cfg.dim, _BF16 if cfg.io_dtype == KDA_BF16 else _F32, dev)
+    return (_ptr("S", S, _F32, dev), _ptr("src_slots", src_slots, _I32T, dev), _ptr("dst_slots", dst_slots, _I32T, dev), r,
+            None if err is None else _ptr("err", err, _I32T, dev))
+
+
+def kda_glr_decode(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor,
+                   n: int, x, a, b, g, out, err=None, stream=None) -> None:
+    """n tokens for each row: x, a, b, g (or None), out [B n, dim], contiguous within a token; S FP32 [max_slots, dim],
+    read at src_slots (-1: zeros) and written at dst_slots."""
+    dev = _current_device()
+    B = src_slots.numel()
+    Sp, sp, dp, r, ep = _glr_call(cfg, params, S, src_slots, dst_slots, B * n, (x, a, b, g, out), err, dev)
+    st = lib().kda_glr_decode(cfg, params, Sp, S.shape[0], sp, dp, B, n, r, ep, _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def kda_glr_workspace_bytes(cfg: kda_glr_config_t, cu_seqlens_host) -> int:
+    cu_h, cu_p = _host_i32(cu_seqlens_host)
+    need = int(lib().kda_glr_workspace_bytes(ctypes.byref(cfg), cu_p, len(cu_h) - 1))
+    if need == 0:
+        raise KdaError(KDA_ERR_INVALID, kda_last_error())
+    return need
+
+
+def kda_glr_chunks(cu_seqlens_host) -> int:
+    """Rows of the `starts` that a kda_glr_prefill of these sequences fills for its backward."""
+    cu_h, cu_p = _host_i32(cu_seqlens_host)
+    n = int(lib().kda_glr_chunks(cu_p, len(cu_h) - 1))
+    if n < 0:
+        raise KdaError(KDA_ERR_INVALID, kda_last_error())
+    return n
+
+
+def _glr_lengths(cu_seqlens_host, N):
+    cu_h = _i32_array(cu_seqlens_host)
+    if cu_h.shape != (N + 1,):
+        raise ValueError("cu_seqlens_host must hold N + 1 entries")
+    return cu_h
+
+
+def _glr_starts(cfg, starts, cu_h, dev):
+    """The address of starts, of as many rows as the sequences' chunks or more."""
+    n = kda_glr_chunks(cu_h)
+    if starts.dim() != 2 or starts.shape[0] < n or starts.shape[1] != cfg.dim:
+        raise ValueError(f"starts must be [{n}, {cfg.dim}] or longer, got {list(starts.shape)}")
+    return _ptr("starts", starts, _F32, dev)
+
+
+def kda_glr_prefill(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor,
+                    cu_seqlens: torch.Tensor, cu_seqlens_host, x, a, b, g, out, workspace: torch.Tensor, starts=None, err=None,
+                    stream=None) -> None:
+    """Packed sequences, rows as in kda_glr_decode with T = cu_seqlens[-1]; workspace of at least
+    kda_glr_workspace_bytes(cfg, cu_seqlens_host) bytes; starts FP32 [kda_glr_chunks(cu_seqlens_host), dim] for a backward."""
+    dev = _current_device()
+    N = src_slots.numel()
+    cu_h = _glr_lengths(cu_seqlens_host, N)
+    Sp, sp, dp, r, ep = _glr_call(cfg, params, S, src_slots, dst_slots, int(cu_h[N]), (x, a, b, g, out), err, dev)
+    st = lib().kda_glr_prefill(cfg, params, Sp, S.shape[0], sp, dp, _ptr("cu_seqlens", cu_seqlens, _I32T, dev, (N + 1,)),
+                               cu_h.ctypes.data, N, r, None if starts is None else _glr_starts(cfg, starts, cu_h, dev),
+                               _ptr("workspace", workspace, None, dev), workspace.nbytes, ep, _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def kda_glr_backward(cfg: kda_glr_config_t, params: kda_glr_params, cu_seqlens: torch.Tensor, cu_seqlens_host, starts: torch.Tensor,
+                     x, a, b, g, dout, dx, da, db, dg, work: torch.Tensor, dS_last=None, dS_first=None, dA_log=None, da_bias=None,
+                     db_bias=None, err=None, stream=None) -> None:
+    """The gradients of a kda_glr_prefill that filled `starts`: rows [T, dim] (dg None where g is), dS_last (None: zeros)
+    and dS_first [N, dim], and FP32 sums over all tokens, dA_log, da_bias, db_bias [dim]; work as the prefill's workspace."""
+    dev = _current_device()
+    N = cu_seqlens.numel() - 1
+    cu_h = _glr_lengths(cu_seqlens_host, N)
+    _glr_params_ok(cfg, params, dev)
+    r = _row_args(kda_glr_grad_rows, _GLR_GRADS, (x, a, b, g, dout, dx, da, db, dg), int(cu_h[N]), cfg.dim,
+                  _BF16 if cfg.io_dtype == KDA_BF16 else _F32, dev)
+    vec, state = (cfg.dim,), (N, cfg.dim)
+    st = lib().kda_glr_backward(cfg, params, _ptr("cu_seqlens", cu_seqlens, _I32T, dev, (N + 1,)), cu_h.ctypes.data, N,
+                                _glr_starts(cfg, starts, cu_h, dev), r, _f32("dS_last", dS_last, dev, state),
+                                _f32("dS_first", dS_first, dev, state), _f32("dA_log", dA_log, dev, vec),
+                                _f32("da_bias", da_bias, dev, vec), _f32("db_bias", db_bias, dev, vec),
+                                _ptr("work", work, None, dev), work.nbytes, None if err is None else _ptr("err", err, _I32T, dev),
+                                _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def kda_block_norm_config(dim: int, io_dtype: int = KDA_BF16) -> kda_block_norm_config_t:
+    cfg = kda_block_norm_config_t()
+    _check(lib().kda_block_norm_config(ctypes.byref(cfg), dim, io_dtype))
+    return cfg
+
+
+def kda_block_norm_params_from(post_w: torch.Tensor, scale: torch.Tensor, pre_w: torch.Tensor) -> kda_block_norm_params:
+    p = kda_block_norm_params()
+    _vectors(p, post_w.device, post_w=post_w, scale=scale, pre_w=pre_w)
+    return p
+
+
+def _norm_params_ok(cfg, params, dev) -> None:
+    if params.dim != cfg.dim or params.device != dev:
+        raise ValueError(f"the parameters must hold {cfg.dim} elements on cuda:{dev}, got {params.dim} on cuda:{params.device}")
+
+
+def kda_block_norm(cfg: kda_block_norm_config_t, params: kda_block_norm_params, x, y=None, g=None, x_out=None, h=None, hs=None,
+                   stream=None) -> None:
+    """x_out = x + scale sigmoid(g) post_w y / rms(y) and h = pre_w x_out / rms(x_out) for rows [M, dim], contiguous within
+    a row; without y only h of x, without h only x_out. h in the rows' type, or float8_e4m3fn with hs FP32 [M, ceil(dim / 128)]."""
+    dev = _current_device()
+    _norm_params_ok(cfg, params, dev)
+    M, D = x.shape[0], cfg.dim
+    dt = _BF16 if cfg.io_dtype == KDA_BF16 else _F32
+    ptrs, strides = [], []
+    for name, t in (("x", x), ("y", y), ("g", g), ("x_out", x_out), ("h", h)):
+        if t is None:
+            ptrs.append(None)
+            strides.append(0)
+            continue
+        want = _F8 if name == "h" and hs is not None else dt
+        if not (isinstance(t, torch.Tensor) and t.dtype is want and t.shape == (M, D) and t.get_device() == dev and (M == 0 or t.stride(1) == 1)):
+            _check_row(name, t, M, D, want, dev)
+        ptrs.append(t.data_ptr())
+        strides.append(t.stride(0) if M > 1 else D)
+    r = kda_block_norm_rows(*ptrs, _f32("hs", hs, dev, (M, -(-D // 128))), *strides)
+    st = lib().kda_block_norm(cfg, params, M, r, _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def kda_block_norm_workspace_bytes(cfg: kda_block_norm_config_t, M: int) -> int:
+    need = int(lib().kda_block_norm_workspace_bytes(ctypes.byref(cfg), int(M)))
+    if need == 0:
+        raise KdaError(KDA_ERR_INVALID, kda_last_error())
+    return need
+
+
+def kda_block_norm_backward(cfg: kda_block_norm_config_t, params: kda_block_norm_params, x_out, dh, dx1, dx, work: torch.Tensor, y=None,
+                            g=None, dy=None, dg=None, dpost_w=None, dscale=None, dpre_w=None, stream=None) -> None:
+    """Gradients of kda_block_norm from its x_out (x where it had no y), the gradient dh of h (None: not used) and that of
+    x_out from elsewhere, dx1 (None: zeros): rows dx, dy, dg [M, dim] and sums over the rows dpost_w, dscale, dpre_w FP32
+    [dim], each or None; work of at least kda_block_norm_workspace_bytes(cfg, M) bytes."""
+    dev = _current_device()
+    _norm_params_ok(cfg, params, dev)
+    r = _row_args(kda_block_norm_grad_rows, _NORM_GRADS, (x_out, dh, dx1, y, g, dx, dy, dg), dx.shape[0], cfg.dim,
+                  _BF16 if cfg.io_dtype == KDA_BF16 else _F32, dev)
+    vec = (cfg.dim,)
+    st = lib().kda_block_norm_backward(cfg, params, dx.shape[0], r, _f32("dpost_w", dpost_w, dev, vec), _f32("dscale", dscale, dev, vec),
+                                       _f32("dpre_w", dpre_w, dev, vec), _ptr("work", work, None, dev), work.nbytes,
+                                       _raw_stream(stream, dev))
     if st:
         _check(st)
 
