@@ -1,11 +1,12 @@
-// kda_glr.cu - the gated linear recurrence: token by token (decode), packed sequences (prefill), its gradients, and the
-// host side of its entry points.
+// kda_glr.cu - the gated linear recurrence: token by token (decode), its gradients, and the host side of its
+// entry points.
 #include <climits>
 #include <cstdarg>
 #include <cstdio>
 
 #include "kda_colsum.cuh"
 #include "kda_glr.cuh"
+#include "kda_glr_scan.cuh"
 #include "kda_launch.cuh"
 
 namespace kda {
@@ -14,7 +15,7 @@ namespace {
 
 // One thread, two channels of one row, through n tokens from row t0 on.
 template <typename T, bool G>
-__device__ __forceinline__ void walk(const Args &p, int src, int dst, int c, int64_t t0, int n, float *starts)
+__device__ __forceinline__ void walk(const Args &p, int src, int dst, int c, int64_t t0, int n)
 {
     Chan ch;
     ch.load(p.A_log, p.a_bias, p.b_bias, c);
@@ -24,7 +25,6 @@ __device__ __forceinline__ void walk(const Args &p, int src, int dst, int c, int
     float2 h = src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
     for (int i = 0; i < n; ++i) {
         const int64_t t = t0 + i;
-        if (starts && i % kChunk == 0) *reinterpret_cast<float2 *>(starts + (size_t)(i / kChunk) * p.D + c) = h;
         float2 e, u;
         gates(ch, Pair<T>::get(ld_pair(xp + t * p.rows.x_stride)), Pair<T>::get(ld_pair(ap + t * p.rows.a_stride)),
               Pair<T>::get(ld_pair(bp + t * p.rows.b_stride)), e, u);
@@ -47,21 +47,7 @@ __global__ void __launch_bounds__(128) glr_decode_kernel(const __grid_constant__
         if (c == 0) set_err(p.err);
         return;
     }
-    walk<T, G>(p, src, dst, c, (int64_t)row * p.n, p.n, nullptr);
-}
-
-template <typename T, bool G>
-__global__ void __launch_bounds__(32) glr_sequence_kernel(const __grid_constant__ Args p)
-{
-    const int slabs = (p.D + kSlab - 1) / kSlab;
-    const int row = blockIdx.x / slabs, c = (blockIdx.x % slabs) * kSlab + 2 * threadIdx.x;
-    int src, dst, t0, t1;
-    if (!bounds_ok(p.cu, row, p.N, p.total_T, t0, t1) || !slots_ok(p, row, src, dst)) {
-        if (threadIdx.x == 0) set_err(p.err);
-        return;
-    }
-    if (c >= p.D) return;
-    walk<T, G>(p, src, dst, c, t0, t1 - t0, p.starts ? p.starts + first_chunk(t0, row) * p.D : nullptr);
+    walk<T, G>(p, src, dst, c, (int64_t)row * p.n, p.n);
 }
 
 // Gradients. From the last token to the first, with c the gradient of the state after the token:
@@ -311,16 +297,12 @@ kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *pa
     p.total_T = T;
     p.starts = starts;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)(N * glr::slabs_of(cfg->dim));
-    const bool f32 = cfg->io_dtype == KDA_F32;
-    if (rows->g) {
-        if (f32) glr::glr_sequence_kernel<float, true><<<grid, 32, 0, s>>>(p);
-        else glr::glr_sequence_kernel<__nv_bfloat16, true><<<grid, 32, 0, s>>>(p);
-    } else {
-        if (f32) glr::glr_sequence_kernel<float, false><<<grid, 32, 0, s>>>(p);
-        else glr::glr_sequence_kernel<__nv_bfloat16, false><<<grid, 32, 0, s>>>(p);
+    int dev = 0, sms = 0;
+    cudaError_t e = current_sms(&dev, &sms);
+    if (e == cudaSuccess) {
+        const int nc = glr::choose_cluster(cu_seqlens_host, N, glr::slabs_of(cfg->dim), glr::kScanTile, glr::kMaxCluster, 16 / glr::kScanWarps * sms);
+        e = glr::launch_scan(p, cfg->io_dtype == KDA_F32, nc, dev, s);
     }
-    const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_prefill: %s", cudaGetErrorString(e));
 }
 

@@ -111,7 +111,7 @@ __device__ __forceinline__ float max_nan(float a, float b)  // NaN if either is
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // exp(x) - 1 for x <= 0 with a relative error of about 2^-24, also near 0: x = k ln 2 + r, |r| <= ln 2 / 2, is
 // 2^k (exp(r) - 1) + (2^k - 1), and exp(r) - 1 = r q(r) with q of degree 5 (Chebyshev interpolation of (exp(r) - 1) / r on
@@ -119,11 +119,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // that of -87, -1 in FP32. NaN stays.
 __device__ __forceinline__ float2 expm1_neg(float2 x)
 {
-    constexpr float kRound = 12582912.f;  // 1.5 x 2^23: adding it rounds to a whole number, in the low bits
     x = make_float2(max_nan(x.x, -87.f), max_nan(x.y, -87.f));
-    const float2 t = f2_fma(x, f2(kLog2e), f2(kRound));
-    const float2 k = f2_add(t, f2(-kRound));
-    const float2 r = f2_fma(k, f2(-kLn2), x);
+    const float2 t = f2_fma(x, f2(kLog2e), f2(12582912.f));  // adding 1.5 x 2^23 rounds to a whole number, in the low bits
+    const float2 k = f2_add(t, f2(-12582912.f));
+    const float2 r = f2_fma(k, f2(-0.6931471805599453f), x);
     float2 q = f2_fma(f2(0.0013933685841038823f), r, f2(0.008369184099137783f));
     q = f2_fma(q, r, f2(0.041666463017463684f));
     q = f2_fma(q, r, f2(0.16666504740715027f));

@@ -1,0 +1,256 @@
+// kda_glr_scan.cu - the gated linear recurrence over packed sequences: prefill and backward, by a scan along the tokens.
+//
+// A step h -> (1 + e) h + u is linear, so 16 of them are h -> A h + H with A the product of the (1 + e) and H what becomes
+// of h = 0, and such pairs join as (A2 A1, A2 H1 + H2). A warp has 16 tokens of 64 channels (two channels a lane), a block
+// of W warps 16 W tokens, a cluster of nc blocks a window of 16 W nc tokens, and it goes through its sequence window by
+// window. For each: every warp works out its tokens' e and u, once, and its pair; the warps' pairs are joined through
+// shared memory, the blocks' through distributed shared memory, in the tokens' order (so results do not depend on timing);
+// then each warp walks its tokens from the state that it now knows, with e and u still in registers. The rows are read
+// once. No block waits for one of another cluster.
+#include "kda_glr_scan.cuh"
+
+namespace kda {
+namespace glr {
+namespace {
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// the float4 at `mine` (shared memory) in block `rank` of the cluster
+__device__ __forceinline__ void st_remote(const float4 *mine, uint32_t rank, float4 v)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// ---------------------------------------------------------------- pairs
+struct Lin {  // h -> A h + H
+    float2 A, H;
+    __device__ __forceinline__ float2 at(float2 h) const { return f2_fma(A, h, H); }
+    __device__ __forceinline__ void then(const Lin &n)  // first this, then n
+    {
+        H = f2_fma(n.A, H, n.H);
+        A = f2_mul(A, n.A);
+    }
+};
+__device__ __forceinline__ Lin lin_identity() { return Lin{f2(1.f), f2(0.f)}; }
+__device__ __forceinline__ Lin ld_lin(const float4 *p)
+{
+    const float4 v = *p;
+    return Lin{make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+__device__ __forceinline__ float4 as_float4(const Lin &l) { return make_float4(l.A.x, l.A.y, l.H.x, l.H.y); }
+
+// The places through which pairs are joined, for two windows in turn: what a window writes is read before the next but one
+// window's barriers are passed.
+template <int W>
+struct Exchange {
+    float4 warp[2][W][32];
+    float4 block[2][kMaxCluster][32];
+};
+
+// From a warp's own pair, what comes before its tokens in the window (back: behind them), applied to `carry`, the state at
+// the window's start; carry becomes that at its end. `turn`: windows so far. All threads of the cluster take part.
+template <int W, bool BACK>
+__device__ __forceinline__ float2 join(Exchange<W> &ex, const Lin &own, float2 &carry, int turn, int nc, int rank, bool first)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, par = turn & 1;
+    ex.warp[par][warp][lane] = as_float4(own);
+    __syncthreads();
+    Lin run = lin_identity(), pre = run;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int w = BACK ? W - 1 - i : i;
+        if (w == warp) pre = run;
+        run.then(ld_lin(&ex.warp[par][w][lane]));
+    }
+    if (nc == 1) {
+        const float2 h = pre.at(carry);
+        carry = run.at(carry);
+        return h;
+    }
+    if (first) cluster_wait();  // every block of the cluster runs: theirs is the arrival at the kernel's start
+    for (int r = warp; r < nc; r += W) st_remote(&ex.block[par][rank][lane], r, as_float4(run));
+    cluster_arrive();
+    cluster_wait();
+    float2 h = carry, mine = carry;
+    for (int i = 0; i < nc; ++i) {
+        const int r = BACK ? nc - 1 - i : i;
+        if (r == rank) mine = h;
+        h = ld_lin(&ex.block[par][r][lane]).at(h);
+    }
+    carry = h;
+    return pre.at(mine);
+}
+
+// ---------------------------------------------------------------- rows in shared memory
+// p += n, not turned into a multiple of n that is kept in registers for every row
+template <typename T> __device__ __forceinline__ void advance(T *&p, int64_t n)
+{
+    p += n;
+    asm volatile("" : "+l"(p));
+}
+// Copies of 16 rows of 64 channels, asked for by 16-byte units; what lies past the sequence or past the row's end is 0.
+template <typename T>
+struct Tile {
+    static constexpr int kUnits = kSlab * (int)sizeof(T) / 16;  // of a row
+    static constexpr int kRowsAt = 32 / kUnits;                 // rows that a warp asks for at once
+    static constexpr int kBytes = kChunk * kSlab * (int)sizeof(T);
+
+    // row0: the first row's place in the slab, of nv rows that exist
+    static __device__ __forceinline__ void fetch(unsigned char *to, const T *row0, int64_t stride, int nv, bool col_ok)
+    {
+        const int lane = threadIdx.x & 31, r0 = lane / kUnits;
+        const T *at = row0 + r0 * stride + (16 / (int)sizeof(T)) * (lane % kUnits);
+#pragma unroll
+        for (int i = 0; i < kChunk / kRowsAt; ++i, advance(at, kRowsAt * stride)) {
+            const bool ok = col_ok && r0 + i * kRowsAt < nv;
+            cp_async16(to + (size_t)(lane + 32 * i) * 16, ok ? at : row0, ok ? 16 : 0);
+        }
+    }
+    static __device__ __forceinline__ float2 get(const unsigned char *tile, int r)
+    {
+        return Pair<T>::get(reinterpret_cast<const typename Pair<T>::Raw *>(tile)[r * (kSlab / 2) + (threadIdx.x & 31)]);
+    }
+};
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// e and u of a warp's 16 tokens. One reciprocal serves both sigmoids: with P = (1 + exp(-a')) (1 + exp(-b')) sigmoid(a') is
+// (1 + exp(-b')) / P. Where P is not below 2^126 (a gate closed by more than about 40, or a NaN) they are taken apart.
+template <typename T>
+__device__ __forceinline__ void all_gates(const Chan &ch, const unsigned char *x, const unsigned char *a, const unsigned char *b,
+                                          float2 (&e)[kChunk], float2 (&u)[kChunk])
+{
+    float most = 0.f;
+#pragma unroll
+    for (int t = 0; t < kChunk; ++t) {
+        const float2 pa = f2_add(neg_exp(Tile<T>::get(a, t), ch.ca), f2(1.f)), pb = f2_add(neg_exp(Tile<T>::get(b, t), ch.cb), f2(1.f));
+        const float2 P = f2_mul(pa, pb), r = rcp2(P);
+        most = max_nan(most, max_nan(P.x, P.y));
+        e[t] = expm1_neg(f2_mul(ch.nA, f2_mul(pb, r)));
+        const float2 z = one_less_square(e[t]);
+        u[t] = f2_mul(f2_mul(f2_mul(z, rsqrt2(z)), f2_mul(pa, r)), Tile<T>::get(x, t));
+    }
+    if (!(most < kHuge)) {  // one token at a time, and back into registers
+        float2 le[kChunk], lu[kChunk];
+#pragma unroll 1
+        for (int t = 0; t < kChunk; ++t) gates(ch, Tile<T>::get(x, t), Tile<T>::get(a, t), Tile<T>::get(b, t), le[t], lu[t]);
+#pragma unroll
+        for (int t = 0; t < kChunk; ++t) e[t] = le[t], u[t] = lu[t];
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- prefill
+template <typename T, bool G, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ Exchange<W> ex;
+    constexpr int kTiles = G ? 4 : 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
+    const int row = cid / slabs, c0 = (cid - row * slabs) * kSlab, c = c0 + 2 * lane;
+    int src, dst, s0, s1;
+    if (!bounds_ok(p.cu, row, p.N, p.total_T, s0, s1) || !slots_ok(p, row, src, dst)) {  // the same for the whole cluster
+        if (threadIdx.x == 0 && rank == 0) set_err(p.err);
+        return;
+    }
+    const bool live = c < p.D;
+    float2 carry = live && src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
+    const int len = s1 - s0;
+    if (len > 0) {
+        if (nc > 1) cluster_arrive();
+        Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
+        if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
+        unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T>::kBytes, *ta = tx + Tile<T>::kBytes, *tb = ta + Tile<T>::kBytes, *tg = tb + Tile<T>::kBytes;
+        const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T>::kUnits) < p.D;
+        const int window = kChunk * W * nc;
+        int t = kChunk * (rank * W + warp);  // this warp's first token of the window
+        const T *xp = static_cast<const T *>(p.rows.x) + (int64_t)s0 * p.rows.x_stride + c0, *ap = static_cast<const T *>(p.rows.a) + (int64_t)s0 * p.rows.a_stride + c0;
+        const T *bp = static_cast<const T *>(p.rows.b) + (int64_t)s0 * p.rows.b_stride + c0, *gp = G ? static_cast<const T *>(p.rows.g) + (int64_t)s0 * p.rows.g_stride + c0 : nullptr;
+        T *op = static_cast<T *>(p.rows.out) + (int64_t)s0 * p.rows.out_stride + c;
+        float *st = p.starts ? p.starts + first_chunk(s0, row) * p.D + c : nullptr;
+        auto fetch = [&](int at) {
+            const int nv = len - at;
+            if (nv > 0) {
+                Tile<T>::fetch(tx, xp + at * p.rows.x_stride, p.rows.x_stride, nv, col_ok);
+                Tile<T>::fetch(ta, ap + at * p.rows.a_stride, p.rows.a_stride, nv, col_ok);
+                Tile<T>::fetch(tb, bp + at * p.rows.b_stride, p.rows.b_stride, nv, col_ok);
+            }
+            commit();
+        };
+        auto fetch_g = [&](int at) {
+            if (G && len - at > 0) Tile<T>::fetch(tg, gp + at * p.rows.g_stride, p.rows.g_stride, len - at, col_ok);
+            commit();
+        };
+        fetch(t);
+        fetch_g(t);
+        const int windows = (len + window - 1) / window;
+#pragma unroll 1
+        for (int k = 0; k < windows; ++k, t += window) {
+            const int nv = min(kChunk, len - t);  // <= 0 behind the sequence's end
+            float2 e[kChunk], u[kChunk];
+            cp_async_wait_all();
+            __syncwarp();
+            Lin own = lin_identity();
+            if (nv > 0) {
+                all_gates<T>(ch, tx, ta, tb, e, u);
+                if (nv < kChunk)
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i)
+                        if (i >= nv) e[i] = u[i] = f2(0.f);
+                fetch(t + window);
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) {
+                    own.H = step(own.H, e[i], u[i]);
+                    own.A = f2_fma(own.A, e[i], own.A);
+                }
+            }
+            float2 h = join<W, false>(ex, own, carry, k, nc, rank, k == 0);
+            if (nv > 0) {
+                if (live) {
+                    if (st) *reinterpret_cast<float2 *>(st + (size_t)(t / kChunk) * p.D) = h;
+                    T *o = op + t * p.rows.out_stride;
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i, advance(o, p.rows.out_stride)) {
+                        h = step(h, e[i], u[i]);
+                        if (i < nv) st_pair(o, G ? f2_mul(h, silu2(Tile<T>::get(tg, i))) : h);
+                    }
+                }
+                __syncwarp();
+                fetch_g(t + window);
+            }
+        }
+    }
+    if (rank == 0 && warp == 0 && live) *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = carry;
+}
+
+template <typename T, bool G, int W>
+cudaError_t launch_scan_t(const Args &p, int nc, int dev, cudaStream_t s)
+{
+    static std::atomic<uint64_t> raised;
+    const int smem = W * (G ? 4 : 3) * Tile<T>::kBytes;
+    const cudaError_t e = raise_smem_on(raised, dev, glr_scan_kernel<T, G, W>, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned clusters = (unsigned)((int64_t)p.N * ((p.D + kSlab - 1) / kSlab));
+    return launch_cluster(glr_scan_kernel<T, G, W>, clusters * nc, nc, 32 * W, smem, s, p, nc);
+}
+
+}  // namespace
+
+cudaError_t launch_scan(const Args &p, bool f32, int nc, int dev, cudaStream_t s)
+{
+    if (p.rows.g) return f32 ? launch_scan_t<float, true, kScanWarps>(p, nc, dev, s) : launch_scan_t<__nv_bfloat16, true, kScanWarps>(p, nc, dev, s);
+    return f32 ? launch_scan_t<float, false, kScanWarps>(p, nc, dev, s) : launch_scan_t<__nv_bfloat16, false, kScanWarps>(p, nc, dev, s);
+}
+
+}  // namespace glr
+}  // namespace kda
