@@ -500,6 +500,7 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
  * call writes for sequences that overlap it is undefined).
  */
 #define KDA_GLR_MAX_DIM 1048576
+#define KDA_GLR_MAX_TOKENS 2147418112  /* of one prefill or backward: 2^31 - 2^16, so that a token past the end is counted in 32 bits */
 typedef struct {
     int32_t dim;       /* channels: a multiple of 8 with BF16 rows, of 4 with FP32 rows, <= KDA_GLR_MAX_DIM */
     int32_t io_dtype;  /* kda_dtype of x, a, b, g, out and of their gradients */

@@ -1,5 +1,4 @@
-// kda_glr.cu - the gated linear recurrence: token by token (decode), its gradients, and the host side of its
-// entry points.
+// kda_glr.cu - the gated linear recurrence: token by token (decode), and the host side of its entry points.
 #include <climits>
 #include <cstdarg>
 #include <cstdio>
@@ -48,75 +47,6 @@ __global__ void __launch_bounds__(128) glr_decode_kernel(const __grid_constant__
         return;
     }
     walk<T, G>(p, src, dst, c, (int64_t)row * p.n, p.n);
-}
-
-// Gradients. From the last token to the first, with c the gradient of the state after the token:
-//   lam = dh + c,  dx = lam m beta,  db = dx x (1 - beta),  c = alpha lam
-//   d gk = lam alpha (h_before - beta x alpha / m),  d A_log = d gk gk,  da = d gk gk (1 - sigmoid(a + a_bias))
-// The states before the tokens are walked again from those that the forward kept every 16 tokens.
-template <typename T, bool G>
-__global__ void __launch_bounds__(32) glr_backward_kernel(const __grid_constant__ BackArgs p)
-{
-    const int slabs = (p.D + kSlab - 1) / kSlab;
-    const int row = blockIdx.x / slabs, c = (blockIdx.x % slabs) * kSlab + 2 * threadIdx.x;
-    if (c >= p.D) return;
-    float2 sA = f2(0.f), sa = sA, sb = sA;
-    int t0, t1;
-    if (!bounds_ok(p.cu, row, p.N, p.total_T, t0, t1)) {
-        set_err(p.err);
-        t1 = t0 = -1;
-    }
-    if (t0 >= 0) {
-        Chan ch;
-        ch.load(p.A_log, p.a_bias, p.b_bias, c);
-        const T *xp = static_cast<const T *>(p.rows.x) + c, *ap = static_cast<const T *>(p.rows.a) + c;
-        const T *bp = static_cast<const T *>(p.rows.b) + c, *gp = static_cast<const T *>(p.rows.g) + c;
-        const T *dp = static_cast<const T *>(p.rows.dout) + c;
-        const float *st = p.starts + first_chunk(t0, row) * p.D + c;
-        const int n = t1 - t0;
-        float2 lc = p.dS_last ? *reinterpret_cast<const float2 *>(p.dS_last + (size_t)row * p.D + c) : f2(0.f);
-        for (int k = (n + kChunk - 1) / kChunk - 1; k >= 0; --k) {
-            const int len = min(kChunk, n - k * kChunk);
-            float2 hb[kChunk];
-            float2 h = *reinterpret_cast<const float2 *>(st + (size_t)k * p.D);
-            for (int i = 0; i < len; ++i) {
-                const int64_t t = t0 + k * kChunk + i;
-                float2 e, u;
-                gates(ch, Pair<T>::get(ld_pair(xp + t * p.rows.x_stride)), Pair<T>::get(ld_pair(ap + t * p.rows.a_stride)),
-                      Pair<T>::get(ld_pair(bp + t * p.rows.b_stride)), e, u);
-                hb[i] = h;
-                h = step(h, e, u);
-            }
-            for (int i = len - 1; i >= 0; --i) {
-                const int64_t t = t0 + k * kChunk + i;
-                const float2 x = Pair<T>::get(ld_pair(xp + t * p.rows.x_stride));
-                Back bk;
-                bk.gates(ch, x, Pair<T>::get(ld_pair(ap + t * p.rows.a_stride)), Pair<T>::get(ld_pair(bp + t * p.rows.b_stride)));
-                float2 dh = Pair<T>::get(ld_pair(dp + t * p.rows.dout_stride));
-                if (G) {
-                    const float2 g = Pair<T>::get(ld_pair(gp + t * p.rows.g_stride));
-                    const float2 E = neg_exp(g, f2(0.f)), s = rcp2(f2_add(E, f2(1.f)));
-                    const float2 ns = make_float2(fminf(E.x, kHuge) * s.x, fminf(E.y, kHuge) * s.y);  // 1 - s
-                    const float2 after = step(hb[i], bk.e, bk.u);
-                    st_pair(static_cast<T *>(p.rows.dg) + c + t * p.rows.dg_stride, f2_mul(f2_mul(dh, after), f2_mul(s, f2_fma(g, ns, f2(1.f)))));
-                    dh = f2_mul(dh, f2_mul(g, s));
-                }
-                float2 dx, da, db, dA;
-                lc = bk.token(f2_add(dh, lc), x, hb[i], dx, da, db, dA);
-                st_pair(static_cast<T *>(p.rows.dx) + c + t * p.rows.dx_stride, dx);
-                st_pair(static_cast<T *>(p.rows.da) + c + t * p.rows.da_stride, da);
-                st_pair(static_cast<T *>(p.rows.db) + c + t * p.rows.db_stride, db);
-                sA = f2_add(sA, dA);
-                sa = f2_add(sa, da);
-                sb = f2_add(sb, db);
-            }
-        }
-        if (p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = lc;
-    }
-    float *part = p.part + (size_t)row * 3 * p.D + c;
-    *reinterpret_cast<float2 *>(part) = sA;
-    *reinterpret_cast<float2 *>(part + p.D) = sa;
-    *reinterpret_cast<float2 *>(part + 2 * (size_t)p.D) = sb;
 }
 
 __global__ void __launch_bounds__(kSumCols *kSumGroups) glr_param_sums_kernel(const float *part, int rows, int D, float *dA_log, float *da_bias, float *db_bias)
@@ -198,18 +128,17 @@ Args make_args(const kda_glr_config_t *c, const kda_glr_params *prm, float *S, i
     return p;
 }
 
-// Checks the host's cu_seqlens; the longest sequence.
-bool lengths_ok(const int32_t *cu, int32_t N, int32_t *longest)
+// Checks the host's cu_seqlens.
+bool lengths_ok(const int32_t *cu, int32_t N)
 {
-    *longest = 0;
     if (N < 0) return fail(KDA_ERR_INVALID, "N must be >= 0 (got %d)", N), false;
     if (N == 0) return true;
     if (!cu) return fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL"), false;
     if (cu[0] != 0) return fail(KDA_ERR_INVALID, "cu_seqlens[0] must be 0 (got %d)", cu[0]), false;
     for (int32_t i = 0; i < N; ++i) {
         if (cu[i + 1] < cu[i]) return fail(KDA_ERR_INVALID, "cu_seqlens decreases at %d", i + 1), false;
-        if (cu[i + 1] - cu[i] > *longest) *longest = cu[i + 1] - cu[i];
     }
+    if (cu[N] > KDA_GLR_MAX_TOKENS) return fail(KDA_ERR_INVALID, "at most %d tokens (got %d)", KDA_GLR_MAX_TOKENS, cu[N]), false;
     return true;
 }
 
@@ -221,7 +150,15 @@ bool workspace_ok(const void *ws, size_t bytes, size_t need)
     return fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed", bytes, need), false;
 }
 
-size_t back_bytes(int32_t D, int32_t N) { return (size_t)N * 3 * D * sizeof(float); }
+// Blocks a cluster in the backward: for a GPU of 152 SMs, whatever the device, since the workspace goes by it.
+int back_cluster(const int32_t *cu, int32_t N, int32_t D)
+{
+    return choose_cluster(cu, back_groups(N, slabs_of(D)) < N ? 0 : N, slabs_of(D), kBackTile, kMaxCluster, 152 * 12 / kBackWarps);
+}
+size_t back_bytes(const int32_t *cu, int32_t N, int32_t D)
+{
+    return N == 0 ? 0 : (size_t)back_groups(N, slabs_of(D)) * back_cluster(cu, N, D) * 3 * D * sizeof(float);
+}
 
 }  // namespace
 }  // namespace glr
@@ -268,15 +205,13 @@ kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *par
 
 size_t kda_glr_workspace_bytes(const kda_glr_config_t *cfg, const int32_t *cu_seqlens_host, int32_t N)
 {
-    int32_t longest;
-    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N, &longest)) return 0;
-    return 256 + glr::back_bytes(cfg->dim, N);
+    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N)) return 0;
+    return 256 + glr::back_bytes(cu_seqlens_host, N, cfg->dim);
 }
 
 int64_t kda_glr_chunks(const int32_t *cu_seqlens_host, int32_t N)
 {
-    int32_t longest;
-    if (!glr::lengths_ok(cu_seqlens_host, N, &longest)) return -1;
+    if (!glr::lengths_ok(cu_seqlens_host, N)) return -1;
     return N == 0 ? 0 : (int64_t)(cu_seqlens_host[N] / glr::kChunk) + N;
 }
 
@@ -284,14 +219,13 @@ kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *pa
                            const int32_t *dst_slots, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int32_t N,
                            const kda_glr_rows *rows, float *starts, void *workspace, size_t workspace_bytes, int32_t *err, void *stream)
 {
-    int32_t longest;
-    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N, &longest)) return KDA_ERR_INVALID;
+    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N)) return KDA_ERR_INVALID;
     if (N == 0) return KDA_OK;
     if (!cu_seqlens) return glr::fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL");
     const int64_t T = cu_seqlens_host[N];
     if (!glr::call_ok(cfg, params, S, max_slots, src_slots, dst_slots, rows, T) || !glr::f32_or_null_ok("starts", starts)) return KDA_ERR_INVALID;
     if (N * glr::slabs_of(cfg->dim) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
-    if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(cfg->dim, N))) return KDA_ERR_INVALID;
+    if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(cu_seqlens_host, N, cfg->dim))) return KDA_ERR_INVALID;
     glr::Args p = glr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, N, rows, err);
     p.cu = cu_seqlens;
     p.total_T = T;
@@ -311,11 +245,11 @@ kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *p
                             const float *dS_last, float *dS_first, float *dA_log, float *da_bias, float *db_bias, void *workspace,
                             size_t workspace_bytes, int32_t *err, void *stream)
 {
-    int32_t longest;
-    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N, &longest)) return KDA_ERR_INVALID;
+    if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N)) return KDA_ERR_INVALID;
     if (!glr::f32_or_null_ok("dA_log", dA_log) || !glr::f32_or_null_ok("da_bias", da_bias) || !glr::f32_or_null_ok("db_bias", db_bias)) return KDA_ERR_INVALID;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int32_t D = cfg->dim;
+    const int groups = N > 0 ? glr::back_groups(N, glr::slabs_of(D)) : 0, nc = N > 0 ? glr::back_cluster(cu_seqlens_host, N, D) : 0;
     cudaError_t e = cudaSuccess;
     if (N > 0) {
         if (!cu_seqlens) return glr::fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL");
@@ -333,26 +267,19 @@ kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *p
             if (r->g && (!glr::row_ok("g", r->g, r->g_stride, T, cfg) || !glr::row_ok("dg", r->dg, r->dg_stride, T, cfg))) return KDA_ERR_INVALID;
         }
         if (N * glr::slabs_of(D) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
-        if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(D, N))) return KDA_ERR_INVALID;
+        if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(cu_seqlens_host, N, D))) return KDA_ERR_INVALID;
         glr::BackArgs p = {};
         p.err = err; p.cu = cu_seqlens; p.N = N; p.total_T = T; p.D = D;
         p.A_log = params->A_log; p.a_bias = params->a_bias; p.b_bias = params->b_bias;
         p.starts = starts; p.rows = *rows; p.dS_last = dS_last; p.dS_first = dS_first;
         p.part = static_cast<float *>(workspace);
-        const unsigned grid = (unsigned)(N * glr::slabs_of(D));
-        const bool f32 = cfg->io_dtype == KDA_F32;
-        if (rows->g) {
-            if (f32) glr::glr_backward_kernel<float, true><<<grid, 32, 0, s>>>(p);
-            else glr::glr_backward_kernel<__nv_bfloat16, true><<<grid, 32, 0, s>>>(p);
-        } else {
-            if (f32) glr::glr_backward_kernel<float, false><<<grid, 32, 0, s>>>(p);
-            else glr::glr_backward_kernel<__nv_bfloat16, false><<<grid, 32, 0, s>>>(p);
-        }
-        e = cudaGetLastError();
+        p.groups = groups;
+        int dev = 0, sms = 0;
+        if ((e = current_sms(&dev, &sms)) == cudaSuccess) e = glr::launch_scan_back(p, cfg->io_dtype == KDA_F32, nc, dev, s);
     }
     if (e == cudaSuccess && (dA_log || da_bias || db_bias)) {  // without sequences: zeros
         glr::glr_param_sums_kernel<<<dim3((D + kSumCols - 1) / kSumCols, 3), dim3(kSumCols, kSumGroups), 0, s>>>(
-            static_cast<const float *>(workspace), N, D, dA_log, da_bias, db_bias);
+            static_cast<const float *>(workspace), nc * groups, D, dA_log, da_bias, db_bias);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_backward: %s", cudaGetErrorString(e));

@@ -44,7 +44,8 @@ struct BackArgs {
     kda_glr_grad_rows rows;
     const float *dS_last;  // may be null: zeros
     float *dS_first;       // may be null
-    float *part;           // sums over tokens: [parts][3][D]
+    float *part;           // sums over tokens: [groups x blocks a cluster][3][D]
+    int32_t groups;        // sequences in work at once
 };
 
 __device__ __forceinline__ void set_err(int32_t *err)
@@ -178,28 +179,31 @@ __device__ __forceinline__ float2 silu2(float2 g)
 
 constexpr float kHuge = 8.507059173023462e37f;  // 2^126: its reciprocal is still a normal number
 
-// One token's part in the gradients.
+// 1 - s of a sigmoid s = 1 / (1 + E), as E s without the difference; where the reciprocal has become 0 it is 1.
+__device__ __forceinline__ float2 one_less(float2 s, float2 E)
+{
+    return make_float2(s.x == 0.f ? 1.f : fminf(E.x, kHuge) * s.x, s.y == 0.f ? 1.f : fminf(E.y, kHuge) * s.y);
+}
+
+// One token's part in the gradients, with c the gradient of the state after it from the tokens behind:
+//   lam = dh + c,  dx = lam m beta,  db = dx x (1 - beta),  c = alpha lam
+//   d gk = lam alpha (h - beta x alpha / m), h the state before it,  d A_log = d gk gk,  da = d gk gk (1 - sigmoid(a + a_bias))
 struct Back {
-    float2 e, u, m, rm, beta, nb, gk, na;  // nb = 1 - beta, na = 1 - sigmoid(a + a_bias): e^-v times the sigmoid, no difference
-    __device__ __forceinline__ void gates(const Chan &p, float2 x, float2 a, float2 b)
+    float2 m, rm, beta, nb, gk, na;  // rm = 1 / m, nb = 1 - beta, na = 1 - sigmoid(a + a_bias)
+    __device__ __forceinline__ void gates(const Chan &p, float2 e, float2 a, float2 b)
     {
-        float2 ea = neg_exp(a, p.ca), eb = neg_exp(b, p.cb);
+        const float2 ea = neg_exp(a, p.ca), eb = neg_exp(b, p.cb);
         const float2 sa = rcp2(f2_add(ea, f2(1.f)));
         beta = rcp2(f2_add(eb, f2(1.f)));
-        ea = make_float2(fminf(ea.x, kHuge), fminf(ea.y, kHuge));
-        eb = make_float2(fminf(eb.x, kHuge), fminf(eb.y, kHuge));
         gk = f2_mul(p.nA, sa);
-        e = expm1_neg(gk);
-        // where the reciprocal has become 0 the sigmoid is, and one minus it is 1
-        na = make_float2(sa.x == 0.f ? 1.f : ea.x * sa.x, sa.y == 0.f ? 1.f : ea.y * sa.y);
-        nb = make_float2(beta.x == 0.f ? 1.f : eb.x * beta.x, beta.y == 0.f ? 1.f : eb.y * beta.y);
+        na = one_less(sa, ea);
+        nb = one_less(beta, eb);
         const float2 z = one_less_square(e);
         rm = rsqrt2(z);
         m = f2_mul(z, rm);
-        u = f2_mul(f2_mul(m, beta), x);
     }
-    // lam: the gradient of the state after the token; h: the state before it. Returns that of the state before it.
-    __device__ __forceinline__ float2 token(float2 lam, float2 x, float2 h, float2 &dx, float2 &da, float2 &db, float2 &dA) const
+    // Returns the next c.
+    __device__ __forceinline__ float2 token(float2 e, float2 lam, float2 x, float2 h, float2 &dx, float2 &da, float2 &db, float2 &dA) const
     {
         const float2 alpha = f2_add(e, f2(1.f));
         dx = f2_mul(f2_mul(lam, m), beta);

@@ -244,7 +244,168 @@ cudaError_t launch_scan_t(const Args &p, int nc, int dev, cudaStream_t s)
     return launch_cluster(glr_scan_kernel<T, G, W>, clusters * nc, nc, 32 * W, smem, s, p, nc);
 }
 
+// ---------------------------------------------------------------- backward
+// The same from the last window to the first, with c the gradient of the state behind a token: c -> alpha (dh + c) is linear
+// too. What a token's gradients need beside it is the state before it, which a warp walks again from the one that the
+// forward kept for its 16 tokens. A cluster has the sequences group, group + groups, .. and adds up its tokens' shares of
+// the parameters' gradients in registers: one row of partial sums a block.
+template <typename T, bool G, int W>
+__global__ void __launch_bounds__(32 * W, 12 / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ Exchange<W> ex;
+    constexpr int kTiles = G ? 5 : 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
+    const int group = cid / slabs, c0 = (cid - group * slabs) * kSlab, c = c0 + 2 * lane;
+    const bool live = c < p.D;
+    Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
+    if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
+    unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T>::kBytes, *ta = tx + Tile<T>::kBytes, *tb = ta + Tile<T>::kBytes;
+    unsigned char *td = tb + Tile<T>::kBytes, *tg = td + Tile<T>::kBytes;
+    const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T>::kUnits) < p.D;
+    const int window = kChunk * W * nc, own_t = kChunk * (rank * W + warp);
+    float2 sA = f2(0.f), sa = sA, sb = sA;
+    int turn = 0;
+    if (nc > 1) cluster_arrive();
+#pragma unroll 1
+    for (int row = group; row < p.N; row += p.groups) {
+        int s0, s1;
+        if (!bounds_ok(p.cu, row, p.N, p.total_T, s0, s1)) {  // the same for the whole cluster
+            if (threadIdx.x == 0 && rank == 0) set_err(p.err);
+            continue;
+        }
+        const int len = s1 - s0;
+        float2 carry = live && p.dS_last ? *reinterpret_cast<const float2 *>(p.dS_last + (size_t)row * p.D + c) : f2(0.f);
+        if (len == 0) {  // no window, and no row that could be asked for
+            if (rank == 0 && warp == 0 && live && p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = carry;
+            continue;
+        }
+        const float *st = p.starts + first_chunk(s0, row) * p.D + c;
+        auto fetch = [&](int at) {
+            const int nv = len - at;
+            const int64_t r = (int64_t)s0 + at;
+            if (nv > 0) {
+                Tile<T>::fetch(tx, static_cast<const T *>(p.rows.x) + r * p.rows.x_stride + c0, p.rows.x_stride, nv, col_ok);
+                Tile<T>::fetch(ta, static_cast<const T *>(p.rows.a) + r * p.rows.a_stride + c0, p.rows.a_stride, nv, col_ok);
+                Tile<T>::fetch(tb, static_cast<const T *>(p.rows.b) + r * p.rows.b_stride + c0, p.rows.b_stride, nv, col_ok);
+                Tile<T>::fetch(td, static_cast<const T *>(p.rows.dout) + r * p.rows.dout_stride + c0, p.rows.dout_stride, nv, col_ok);
+                if (G) Tile<T>::fetch(tg, static_cast<const T *>(p.rows.g) + r * p.rows.g_stride + c0, p.rows.g_stride, nv, col_ok);
+            }
+            commit();
+        };
+        int t = (len + window - 1) / window * window - window + own_t;
+        fetch(t);
+#pragma unroll 1
+        for (; t >= own_t; t -= window, ++turn) {
+            const int nv = min(kChunk, len - t);  // <= 0 behind the sequence's end
+            float2 e[kChunk], u[kChunk], h = f2(0.f);
+            if (nv > 0 && live) h = __ldg(reinterpret_cast<const float2 *>(st + (size_t)(t / kChunk) * p.D));
+            cp_async_wait_all();
+            __syncwarp();
+            Lin own = lin_identity();
+            if (nv > 0) {
+                all_gates<T>(ch, tx, ta, tb, e, u);
+                if (nv < kChunk)
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i)
+                        if (i >= nv) e[i] = u[i] = f2(0.f);
+#pragma unroll
+                for (int i = kChunk - 1; i >= 0; --i) {  // the rows of dout past the end are 0
+                    float2 dh = Tile<T>::get(td, i);
+                    if (G) dh = f2_mul(dh, silu2(Tile<T>::get(tg, i)));
+                    own.H = f2_add(own.H, dh);
+                    own.H = f2_fma(e[i], own.H, own.H);
+                    own.A = f2_fma(own.A, e[i], own.A);
+                }
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) {  // u: the state before the token
+                    const float2 before = h;
+                    h = step(h, e[i], u[i]);
+                    u[i] = before;
+                }
+            }
+            float2 lc = join<W, true>(ex, own, carry, turn, nc, rank, turn == 0);
+            if (nv > 0) {
+                const int64_t r = (int64_t)s0 + t + nv - 1;
+                T *dxp = static_cast<T *>(p.rows.dx) + r * p.rows.dx_stride + c, *dap = static_cast<T *>(p.rows.da) + r * p.rows.da_stride + c;
+                T *dbp = static_cast<T *>(p.rows.db) + r * p.rows.db_stride + c, *dgp = G ? static_cast<T *>(p.rows.dg) + r * p.rows.dg_stride + c : nullptr;
+                float2 wA = f2(0.f), wa = wA, wb = wA;  // of this window
+#pragma unroll
+                for (int i = kChunk - 1; i >= 0; --i) {
+                    if (i < nv) {
+                        const float2 x = Tile<T>::get(tx, i);
+                        float2 dh = Tile<T>::get(td, i);
+                        Back bk;
+                        bk.gates(ch, e[i], Tile<T>::get(ta, i), Tile<T>::get(tb, i));
+                        if (G) {
+                            const float2 g = Tile<T>::get(tg, i);
+                            const float2 E = neg_exp(g, f2(0.f)), s = rcp2(f2_add(E, f2(1.f)));
+                            const float2 ns = one_less(s, E);
+                            if (live) st_pair(dgp, f2_mul(f2_mul(dh, h), f2_mul(s, f2_fma(g, ns, f2(1.f)))));
+                            advance(dgp, -p.rows.dg_stride);
+                            dh = f2_mul(dh, f2_mul(g, s));
+                        }
+                        h = u[i];
+                        float2 dx, da, db, dA;
+                        lc = bk.token(e[i], f2_add(dh, lc), x, h, dx, da, db, dA);
+                        if (live) {
+                            st_pair(dxp, dx);
+                            st_pair(dap, da);
+                            st_pair(dbp, db);
+                        }
+                        advance(dxp, -p.rows.dx_stride);
+                        advance(dap, -p.rows.da_stride);
+                        advance(dbp, -p.rows.db_stride);
+                        wA = f2_add(wA, dA);
+                        wa = f2_add(wa, da);
+                        wb = f2_add(wb, db);
+                    }
+                }
+                sA = f2_add(sA, wA);
+                sa = f2_add(sa, wa);
+                sb = f2_add(sb, wb);
+                __syncwarp();
+            }
+            if (t >= own_t + window) fetch(t - window);
+        }
+        if (rank == 0 && warp == 0 && live && p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = carry;
+    }
+    if (nc > 1 && turn == 0) cluster_wait();
+    // the warps' sums, in their order
+    __syncthreads();
+    float2(*sh)[W][32] = reinterpret_cast<float2(*)[W][32]>(&ex);
+    static_assert(sizeof(ex) >= 3 * W * 32 * sizeof(float2), "room for three sums a lane");
+    sh[0][warp][lane] = sA;
+    sh[1][warp][lane] = sa;
+    sh[2][warp][lane] = sb;
+    __syncthreads();
+    for (int q = warp; q < 3; q += W) {
+        float2 s = sh[q][0][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) s = f2_add(s, sh[q][w][lane]);
+        if (live) *reinterpret_cast<float2 *>(p.part + ((size_t)(group * nc + rank) * 3 + q) * p.D + c) = s;
+    }
+}
+
+template <typename T, bool G, int W>
+cudaError_t launch_back_t(const BackArgs &p, int nc, int dev, cudaStream_t s)
+{
+    static std::atomic<uint64_t> raised;
+    const int smem = W * (G ? 5 : 4) * Tile<T>::kBytes;
+    const cudaError_t e = raise_smem_on(raised, dev, glr_back_kernel<T, G, W>, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned clusters = (unsigned)((int64_t)p.groups * ((p.D + kSlab - 1) / kSlab));
+    return launch_cluster(glr_back_kernel<T, G, W>, clusters * nc, nc, 32 * W, smem, s, p, nc);
+}
+
 }  // namespace
+
+cudaError_t launch_scan_back(const BackArgs &p, bool f32, int nc, int dev, cudaStream_t s)
+{
+    if (p.rows.g) return f32 ? launch_back_t<float, true, kBackWarps>(p, nc, dev, s) : launch_back_t<__nv_bfloat16, true, kBackWarps>(p, nc, dev, s);
+    return f32 ? launch_back_t<float, false, kBackWarps>(p, nc, dev, s) : launch_back_t<__nv_bfloat16, false, kBackWarps>(p, nc, dev, s);
+}
 
 cudaError_t launch_scan(const Args &p, bool f32, int nc, int dev, cudaStream_t s)
 {

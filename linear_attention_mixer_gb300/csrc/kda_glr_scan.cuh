@@ -10,6 +10,8 @@ namespace glr {
 constexpr int kMaxCluster = 8;
 constexpr int kScanWarps = 8;                      // of a block: 128 tokens
 constexpr int kScanTile = kChunk * kScanWarps;
+constexpr int kBackWarps = 4;
+constexpr int kBackTile = kChunk * kBackWarps;
 
 // A launch of clusters of nc blocks (nc 1: without).
 template <typename... P, typename... A>
@@ -49,7 +51,16 @@ inline int choose_cluster(const int32_t *cu, int32_t N, int64_t slabs, int tile,
     return best;
 }
 
+// Sequences that are in work at once in a backward: as many as give every SM's blocks several turns. Each has its rows
+// of partial sums, so that these stay few beside the tokens' rows.
+inline int back_groups(int32_t N, int64_t slabs)
+{
+    const int64_t g = (2432 + slabs - 1) / slabs;
+    return (int)(N < g ? N : g < 64 ? (N < 64 ? N : 64) : g);
+}
+
 cudaError_t launch_scan(const Args &p, bool f32, int nc, int dev, cudaStream_t s);
+cudaError_t launch_scan_back(const BackArgs &p, bool f32, int nc, int dev, cudaStream_t s);
 
 }  // namespace glr
 }  // namespace kda

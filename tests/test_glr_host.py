@@ -42,7 +42,7 @@ def test_configs(K):
 
 def test_lengths(K):
     c = K.kda_glr_config(64)
-    for cu in ([1, 2], [0, 5, 4], [0, -1]):
+    for cu in ([1, 2], [0, 5, 4], [0, -1], [0, 2 ** 31 - 2 ** 16 + 1], [0, 2 ** 31 - 1]):
         with pytest.raises(K.KdaError):
             K.kda_glr_workspace_bytes(c, cu)
         with pytest.raises(K.KdaError):
@@ -52,7 +52,7 @@ def test_lengths(K):
             K.kda_glr_chunks(cu)
     # every sequence's chunks of 16 tokens have rows of their own
     rng = np.random.default_rng(0)
-    for lens in ([0], [1], [16], [17], [15, 1, 16, 0, 0, 33], list(rng.integers(0, 40, 50)), [2 ** 31 - 1]):
+    for lens in ([0], [1], [16], [17], [15, 1, 16, 0, 0, 33], list(rng.integers(0, 40, 50)), [2 ** 31 - 2 ** 16]):
         cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
         used = [cu[s] // 16 + s + k for s in range(len(lens)) for k in (range(-(-int(lens[s]) // 16)) if lens[s] < 10 ** 6 else [-(-int(lens[s]) // 16) - 1])]
         assert len(set(used)) == len(used) and (not used or max(used) < K.kda_glr_chunks(cu))
