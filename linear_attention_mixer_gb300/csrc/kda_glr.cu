@@ -150,15 +150,7 @@ bool workspace_ok(const void *ws, size_t bytes, size_t need)
     return fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed", bytes, need), false;
 }
 
-// Blocks a cluster in the backward: for a GPU of 152 SMs, whatever the device, since the workspace goes by it.
-int back_cluster(const int32_t *cu, int32_t N, int32_t D)
-{
-    return choose_cluster(cu, back_groups(N, slabs_of(D)) < N ? 0 : N, slabs_of(D), kBackTile, kMaxCluster, 152 * 12 / kBackWarps);
-}
-size_t back_bytes(const int32_t *cu, int32_t N, int32_t D)
-{
-    return N == 0 ? 0 : (size_t)back_groups(N, slabs_of(D)) * back_cluster(cu, N, D) * 3 * D * sizeof(float);
-}
+size_t back_bytes(int32_t N, int32_t D) { return N == 0 ? 0 : (size_t)back_parts(N, slabs_of(D)) * 3 * D * sizeof(float); }
 
 }  // namespace
 }  // namespace glr
@@ -206,7 +198,7 @@ kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *par
 size_t kda_glr_workspace_bytes(const kda_glr_config_t *cfg, const int32_t *cu_seqlens_host, int32_t N)
 {
     if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N)) return 0;
-    return 256 + glr::back_bytes(cu_seqlens_host, N, cfg->dim);
+    return 256 + glr::back_bytes(N, cfg->dim);
 }
 
 int64_t kda_glr_chunks(const int32_t *cu_seqlens_host, int32_t N)
@@ -225,7 +217,7 @@ kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *pa
     const int64_t T = cu_seqlens_host[N];
     if (!glr::call_ok(cfg, params, S, max_slots, src_slots, dst_slots, rows, T) || !glr::f32_or_null_ok("starts", starts)) return KDA_ERR_INVALID;
     if (N * glr::slabs_of(cfg->dim) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
-    if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(cu_seqlens_host, N, cfg->dim))) return KDA_ERR_INVALID;
+    if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(N, cfg->dim))) return KDA_ERR_INVALID;
     glr::Args p = glr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, N, rows, err);
     p.cu = cu_seqlens;
     p.total_T = T;
@@ -233,10 +225,7 @@ kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *pa
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int dev = 0, sms = 0;
     cudaError_t e = current_sms(&dev, &sms);
-    if (e == cudaSuccess) {
-        const int nc = glr::choose_cluster(cu_seqlens_host, N, glr::slabs_of(cfg->dim), glr::kScanTile, glr::kMaxCluster, 16 / glr::kScanWarps * sms);
-        e = glr::launch_scan(p, cfg->io_dtype == KDA_F32, nc, dev, s);
-    }
+    if (e == cudaSuccess) e = glr::launch_scan(p, cfg->io_dtype == KDA_F32, cu_seqlens_host, dev, sms, s);
     return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_prefill: %s", cudaGetErrorString(e));
 }
 
@@ -249,7 +238,7 @@ kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *p
     if (!glr::f32_or_null_ok("dA_log", dA_log) || !glr::f32_or_null_ok("da_bias", da_bias) || !glr::f32_or_null_ok("db_bias", db_bias)) return KDA_ERR_INVALID;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int32_t D = cfg->dim;
-    const int groups = N > 0 ? glr::back_groups(N, glr::slabs_of(D)) : 0, nc = N > 0 ? glr::back_cluster(cu_seqlens_host, N, D) : 0;
+    int parts = 0;
     cudaError_t e = cudaSuccess;
     if (N > 0) {
         if (!cu_seqlens) return glr::fail(KDA_ERR_INVALID, "cu_seqlens or cu_seqlens_host is NULL");
@@ -267,19 +256,19 @@ kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *p
             if (r->g && (!glr::row_ok("g", r->g, r->g_stride, T, cfg) || !glr::row_ok("dg", r->dg, r->dg_stride, T, cfg))) return KDA_ERR_INVALID;
         }
         if (N * glr::slabs_of(D) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
-        if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(cu_seqlens_host, N, D))) return KDA_ERR_INVALID;
+        if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(N, D))) return KDA_ERR_INVALID;
         glr::BackArgs p = {};
         p.err = err; p.cu = cu_seqlens; p.N = N; p.total_T = T; p.D = D;
         p.A_log = params->A_log; p.a_bias = params->a_bias; p.b_bias = params->b_bias;
         p.starts = starts; p.rows = *rows; p.dS_last = dS_last; p.dS_first = dS_first;
         p.part = static_cast<float *>(workspace);
-        p.groups = groups;
+        p.groups = glr::back_groups(N, glr::slabs_of(D));
         int dev = 0, sms = 0;
-        if ((e = current_sms(&dev, &sms)) == cudaSuccess) e = glr::launch_scan_back(p, cfg->io_dtype == KDA_F32, nc, dev, s);
+        if ((e = current_sms(&dev, &sms)) == cudaSuccess) e = glr::launch_scan_back(p, cfg->io_dtype == KDA_F32, cu_seqlens_host, &parts, dev, sms, s);
     }
     if (e == cudaSuccess && (dA_log || da_bias || db_bias)) {  // without sequences: zeros
         glr::glr_param_sums_kernel<<<dim3((D + kSumCols - 1) / kSumCols, 3), dim3(kSumCols, kSumGroups), 0, s>>>(
-            static_cast<const float *>(workspace), nc * groups, D, dA_log, da_bias, db_bias);
+            static_cast<const float *>(workspace), parts, D, dA_log, da_bias, db_bias);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_backward: %s", cudaGetErrorString(e));

@@ -48,9 +48,9 @@ struct BackArgs {
     int32_t groups;        // sequences in work at once
 };
 
-__device__ __forceinline__ void set_err(int32_t *err)
+__device__ __forceinline__ void set_err(int32_t *err, int32_t what = kErrBadSlot)
 {
-    if (err) atomicExch(err, kErrBadSlot);
+    if (err) atomicExch(err, what);
 }
 
 // Slots of a row: false when one is out of range. src may be -1: a zero state.
@@ -112,27 +112,28 @@ __device__ __forceinline__ float max_nan(float a, float b)  // NaN if either is
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// exp(x) - 1 for x <= 0 with a relative error of about 2^-24, also near 0: x = k ln 2 + r, |r| <= ln 2 / 2, is
+// exp(x) - 1 for -87 <= x <= 0 with a relative error of about 2^-24, also near 0: x = k ln 2 + r, |r| <= ln 2 / 2, is
 // 2^k (exp(r) - 1) + (2^k - 1), and exp(r) - 1 = r q(r) with q of degree 5 (Chebyshev interpolation of (exp(r) - 1) / r on
-// that interval; its error is 1.3e-8). No special function and, for two channels, packed instructions. Below -87 it is
-// that of -87, -1 in FP32. NaN stays.
-__device__ __forceinline__ float2 expm1_neg(float2 x)
+// that interval; its error is 1.3e-8). No special function and, for two channels, packed instructions. NaN stays.
+__device__ __forceinline__ float2 expm1_from_87(float2 x)
 {
-    x = make_float2(max_nan(x.x, -87.f), max_nan(x.y, -87.f));
-    const float2 t = f2_fma(x, f2(kLog2e), f2(12582912.f));  // adding 1.5 x 2^23 rounds to a whole number, in the low bits
-    const float2 k = f2_add(t, f2(-12582912.f));
-    const float2 r = f2_fma(k, f2(-0.6931471805599453f), x);
+    constexpr float kRound = 12582912.f + 127.f;  // 1.5 x 2^23 rounds to a whole number in the low bits, to which 2^0's exponent is added
+    const float2 t = f2_fma(x, f2(kLog2e), f2(kRound));
+    const float2 k = f2_add(t, f2(-kRound));
+    const float2 r = f2_fma(k, f2(-kLn2), x);
     float2 q = f2_fma(f2(0.0013933685841038823f), r, f2(0.008369184099137783f));
     q = f2_fma(q, r, f2(0.041666463017463684f));
     q = f2_fma(q, r, f2(0.16666504740715027f));
     q = f2_fma(q, r, f2(0.5f));
     q = f2_fma(q, r, f2(1.f));
     q = f2_mul(q, r);
-    const float2 s = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3F800000), __int_as_float((__float_as_int(t.y) << 23) + 0x3F800000));
+    const float2 s = make_float2(__int_as_float(__float_as_int(t.x) << 23), __int_as_float(__float_as_int(t.y) << 23));
     return f2_fma(s, q, f2_add(s, f2(-1.f)));
 }
+// The same for any x <= 0: below -87 it is that of -87, -1 in FP32.
+__device__ __forceinline__ float2 expm1_neg(float2 x) { return expm1_from_87(make_float2(max_nan(x.x, -87.f), max_nan(x.y, -87.f))); }
 
 // The parameters of two channels.
 struct Chan {
@@ -156,13 +157,12 @@ __device__ __forceinline__ float2 neg_exp(float2 v, float2 c)
 __device__ __forceinline__ float2 rcp2(float2 v) { return make_float2(rcp_ftz(v.x), rcp_ftz(v.y)); }
 
 // z = 1 - alpha^2 from e, and 1 / sqrt(z), which is large and finite at z = 0
-__device__ __forceinline__ float2 one_less_square(float2 e) { return f2_mul(make_float2(-e.x, -e.y), f2_add(e, f2(2.f))); }
+__device__ __forceinline__ float2 one_less_square(float2 e) { return f2_mul(e, f2_fma(e, f2(-1.f), f2(-2.f))); }
 __device__ __forceinline__ float2 rsqrt2(float2 z)
 {
     const float2 t = f2_add(z, f2(1e-36f));
     return make_float2(rsqrt_ftz(t.x), rsqrt_ftz(t.y));
 }
-
 // e = alpha - 1 and u = m beta x of one token.
 __device__ __forceinline__ void gates(const Chan &p, float2 x, float2 a, float2 b, float2 &e, float2 &u)
 {

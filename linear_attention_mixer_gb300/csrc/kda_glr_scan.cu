@@ -22,12 +22,27 @@ __device__ __forceinline__ uint32_t cluster_rank()
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// the float4 at `mine` (shared memory) in block `rank` of the cluster
-__device__ __forceinline__ void st_remote(const float4 *mine, uint32_t rank, float4 v)
+// The float4 at `mine` (shared memory) in block `rank` of the cluster, counted by its barrier at `bar`.
+__device__ __forceinline__ void st_remote(const float4 *mine, const uint64_t *bar, uint32_t rank, float4 v)
 {
-    uint32_t a;
+    uint32_t a, b;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w), "r"(b) : "memory");
+}
+// Polls before a wait gives up (a test builds this file with a limit that runs out).
+#ifndef KDA_GLR_WAIT_LIMIT
+#define KDA_GLR_WAIT_LIMIT (1u << 24)
+#endif
+// Until what other blocks of the cluster sent has arrived; false when the limit ran out.
+__device__ __forceinline__ bool wait_cluster(const uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok = 0;
+    for (uint32_t i = 0; i < KDA_GLR_WAIT_LIMIT && !ok; ++i)
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return __all_sync(0xFFFFFFFFu, ok != 0);
 }
 
 // ---------------------------------------------------------------- pairs
@@ -48,21 +63,30 @@ __device__ __forceinline__ Lin ld_lin(const float4 *p)
 }
 __device__ __forceinline__ float4 as_float4(const Lin &l) { return make_float4(l.A.x, l.A.y, l.H.x, l.H.y); }
 
-// The places through which pairs are joined, for two windows in turn: what a window writes is read before the next but one
-// window's barriers are passed.
-template <int W>
+// The places through which pairs are joined, for two windows in turn: a block sends for a window when it has joined the
+// one before, to which every block sends when all its warps have read the one before that.
+template <int W, int MAX>
 struct Exchange {
     float4 warp[2][W][32];
-    float4 block[2][kMaxCluster][32];
+    float4 block[2][MAX][32];
+    uint64_t bar[2];
+    __device__ __forceinline__ void open()  // one thread
+    {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        fence_mbar_init();
+    }
 };
 
 // From a warp's own pair, what comes before its tokens in the window (back: behind them), applied to `carry`, the state at
-// the window's start; carry becomes that at its end. `turn`: windows so far. All threads of the cluster take part.
-template <int W, bool BACK>
-__device__ __forceinline__ float2 join(Exchange<W> &ex, const Lin &own, float2 &carry, int turn, int nc, int rank, bool first)
+// the window's start; carry becomes that at its end. `turn`: windows so far; good: no wait has given up (then
+// nothing more is sent or waited for). All threads of the cluster take part.
+template <bool BACK, int W, int MAX>
+__device__ __forceinline__ float2 join(Exchange<W, MAX> &ex, const Lin &own, float2 &carry, int turn, int nc, int rank, bool &good)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, par = turn & 1;
     ex.warp[par][warp][lane] = as_float4(own);
+    if (nc > 1 && threadIdx.x == 0 && good) mbar_arrive_expect_tx(&ex.bar[par], (uint32_t)nc * 32 * sizeof(float4));
     __syncthreads();
     Lin run = lin_identity(), pre = run;
 #pragma unroll
@@ -76,18 +100,37 @@ __device__ __forceinline__ float2 join(Exchange<W> &ex, const Lin &own, float2 &
         carry = run.at(carry);
         return h;
     }
-    if (first) cluster_wait();  // every block of the cluster runs: theirs is the arrival at the kernel's start
-    for (int r = warp; r < nc; r += W) st_remote(&ex.block[par][rank][lane], r, as_float4(run));
-    cluster_arrive();
-    cluster_wait();
+    if (turn == 0) cluster_wait();  // every block of the cluster runs and has its barriers: theirs is the arrival at the start
+    if (good)
+        for (int r = warp; r < nc; r += W) st_remote(&ex.block[par][rank][lane], &ex.bar[par], r, as_float4(run));
+    if (good) good = wait_cluster(&ex.bar[par], (uint32_t)(turn >> 1) & 1);
     float2 h = carry, mine = carry;
-    for (int i = 0; i < nc; ++i) {
-        const int r = BACK ? nc - 1 - i : i;
-        if (r == rank) mine = h;
-        h = ld_lin(&ex.block[par][r][lane]).at(h);
+#pragma unroll
+    for (int j = 0; j < MAX; j += 4) {
+        if (j >= nc) break;
+        Lin l[4];  // loaded before they are needed one after the other
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[i] = j + i < nc ? ld_lin(&ex.block[par][BACK ? nc - 1 - j - i : j + i][lane]) : lin_identity();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if ((BACK ? nc - 1 - j - i : j + i) == rank) mine = h;
+            h = l[i].at(h);
+        }
     }
     carry = h;
     return pre.at(mine);
+}
+// Before a block of a cluster ends: none sends to it any more. What was sent to it has arrived, as it has waited for that;
+// where a wait gave up, it gets some time to.
+__device__ __forceinline__ void leave(int nc, bool joined, bool good)
+{
+    if (nc == 1) return;
+    if (!joined) cluster_wait();  // the arrival at the start
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (!good)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 // ---------------------------------------------------------------- rows in shared memory
@@ -123,22 +166,23 @@ struct Tile {
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // e and u of a warp's 16 tokens. One reciprocal serves both sigmoids: with P = (1 + exp(-a')) (1 + exp(-b')) sigmoid(a') is
-// (1 + exp(-b')) / P. Where P is not below 2^126 (a gate closed by more than about 40, or a NaN) they are taken apart.
+// (1 + exp(-b')) / P. Where a P is not below 2^126 (a gate closed by more than about 40, or a NaN; their sum shows it), or where
+// exp(A_log) is above 87 (`wild`), all are worked out with a reciprocal each and a decay's logarithm cut at -87.
 template <typename T>
-__device__ __forceinline__ void all_gates(const Chan &ch, const unsigned char *x, const unsigned char *a, const unsigned char *b,
+__device__ __forceinline__ void all_gates(const Chan &ch, bool wild, const unsigned char *x, const unsigned char *a, const unsigned char *b,
                                           float2 (&e)[kChunk], float2 (&u)[kChunk])
 {
-    float most = 0.f;
+    float2 sum = f2(0.f);
 #pragma unroll
     for (int t = 0; t < kChunk; ++t) {
         const float2 pa = f2_add(neg_exp(Tile<T>::get(a, t), ch.ca), f2(1.f)), pb = f2_add(neg_exp(Tile<T>::get(b, t), ch.cb), f2(1.f));
         const float2 P = f2_mul(pa, pb), r = rcp2(P);
-        most = max_nan(most, max_nan(P.x, P.y));
-        e[t] = expm1_neg(f2_mul(ch.nA, f2_mul(pb, r)));
+        sum = f2_add(sum, P);
+        e[t] = expm1_from_87(f2_mul(ch.nA, f2_mul(pb, r)));
         const float2 z = one_less_square(e[t]);
         u[t] = f2_mul(f2_mul(f2_mul(z, rsqrt2(z)), f2_mul(pa, r)), Tile<T>::get(x, t));
     }
-    if (!(most < kHuge)) {  // one token at a time, and back into registers
+    if (wild || !(sum.x < kHuge && sum.y < kHuge)) {  // one token at a time, and back into registers
         float2 le[kChunk], lu[kChunk];
 #pragma unroll 1
         for (int t = 0; t < kChunk; ++t) gates(ch, Tile<T>::get(x, t), Tile<T>::get(a, t), Tile<T>::get(b, t), le[t], lu[t]);
@@ -150,10 +194,10 @@ __device__ __forceinline__ void all_gates(const Chan &ch, const unsigned char *x
 
 // ---------------------------------------------------------------- prefill
 template <typename T, bool G, int W>
-__global__ void __launch_bounds__(32 * W, 16 / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
+__global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ Exchange<W> ex;
+    __shared__ Exchange<W, max_cluster<T>()> ex;
     constexpr int kTiles = G ? 4 : 3;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
@@ -167,9 +211,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W) glr_scan_kernel(const __grid_c
     float2 carry = live && src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
     const int len = s1 - s0;
     if (len > 0) {
-        if (nc > 1) cluster_arrive();
+        if (nc > 1) {
+            if (threadIdx.x == 0) ex.open();
+            __syncwarp();
+            cluster_arrive();
+        }
+        bool good = true;
         Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
         if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
+        const bool wild = !(fminf(ch.nA.x, ch.nA.y) >= -87.f);
         unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T>::kBytes, *ta = tx + Tile<T>::kBytes, *tb = ta + Tile<T>::kBytes, *tg = tb + Tile<T>::kBytes;
         const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T>::kUnits) < p.D;
         const int window = kChunk * W * nc;
@@ -202,7 +252,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) glr_scan_kernel(const __grid_c
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
-                all_gates<T>(ch, tx, ta, tb, e, u);
+                all_gates<T>(ch, wild, tx, ta, tb, e, u);
                 if (nv < kChunk)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i)
@@ -214,7 +264,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) glr_scan_kernel(const __grid_c
                     own.A = f2_fma(own.A, e[i], own.A);
                 }
             }
-            float2 h = join<W, false>(ex, own, carry, k, nc, rank, k == 0);
+            float2 h = join<false>(ex, own, carry, k, nc, rank, good);
             if (nv > 0) {
                 if (live) {
                     if (st) *reinterpret_cast<float2 *>(st + (size_t)(t / kChunk) * p.D) = h;
@@ -229,19 +279,24 @@ __global__ void __launch_bounds__(32 * W, 16 / W) glr_scan_kernel(const __grid_c
                 fetch_g(t + window);
             }
         }
+        leave(nc, true, good);
+        if (!good && lane == 0) set_err(p.err, KDA_ERR_TIMEOUT);
     }
     if (rank == 0 && warp == 0 && live) *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = carry;
 }
 
-template <typename T, bool G, int W>
-cudaError_t launch_scan_t(const Args &p, int nc, int dev, cudaStream_t s)
+template <typename T, bool G>
+cudaError_t launch_scan_t(const Args &p, const int32_t *cu, int dev, int sms, cudaStream_t s)
 {
+    constexpr int W = scan_warps<T>();
     static std::atomic<uint64_t> raised;
+    static ClusterRoom room;
     const int smem = W * (G ? 4 : 3) * Tile<T>::kBytes;
     const cudaError_t e = raise_smem_on(raised, dev, glr_scan_kernel<T, G, W>, smem);
     if (e != cudaSuccess) return e;
-    const unsigned clusters = (unsigned)((int64_t)p.N * ((p.D + kSlab - 1) / kSlab));
-    return launch_cluster(glr_scan_kernel<T, G, W>, clusters * nc, nc, 32 * W, smem, s, p, nc);
+    const int64_t slabs = (p.D + kSlab - 1) / kSlab;
+    const int nc = choose_cluster(cu, p.N, p.N, slabs, kChunk * W, max_cluster<T>(), sms, [&](int n) { return room.of(glr_scan_kernel<T, G, W>, n, 32 * W, smem, dev); });
+    return launch_cluster(glr_scan_kernel<T, G, W>, (unsigned)(p.N * slabs * nc), nc, 32 * W, smem, s, p, nc);
 }
 
 // ---------------------------------------------------------------- backward
@@ -250,10 +305,10 @@ cudaError_t launch_scan_t(const Args &p, int nc, int dev, cudaStream_t s)
 // forward kept for its 16 tokens. A cluster has the sequences group, group + groups, .. and adds up its tokens' shares of
 // the parameters' gradients in registers: one row of partial sums a block.
 template <typename T, bool G, int W>
-__global__ void __launch_bounds__(32 * W, 12 / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
+__global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ Exchange<W> ex;
+    __shared__ Exchange<W, max_cluster<T>()> ex;
     constexpr int kTiles = G ? 5 : 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
@@ -261,13 +316,19 @@ __global__ void __launch_bounds__(32 * W, 12 / W) glr_back_kernel(const __grid_c
     const bool live = c < p.D;
     Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
     if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
+    const bool wild = !(fminf(ch.nA.x, ch.nA.y) >= -87.f);
     unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T>::kBytes, *ta = tx + Tile<T>::kBytes, *tb = ta + Tile<T>::kBytes;
     unsigned char *td = tb + Tile<T>::kBytes, *tg = td + Tile<T>::kBytes;
     const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T>::kUnits) < p.D;
     const int window = kChunk * W * nc, own_t = kChunk * (rank * W + warp);
     float2 sA = f2(0.f), sa = sA, sb = sA;
     int turn = 0;
-    if (nc > 1) cluster_arrive();
+    bool good = true;
+    if (nc > 1) {
+        if (threadIdx.x == 0) ex.open();
+        __syncwarp();
+        cluster_arrive();
+    }
 #pragma unroll 1
     for (int row = group; row < p.N; row += p.groups) {
         int s0, s1;
@@ -305,7 +366,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) glr_back_kernel(const __grid_c
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
-                all_gates<T>(ch, tx, ta, tb, e, u);
+                all_gates<T>(ch, wild, tx, ta, tb, e, u);
                 if (nv < kChunk)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i)
@@ -325,7 +386,7 @@ __global__ void __launch_bounds__(32 * W, 12 / W) glr_back_kernel(const __grid_c
                     u[i] = before;
                 }
             }
-            float2 lc = join<W, true>(ex, own, carry, turn, nc, rank, turn == 0);
+            float2 lc = join<true>(ex, own, carry, turn, nc, rank, good);
             if (nv > 0) {
                 const int64_t r = (int64_t)s0 + t + nv - 1;
                 T *dxp = static_cast<T *>(p.rows.dx) + r * p.rows.dx_stride + c, *dap = static_cast<T *>(p.rows.da) + r * p.rows.da_stride + c;
@@ -371,7 +432,8 @@ __global__ void __launch_bounds__(32 * W, 12 / W) glr_back_kernel(const __grid_c
         }
         if (rank == 0 && warp == 0 && live && p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = carry;
     }
-    if (nc > 1 && turn == 0) cluster_wait();
+    leave(nc, turn > 0, good);
+    if (!good && lane == 0) set_err(p.err, KDA_ERR_TIMEOUT);
     // the warps' sums, in their order
     __syncthreads();
     float2(*sh)[W][32] = reinterpret_cast<float2(*)[W][32]>(&ex);
@@ -388,29 +450,34 @@ __global__ void __launch_bounds__(32 * W, 12 / W) glr_back_kernel(const __grid_c
     }
 }
 
-template <typename T, bool G, int W>
-cudaError_t launch_back_t(const BackArgs &p, int nc, int dev, cudaStream_t s)
+template <typename T, bool G>
+cudaError_t launch_back_t(const BackArgs &p, const int32_t *cu, int *parts, int dev, int sms, cudaStream_t s)
 {
+    constexpr int W = kBackWarps;
     static std::atomic<uint64_t> raised;
+    static ClusterRoom room;
     const int smem = W * (G ? 5 : 4) * Tile<T>::kBytes;
     const cudaError_t e = raise_smem_on(raised, dev, glr_back_kernel<T, G, W>, smem);
     if (e != cudaSuccess) return e;
-    const unsigned clusters = (unsigned)((int64_t)p.groups * ((p.D + kSlab - 1) / kSlab));
-    return launch_cluster(glr_back_kernel<T, G, W>, clusters * nc, nc, 32 * W, smem, s, p, nc);
+    const int64_t slabs = (p.D + kSlab - 1) / kSlab;
+    const int nc = choose_cluster(cu, p.N, p.groups, slabs, kChunk * W, max_cluster<T>(), sms, [&](int n) { return room.of(glr_back_kernel<T, G, W>, n, 32 * W, smem, dev); });
+    *parts = p.groups * nc;
+    return launch_cluster(glr_back_kernel<T, G, W>, (unsigned)(p.groups * slabs * nc), nc, 32 * W, smem, s, p, nc);
 }
 
 }  // namespace
 
-cudaError_t launch_scan_back(const BackArgs &p, bool f32, int nc, int dev, cudaStream_t s)
+cudaError_t launch_scan(const Args &p, bool f32, const int32_t *cu, int dev, int sms, cudaStream_t s)
 {
-    if (p.rows.g) return f32 ? launch_back_t<float, true, kBackWarps>(p, nc, dev, s) : launch_back_t<__nv_bfloat16, true, kBackWarps>(p, nc, dev, s);
-    return f32 ? launch_back_t<float, false, kBackWarps>(p, nc, dev, s) : launch_back_t<__nv_bfloat16, false, kBackWarps>(p, nc, dev, s);
+    if (p.rows.g) return f32 ? launch_scan_t<float, true>(p, cu, dev, sms, s) : launch_scan_t<__nv_bfloat16, true>(p, cu, dev, sms, s);
+    return f32 ? launch_scan_t<float, false>(p, cu, dev, sms, s) : launch_scan_t<__nv_bfloat16, false>(p, cu, dev, sms, s);
 }
 
-cudaError_t launch_scan(const Args &p, bool f32, int nc, int dev, cudaStream_t s)
+cudaError_t launch_scan_back(const BackArgs &p, bool f32, const int32_t *cu, int *parts, int dev, int sms, cudaStream_t s)
 {
-    if (p.rows.g) return f32 ? launch_scan_t<float, true, kScanWarps>(p, nc, dev, s) : launch_scan_t<__nv_bfloat16, true, kScanWarps>(p, nc, dev, s);
-    return f32 ? launch_scan_t<float, false, kScanWarps>(p, nc, dev, s) : launch_scan_t<__nv_bfloat16, false, kScanWarps>(p, nc, dev, s);
+    if (p.rows.g)
+        return f32 ? launch_back_t<float, true>(p, cu, parts, dev, sms, s) : launch_back_t<__nv_bfloat16, true>(p, cu, parts, dev, sms, s);
+    return f32 ? launch_back_t<float, false>(p, cu, parts, dev, sms, s) : launch_back_t<__nv_bfloat16, false>(p, cu, parts, dev, sms, s);
 }
 
 }  // namespace glr

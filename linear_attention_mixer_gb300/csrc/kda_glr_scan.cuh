@@ -7,46 +7,97 @@
 namespace kda {
 namespace glr {
 
-constexpr int kMaxCluster = 8;
-constexpr int kScanWarps = 8;                      // of a block: 128 tokens
-constexpr int kScanTile = kChunk * kScanWarps;
-constexpr int kBackWarps = 4;
-constexpr int kBackTile = kChunk * kBackWarps;
+constexpr int kBackWarps = 4;                        // warps of a block: 64 tokens
+constexpr int kScanPerSm = 16, kBackPerSm = 12;      // warps that an SM's registers hold (128 and 168 a thread)
+template <typename T> constexpr int scan_warps() { return sizeof(T) == 4 ? 8 : 4; }
+// Blocks of a cluster at most. FP32 rows leave no room in shared memory for the pairs of more than 8.
+template <typename T> constexpr int max_cluster() { return sizeof(T) == 4 ? 8 : 16; }
+// Blocks that work on clusters of more than one, over all channels and sequences, at most: what bounds the workspace.
+constexpr int kMaxShared = 2432;
+
+inline cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *at, unsigned grid, int nc, int threads, size_t smem, cudaStream_t stream)
+{
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = (unsigned)nc;
+    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = nc > 1 ? 1 : 0;
+    return cfg;
+}
 
 // A launch of clusters of nc blocks (nc 1: without).
 template <typename... P, typename... A>
 inline cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, int nc, int threads, size_t smem, cudaStream_t stream, A &&...args)
 {
     cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)nc;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &at;
-    cfg.numAttrs = nc > 1 ? 1 : 0;
+    const cudaLaunchConfig_t cfg = cluster_config(&at, grid, nc, threads, smem, stream);
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-// Blocks that share a sequence's 64 channels: as many as make the call shortest, where the longest sequence takes
-// ceil(its tiles / nc) turns and, if the blocks do not all run at once, the work of all of them counts.
-inline int choose_cluster(const int32_t *cu, int32_t N, int64_t slabs, int tile, int most, int slots)
+// How many clusters of n blocks of a kernel run at once, asked once for each device and n. Not n times fewer than single
+// blocks: a cluster stays within a group of SMs, and what does not divide there stays idle.
+struct ClusterRoom {
+    std::atomic<int> known[8][17];
+    template <typename Fn>
+    int of(Fn *kernel, int n, int threads, size_t smem, int dev)
+    {
+        std::atomic<int> *slot = dev >= 0 && dev < 8 ? &known[dev][n] : nullptr;
+        int got = slot ? slot->load(std::memory_order_relaxed) : 0;
+        if (got) return got;
+        cudaLaunchAttribute at = {};
+        const cudaLaunchConfig_t cfg = cluster_config(&at, (unsigned)n, n, threads, smem, nullptr);
+        cudaError_t e = cudaSuccess;
+        if (n > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) {
+            cudaLaunchAttribute one = at;
+            cudaLaunchConfig_t c = cfg;
+            c.attrs = &one;
+            c.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&got, kernel, &c);
+        }
+        if (e != cudaSuccess || got < 1) {
+            cudaGetLastError();  // such clusters cannot be launched
+            got = -1;
+        }
+        if (slot) slot->store(got, std::memory_order_relaxed);
+        return got;
+    }
+};
+
+// Blocks that share a sequence's 64 channels, of `groups` sequences at once: as many as make the call shortest. A window
+// takes a while however few blocks an SM has (about as long as 192 tokens of one block's work, less without a cluster)
+// and the work of all of the SM's blocks; where all clusters run at once the longest sequence's windows count,
+// else the work of all. Any number, or, to look at many sequences quickly, powers of two.
+template <typename Room>
+inline int choose_cluster(const int32_t *cu, int32_t N, int32_t groups, int64_t slabs, int tile, int most, int sms, Room room)
 {
     int best = 1;
     double least = 0;
-    for (int nc = 1; nc <= most; nc *= 2) {
-        int64_t path = 0, all = 0;
-        const int64_t span = (int64_t)tile * nc;
+    for (int nc = 1; nc <= most; nc += N > 64 ? nc : 1) {
+        if (nc > 1 && groups * slabs * nc > kMaxShared) break;
+        const int at_once = room(nc);
+        if (at_once < 0) continue;
+        const uint32_t span = (uint32_t)(tile * nc);
+        const int shift = __builtin_ctz(span);
+        uint32_t path = 0;
+        int64_t all = 0;
         for (int32_t i = 0; i < N; ++i) {
-            const int64_t w = (cu[i + 1] - cu[i] + span - 1) / span;
+            const uint32_t n = (uint32_t)(cu[i + 1] - cu[i]) + span - 1, w = N > 64 ? n >> shift : n / span;
             all += w;
             if (w > path) path = w;
         }
-        const double cost = N * slabs * nc <= slots ? (double)path : (double)all * nc * slabs / slots + 0.5 * path;
-        if (nc == 1 || cost < 0.95 * least) least = cost, best = nc;
+        const double still = nc == 1 ? 128.0 : 192.0;  // in tokens
+        double cost = path * (still + tile * (double)(groups * slabs * nc) / sms);
+        // not all at once: the SMs are full, with `at_once` clusters on them, until the work is done
+        if (groups < N || groups * slabs > at_once)
+            cost = (double)all * slabs / at_once * (still + tile * (double)at_once * nc / sms) + 0.25 * path * (still + tile);
+        if (nc == 1 || cost < 0.97 * least) least = cost, best = nc;
+        if (path <= 1) break;  // more blocks would stand idle
     }
     return best;
 }
@@ -58,9 +109,16 @@ inline int back_groups(int32_t N, int64_t slabs)
     const int64_t g = (2432 + slabs - 1) / slabs;
     return (int)(N < g ? N : g < 64 ? (N < 64 ? N : 64) : g);
 }
+// Rows of partial sums of a backward at most, whatever the device.
+inline int64_t back_parts(int32_t N, int64_t slabs)
+{
+    const int64_t groups = back_groups(N, slabs), shared = kMaxShared / slabs;
+    return groups > shared ? groups : shared;
+}
 
-cudaError_t launch_scan(const Args &p, bool f32, int nc, int dev, cudaStream_t s);
-cudaError_t launch_scan_back(const BackArgs &p, bool f32, int nc, int dev, cudaStream_t s);
+// cu: the host's cu_seqlens
+cudaError_t launch_scan(const Args &p, bool f32, const int32_t *cu, int dev, int sms, cudaStream_t s);
+cudaError_t launch_scan_back(const BackArgs &p, bool f32, const int32_t *cu, int *parts, int dev, int sms, cudaStream_t s);
 
 }  // namespace glr
 }  // namespace kda

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from array import array
 
 import numpy as np
@@ -75,6 +76,9 @@ class kda_glr_params(ctypes.Structure):
 _GLR_ROWS, _GLR_GRADS = ("x", "a", "b", "g", "out"), ("x", "a", "b", "g", "dout", "dx", "da", "db", "dg")
 
 
+_PACK_GLR_ROWS, _PACK_GLR_GRADS = struct.Struct("5P5q").pack, struct.Struct("9P9q").pack
+
+
 class kda_glr_rows(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _GLR_ROWS] + [(n + "_stride", ctypes.c_int64) for n in _GLR_ROWS]
 
@@ -97,6 +101,9 @@ class kda_block_norm_rows(ctypes.Structure):
         [(n + "_stride", ctypes.c_int64) for n in ("x", "y", "g", "x_out", "h")]
 
 
+_NORM_ROWS = ("x", "y", "g", "x_out", "h")
+_PACK_NORM_ROWS, _PACK_NORM_GRADS = struct.Struct("6P5q").pack, struct.Struct("8P8q").pack
+_PACK_NORM_ROWS5 = struct.Struct("5P8x5q").pack  # without hs
 _NORM_GRADS = ("x_out", "dh", "dx1", "y", "g", "dx", "dy", "dg")
 
 
@@ -157,19 +164,19 @@ SIGNATURES = [
                                _VP, _VP, _I32, ctypes.POINTER(kda_gdr_rows), _VP, ctypes.c_size_t, _VP, _VP]),
     ("kda_glr_config", _I32, [ctypes.POINTER(kda_glr_config_t), _I32, _I32]),
     ("kda_glr_decode", _I32, [ctypes.POINTER(kda_glr_config_t), ctypes.POINTER(kda_glr_params), _VP, _I32, _VP, _VP, _I32, _I32,
-                              ctypes.POINTER(kda_glr_rows), _VP, _VP]),
+                              _VP, _VP, _VP]),
     ("kda_glr_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(kda_glr_config_t), _PI32, _I32]),
-    ("kda_glr_chunks", ctypes.c_int64, [_PI32, _I32]),
+    ("kda_glr_chunks", ctypes.c_int64, [_VP, _I32]),
     ("kda_glr_prefill", _I32, [ctypes.POINTER(kda_glr_config_t), ctypes.POINTER(kda_glr_params), _VP, _I32, _VP, _VP, _VP, _VP, _I32,
-                               ctypes.POINTER(kda_glr_rows), _VP, _VP, ctypes.c_size_t, _VP, _VP]),
+                               _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP]),
     ("kda_glr_backward", _I32, [ctypes.POINTER(kda_glr_config_t), ctypes.POINTER(kda_glr_params), _VP, _VP, _I32, _VP,
-                                ctypes.POINTER(kda_glr_grad_rows), _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP]),
+                                _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP]),
     ("kda_block_norm_config", _I32, [ctypes.POINTER(kda_block_norm_config_t), _I32, _I32]),
     ("kda_block_norm", _I32, [ctypes.POINTER(kda_block_norm_config_t), ctypes.POINTER(kda_block_norm_params), ctypes.c_int64,
-                              ctypes.POINTER(kda_block_norm_rows), _VP]),
+                              _VP, _VP]),
     ("kda_block_norm_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(kda_block_norm_config_t), ctypes.c_int64]),
     ("kda_block_norm_backward", _I32, [ctypes.POINTER(kda_block_norm_config_t), ctypes.POINTER(kda_block_norm_params), ctypes.c_int64,
-                                       ctypes.POINTER(kda_block_norm_grad_rows), _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+                                       _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     ("kda_photo_store_create", _I32, [_I32, ctypes.c_char_p, ctypes.POINTER(_VP)]),
     ("kda_photo_store_free", _I32, [_VP]),
     ("kda_photo_count", _I32, [_VP]),
@@ -679,41 +686,45 @@ def kda_glr_params_from(A_log: torch.Tensor, a_bias: torch.Tensor, b_bias: torch
     return p
 
 
-def _row_args(struct, names, tensors, T, width, dt, dev):
-    """The checked row struct: [T, width] tensors of dt on device dev, contiguous within a token (None: not given)."""
-    shape = (T, width)
-    ptrs, strides = [], []
-    for name, t in zip(names, tensors):
+def _row_args(pack, names, tensors, T, width, dt, dev):
+    """A row struct (as `pack` makes it: bytes), its pointers, then its strides, from checked tensors [T, width] of dt on device dev, contiguous
+    within a token (None: not given)."""
+    shape, ptrs, strides = (T, width), [], []
+    for i, t in enumerate(tensors):
         if t is None:
-            ptrs.append(None)
+            ptrs.append(0)
             strides.append(0)
             continue
-        if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.get_device() == dev and (T == 0 or t.stride(1) == 1)):
-            _check_row(name, t, T, width, dt, dev)
+        try:
+            step, one = t.stride()
+            ok = t.dtype is dt and t.shape == shape and t.get_device() == dev and one == 1
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            _check_row(names[i], t, T, width, dt, dev)
         ptrs.append(t.data_ptr())
-        strides.append(t.stride(0) if T > 1 else width)
-    return struct(*ptrs, *strides)
+        strides.append(step if T > 1 else width)
+    return pack(*ptrs, *strides)
+
+
+def _tuple(*v):
+    return v
 
 
 def _f32(name, t, dev, shape):
     return None if t is None else _ptr(name, t, _F32, dev, shape)
 
 
-def _glr_params_ok(cfg, params, dev) -> None:
+def _params_ok(cfg, params, dev) -> None:
     if params.dim != cfg.dim or params.device != dev:
         raise ValueError(f"the parameters must hold {cfg.dim} elements on cuda:{dev}, got {params.dim} on cuda:{params.device}")
 
 
-def _glr_call(cfg, params, S, src_slots, dst_slots, T, rows, err, dev):
-    """The checked pointers of a call over T tokens: S, src, dst, rows, err."""
-    _glr_params_ok(cfg, params, dev)
+def _states_ok(cfg, S, src_slots, dst_slots) -> None:
     if S.dim() != 2 or S.shape[1] != cfg.dim:
         raise ValueError(f"S must be [max_slots, {cfg.dim}], got {list(S.shape)}")
     if src_slots.numel() != dst_slots.numel():
         raise ValueError("src_slots and dst_slots must have the same length")
-    r = _row_args(kda_glr_rows, _GLR_ROWS, rows, T, cfg.dim, _BF16 if cfg.io_dtype == KDA_BF16 else _F32, dev)
-    return (_ptr("S", S, _F32, dev), _ptr("src_slots", src_slots, _I32T, dev), _ptr("dst_slots", dst_slots, _I32T, dev), r,
-            None if err is None else _ptr("err", err, _I32T, dev))
 
 
 def kda_glr_decode(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor,
@@ -722,8 +733,12 @@ def kda_glr_decode(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tenso
     read at src_slots (-1: zeros) and written at dst_slots."""
     dev = _current_device()
     B = src_slots.numel()
-    Sp, sp, dp, r, ep = _glr_call(cfg, params, S, src_slots, dst_slots, B * n, (x, a, b, g, out), err, dev)
-    st = lib().kda_glr_decode(cfg, params, Sp, S.shape[0], sp, dp, B, n, r, ep, _raw_stream(stream, dev))
+    _params_ok(cfg, params, dev)
+    _states_ok(cfg, S, src_slots, dst_slots)
+    r = _row_args(_PACK_GLR_ROWS, _GLR_ROWS, (x, a, b, g, out), B * n, cfg.dim, _F32 if cfg.io_dtype == KDA_F32 else _BF16, dev)
+    st = lib().kda_glr_decode(cfg, params, _ptr("S", S, _F32, dev), S.shape[0], _ptr("src_slots", src_slots, _I32T, dev),
+                              _ptr("dst_slots", dst_slots, _I32T, dev), B, n, r, None if err is None else _ptr("err", err, _I32T, dev),
+                              _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -736,25 +751,32 @@ def kda_glr_workspace_bytes(cfg: kda_glr_config_t, cu_seqlens_host) -> int:
     return need
 
 
+def _lengths(cu_seqlens_host):
+    """A host cu_seqlens as 32-bit numbers: what keeps them, their address, how many, and the last."""
+    if isinstance(cu_seqlens_host, (list, tuple)):
+        try:
+            a = array("i", cu_seqlens_host)
+            return a, a.buffer_info()[0], len(a), a[-1] if a else 0
+        except (OverflowError, TypeError):  # refused, or taken as other numbers, below
+            pass
+    a = _i32_array(cu_seqlens_host).reshape(-1)
+    return a, a.ctypes.data, len(a), int(a[-1]) if len(a) else 0
+
+
 def kda_glr_chunks(cu_seqlens_host) -> int:
     """Rows of the `starts` that a kda_glr_prefill of these sequences fills for its backward."""
-    cu_h, cu_p = _host_i32(cu_seqlens_host)
-    n = int(lib().kda_glr_chunks(cu_p, len(cu_h) - 1))
+    keep, at, count, _ = _lengths(cu_seqlens_host)
+    n = lib().kda_glr_chunks(at, count - 1)
     if n < 0:
         raise KdaError(KDA_ERR_INVALID, kda_last_error())
     return n
 
 
-def _glr_lengths(cu_seqlens_host, N):
-    cu_h = _i32_array(cu_seqlens_host)
-    if cu_h.shape != (N + 1,):
-        raise ValueError("cu_seqlens_host must hold N + 1 entries")
-    return cu_h
-
-
-def _glr_starts(cfg, starts, cu_h, dev):
+def _glr_starts(cfg, starts, at, N, dev):
     """The address of starts, of as many rows as the sequences' chunks or more."""
-    n = kda_glr_chunks(cu_h)
+    n = lib().kda_glr_chunks(at, N)
+    if n < 0:
+        raise KdaError(KDA_ERR_INVALID, kda_last_error())
     if starts.dim() != 2 or starts.shape[0] < n or starts.shape[1] != cfg.dim:
         raise ValueError(f"starts must be [{n}, {cfg.dim}] or longer, got {list(starts.shape)}")
     return _ptr("starts", starts, _F32, dev)
@@ -767,11 +789,16 @@ def kda_glr_prefill(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tens
     kda_glr_workspace_bytes(cfg, cu_seqlens_host) bytes; starts FP32 [kda_glr_chunks(cu_seqlens_host), dim] for a backward."""
     dev = _current_device()
     N = src_slots.numel()
-    cu_h = _glr_lengths(cu_seqlens_host, N)
-    Sp, sp, dp, r, ep = _glr_call(cfg, params, S, src_slots, dst_slots, int(cu_h[N]), (x, a, b, g, out), err, dev)
-    st = lib().kda_glr_prefill(cfg, params, Sp, S.shape[0], sp, dp, _ptr("cu_seqlens", cu_seqlens, _I32T, dev, (N + 1,)),
-                               cu_h.ctypes.data, N, r, None if starts is None else _glr_starts(cfg, starts, cu_h, dev),
-                               _ptr("workspace", workspace, None, dev), workspace.nbytes, ep, _raw_stream(stream, dev))
+    keep, at, count, T = _lengths(cu_seqlens_host)
+    if count != N + 1 or cu_seqlens.numel() != count:
+        raise ValueError("cu_seqlens and cu_seqlens_host must hold N + 1 entries")
+    _params_ok(cfg, params, dev)
+    _states_ok(cfg, S, src_slots, dst_slots)
+    r = _row_args(_PACK_GLR_ROWS, _GLR_ROWS, (x, a, b, g, out), T, cfg.dim, _F32 if cfg.io_dtype == KDA_F32 else _BF16, dev)
+    st = lib().kda_glr_prefill(cfg, params, _ptr("S", S, _F32, dev), S.shape[0], _ptr("src_slots", src_slots, _I32T, dev),
+                               _ptr("dst_slots", dst_slots, _I32T, dev), _ptr("cu_seqlens", cu_seqlens, _I32T, dev), at, N, r,
+                               None if starts is None else _glr_starts(cfg, starts, at, N, dev), _ptr("workspace", workspace, None, dev),
+                               workspace.nbytes, None if err is None else _ptr("err", err, _I32T, dev), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -782,18 +809,17 @@ def kda_glr_backward(cfg: kda_glr_config_t, params: kda_glr_params, cu_seqlens: 
     """The gradients of a kda_glr_prefill that filled `starts`: rows [T, dim] (dg None where g is), dS_last (None: zeros)
     and dS_first [N, dim], and FP32 sums over all tokens, dA_log, da_bias, db_bias [dim]; work as the prefill's workspace."""
     dev = _current_device()
-    N = cu_seqlens.numel() - 1
-    cu_h = _glr_lengths(cu_seqlens_host, N)
-    _glr_params_ok(cfg, params, dev)
-    r = _row_args(kda_glr_grad_rows, _GLR_GRADS, (x, a, b, g, dout, dx, da, db, dg), int(cu_h[N]), cfg.dim,
-                  _BF16 if cfg.io_dtype == KDA_BF16 else _F32, dev)
+    keep, at, count, T = _lengths(cu_seqlens_host)
+    N = count - 1
+    if cu_seqlens.numel() != count:
+        raise ValueError("cu_seqlens and cu_seqlens_host must hold N + 1 entries")
+    _params_ok(cfg, params, dev)
+    r = _row_args(_PACK_GLR_GRADS, _GLR_GRADS, (x, a, b, g, dout, dx, da, db, dg), T, cfg.dim, _F32 if cfg.io_dtype == KDA_F32 else _BF16, dev)
     vec, state = (cfg.dim,), (N, cfg.dim)
-    st = lib().kda_glr_backward(cfg, params, _ptr("cu_seqlens", cu_seqlens, _I32T, dev, (N + 1,)), cu_h.ctypes.data, N,
-                                _glr_starts(cfg, starts, cu_h, dev), r, _f32("dS_last", dS_last, dev, state),
-                                _f32("dS_first", dS_first, dev, state), _f32("dA_log", dA_log, dev, vec),
-                                _f32("da_bias", da_bias, dev, vec), _f32("db_bias", db_bias, dev, vec),
-                                _ptr("work", work, None, dev), work.nbytes, None if err is None else _ptr("err", err, _I32T, dev),
-                                _raw_stream(stream, dev))
+    st = lib().kda_glr_backward(cfg, params, _ptr("cu_seqlens", cu_seqlens, _I32T, dev), at, N, _glr_starts(cfg, starts, at, N, dev), r,
+                                _f32("dS_last", dS_last, dev, state), _f32("dS_first", dS_first, dev, state), _f32("dA_log", dA_log, dev, vec),
+                                _f32("da_bias", da_bias, dev, vec), _f32("db_bias", db_bias, dev, vec), _ptr("work", work, None, dev),
+                                work.nbytes, None if err is None else _ptr("err", err, _I32T, dev), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -810,31 +836,20 @@ def kda_block_norm_params_from(post_w: torch.Tensor, scale: torch.Tensor, pre_w:
     return p
 
 
-def _norm_params_ok(cfg, params, dev) -> None:
-    if params.dim != cfg.dim or params.device != dev:
-        raise ValueError(f"the parameters must hold {cfg.dim} elements on cuda:{dev}, got {params.dim} on cuda:{params.device}")
-
-
 def kda_block_norm(cfg: kda_block_norm_config_t, params: kda_block_norm_params, x, y=None, g=None, x_out=None, h=None, hs=None,
                    stream=None) -> None:
     """x_out = x + scale sigmoid(g) post_w y / rms(y) and h = pre_w x_out / rms(x_out) for rows [M, dim], contiguous within
     a row; without y only h of x, without h only x_out. h in the rows' type, or float8_e4m3fn with hs FP32 [M, ceil(dim / 128)]."""
     dev = _current_device()
-    _norm_params_ok(cfg, params, dev)
+    _params_ok(cfg, params, dev)
     M, D = x.shape[0], cfg.dim
-    dt = _BF16 if cfg.io_dtype == KDA_BF16 else _F32
-    ptrs, strides = [], []
-    for name, t in (("x", x), ("y", y), ("g", g), ("x_out", x_out), ("h", h)):
-        if t is None:
-            ptrs.append(None)
-            strides.append(0)
-            continue
-        want = _F8 if name == "h" and hs is not None else dt
-        if not (isinstance(t, torch.Tensor) and t.dtype is want and t.shape == (M, D) and t.get_device() == dev and (M == 0 or t.stride(1) == 1)):
-            _check_row(name, t, M, D, want, dev)
-        ptrs.append(t.data_ptr())
-        strides.append(t.stride(0) if M > 1 else D)
-    r = kda_block_norm_rows(*ptrs, _f32("hs", hs, dev, (M, -(-D // 128))), *strides)
+    dt = _F32 if cfg.io_dtype == KDA_F32 else _BF16
+    if hs is None:
+        r = _row_args(_PACK_NORM_ROWS5, _NORM_ROWS, (x, y, g, x_out, h), M, D, dt, dev)
+    else:
+        e = _row_args(_tuple, ("h",), (h,), M, D, _F8, dev)
+        p = _row_args(_tuple, _NORM_ROWS, (x, y, g, x_out), M, D, dt, dev)
+        r = _PACK_NORM_ROWS(*p[:4], e[0], _f32("hs", hs, dev, (M, -(-D // 128))), *p[4:], e[1])
     st = lib().kda_block_norm(cfg, params, M, r, _raw_stream(stream, dev))
     if st:
         _check(st)
@@ -853,9 +868,9 @@ def kda_block_norm_backward(cfg: kda_block_norm_config_t, params: kda_block_norm
     x_out from elsewhere, dx1 (None: zeros): rows dx, dy, dg [M, dim] and sums over the rows dpost_w, dscale, dpre_w FP32
     [dim], each or None; work of at least kda_block_norm_workspace_bytes(cfg, M) bytes."""
     dev = _current_device()
-    _norm_params_ok(cfg, params, dev)
-    r = _row_args(kda_block_norm_grad_rows, _NORM_GRADS, (x_out, dh, dx1, y, g, dx, dy, dg), dx.shape[0], cfg.dim,
-                  _BF16 if cfg.io_dtype == KDA_BF16 else _F32, dev)
+    _params_ok(cfg, params, dev)
+    r = _row_args(_PACK_NORM_GRADS, _NORM_GRADS, (x_out, dh, dx1, y, g, dx, dy, dg), dx.shape[0], cfg.dim,
+                  _F32 if cfg.io_dtype == KDA_F32 else _BF16, dev)
     vec = (cfg.dim,)
     st = lib().kda_block_norm_backward(cfg, params, dx.shape[0], r, _f32("dpost_w", dpost_w, dev, vec), _f32("dscale", dscale, dev, vec),
                                        _f32("dpre_w", dpre_w, dev, vec), _ptr("work", work, None, dev), work.nbytes,
