@@ -12,41 +12,53 @@ namespace kda {
 namespace glr {
 namespace {
 
-// One thread, two channels of one row, through n tokens from row t0 on.
-template <typename T, bool G>
-__device__ __forceinline__ void walk(const Args &p, int src, int dst, int c, int64_t t0, int n)
-{
-    Chan ch;
-    ch.load(p.A_log, p.a_bias, p.b_bias, c);
-    const T *xp = static_cast<const T *>(p.rows.x) + c, *ap = static_cast<const T *>(p.rows.a) + c;
-    const T *bp = static_cast<const T *>(p.rows.b) + c, *gp = static_cast<const T *>(p.rows.g) + c;
-    T *op = static_cast<T *>(p.rows.out) + c;
-    float2 h = src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
-    for (int i = 0; i < n; ++i) {
-        const int64_t t = t0 + i;
-        float2 e, u;
-        gates(ch, Pair<T>::get(ld_pair(xp + t * p.rows.x_stride)), Pair<T>::get(ld_pair(ap + t * p.rows.a_stride)),
-              Pair<T>::get(ld_pair(bp + t * p.rows.b_stride)), e, u);
-        h = step(h, e, u);
-        float2 o = h;
-        if (G) o = f2_mul(o, silu2(Pair<T>::get(ld_pair(gp + t * p.rows.g_stride))));
-        st_pair(op + t * p.rows.out_stride, o);
-    }
-    *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = h;
-}
-
-template <typename T, bool G>
+// Decode: one thread has two channels of one row through its n <= N tokens, all of which it asks for before it begins.
+template <typename T, bool G, int N>
 __global__ void __launch_bounds__(128) glr_decode_kernel(const __grid_constant__ Args p)
 {
     const int half = p.D / 2, unit = blockIdx.x * 128 + threadIdx.x;
     const int row = unit / half, c = 2 * (unit - row * half);
     if (row >= p.N) return;
     int src, dst;
-    if (!slots_ok(p, row, src, dst)) {
+    const bool ok = slots_ok(p, row, src, dst);
+    const int64_t t0 = (int64_t)row * p.n;
+    const T *xp = static_cast<const T *>(p.rows.x) + t0 * p.rows.x_stride + c, *ap = static_cast<const T *>(p.rows.a) + t0 * p.rows.a_stride + c;
+    const T *bp = static_cast<const T *>(p.rows.b) + t0 * p.rows.b_stride + c, *gp = G ? static_cast<const T *>(p.rows.g) + t0 * p.rows.g_stride + c : nullptr;
+    T *op = static_cast<T *>(p.rows.out) + t0 * p.rows.out_stride + c;
+    typename Pair<T>::Raw x[N], a[N], b[N], g[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < p.n) {
+            x[i] = ld_pair(xp + i * p.rows.x_stride);
+            a[i] = ld_pair(ap + i * p.rows.a_stride);
+            b[i] = ld_pair(bp + i * p.rows.b_stride);
+            if (G) g[i] = ld_pair(gp + i * p.rows.g_stride);
+        }
+    if (!ok) {
         if (c == 0) set_err(p.err);
         return;
     }
-    walk<T, G>(p, src, dst, c, (int64_t)row * p.n, p.n);
+    float2 h = src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
+    Chan ch;
+    ch.load(p.A_log, p.a_bias, p.b_bias, c);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < p.n) {
+            float2 e, u;
+            gates(ch, Pair<T>::get(x[i]), Pair<T>::get(a[i]), Pair<T>::get(b[i]), e, u);
+            h = step(h, e, u);
+            st_pair(op + i * p.rows.out_stride, G ? f2_mul(h, silu2(Pair<T>::get(g[i]))) : h);
+        }
+    *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = h;
+}
+
+template <typename T, bool G>
+void launch_decode(const Args &p, unsigned blocks, cudaStream_t s)
+{
+    if (p.n == 1) glr_decode_kernel<T, G, 1><<<blocks, 128, 0, s>>>(p);
+    else if (p.n == 2) glr_decode_kernel<T, G, 2><<<blocks, 128, 0, s>>>(p);
+    else if (p.n <= 4) glr_decode_kernel<T, G, 4><<<blocks, 128, 0, s>>>(p);
+    else glr_decode_kernel<T, G, 8><<<blocks, 128, 0, s>>>(p);
 }
 
 __global__ void __launch_bounds__(kSumCols *kSumGroups) glr_param_sums_kernel(const float *part, int rows, int D, float *dA_log, float *da_bias, float *db_bias)
@@ -185,11 +197,11 @@ kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *par
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = cfg->io_dtype == KDA_F32;
     if (rows->g) {
-        if (f32) glr::glr_decode_kernel<float, true><<<(unsigned)blocks, 128, 0, s>>>(p);
-        else glr::glr_decode_kernel<__nv_bfloat16, true><<<(unsigned)blocks, 128, 0, s>>>(p);
+        if (f32) glr::launch_decode<float, true>(p, (unsigned)blocks, s);
+        else glr::launch_decode<__nv_bfloat16, true>(p, (unsigned)blocks, s);
     } else {
-        if (f32) glr::glr_decode_kernel<float, false><<<(unsigned)blocks, 128, 0, s>>>(p);
-        else glr::glr_decode_kernel<__nv_bfloat16, false><<<(unsigned)blocks, 128, 0, s>>>(p);
+        if (f32) glr::launch_decode<float, false>(p, (unsigned)blocks, s);
+        else glr::launch_decode<__nv_bfloat16, false>(p, (unsigned)blocks, s);
     }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_decode: %s", cudaGetErrorString(e));

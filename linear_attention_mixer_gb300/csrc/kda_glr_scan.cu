@@ -78,11 +78,14 @@ struct Exchange {
     }
 };
 
-// From a warp's own pair, what comes before its tokens in the window (back: behind them), applied to `carry`, the state at
-// the window's start; carry becomes that at its end. `turn`: windows so far; good: no wait has given up (then
-// nothing more is sent or waited for). All threads of the cluster take part.
+// Joining the pairs of a window's warps, in two parts, so that a warp has something to do while they travel.
+// post: this warp's own pair goes to the others. Returns what comes before its tokens within the block (BACK: behind them)
+// and, in a cluster, sends the block's pair to all its blocks; without one `all` becomes it.
+// meet: the state before the warp's tokens (behind them), from `carry`, that at the window's start, which becomes that at its end.
+// `turn`: windows so far; good: no wait has given up (then nothing more is sent or waited for). All threads of the cluster
+// take part.
 template <bool BACK, int W, int MAX>
-__device__ __forceinline__ float2 join(Exchange<W, MAX> &ex, const Lin &own, float2 &carry, int turn, int nc, int rank, bool &good)
+__device__ __forceinline__ Lin post(Exchange<W, MAX> &ex, const Lin &own, Lin &all, int turn, int nc, int rank, bool good)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, par = turn & 1;
     ex.warp[par][warp][lane] = as_float4(own);
@@ -95,14 +98,23 @@ __device__ __forceinline__ float2 join(Exchange<W, MAX> &ex, const Lin &own, flo
         if (w == warp) pre = run;
         run.then(ld_lin(&ex.warp[par][w][lane]));
     }
+    all = run;
+    if (nc > 1) {
+        if (turn == 0) cluster_wait();  // every block of the cluster runs and has its barriers: theirs is the arrival at the start
+        if (good)
+            for (int r = warp; r < nc; r += W) st_remote(&ex.block[par][rank][lane], &ex.bar[par], r, as_float4(run));
+    }
+    return pre;
+}
+template <bool BACK, int W, int MAX>
+__device__ __forceinline__ float2 meet(Exchange<W, MAX> &ex, const Lin &pre, const Lin &all, float2 &carry, int turn, int nc, int rank, bool &good)
+{
+    const int lane = threadIdx.x & 31, par = turn & 1;
     if (nc == 1) {
         const float2 h = pre.at(carry);
-        carry = run.at(carry);
+        carry = all.at(carry);
         return h;
     }
-    if (turn == 0) cluster_wait();  // every block of the cluster runs and has its barriers: theirs is the arrival at the start
-    if (good)
-        for (int r = warp; r < nc; r += W) st_remote(&ex.block[par][rank][lane], &ex.bar[par], r, as_float4(run));
     if (good) good = wait_cluster(&ex.bar[par], (uint32_t)(turn >> 1) & 1);
     float2 h = carry, mine = carry;
 #pragma unroll
@@ -140,22 +152,31 @@ template <typename T> __device__ __forceinline__ void advance(T *&p, int64_t n)
     p += n;
     asm volatile("" : "+l"(p));
 }
-// Copies of 16 rows of 64 channels, asked for by 16-byte units; what lies past the sequence or past the row's end is 0.
-template <typename T>
+__device__ __forceinline__ void cp_async16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Copies of R rows of 64 channels, asked for by 16-byte units; what lies past the sequence or past the row's end is 0.
+template <typename T, int R>
 struct Tile {
     static constexpr int kUnits = kSlab * (int)sizeof(T) / 16;  // of a row
     static constexpr int kRowsAt = 32 / kUnits;                 // rows that a warp asks for at once
-    static constexpr int kBytes = kChunk * kSlab * (int)sizeof(T);
+    static constexpr int kBytes = R * kSlab * (int)sizeof(T);
 
     // row0: the first row's place in the slab, of nv rows that exist
     static __device__ __forceinline__ void fetch(unsigned char *to, const T *row0, int64_t stride, int nv, bool col_ok)
     {
         const int lane = threadIdx.x & 31, r0 = lane / kUnits;
         const T *at = row0 + r0 * stride + (16 / (int)sizeof(T)) * (lane % kUnits);
+        if (nv >= R && col_ok) {  // all of this lane's rows
 #pragma unroll
-        for (int i = 0; i < kChunk / kRowsAt; ++i, advance(at, kRowsAt * stride)) {
+            for (int i = 0; i < R / kRowsAt; ++i, advance(at, kRowsAt * stride)) cp_async16(to + (size_t)(lane + 32 * i) * 16, at);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < R / kRowsAt; ++i, advance(at, kRowsAt * stride)) {
             const bool ok = col_ok && r0 + i * kRowsAt < nv;
-            cp_async16(to + (size_t)(lane + 32 * i) * 16, ok ? at : row0, ok ? 16 : 0);
+            kda::cp_async16(to + (size_t)(lane + 32 * i) * 16, ok ? at : row0, ok ? 16 : 0);
         }
     }
     static __device__ __forceinline__ float2 get(const unsigned char *tile, int r)
@@ -165,40 +186,25 @@ struct Tile {
 };
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// e and u of a warp's 16 tokens. One reciprocal serves both sigmoids: with P = (1 + exp(-a')) (1 + exp(-b')) sigmoid(a') is
-// (1 + exp(-b')) / P. Where a P is not below 2^126 (a gate closed by more than about 40, or a NaN; their sum shows it), or where
-// exp(A_log) is above 87 (`wild`), all are worked out with a reciprocal each and a decay's logarithm cut at -87.
-template <typename T>
-__device__ __forceinline__ void all_gates(const Chan &ch, bool wild, const unsigned char *x, const unsigned char *a, const unsigned char *b,
-                                          float2 (&e)[kChunk], float2 (&u)[kChunk])
+// e and u of a warp's R tokens. (A reciprocal each for the two sigmoids: one for their product costs five multiplications
+// and a test of its range, which is more than the special function unit's time for another; 574 us for 535.)
+template <typename T, int R>
+__device__ __forceinline__ void all_gates(const Chan &ch, const unsigned char *x, const unsigned char *a, const unsigned char *b,
+                                          float2 (&e)[R], float2 (&u)[R])
 {
-    float2 sum = f2(0.f);
 #pragma unroll
-    for (int t = 0; t < kChunk; ++t) {
-        const float2 pa = f2_add(neg_exp(Tile<T>::get(a, t), ch.ca), f2(1.f)), pb = f2_add(neg_exp(Tile<T>::get(b, t), ch.cb), f2(1.f));
-        const float2 P = f2_mul(pa, pb), r = rcp2(P);
-        sum = f2_add(sum, P);
-        e[t] = expm1_from_87(f2_mul(ch.nA, f2_mul(pb, r)));
-        const float2 z = one_less_square(e[t]);
-        u[t] = f2_mul(f2_mul(f2_mul(z, rsqrt2(z)), f2_mul(pa, r)), Tile<T>::get(x, t));
-    }
-    if (wild || !(sum.x < kHuge && sum.y < kHuge)) {  // one token at a time, and back into registers
-        float2 le[kChunk], lu[kChunk];
-#pragma unroll 1
-        for (int t = 0; t < kChunk; ++t) gates(ch, Tile<T>::get(x, t), Tile<T>::get(a, t), Tile<T>::get(b, t), le[t], lu[t]);
-#pragma unroll
-        for (int t = 0; t < kChunk; ++t) e[t] = le[t], u[t] = lu[t];
-    }
+    for (int t = 0; t < R; ++t) gates(ch, Tile<T, R>::get(x, t), Tile<T, R>::get(a, t), Tile<T, R>::get(b, t), e[t], u[t]);
     __syncwarp();
 }
 
 // ---------------------------------------------------------------- prefill
-template <typename T, bool G, int W>
-__global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
+template <typename T, bool G, int W, int R>
+__global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ Exchange<W, max_cluster<T>()> ex;
     constexpr int kTiles = G ? 4 : 3;
+    using Tl = Tile<T, R>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
     const int row = cid / slabs, c0 = (cid - row * slabs) * kSlab, c = c0 + 2 * lane;
@@ -219,11 +225,10 @@ __global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const 
         bool good = true;
         Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
         if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
-        const bool wild = !(fminf(ch.nA.x, ch.nA.y) >= -87.f);
-        unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T>::kBytes, *ta = tx + Tile<T>::kBytes, *tb = ta + Tile<T>::kBytes, *tg = tb + Tile<T>::kBytes;
-        const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T>::kUnits) < p.D;
-        const int window = kChunk * W * nc;
-        int t = kChunk * (rank * W + warp);  // this warp's first token of the window
+        unsigned char *tx = smem + (size_t)warp * kTiles * Tl::kBytes, *ta = tx + Tl::kBytes, *tb = ta + Tl::kBytes, *tg = tb + Tl::kBytes;
+        const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tl::kUnits) < p.D;
+        const int window = R * W * nc;
+        int t = R * (rank * W + warp);  // this warp's first token of the window
         const T *xp = static_cast<const T *>(p.rows.x) + (int64_t)s0 * p.rows.x_stride + c0, *ap = static_cast<const T *>(p.rows.a) + (int64_t)s0 * p.rows.a_stride + c0;
         const T *bp = static_cast<const T *>(p.rows.b) + (int64_t)s0 * p.rows.b_stride + c0, *gp = G ? static_cast<const T *>(p.rows.g) + (int64_t)s0 * p.rows.g_stride + c0 : nullptr;
         T *op = static_cast<T *>(p.rows.out) + (int64_t)s0 * p.rows.out_stride + c;
@@ -231,14 +236,14 @@ __global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const 
         auto fetch = [&](int at) {
             const int nv = len - at;
             if (nv > 0) {
-                Tile<T>::fetch(tx, xp + at * p.rows.x_stride, p.rows.x_stride, nv, col_ok);
-                Tile<T>::fetch(ta, ap + at * p.rows.a_stride, p.rows.a_stride, nv, col_ok);
-                Tile<T>::fetch(tb, bp + at * p.rows.b_stride, p.rows.b_stride, nv, col_ok);
+                Tl::fetch(tx, xp + at * p.rows.x_stride, p.rows.x_stride, nv, col_ok);
+                Tl::fetch(ta, ap + at * p.rows.a_stride, p.rows.a_stride, nv, col_ok);
+                Tl::fetch(tb, bp + at * p.rows.b_stride, p.rows.b_stride, nv, col_ok);
             }
             commit();
         };
         auto fetch_g = [&](int at) {
-            if (G && len - at > 0) Tile<T>::fetch(tg, gp + at * p.rows.g_stride, p.rows.g_stride, len - at, col_ok);
+            if (G && len - at > 0) Tl::fetch(tg, gp + at * p.rows.g_stride, p.rows.g_stride, len - at, col_ok);
             commit();
         };
         fetch(t);
@@ -246,33 +251,43 @@ __global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const 
         const int windows = (len + window - 1) / window;
 #pragma unroll 1
         for (int k = 0; k < windows; ++k, t += window) {
-            const int nv = min(kChunk, len - t);  // <= 0 behind the sequence's end
-            float2 e[kChunk], u[kChunk];
+            const int nv = min(R, len - t);  // <= 0 behind the sequence's end
+            float2 e[R], u[R];
             cp_async_wait_all();
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
-                all_gates<T>(ch, wild, tx, ta, tb, e, u);
-                if (nv < kChunk)
+                all_gates<T, R>(ch, tx, ta, tb, e, u);
+                if (nv < R)
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i)
+                    for (int i = 0; i < R; ++i)
                         if (i >= nv) e[i] = u[i] = f2(0.f);
                 fetch(t + window);
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) {
+                for (int i = 0; i < R; ++i) {
                     own.H = step(own.H, e[i], u[i]);
                     own.A = f2_fma(own.A, e[i], own.A);
                 }
             }
-            float2 h = join<false>(ex, own, carry, k, nc, rank, good);
+            Lin all;
+            const Lin pre = post<false>(ex, own, all, k, nc, rank, good);
+            float2 h = meet<false>(ex, pre, all, carry, k, nc, rank, good);
             if (nv > 0) {
                 if (live) {
-                    if (st) *reinterpret_cast<float2 *>(st + (size_t)(t / kChunk) * p.D) = h;
+                    if (st && (R == kChunk || t % kChunk == 0)) *reinterpret_cast<float2 *>(st + (size_t)(t / kChunk) * p.D) = h;
                     T *o = op + t * p.rows.out_stride;
+                    if (nv == R) {
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i, advance(o, p.rows.out_stride)) {
-                        h = step(h, e[i], u[i]);
-                        if (i < nv) st_pair(o, G ? f2_mul(h, silu2(Tile<T>::get(tg, i))) : h);
+                        for (int i = 0; i < R; ++i, advance(o, p.rows.out_stride)) {
+                            h = step(h, e[i], u[i]);
+                            st_pair(o, G ? f2_mul(h, silu2(Tl::get(tg, i))) : h);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < R; ++i, advance(o, p.rows.out_stride)) {
+                            h = step(h, e[i], u[i]);
+                            if (i < nv) st_pair(o, G ? f2_mul(h, silu2(Tl::get(tg, i))) : h);
+                        }
                     }
                 }
                 __syncwarp();
@@ -288,15 +303,15 @@ __global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const 
 template <typename T, bool G>
 cudaError_t launch_scan_t(const Args &p, const int32_t *cu, int dev, int sms, cudaStream_t s)
 {
-    constexpr int W = scan_warps<T>();
+    constexpr int W = scan_warps<T>(), R = scan_rows<T>();
     static std::atomic<uint64_t> raised;
     static ClusterRoom room;
-    const int smem = W * (G ? 4 : 3) * Tile<T>::kBytes;
-    const cudaError_t e = raise_smem_on(raised, dev, glr_scan_kernel<T, G, W>, smem);
+    const int smem = W * (G ? 4 : 3) * Tile<T, R>::kBytes;
+    const cudaError_t e = raise_smem_on(raised, dev, glr_scan_kernel<T, G, W, R>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;
-    const int nc = choose_cluster(cu, p.N, p.N, slabs, kChunk * W, max_cluster<T>(), sms, [&](int n) { return room.of(glr_scan_kernel<T, G, W>, n, 32 * W, smem, dev); });
-    return launch_cluster(glr_scan_kernel<T, G, W>, (unsigned)(p.N * slabs * nc), nc, 32 * W, smem, s, p, nc);
+    const int nc = choose_cluster(cu, p.N, p.N, slabs, R * W, max_cluster<T>(), sms, [&](int n) { return room.of(glr_scan_kernel<T, G, W, R>, n, 32 * W, smem, dev); });
+    return launch_cluster(glr_scan_kernel<T, G, W, R>, (unsigned)(p.N * slabs * nc), nc, 32 * W, smem, s, p, nc);
 }
 
 // ---------------------------------------------------------------- backward
@@ -316,10 +331,9 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
     const bool live = c < p.D;
     Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
     if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
-    const bool wild = !(fminf(ch.nA.x, ch.nA.y) >= -87.f);
-    unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T>::kBytes, *ta = tx + Tile<T>::kBytes, *tb = ta + Tile<T>::kBytes;
-    unsigned char *td = tb + Tile<T>::kBytes, *tg = td + Tile<T>::kBytes;
-    const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T>::kUnits) < p.D;
+    unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T, kChunk>::kBytes, *ta = tx + Tile<T, kChunk>::kBytes, *tb = ta + Tile<T, kChunk>::kBytes;
+    unsigned char *td = tb + Tile<T, kChunk>::kBytes, *tg = td + Tile<T, kChunk>::kBytes;
+    const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T, kChunk>::kUnits) < p.D;
     const int window = kChunk * W * nc, own_t = kChunk * (rank * W + warp);
     float2 sA = f2(0.f), sa = sA, sb = sA;
     int turn = 0;
@@ -347,11 +361,11 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
             const int nv = len - at;
             const int64_t r = (int64_t)s0 + at;
             if (nv > 0) {
-                Tile<T>::fetch(tx, static_cast<const T *>(p.rows.x) + r * p.rows.x_stride + c0, p.rows.x_stride, nv, col_ok);
-                Tile<T>::fetch(ta, static_cast<const T *>(p.rows.a) + r * p.rows.a_stride + c0, p.rows.a_stride, nv, col_ok);
-                Tile<T>::fetch(tb, static_cast<const T *>(p.rows.b) + r * p.rows.b_stride + c0, p.rows.b_stride, nv, col_ok);
-                Tile<T>::fetch(td, static_cast<const T *>(p.rows.dout) + r * p.rows.dout_stride + c0, p.rows.dout_stride, nv, col_ok);
-                if (G) Tile<T>::fetch(tg, static_cast<const T *>(p.rows.g) + r * p.rows.g_stride + c0, p.rows.g_stride, nv, col_ok);
+                Tile<T, kChunk>::fetch(tx, static_cast<const T *>(p.rows.x) + r * p.rows.x_stride + c0, p.rows.x_stride, nv, col_ok);
+                Tile<T, kChunk>::fetch(ta, static_cast<const T *>(p.rows.a) + r * p.rows.a_stride + c0, p.rows.a_stride, nv, col_ok);
+                Tile<T, kChunk>::fetch(tb, static_cast<const T *>(p.rows.b) + r * p.rows.b_stride + c0, p.rows.b_stride, nv, col_ok);
+                Tile<T, kChunk>::fetch(td, static_cast<const T *>(p.rows.dout) + r * p.rows.dout_stride + c0, p.rows.dout_stride, nv, col_ok);
+                if (G) Tile<T, kChunk>::fetch(tg, static_cast<const T *>(p.rows.g) + r * p.rows.g_stride + c0, p.rows.g_stride, nv, col_ok);
             }
             commit();
         };
@@ -366,19 +380,23 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
-                all_gates<T>(ch, wild, tx, ta, tb, e, u);
+                all_gates<T, kChunk>(ch, tx, ta, tb, e, u);
                 if (nv < kChunk)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i)
                         if (i >= nv) e[i] = u[i] = f2(0.f);
 #pragma unroll
                 for (int i = kChunk - 1; i >= 0; --i) {  // the rows of dout past the end are 0
-                    float2 dh = Tile<T>::get(td, i);
-                    if (G) dh = f2_mul(dh, silu2(Tile<T>::get(tg, i)));
+                    float2 dh = Tile<T, kChunk>::get(td, i);
+                    if (G) dh = f2_mul(dh, silu2(Tile<T, kChunk>::get(tg, i)));
                     own.H = f2_add(own.H, dh);
                     own.H = f2_fma(e[i], own.H, own.H);
                     own.A = f2_fma(own.A, e[i], own.A);
                 }
+            }
+            Lin all;
+            const Lin pre = post<true>(ex, own, all, turn, nc, rank, good);
+            if (nv > 0) {
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {  // u: the state before the token
                     const float2 before = h;
@@ -386,7 +404,7 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
                     u[i] = before;
                 }
             }
-            float2 lc = join<true>(ex, own, carry, turn, nc, rank, good);
+            float2 lc = meet<true>(ex, pre, all, carry, turn, nc, rank, good);
             if (nv > 0) {
                 const int64_t r = (int64_t)s0 + t + nv - 1;
                 T *dxp = static_cast<T *>(p.rows.dx) + r * p.rows.dx_stride + c, *dap = static_cast<T *>(p.rows.da) + r * p.rows.da_stride + c;
@@ -395,14 +413,14 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
 #pragma unroll
                 for (int i = kChunk - 1; i >= 0; --i) {
                     if (i < nv) {
-                        const float2 x = Tile<T>::get(tx, i);
-                        float2 dh = Tile<T>::get(td, i);
+                        const float2 x = Tile<T, kChunk>::get(tx, i);
+                        float2 dh = Tile<T, kChunk>::get(td, i);
                         Back bk;
-                        bk.gates(ch, e[i], Tile<T>::get(ta, i), Tile<T>::get(tb, i));
+                        bk.gates(ch, e[i], Tile<T, kChunk>::get(ta, i), Tile<T, kChunk>::get(tb, i));
                         if (G) {
-                            const float2 g = Tile<T>::get(tg, i);
-                            const float2 E = neg_exp(g, f2(0.f)), s = rcp2(f2_add(E, f2(1.f)));
-                            const float2 ns = one_less(s, E);
+                            const float2 g = Tile<T, kChunk>::get(tg, i);
+                            float2 s, ns;
+                            both_sigmoids(neg_exp(g, f2(0.f)), s, ns);
                             if (live) st_pair(dgp, f2_mul(f2_mul(dh, h), f2_mul(s, f2_fma(g, ns, f2(1.f)))));
                             advance(dgp, -p.rows.dg_stride);
                             dh = f2_mul(dh, f2_mul(g, s));
@@ -456,7 +474,7 @@ cudaError_t launch_back_t(const BackArgs &p, const int32_t *cu, int *parts, int 
     constexpr int W = kBackWarps;
     static std::atomic<uint64_t> raised;
     static ClusterRoom room;
-    const int smem = W * (G ? 5 : 4) * Tile<T>::kBytes;
+    const int smem = W * (G ? 5 : 4) * Tile<T, kChunk>::kBytes;
     const cudaError_t e = raise_smem_on(raised, dev, glr_back_kernel<T, G, W>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;
