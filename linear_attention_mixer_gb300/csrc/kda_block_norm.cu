@@ -91,9 +91,22 @@ struct W8 {
         r[1] = c + 4 < D ? __ldg(reinterpret_cast<const float4 *>(p + c) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __device__ __forceinline__ float2 get(int i) const { return i & 1 ? make_float2(r[i >> 1].z, r[i >> 1].w) : make_float2(r[i >> 1].x, r[i >> 1].y); }
+    __device__ __forceinline__ W8 times(const W8 &o) const
+    {
+        return W8{{make_float4(r[0].x * o.r[0].x, r[0].y * o.r[0].y, r[0].z * o.r[0].z, r[0].w * o.r[0].w),
+                   make_float4(r[1].x * o.r[1].x, r[1].y * o.r[1].y, r[1].z * o.r[1].z, r[1].w * o.r[1].w)}};
+    }
 };
 
 __device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
+// sigmoid(g) and 1 - sigmoid(g) = exp(-g) sigmoid(g), without the difference; where sigmoid(g) is 0 the second is not used
+__device__ __forceinline__ float2 both_sigmoids(float2 g, float2 &ns)
+{
+    constexpr float kHuge = 8.507059173023462e37f;  // 2^126
+    const float2 E = make_float2(exp_ftz(-g.x), exp_ftz(-g.y)), s = make_float2(rcp_ftz(1.f + E.x), rcp_ftz(1.f + E.y));
+    ns = make_float2(fminf(E.x, kHuge) * s.x, fminf(E.y, kHuge) * s.y);
+    return s;
+}
 __device__ __forceinline__ float2 sigmoid2(float2 g) { return make_float2(sigmoid_ftz(g.x), sigmoid_ftz(g.y)); }
 
 // Sums over the NT threads that have a row; each thread gets them. A block of more than one warp has one row.
@@ -117,67 +130,60 @@ __device__ __forceinline__ void row_sum(float (&s)[K], float (*sh)[K])
     }
 }
 
-template <typename T, int NT, int VPT, bool F8>
-__global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_kernel(const __grid_constant__ Args p)
+// What rows a call has: known to the compiler where it has all of them (kAll with a gate, kNoGate without), else asked (kAny).
+enum { kAny, kNoGate, kAll };
+
+// What is done to a row once its channels are in registers. W: pairs of the parameters of vector i: post_w times scale, and
+// pre_w. sh: room for two sums a warp.
+template <int HAS, typename T, int NT, int VPT, bool F8, typename PostW, typename PreW>
+__device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, V8<T> (&x)[VPT], const V8<T> (&y)[VPT], const V8<T> (&g)[VPT],
+                                           float (*sh0)[1], float (*sh1)[1], PostW post_w, PreW pre_w)
 {
-    constexpr int kRows = NT == 32 ? 4 : 1;
-    __shared__ float sh[2][32][1];
-    const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = (int64_t)blockIdx.x * kRows + (NT == 32 ? threadIdx.x >> 5 : 0);
-    if (row >= p.M) return;  // a whole warp
-    V8<T> x[VPT], y[VPT], g[VPT];
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (c < p.D) {
-            load8(x[i], p.r.x, row * p.r.x_stride + c, c, p.D);
-            if (p.r.y) load8(y[i], p.r.y, row * p.r.y_stride + c, c, p.D);
-            if (p.r.g) load8(g[i], p.r.g, row * p.r.g_stride + c, c, p.D);
-        }
-    }
     const float inv_D = 1.f / p.D;
-    if (p.r.y) {
-        float2 q = f2(0.f);
+    const bool has_y = HAS != kAny || p.r.y, has_g = HAS == kAny ? p.r.g != nullptr : HAS == kAll, has_h = HAS != kAny || p.r.h;
+    float s[1] = {0.f};
+    float2 q = f2(0.f);
+    if (has_y) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (8 * (tid + i * NT) < p.D)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q = f2_fma(y[i].get(j), y[i].get(j), q);
         s[0] = q.x + q.y;
-        row_sum<NT, 1>(s, sh[0]);
+        row_sum<NT, 1>(s, sh0);
     }
     const float ry = rsqrtf(fmaf(s[0], inv_D, p.eps));
-    float2 f[VPT][4], q = f2(0.f);
+    float2 f[VPT][4];
+    q = f2(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = 8 * (tid + i * NT);
         if (c >= p.D) continue;
-        W8 w, sc;
-        if (p.r.y) w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
+        W8 w;
+        if (has_y) w = post_w(i, c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f[i][j] = x[i].get(j);
-            if (p.r.y) {
-                float2 t = f2_mul(sc.get(j), f2_mul(w.get(j), f2_mul(y[i].get(j), f2(ry))));
-                if (p.r.g) t = f2_mul(t, sigmoid2(g[i].get(j)));
+            if (has_y) {
+                float2 t = f2_mul(w.get(j), f2_mul(y[i].get(j), f2(ry)));
+                if (has_g) t = f2_mul(t, sigmoid2(g[i].get(j)));
                 f[i][j] = f2_add(f[i][j], t);
                 x[i].set(j, f[i][j]);
             }
             q = f2_fma(f[i][j], f[i][j], q);
         }
-        if (p.r.x_out) store8(x[i], p.r.x_out, row * p.r.x_out_stride + c, c, p.D);
+        if (has_y) store8(x[i], p.r.x_out, row * p.r.x_out_stride + c, c, p.D);
     }
-    if (!p.r.h) return;
+    if (!has_h) return;
     s[0] = q.x + q.y;
-    row_sum<NT, 1>(s, sh[1]);
+    row_sum<NT, 1>(s, sh1);
     const float rx = rsqrtf(fmaf(s[0], inv_D, p.eps));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = 8 * (tid + i * NT);
         if (!F8 && c >= p.D) continue;
         W8 w;
-        if (c < p.D) w.load(p.pre_w, c, p.D);
+        if (c < p.D) w = pre_w(i, c);
         if (!F8) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[i].set(j, f2_mul(w.get(j), f2_mul(f[i][j], f2(rx))));
@@ -211,9 +217,201 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_kernel(const _
     }
 }
 
+// One row a block (a warp of four for the shortest rows).
+template <typename T, int NT, int VPT, bool F8>
+__global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_kernel(const __grid_constant__ Args p)
+{
+    constexpr int kRows = NT == 32 ? 4 : 1;
+    __shared__ float sh[2][32][1];
+    const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * kRows + (NT == 32 ? threadIdx.x >> 5 : 0);
+    if (row >= p.M) return;  // a whole warp
+    V8<T> x[VPT], y[VPT], g[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 8 * (tid + i * NT);
+        if (c < p.D) {
+            load8(x[i], p.r.x, row * p.r.x_stride + c, c, p.D);
+            if (p.r.y) load8(y[i], p.r.y, row * p.r.y_stride + c, c, p.D);
+            if (p.r.g) load8(g[i], p.r.g, row * p.r.g_stride + c, c, p.D);
+        }
+    }
+    finish_row<kAny, T, NT, VPT, F8>(p, row, tid, x, y, g, sh[0], sh[1],
+        [&](int, int c) {
+            W8 w, sc;
+            w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
+            return w.times(sc);
+        },
+        [&](int, int c) {
+            W8 w;
+            w.load(p.pre_w, c, p.D);
+            return w;
+        });
+}
+
+// Many rows: blocks that stay, with the parameters in shared memory (from L2 they are as many bytes as the rows), and
+// with the next row on its way into shared memory while one is worked on. A thread copies, and reads, its own columns.
+template <typename T, int NT, int VPT>
+struct Stage {
+    float4 w[4][VPT][NT];                        // post_w scale, pre_w: four channels each
+    V8<T> rows[3][VPT][NT];                      // x, y, g
+};
+template <typename T> __device__ __forceinline__ void copy8(V8<T> *to, const void *p, int64_t at, int c, int D)
+{
+    cp_async16(&to->r, static_cast<const T *>(p) + at, 16);
+}
+template <> __device__ __forceinline__ void copy8(V8<float> *to, const void *p, int64_t at, int c, int D)
+{
+    const float *from = static_cast<const float *>(p) + at;
+    cp_async16(&to->r[0], from, 16);
+    cp_async16(&to->r[1], c + 4 < D ? from + 4 : from, c + 4 < D ? 16 : 0);
+}
+
+template <typename T, int NT, int VPT, bool F8, int HAS>
+__global__ void __launch_bounds__(NT, 512 / NT) block_norm_rows_kernel(const __grid_constant__ Args p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    Stage<T, NT, VPT> &st = *reinterpret_cast<Stage<T, NT, VPT> *>(smem);
+    __shared__ float sh[2][2][32][1];
+    const int tid = threadIdx.x;
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 8 * (tid + i * NT);
+            if (c >= p.D) continue;
+            copy8(&st.rows[0][i][tid], p.r.x, row * p.r.x_stride + c, c, p.D);
+            copy8(&st.rows[1][i][tid], p.r.y, row * p.r.y_stride + c, c, p.D);
+            if (HAS == kAll) copy8(&st.rows[2][i][tid], p.r.g, row * p.r.g_stride + c, c, p.D);
+        }
+    };
+    fetch(blockIdx.x);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 8 * (tid + i * NT);
+        if (c >= p.D) continue;
+        W8 w, sc;
+        w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
+        w = w.times(sc);
+        st.w[0][i][tid] = w.r[0], st.w[1][i][tid] = w.r[1];
+        w.load(p.pre_w, c, p.D);
+        st.w[2][i][tid] = w.r[0], st.w[3][i][tid] = w.r[1];
+    }
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
+        V8<T> x[VPT], y[VPT], g[VPT];
+        cp_async_wait_all();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            x[i] = st.rows[0][i][tid];
+            y[i] = st.rows[1][i][tid];
+            if (HAS == kAll) g[i] = st.rows[2][i][tid];
+        }
+        if (row + gridDim.x < p.M) fetch(row + gridDim.x);
+        finish_row<HAS, T, NT, VPT, F8>(p, row, tid, x, y, g, sh[turn][0], sh[turn][1],
+            [&](int i, int) { return W8{{st.w[0][i][tid], st.w[1][i][tid]}}; }, [&](int i, int) { return W8{{st.w[2][i][tid], st.w[3][i][tid]}}; });
+    }
+}
+
 // Gradients, a row at a time: with n = z / rms(z) a norm's gradient is dz = (w - n mean(w n)) / rms(z), w that of n.
 //   dx = dx' + (gradient of h's norm),  d(scale sigmoid(g) post_w n_y) = dx
-// A thread keeps its columns' sums over the block's rows.
+// A thread adds up its columns' sums over the block's rows, sq for post_w and scale, sp for pre_w.
+template <int HAS, typename T, int NT, int VPT, typename PostW, typename PreW>
+__device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, int tid, V8<T> (&x)[VPT], const V8<T> (&dh)[VPT], const V8<T> (&dx1)[VPT],
+                                         V8<T> (&y)[VPT], V8<T> (&g)[VPT], float2 (&sq)[VPT][4], float2 (&sp)[VPT][4], float (*sh)[3], float (*sh1)[1],
+                                         PostW post_w, PreW pre_w)
+{
+    const float inv_D = 1.f / p.D;
+    const bool has_y = HAS != kAny || p.r.y, has_g = HAS == kAny ? p.r.g != nullptr : HAS == kAll, has_h = HAS != kAny || p.r.dh, has_dx1 = HAS != kAny || p.r.dx1;
+    float s[3] = {0.f, 0.f, 0.f};  // x^2, x dh pre_w, y^2
+    float2 s0 = f2(0.f), s1 = s0, s2 = s0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 8 * (tid + i * NT);
+        if (c >= p.D) continue;
+        W8 w;
+        if (has_h) w = pre_w(i, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (has_h) {
+                s0 = f2_fma(x[i].get(j), x[i].get(j), s0);
+                s1 = f2_fma(f2_mul(dh[i].get(j), w.get(j)), x[i].get(j), s1);
+            }
+            if (has_y) s2 = f2_fma(y[i].get(j), y[i].get(j), s2);
+        }
+    }
+    s[0] = s0.x + s0.y, s[1] = s1.x + s1.y, s[2] = s2.x + s2.y;
+    row_sum<NT, 3>(s, sh);
+    const float rx = rsqrtf(fmaf(s[0], inv_D, p.eps)), ry = rsqrtf(fmaf(s[2], inv_D, p.eps));
+    const float mx = s[1] * rx * inv_D;  // mean(w n)
+    float2 m = f2(0.f), d[VPT][4];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 8 * (tid + i * NT);
+        if (c >= p.D) continue;
+        W8 w, pw;
+        if (has_h) w = pre_w(i, c);
+        if (has_y) pw = post_w(i, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            d[i][j] = has_dx1 ? dx1[i].get(j) : f2(0.f);
+            if (has_h) {
+                const float2 n = f2_mul(x[i].get(j), f2(rx)), e = dh[i].get(j);
+                d[i][j] = f2_fma(f2(rx), f2_fma(n, f2(-mx), f2_mul(e, w.get(j))), d[i][j]);
+                sp[i][j] = f2_fma(e, n, sp[i][j]);
+            }
+            x[i].set(j, d[i][j]);
+            if (has_y) {
+                const float2 n = f2_mul(y[i].get(j), f2(ry));
+                float2 k = d[i][j], o;
+                if (has_g) {
+                    const float2 s = both_sigmoids(g[i].get(j), o);
+                    k = f2_mul(k, s);
+                }
+                sq[i][j] = f2_fma(k, n, sq[i][j]);
+                d[i][j] = f2_mul(k, pw.get(j));  // the gradient of n
+                const float2 dn = f2_mul(d[i][j], n);
+                m = f2_add(m, dn);
+                if (has_g) g[i].set(j, f2_mul(dn, o));  // d sigmoid = s (1 - s); dn has a factor s
+            }
+        }
+        store8(x[i], p.r.dx, row * p.r.dx_stride + c, c, p.D);
+        if (has_g) store8(g[i], p.r.dg, row * p.r.dg_stride + c, c, p.D);
+    }
+    if (!has_y) return;
+    float t[1] = {m.x + m.y};
+    row_sum<NT, 1>(t, sh1);
+    const float my = t[0] * inv_D;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 8 * (tid + i * NT);
+        if (c >= p.D) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 n = f2_mul(y[i].get(j), f2(ry));
+            y[i].set(j, f2_mul(f2(ry), f2_fma(n, f2(-my), d[i][j])));
+        }
+        store8(y[i], p.r.dy, row * p.r.dy_stride + c, c, p.D);
+    }
+}
+
+template <int NT, int VPT>
+__device__ __forceinline__ void store_sums(const BackArgs &p, int part, int tid, const float2 (&sq)[VPT][4], const float2 (&sp)[VPT][4])
+{
+    float *out = p.part + (int64_t)part * 2 * p.D;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = 8 * (tid + i * NT);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + 2 * j < p.D) {
+                *reinterpret_cast<float2 *>(out + c + 2 * j) = sq[i][j];
+                *reinterpret_cast<float2 *>(out + p.D + c + 2 * j) = sp[i][j];
+            }
+    }
+}
+
+// Rows straight from global memory: a warp each for the shortest ones, and those too long for the kernel below.
 template <typename T, int NT, int VPT>
 __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_back_kernel(const __grid_constant__ BackArgs p, int parts)
 {
@@ -227,104 +425,93 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_back_kernel(co
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sq[i][j] = sp[i][j] = f2(0.f);
-    const float inv_D = 1.f / p.D;
-    const bool has_y = p.r.y, has_g = p.r.g, has_h = p.r.dh, has_dx1 = p.r.dx1;
     int turn = 0;
     for (int64_t row = part; row < p.M; row += parts, turn ^= 1) {
         V8<T> x[VPT], dh[VPT], dx1[VPT], y[VPT], g[VPT];
-        float s[3] = {0.f, 0.f, 0.f};  // x^2, x dh pre_w, y^2
-        float2 s0 = f2(0.f), s1 = s0, s2 = s0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (tid + i * NT);
             if (c >= p.D) continue;
-            if (has_h) {
+            if (p.r.dh) {
                 load8(x[i], p.r.x_out, row * p.r.x_out_stride + c, c, p.D);
                 load8(dh[i], p.r.dh, row * p.r.dh_stride + c, c, p.D);
             }
-            if (has_dx1) load8(dx1[i], p.r.dx1, row * p.r.dx1_stride + c, c, p.D);
-            if (has_y) load8(y[i], p.r.y, row * p.r.y_stride + c, c, p.D);
-            if (has_g) load8(g[i], p.r.g, row * p.r.g_stride + c, c, p.D);
+            if (p.r.dx1) load8(dx1[i], p.r.dx1, row * p.r.dx1_stride + c, c, p.D);
+            if (p.r.y) load8(y[i], p.r.y, row * p.r.y_stride + c, c, p.D);
+            if (p.r.g) load8(g[i], p.r.g, row * p.r.g_stride + c, c, p.D);
         }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (tid + i * NT);
-            if (c >= p.D) continue;
-            W8 w;
-            if (has_h) w.load(p.pre_w, c, p.D);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (has_h) {
-                    s0 = f2_fma(x[i].get(j), x[i].get(j), s0);
-                    s1 = f2_fma(f2_mul(dh[i].get(j), w.get(j)), x[i].get(j), s1);
-                }
-                if (has_y) s2 = f2_fma(y[i].get(j), y[i].get(j), s2);
-            }
-        }
-        s[0] = s0.x + s0.y, s[1] = s1.x + s1.y, s[2] = s2.x + s2.y;
-        row_sum<NT, 3>(s, sh[turn]);
-        const float rx = rsqrtf(fmaf(s[0], inv_D, p.eps)), ry = rsqrtf(fmaf(s[2], inv_D, p.eps));
-        const float mx = s[1] * rx * inv_D;  // mean(w n)
-        float2 m = f2(0.f), d[VPT][4];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (tid + i * NT);
-            if (c >= p.D) continue;
-            W8 w, pw, sc;
-            if (has_h) w.load(p.pre_w, c, p.D);
-            if (has_y) pw.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                d[i][j] = has_dx1 ? dx1[i].get(j) : f2(0.f);
-                if (has_h) {
-                    const float2 n = f2_mul(x[i].get(j), f2(rx)), e = dh[i].get(j);
-                    d[i][j] = f2_fma(f2(rx), f2_fma(n, f2(-mx), f2_mul(e, w.get(j))), d[i][j]);
-                    sp[i][j] = f2_fma(e, n, sp[i][j]);
-                }
-                x[i].set(j, d[i][j]);
-                if (has_y) {
-                    const float2 n = f2_mul(y[i].get(j), f2(ry));
-                    float2 k = d[i][j];
-                    if (has_g) k = f2_mul(k, sigmoid2(g[i].get(j)));
-                    sq[i][j] = f2_fma(k, n, sq[i][j]);
-                    d[i][j] = f2_mul(k, f2_mul(sc.get(j), pw.get(j)));  // the gradient of n
-                    m = f2_fma(d[i][j], n, m);
-                }
-            }
-            store8(x[i], p.r.dx, row * p.r.dx_stride + c, c, p.D);
-        }
-        if (!has_y) continue;
-        float t[1] = {m.x + m.y};
-        row_sum<NT, 1>(t, sh1[turn]);
-        const float my = t[0] * inv_D;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (tid + i * NT);
-            if (c >= p.D) continue;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 n = f2_mul(y[i].get(j), f2(ry));
-                if (has_g) {  // d sigmoid = s (1 - s); d[i][j] has a factor s
-                    const float2 gg = g[i].get(j), o = sigmoid2(make_float2(-gg.x, -gg.y));
-                    g[i].set(j, f2_mul(f2_mul(d[i][j], n), o));
-                }
-                y[i].set(j, f2_mul(f2(ry), f2_fma(n, f2(-my), d[i][j])));
-            }
-            store8(y[i], p.r.dy, row * p.r.dy_stride + c, c, p.D);
-            if (has_g) store8(g[i], p.r.dg, row * p.r.dg_stride + c, c, p.D);
-        }
+        back_row<kAny, T, NT, VPT>(p, row, tid, x, dh, dx1, y, g, sq, sp, sh[turn], sh1[turn],
+            [&](int, int c) {
+                W8 w, sc;
+                w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
+                return w.times(sc);
+            },
+            [&](int, int c) {
+                W8 w;
+                w.load(p.pre_w, c, p.D);
+                return w;
+            });
     }
-    float *out = p.part + (int64_t)part * 2 * p.D;
+    store_sums<NT, VPT>(p, part, tid, sq, sp);
+}
+
+// As block_norm_rows_kernel: the parameters and the next row in shared memory.
+template <typename T, int NT, int VPT>
+struct BackStage {
+    float4 w[4][VPT][NT];    // post_w scale, pre_w: four channels each
+    V8<T> rows[5][VPT][NT];  // x', dh, dx', y, g
+};
+template <typename T, int NT, int VPT, int HAS>
+__global__ void __launch_bounds__(NT, 512 / NT) block_norm_back_rows_kernel(const __grid_constant__ BackArgs p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    BackStage<T, NT, VPT> &st = *reinterpret_cast<BackStage<T, NT, VPT> *>(smem);
+    __shared__ float sh[2][32][3], sh1[2][32][1];
+    const int tid = threadIdx.x;
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 8 * (tid + i * NT);
+            if (c >= p.D) continue;
+            copy8(&st.rows[0][i][tid], p.r.x_out, row * p.r.x_out_stride + c, c, p.D);
+            copy8(&st.rows[1][i][tid], p.r.dh, row * p.r.dh_stride + c, c, p.D);
+            copy8(&st.rows[2][i][tid], p.r.dx1, row * p.r.dx1_stride + c, c, p.D);
+            copy8(&st.rows[3][i][tid], p.r.y, row * p.r.y_stride + c, c, p.D);
+            if (HAS == kAll) copy8(&st.rows[4][i][tid], p.r.g, row * p.r.g_stride + c, c, p.D);
+        }
+    };
+    fetch(blockIdx.x);
+    float2 sq[VPT][4], sp[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = 8 * (tid + i * NT);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + 2 * j < p.D) {
-                *reinterpret_cast<float2 *>(out + c + 2 * j) = sq[i][j];
-                *reinterpret_cast<float2 *>(out + p.D + c + 2 * j) = sp[i][j];
-            }
+        for (int j = 0; j < 4; ++j) sq[i][j] = sp[i][j] = f2(0.f);
+        if (c >= p.D) continue;
+        W8 w, sc;
+        w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
+        w = w.times(sc);
+        st.w[0][i][tid] = w.r[0], st.w[1][i][tid] = w.r[1];
+        w.load(p.pre_w, c, p.D);
+        st.w[2][i][tid] = w.r[0], st.w[3][i][tid] = w.r[1];
     }
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
+        V8<T> x[VPT], dh[VPT], dx1[VPT], y[VPT], g[VPT];
+        cp_async_wait_all();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            x[i] = st.rows[0][i][tid], dh[i] = st.rows[1][i][tid];
+            dx1[i] = st.rows[2][i][tid];
+            y[i] = st.rows[3][i][tid];
+            if (HAS == kAll) g[i] = st.rows[4][i][tid];
+        }
+        if (row + gridDim.x < p.M) fetch(row + gridDim.x);
+        back_row<HAS, T, NT, VPT>(p, row, tid, x, dh, dx1, y, g, sq, sp, sh[turn], sh1[turn],
+            [&](int i, int) { return W8{{st.w[0][i][tid], st.w[1][i][tid]}}; }, [&](int i, int) { return W8{{st.w[2][i][tid], st.w[3][i][tid]}}; });
+    }
+    store_sums<NT, VPT>(p, blockIdx.x, tid, sq, sp);
 }
 
 __global__ void __launch_bounds__(kSumCols *kSumGroups)
@@ -395,15 +582,42 @@ bool rows_ok(int64_t M)
 
 int64_t parts_of(int32_t D, int64_t M)
 {
-    const int64_t most = D <= 512 ? 1216 : 304;
+    const int64_t most = D <= 512 ? 1216 : D <= 2048 ? 608 : 304;
     return M < most ? M : most;
 }
 size_t back_bytes(int32_t D, int64_t M) { return 256 + (size_t)parts_of(D, M) * 2 * D * sizeof(float); }
 
+// Blocks of nt threads that stay on an SM: as many threads in all, as far as shared memory goes.
+constexpr int blocks_per_sm(int threads, int nt, size_t smem)
+{
+    const int by_smem = (int)(233472 / (smem + 2048));
+    return threads / nt < by_smem ? threads / nt : by_smem;
+}
+
+template <typename T, int NT, int VPT, bool F8, int HAS = kAny>
+cudaError_t launch_rows(const Args &p, int dev, int sms, cudaStream_t s)
+{
+    if (HAS == kAny) return p.r.g ? launch_rows<T, NT, VPT, F8, kAll>(p, dev, sms, s) : launch_rows<T, NT, VPT, F8, kNoGate>(p, dev, sms, s);
+    constexpr int kHas = HAS == kAny ? kAll : HAS;
+    static std::atomic<uint64_t> raised;
+    const int smem = (int)sizeof(Stage<T, NT, VPT>);
+    const cudaError_t e = raise_smem_on(raised, dev, block_norm_rows_kernel<T, NT, VPT, F8, kHas>, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)sms * blocks_per_sm(512, NT, sizeof(Stage<T, NT, VPT>));
+    block_norm_rows_kernel<T, NT, VPT, F8, kHas><<<(unsigned)(p.M < most ? p.M : most), NT, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T, bool F8>
-void launch(const Args &p, cudaStream_t s)
+cudaError_t launch(const Args &p, int dev, int sms, cudaStream_t s)
 {
     const unsigned M = (unsigned)p.M, M4 = (unsigned)((p.M + 3) / 4);
+    if (p.M >= 8 * sms && p.D > 512 && p.D <= 8192 && p.r.y && p.r.h) {
+        if (p.D <= 1024) return launch_rows<T, 64, 2, F8>(p, dev, sms, s);
+        if (p.D <= 2048) return launch_rows<T, 128, 2, F8>(p, dev, sms, s);
+        if (p.D <= 4096) return launch_rows<T, 128, 4, F8>(p, dev, sms, s);
+        return launch_rows<T, 256, 4, F8>(p, dev, sms, s);
+    }
     if (p.D <= 256) block_norm_kernel<T, 32, 1, F8><<<M4, 128, 0, s>>>(p);
     else if (p.D <= 512) block_norm_kernel<T, 32, 2, F8><<<M4, 128, 0, s>>>(p);
     else if (p.D <= 1024) block_norm_kernel<T, 128, 1, F8><<<M, 128, 0, s>>>(p);
@@ -411,19 +625,43 @@ void launch(const Args &p, cudaStream_t s)
     else if (p.D <= 4096) block_norm_kernel<T, 256, 2, F8><<<M, 256, 0, s>>>(p);
     else if (p.D <= 8192) block_norm_kernel<T, 512, 2, F8><<<M, 512, 0, s>>>(p);
     else block_norm_kernel<T, 1024, 2, F8><<<M, 1024, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
-template <typename T>
-void launch_back(const BackArgs &p, int parts, cudaStream_t s)
+template <typename T, int NT, int VPT, int HAS = kAny>
+cudaError_t launch_back_rows(const BackArgs &p, int *parts, int dev, int sms, cudaStream_t s)
 {
-    const unsigned n = (unsigned)parts, n4 = (unsigned)((parts + 3) / 4);
-    if (p.D <= 256) block_norm_back_kernel<T, 32, 1><<<n4, 128, 0, s>>>(p, parts);
-    else if (p.D <= 512) block_norm_back_kernel<T, 32, 2><<<n4, 128, 0, s>>>(p, parts);
-    else if (p.D <= 1024) block_norm_back_kernel<T, 128, 1><<<n, 128, 0, s>>>(p, parts);
-    else if (p.D <= 2048) block_norm_back_kernel<T, 128, 2><<<n, 128, 0, s>>>(p, parts);
-    else if (p.D <= 4096) block_norm_back_kernel<T, 256, 2><<<n, 256, 0, s>>>(p, parts);
-    else if (p.D <= 8192) block_norm_back_kernel<T, 512, 2><<<n, 512, 0, s>>>(p, parts);
-    else block_norm_back_kernel<T, 1024, 2><<<n, 1024, 0, s>>>(p, parts);
+    if (HAS == kAny) return p.r.g ? launch_back_rows<T, NT, VPT, kAll>(p, parts, dev, sms, s) : launch_back_rows<T, NT, VPT, kNoGate>(p, parts, dev, sms, s);
+    constexpr int kHas = HAS == kAny ? kAll : HAS;
+    static std::atomic<uint64_t> raised;
+    const int smem = (int)sizeof(BackStage<T, NT, VPT>);
+    const cudaError_t e = raise_smem_on(raised, dev, block_norm_back_rows_kernel<T, NT, VPT, kHas>, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)sms * blocks_per_sm(512, NT, sizeof(BackStage<T, NT, VPT>));
+    *parts = (int)(most < *parts ? most : *parts);
+    block_norm_back_rows_kernel<T, NT, VPT, kHas><<<(unsigned)*parts, NT, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+// parts: rows of partial sums that the workspace has room for, and then those that are written
+template <typename T>
+cudaError_t launch_back(const BackArgs &p, int *parts, int dev, int sms, cudaStream_t s)
+{
+    const unsigned n = (unsigned)*parts, n4 = (unsigned)((*parts + 3) / 4);
+    if (p.M >= 8 * sms && p.D > 512 && p.D <= 8192 && p.r.y && p.r.dh && p.r.dx1) {
+        if (p.D <= 1024) return launch_back_rows<T, 128, 1>(p, parts, dev, sms, s);
+        if (p.D <= 2048) return launch_back_rows<T, 128, 2>(p, parts, dev, sms, s);
+        if (p.D <= 4096) return launch_back_rows<T, 256, 2>(p, parts, dev, sms, s);
+        return launch_back_rows<T, 512, 2>(p, parts, dev, sms, s);
+    }
+    if (p.D <= 256) block_norm_back_kernel<T, 32, 1><<<n4, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 512) block_norm_back_kernel<T, 32, 2><<<n4, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 1024) block_norm_back_kernel<T, 128, 1><<<n, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 2048) block_norm_back_kernel<T, 128, 2><<<n, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 4096) block_norm_back_kernel<T, 256, 2><<<n, 256, 0, s>>>(p, *parts);
+    else if (p.D <= 8192) block_norm_back_kernel<T, 512, 2><<<n, 512, 0, s>>>(p, *parts);
+    else block_norm_back_kernel<T, 1024, 2><<<n, 1024, 0, s>>>(p, *parts);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -463,14 +701,12 @@ kda_status kda_block_norm(const kda_block_norm_config_t *cfg, const kda_block_no
     if (r.hs && (reinterpret_cast<uintptr_t>(r.hs) & 3u)) return bn::fail(KDA_ERR_INVALID, "hs must be 4-byte aligned");
     const bn::Args p = {M, D, cfg->eps, params->post_w, params->scale, params->pre_w, r};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cfg->io_dtype == KDA_F32) {
-        if (r.hs) bn::launch<float, true>(p, s);
-        else bn::launch<float, false>(p, s);
-    } else {
-        if (r.hs) bn::launch<__nv_bfloat16, true>(p, s);
-        else bn::launch<__nv_bfloat16, false>(p, s);
+    int dev = 0, sms = 0;
+    cudaError_t err = current_sms(&dev, &sms);
+    if (err == cudaSuccess) {
+        if (cfg->io_dtype == KDA_F32) err = r.hs ? bn::launch<float, true>(p, dev, sms, s) : bn::launch<float, false>(p, dev, sms, s);
+        else err = r.hs ? bn::launch<__nv_bfloat16, true>(p, dev, sms, s) : bn::launch<__nv_bfloat16, false>(p, dev, sms, s);
     }
-    const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? KDA_OK : bn::fail(KDA_ERR_CUDA, "kda_block_norm: %s", cudaGetErrorString(err));
 }
 
@@ -507,13 +743,12 @@ kda_status kda_block_norm_backward(const kda_block_norm_config_t *cfg, const kda
             return bn::fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed", workspace_bytes, need);
     }
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int parts = (int)bn::parts_of(D, M);
+    int parts = (int)bn::parts_of(D, M), dev = 0, sms = 0;
     cudaError_t err = cudaSuccess;
     if (M > 0) {
         const bn::BackArgs p = {M, D, cfg->eps, params->post_w, params->scale, params->pre_w, r, static_cast<float *>(workspace)};
-        if (cfg->io_dtype == KDA_F32) bn::launch_back<float>(p, parts, s);
-        else bn::launch_back<__nv_bfloat16>(p, parts, s);
-        err = cudaGetLastError();
+        if ((err = current_sms(&dev, &sms)) == cudaSuccess)
+            err = cfg->io_dtype == KDA_F32 ? bn::launch_back<float>(p, &parts, dev, sms, s) : bn::launch_back<__nv_bfloat16>(p, &parts, dev, sms, s);
     }
     if (err == cudaSuccess && (dpost_w || dscale || dpre_w)) {  // without rows: zeros
         bn::block_norm_sums_kernel<<<dim3((D + kSumCols - 1) / kSumCols, 2), dim3(kSumCols, kSumGroups), 0, s>>>(

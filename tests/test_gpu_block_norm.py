@@ -118,6 +118,26 @@ def test_more_rows_than_partial_sums():
         p.check_back(p.backward())
 
 
+@pytest.mark.parametrize("D,bf16,gate,strided", [(520, True, True, False), (1024, False, False, True), (1032, True, False, True), (2048, False, True, False),
+                                                (2056, True, True, True), (4096, False, False, False), (4100, False, True, True), (7168, True, True, False),
+                                                (8192, True, False, False), (8188, False, True, False)])
+def test_many_rows(D, bf16, gate, strided):
+    """Blocks that stay and take one row after the other."""
+    p = Problem(1301, D, bf16, gate, seed=8, strided=strided)
+    x1, h = p.forward()
+    r = p.ref()
+    near(x1, r["x1"], r["x1_err"], bf16)
+    near(h, r["h"], r["h_err"], bf16)
+    got = p.backward()
+    p.check_back(got)
+    again = p.backward()
+    assert all(torch.equal(got[n], again[n]) for n in got)
+    for t in (x1, h, got["dx"], got["dy"]):  # the row behind the last
+        assert bool((torch.as_strided(t, (1, D), (1, 1), t.storage_offset() + p.M * t.stride(0)) == -7.0).all())
+    for kw in ({"y": False}, {"dh": False}, {"dx1": False}):
+        p.check_back(p.backward(**kw), **kw)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_only_one_of_the_norms(bf16):
     p = Problem(40, 200, bf16, True, seed=2)
@@ -143,7 +163,7 @@ def test_in_place():
     assert torch.equal(x, x1) and torch.equal(first, p.dev["dx1"]) and torch.equal(g["dy"], g2["dy"])
 
 
-@pytest.mark.parametrize("M,D,bf16", [(1, 16, True), (5, 128, False), (70, 400, True), (3, 1040, True), (17, 7168, True), (3, 16384, False)])
+@pytest.mark.parametrize("M,D,bf16", [(1, 16, True), (5, 128, False), (70, 400, True), (3, 1040, True), (17, 7168, True), (3, 16384, False), (1300, 528, True), (1250, 4096, False)])
 def test_fp8(M, D, bf16):
     """The scale is the power of two for the group's largest value (or for one that FP32 could have in its place), and the
     codes are h / scale to half a step."""
