@@ -1,4 +1,4 @@
-"""Whole layers - a KDA layer and a gated delta rule layer - on the library's kernels only.
+"""Whole layers - a KDA layer, a gated delta rule layer and a gated linear recurrence layer - on the library's kernels only.
 
 Per token of each sequence (kimi_k3.c header comment, block "KDA per-head
 recurrence"; struct Kda: W q, k, v, o, g, fa, fb, bp):
@@ -25,8 +25,15 @@ It is the recurrence between two products and no published model's layer: there 
 SiLU, no output norm and no gate around the recurrence. A model that has them applies them to the columns
 and to o itself, between the library's calls.
 
-The dense products of either layer run in BF16 (kda_linear) or, for weights given as
-Fp8Weight, in FP8 (kda_quant_fp8 of the activations, kda_linear_fp8).
+The gated linear recurrence layer is a block of a stack with norms before and after it:
+
+    x, a, b, g = columns of W_in h                 one product; g only with an output gate
+    o          = kda_glr_decode / kda_glr_prefill
+    y          = W_o o
+    x', h'     = kda_block_norm(x, y)              x' the stream, h' the next layer's input
+
+The dense products of a layer run in BF16 (kda_linear) or, for weights given as
+Fp8Weight, in FP8 (kda_quant_fp8 of the activations, kda_linear_fp8; h' comes from kda_block_norm in FP8).
 """
 from __future__ import annotations
 
@@ -79,10 +86,13 @@ class Products:
         if not self.fp8:
             K.kda_linear(x, w, y, self.ws, r=r, ysplit=ysplit, stream=stream)
             return
-        n, Kx = x.shape
-        xq, xs = self.xq[:n * Kx].view(n, Kx), self.xs[:n * -(-Kx // 128)].view(n, -(-Kx // 128))
+        xq, xs = self.operand(*x.shape)
         K.kda_quant_fp8(x, xq, xs, stream=stream)
         K.kda_linear_fp8(xq, xs, w.q, w.s, y, self.ws, r=r, ysplit=ysplit, stream=stream)
+
+    def operand(self, n: int, Kx: int):
+        """The buffers that hold n rows of Kx columns in FP8, and their scales."""
+        return self.xq[:n * Kx].view(n, Kx), self.xs[:n * -(-Kx // 128)].view(n, -(-Kx // 128))
 
 
 @dataclass
@@ -185,7 +195,29 @@ def _capturing(stream) -> bool:
         return torch.cuda.is_current_stream_capturing()
 
 
-class GdrLayerRunner:
+class _Workspace:
+    """A prefill's workspace, which grows with the batches."""
+
+    def __init__(self, device):
+        self.ws = torch.empty(0, dtype=torch.uint8, device=device)
+        self._captured = []  # workspaces that a captured prefill writes to
+
+    def _fit(self, need: int, stream) -> torch.Tensor:
+        """The workspace, of `need` bytes or more. Growing waits for the device; not while a graph is captured."""
+        capturing = _capturing(stream)
+        if self.ws.numel() < need:
+            if capturing or torch.cuda.is_current_stream_capturing():  # neither capture would survive the waits below
+                raise RuntimeError(f"the workspace must grow to {need} bytes: run a prefill of this size before one is captured")
+            device = self.ws.device
+            torch.cuda.synchronize(device)  # calls on other streams may be using the old one
+            self.ws = torch.empty(need, dtype=torch.uint8, device=device)
+            torch.cuda.synchronize(device)  # and the new one's memory may have had another use
+        if capturing and not any(w is self.ws for w in self._captured):
+            self._captured.append(self.ws)  # a graph keeps writing to it
+        return self.ws
+
+
+class GdrLayerRunner(_Workspace):
     """Buffers for running gated delta rule layers on a batch of up to `rows` tokens at a time, made on
     the current stream."""
 
@@ -197,8 +229,7 @@ class GdrLayerRunner:
         self.proj = torch.empty(rows, W, dtype=torch.bfloat16, device=device)
         self.o = torch.empty(rows, D, dtype=torch.bfloat16, device=device)
         self.products = Products([(W, hidden), (hidden, D)], rows, device, fp8)
-        self.ws = torch.empty(0, dtype=torch.uint8, device=device)
-        self._captured = []  # workspaces that a captured prefill writes to
+        super().__init__(device)
 
     def _inputs(self, lw: GdrLayerWeights, x: torch.Tensor, stream):
         n = x.shape[0]
@@ -221,17 +252,91 @@ class GdrLayerRunner:
         """Packed variable-length prefill of x.shape[0] tokens: x_out = x + W_o o. When a batch needs more
         chunks than any before, the workspace grows, which waits for the device; not while a graph is
         captured (run a prefill of that size first)."""
-        need = K.kda_gdr_workspace_bytes(self.cfg, cu_seqlens_host)
-        capturing = _capturing(stream)
-        if self.ws.numel() < need:
-            if capturing or torch.cuda.is_current_stream_capturing():  # neither capture would survive the waits below
-                raise RuntimeError(f"the workspace must grow to {need} bytes: run a prefill of this size before one is captured")
-            torch.cuda.synchronize(self.proj.device)  # calls on other streams may be using the old one
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.proj.device)
-            torch.cuda.synchronize(self.proj.device)  # and the new one's memory may have had another use
-        if capturing and not any(w is self.ws for w in self._captured):
-            self._captured.append(self.ws)  # a graph keeps writing to it
+        ws = self._fit(K.kda_gdr_workspace_bytes(self.cfg, cu_seqlens_host), stream)
         rows = self._inputs(lw, x, stream)
-        K.kda_gdr_prefill(self.cfg, lw.params, S, src_slots, dst_slots, cu_seqlens, cu_seqlens_host, *rows, self.ws,
+        K.kda_gdr_prefill(self.cfg, lw.params, S, src_slots, dst_slots, cu_seqlens, cu_seqlens_host, *rows, ws,
                           err=err, stream=stream)
         self.products(rows[-1], lw.w_o, x_out, r=x, stream=stream)
+
+
+@dataclass
+class GlrLayerWeights:
+    """Device weights of one gated linear recurrence layer; w_in and w_o BF16 or Fp8Weight."""
+    w_in: torch.Tensor     # [glr_width(cfg, gate), hidden]: rows of W_x, W_a, W_b (, W_g) [dim], then padding
+    w_o: torch.Tensor      # [hidden, dim]
+    params: K.kda_glr_params          # A_log, a_bias, b_bias (FP32)
+    norm: K.kda_block_norm_params     # post_w and scale of this layer, pre_w of the next one (FP32, [hidden])
+
+
+def glr_width(cfg: K.kda_glr_config_t, gate: bool = True) -> int:
+    """Rows of w_in: x, a, b and g side by side, up to a multiple of 128 (what the BF16 product takes)."""
+    return -(-(4 if gate else 3) * cfg.dim // 128) * 128
+
+
+class GlrLayerRunner(_Workspace):
+    """Buffers for running a stack of gated linear recurrence layers on a batch of up to `rows` tokens at a time, made on the
+    current stream. The runner holds the current layer's input h: `enter` makes the first layer's, and each layer the next
+    one's. gate: with an output gate; fp8: with the products, and h, in FP8."""
+
+    def __init__(self, cfg: K.kda_glr_config_t, hidden: int, rows: int, device, gate: bool = True, fp8: bool = False):
+        if cfg.io_dtype != K.KDA_BF16:
+            raise ValueError("the layer's products are BF16")
+        super().__init__(device)
+        self.cfg, self.hidden, self.rows, self.gate, self.fp8 = cfg, hidden, rows, gate, fp8
+        self.norm_cfg = K.kda_block_norm_config(hidden)
+        W, bf = glr_width(cfg, gate), torch.bfloat16
+        self.proj = torch.empty(rows, W, dtype=bf, device=device)
+        self.o = torch.empty(rows, cfg.dim, dtype=bf, device=device)
+        self.y = torch.empty(rows, hidden, dtype=bf, device=device)
+        self.h = torch.empty(rows, hidden, dtype=torch.float8_e4m3fn if fp8 else bf, device=device)
+        self.hs = torch.empty(rows, -(-hidden // 128), dtype=torch.float32, device=device) if fp8 else None
+        self.products = Products([(W, hidden), (hidden, cfg.dim)], rows, device, fp8)
+
+    def _norm(self, norm, x, y, x_out, last, stream):
+        n = x.shape[0]
+        K.kda_block_norm(self.norm_cfg, norm, x, y=y, x_out=x_out, h=None if last else self.h[:n],
+                         hs=None if last or not self.fp8 else self.hs[:n], stream=stream)
+
+    def enter(self, norm: K.kda_block_norm_params, x: torch.Tensor, stream=None) -> None:
+        """h of the first layer, from the stream x and that layer's pre_w (norm's post_w and scale are not read)."""
+        if x.shape[0] > self.rows:
+            raise ValueError(f"{x.shape[0]} rows, the runner was made for {self.rows}")
+        self._norm(norm, x, None, None, False, stream)
+
+    def _inputs(self, lw: GlrLayerWeights, n: int, stream):
+        if n > self.rows:
+            raise ValueError(f"{n} rows, the runner was made for {self.rows}")
+        if isinstance(lw.w_in, Fp8Weight) != self.fp8:
+            raise TypeError("an FP8 runner takes Fp8Weight products, a BF16 runner BF16 tensors")
+        proj = self.proj[:n]
+        if self.fp8:
+            K.kda_linear_fp8(self.h[:n], self.hs[:n], lw.w_in.q, lw.w_in.s, proj, self.products.ws, stream=stream)
+        else:
+            self.products(self.h[:n], lw.w_in, proj, stream=stream)
+        D = self.cfg.dim
+        cols = [proj[:, i * D:i * D + D] for i in range(4 if self.gate else 3)]
+        return (*cols, self.o[:n]) if self.gate else (*cols, None, self.o[:n])
+
+    def _outputs(self, lw: GlrLayerWeights, x, x_out, last, stream):
+        n = x.shape[0]
+        y = self.y[:n]
+        self.products(self.o[:n], lw.w_o, y, stream=stream)
+        self._norm(lw.norm, x, y, x_out, last, stream)
+
+    def decode(self, lw: GlrLayerWeights, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor, n: int,
+               x: torch.Tensor, x_out: torch.Tensor, last: bool = False, err=None, stream=None) -> None:
+        """n tokens for each of src_slots.numel() sequences, rows r n + t of x, the stream: x_out (which may be x) is the stream
+        after the layer; last: no layer follows, h is not made."""
+        rows = self._inputs(lw, x.shape[0], stream)
+        K.kda_glr_decode(self.cfg, lw.params, S, src_slots, dst_slots, n, *rows, err=err, stream=stream)
+        self._outputs(lw, x, x_out, last, stream)
+
+    def prefill(self, lw: GlrLayerWeights, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor, cu_seqlens: torch.Tensor,
+                cu_seqlens_host, x: torch.Tensor, x_out: torch.Tensor, last: bool = False, err=None, stream=None) -> None:
+        """Packed variable-length prefill of x.shape[0] tokens, x and x_out as in decode. When a batch needs a larger
+        workspace than any before, it grows, which waits for the device; not while a graph is captured (run a prefill of
+        that size first)."""
+        ws = self._fit(K.kda_glr_workspace_bytes(self.cfg, cu_seqlens_host), stream)
+        rows = self._inputs(lw, x.shape[0], stream)
+        K.kda_glr_prefill(self.cfg, lw.params, S, src_slots, dst_slots, cu_seqlens, cu_seqlens_host, *rows, ws, err=err, stream=stream)
+        self._outputs(lw, x, x_out, last, stream)
