@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(kSumCols *kSumGroups)
 block_norm_sums_kernel(const float *part, int parts, int D, const float *post_w, const float *scale, float *dpost_w, float *dscale, float *dpre_w)
 {
     __shared__ float sh[kSumGroups][kSumCols];
+    wait_for_previous();
     if (blockIdx.y == 0 ? !dpost_w && !dscale : !dpre_w) return;
     const float s = column_sum(part + (int64_t)blockIdx.y * D, parts, 2 * (int64_t)D, blockIdx.x * kSumCols, D, sh);
     const int c = blockIdx.x * kSumCols + threadIdx.x;
@@ -582,7 +583,7 @@ bool rows_ok(int64_t M)
 
 int64_t parts_of(int32_t D, int64_t M)
 {
-    const int64_t most = D <= 512 ? 1216 : D <= 2048 ? 608 : 304;
+    const int64_t most = D <= 512 ? 1216 : 304;
     return M < most ? M : most;
 }
 size_t back_bytes(int32_t D, int64_t M) { return 256 + (size_t)parts_of(D, M) * 2 * D * sizeof(float); }
@@ -751,9 +752,12 @@ kda_status kda_block_norm_backward(const kda_block_norm_config_t *cfg, const kda
             err = cfg->io_dtype == KDA_F32 ? bn::launch_back<float>(p, &parts, dev, sms, s) : bn::launch_back<__nv_bfloat16>(p, &parts, dev, sms, s);
     }
     if (err == cudaSuccess && (dpost_w || dscale || dpre_w)) {  // without rows: zeros
-        bn::block_norm_sums_kernel<<<dim3((D + kSumCols - 1) / kSumCols, 2), dim3(kSumCols, kSumGroups), 0, s>>>(
-            static_cast<const float *>(workspace), parts, D, params->post_w, params->scale, dpost_w, dscale, dpre_w);
-        err = cudaGetLastError();
+        const dim3 grid((D + kSumCols - 1) / kSumCols, 2);
+        const float *part = static_cast<const float *>(workspace);
+        // without rows no kernel of this call comes before it
+        if (M > 0) err = launch_after(bn::block_norm_sums_kernel, grid, sum_block(parts), 0, s, part, parts, D, params->post_w, params->scale, dpost_w, dscale, dpre_w);
+        else bn::block_norm_sums_kernel<<<grid, sum_block(0), 0, s>>>(part, 0, D, params->post_w, params->scale, dpost_w, dscale, dpre_w), err = cudaGetLastError();
+
     }
     return err == cudaSuccess ? KDA_OK : bn::fail(KDA_ERR_CUDA, "kda_block_norm_backward: %s", cudaGetErrorString(err));
 }

@@ -7,21 +7,37 @@ namespace kda {
 
 constexpr int kSumCols = 32, kSumGroups = 32;
 
-// This block's 32 columns from col0 on of part [rows][stride]: group y of the block adds the rows y, y + 32, ... and the
+// A block for it: up to 32 groups of threads, as many as there are rows.
+inline dim3 sum_block(int rows)
+{
+    int groups = 1;
+    while (groups < rows && groups < kSumGroups) groups *= 2;
+    return dim3(kSumCols, (unsigned)groups);
+}
+
+// This block's 32 columns from col0 on of part [rows][stride]: group y of the block's n adds the rows y, y + n, ... and the
 // groups' sums are added in order. The result is valid in the threads with threadIdx.y == 0.
 __device__ __forceinline__ float column_sum(const float *part, int rows, int64_t stride, int col0, int cols, float (&sh)[kSumGroups][kSumCols])
 {
     const int c = col0 + threadIdx.x;
     float s = 0.f;
-    if (c < cols)
-#pragma unroll 4
-        for (int r = threadIdx.y; r < rows; r += kSumGroups) s += part[r * stride + c];
-    __syncthreads();
+    if (c < cols) {
+        const int n = blockDim.y;
+        for (int r0 = threadIdx.y; r0 < rows; r0 += 8 * n) {
+            float v[8];  // asked for together
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = r0 + i * n < rows ? part[(r0 + i * n) * stride + c] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
+        }
+    }
+    if (blockDim.y == 1) return s;
     sh[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
+    if (threadIdx.y != 0) return 0.f;
     s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kSumGroups; ++i) s += sh[i][threadIdx.x];
+#pragma unroll 8
+    for (int i = 0; i < (int)blockDim.y; ++i) s += sh[i][threadIdx.x];
     return s;
 }
 

@@ -64,6 +64,7 @@ void launch_decode(const Args &p, unsigned blocks, cudaStream_t s)
 __global__ void __launch_bounds__(kSumCols *kSumGroups) glr_param_sums_kernel(const float *part, int rows, int D, float *dA_log, float *da_bias, float *db_bias)
 {
     __shared__ float sh[kSumGroups][kSumCols];
+    wait_for_previous();
     float *out = blockIdx.y == 0 ? dA_log : blockIdx.y == 1 ? da_bias : db_bias;
     if (!out) return;
     const float s = column_sum(part + (size_t)blockIdx.y * D, rows, 3 * (int64_t)D, blockIdx.x * kSumCols, D, sh);
@@ -279,9 +280,12 @@ kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *p
         if ((e = current_sms(&dev, &sms)) == cudaSuccess) e = glr::launch_scan_back(p, cfg->io_dtype == KDA_F32, cu_seqlens_host, &parts, dev, sms, s);
     }
     if (e == cudaSuccess && (dA_log || da_bias || db_bias)) {  // without sequences: zeros
-        glr::glr_param_sums_kernel<<<dim3((D + kSumCols - 1) / kSumCols, 3), dim3(kSumCols, kSumGroups), 0, s>>>(
-            static_cast<const float *>(workspace), parts, D, dA_log, da_bias, db_bias);
-        e = cudaGetLastError();
+        const dim3 grid((D + kSumCols - 1) / kSumCols, 3);
+        const float *part = static_cast<const float *>(workspace);
+        // without sequences no kernel of this call comes before it
+        if (parts > 0) e = launch_after(glr::glr_param_sums_kernel, grid, sum_block(parts), 0, s, part, parts, D, dA_log, da_bias, db_bias);
+        else glr::glr_param_sums_kernel<<<grid, sum_block(0), 0, s>>>(part, 0, D, dA_log, da_bias, db_bias), e = cudaGetLastError();
+
     }
     return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_backward: %s", cudaGetErrorString(e));
 }
