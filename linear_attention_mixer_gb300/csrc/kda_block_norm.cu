@@ -109,6 +109,9 @@ __device__ __forceinline__ float2 both_sigmoids(float2 g, float2 &ns)
 }
 __device__ __forceinline__ float2 sigmoid2(float2 g) { return make_float2(sigmoid_ftz(g.x), sigmoid_ftz(g.y)); }
 
+// 1 / sqrt(sum / D + eps), rounded as well as FP32 can: it is one number a row, and every element's
+__device__ __forceinline__ float rstd(float sum, int D, float eps) { return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)D), eps)); }
+
 // Sums over the NT threads that have a row; each thread gets them. A block of more than one warp has one row.
 template <int NT, int K>
 __device__ __forceinline__ void row_sum(float (&s)[K], float (*sh)[K])
@@ -139,7 +142,6 @@ template <int HAS, typename T, int NT, int VPT, bool F8, typename PostW, typenam
 __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, V8<T> (&x)[VPT], const V8<T> (&y)[VPT], const V8<T> (&g)[VPT],
                                            float (*sh0)[1], float (*sh1)[1], PostW post_w, PreW pre_w)
 {
-    const float inv_D = 1.f / p.D;
     const bool has_y = HAS != kAny || p.r.y, has_g = HAS == kAny ? p.r.g != nullptr : HAS == kAll, has_h = HAS != kAny || p.r.h;
     float s[1] = {0.f};
     float2 q = f2(0.f);
@@ -152,7 +154,7 @@ __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, 
         s[0] = q.x + q.y;
         row_sum<NT, 1>(s, sh0);
     }
-    const float ry = rsqrtf(fmaf(s[0], inv_D, p.eps));
+    const float ry = rstd(s[0], p.D, p.eps);
     float2 f[VPT][4];
     q = f2(0.f);
 #pragma unroll
@@ -177,7 +179,7 @@ __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, 
     if (!has_h) return;
     s[0] = q.x + q.y;
     row_sum<NT, 1>(s, sh1);
-    const float rx = rsqrtf(fmaf(s[0], inv_D, p.eps));
+    const float rx = rstd(s[0], p.D, p.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = 8 * (tid + i * NT);
@@ -342,7 +344,7 @@ __device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, int tid
     }
     s[0] = s0.x + s0.y, s[1] = s1.x + s1.y, s[2] = s2.x + s2.y;
     row_sum<NT, 3>(s, sh);
-    const float rx = rsqrtf(fmaf(s[0], inv_D, p.eps)), ry = rsqrtf(fmaf(s[2], inv_D, p.eps));
+    const float rx = rstd(s[0], p.D, p.eps), ry = rstd(s[2], p.D, p.eps);
     const float mx = s[1] * rx * inv_D;  // mean(w n)
     float2 m = f2(0.f), d[VPT][4];
 #pragma unroll

@@ -687,23 +687,23 @@ def kda_glr_params_from(A_log: torch.Tensor, a_bias: torch.Tensor, b_bias: torch
 
 
 def _row_args(pack, names, tensors, T, width, dt, dev):
-    """A row struct (as `pack` makes it: bytes), its pointers, then its strides, from checked tensors [T, width] of dt on device dev, contiguous
-    within a token (None: not given)."""
-    shape, ptrs, strides = (T, width), [], []
-    for i, t in enumerate(tensors):
+    """A row struct (as `pack` makes it: bytes), its pointers, then its strides, from checked tensors [T, width] of dt on device
+    dev, contiguous within a token (None: not given)."""
+    shape, ptrs, strides, many = (T, width), [], [], T > 1
+    for name, t in zip(names, tensors):
         if t is None:
             ptrs.append(0)
             strides.append(0)
             continue
         try:
             step, one = t.stride()
-            ok = t.dtype is dt and t.shape == shape and t.get_device() == dev and one == 1
+            if t.dtype is not dt or t.shape != shape or t.get_device() != dev or one != 1:
+                _check_row(name, t, T, width, dt, dev)
         except (AttributeError, ValueError):
-            ok = False
-        if not ok:
-            _check_row(names[i], t, T, width, dt, dev)
+            _check_row(name, t, T, width, dt, dev)
+            raise
         ptrs.append(t.data_ptr())
-        strides.append(step if T > 1 else width)
+        strides.append(step if many else width)
     return pack(*ptrs, *strides)
 
 
@@ -720,11 +720,16 @@ def _params_ok(cfg, params, dev) -> None:
         raise ValueError(f"the parameters must hold {cfg.dim} elements on cuda:{dev}, got {params.dim} on cuda:{params.device}")
 
 
-def _states_ok(cfg, S, src_slots, dst_slots) -> None:
-    if S.dim() != 2 or S.shape[1] != cfg.dim:
-        raise ValueError(f"S must be [max_slots, {cfg.dim}], got {list(S.shape)}")
+def _states(cfg, S, src_slots, dst_slots, dev):
+    """The checked addresses of S, src_slots and dst_slots."""
     if src_slots.numel() != dst_slots.numel():
         raise ValueError("src_slots and dst_slots must have the same length")
+    if S.dim() != 2 or S.shape[1] != cfg.dim:
+        raise ValueError(f"S must be [max_slots, {cfg.dim}], got {list(S.shape)}")
+    if (S.dtype is _F32 and src_slots.dtype is _I32T and dst_slots.dtype is _I32T and S.get_device() == src_slots.get_device() == dst_slots.get_device() == dev
+            and S.is_contiguous() and src_slots.is_contiguous() and dst_slots.is_contiguous()):
+        return S.data_ptr(), src_slots.data_ptr(), dst_slots.data_ptr()
+    return _ptr("S", S, _F32, dev), _ptr("src_slots", src_slots, _I32T, dev), _ptr("dst_slots", dst_slots, _I32T, dev)
 
 
 def kda_glr_decode(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tensor, src_slots: torch.Tensor, dst_slots: torch.Tensor,
@@ -734,10 +739,9 @@ def kda_glr_decode(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tenso
     dev = _current_device()
     B = src_slots.numel()
     _params_ok(cfg, params, dev)
-    _states_ok(cfg, S, src_slots, dst_slots)
+    Sp, sp, dp = _states(cfg, S, src_slots, dst_slots, dev)
     r = _row_args(_PACK_GLR_ROWS, _GLR_ROWS, (x, a, b, g, out), B * n, cfg.dim, _F32 if cfg.io_dtype == KDA_F32 else _BF16, dev)
-    st = lib().kda_glr_decode(cfg, params, _ptr("S", S, _F32, dev), S.shape[0], _ptr("src_slots", src_slots, _I32T, dev),
-                              _ptr("dst_slots", dst_slots, _I32T, dev), B, n, r, None if err is None else _ptr("err", err, _I32T, dev),
+    st = lib().kda_glr_decode(cfg, params, Sp, S.shape[0], sp, dp, B, n, r, None if err is None else _ptr("err", err, _I32T, dev),
                               _raw_stream(stream, dev))
     if st:
         _check(st)
@@ -793,10 +797,9 @@ def kda_glr_prefill(cfg: kda_glr_config_t, params: kda_glr_params, S: torch.Tens
     if count != N + 1 or cu_seqlens.numel() != count:
         raise ValueError("cu_seqlens and cu_seqlens_host must hold N + 1 entries")
     _params_ok(cfg, params, dev)
-    _states_ok(cfg, S, src_slots, dst_slots)
+    Sp, sp, dp = _states(cfg, S, src_slots, dst_slots, dev)
     r = _row_args(_PACK_GLR_ROWS, _GLR_ROWS, (x, a, b, g, out), T, cfg.dim, _F32 if cfg.io_dtype == KDA_F32 else _BF16, dev)
-    st = lib().kda_glr_prefill(cfg, params, _ptr("S", S, _F32, dev), S.shape[0], _ptr("src_slots", src_slots, _I32T, dev),
-                               _ptr("dst_slots", dst_slots, _I32T, dev), _ptr("cu_seqlens", cu_seqlens, _I32T, dev), at, N, r,
+    st = lib().kda_glr_prefill(cfg, params, Sp, S.shape[0], sp, dp, _ptr("cu_seqlens", cu_seqlens, _I32T, dev), at, N, r,
                                None if starts is None else _glr_starts(cfg, starts, at, N, dev), _ptr("workspace", workspace, None, dev),
                                workspace.nbytes, None if err is None else _ptr("err", err, _I32T, dev), _raw_stream(stream, dev))
     if st:
