@@ -323,7 +323,7 @@ template <typename T, bool G, int W>
 __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ Exchange<W, max_cluster<T>()> ex;
+    __shared__ Exchange<W, W == 1 ? 1 : max_cluster<T>()> ex;
     constexpr int kTiles = G ? 5 : 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
@@ -468,17 +468,16 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
     }
 }
 
-template <typename T, bool G>
+template <typename T, bool G, int W>
 cudaError_t launch_back_t(const BackArgs &p, const int32_t *cu, int *parts, int dev, int sms, cudaStream_t s)
 {
-    constexpr int W = kBackWarps;
     static std::atomic<uint64_t> raised;
     static ClusterRoom room;
     const int smem = W * (G ? 5 : 4) * Tile<T, kChunk>::kBytes;
     const cudaError_t e = raise_smem_on(raised, dev, glr_back_kernel<T, G, W>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;
-    const int nc = choose_cluster(cu, p.N, p.groups, slabs, kChunk * W, max_cluster<T>(), sms, [&](int n) { return room.of(glr_back_kernel<T, G, W>, n, 32 * W, smem, dev); });
+    const int nc = choose_cluster(cu, p.N, p.groups, slabs, kChunk * W, W == 1 ? 1 : max_cluster<T>(), sms, [&](int n) { return room.of(glr_back_kernel<T, G, W>, n, 32 * W, smem, dev); });
     *parts = p.groups * nc;
     return launch_cluster(glr_back_kernel<T, G, W>, (unsigned)(p.groups * slabs * nc), nc, 32 * W, smem, s, p, nc);
 }
@@ -487,15 +486,20 @@ cudaError_t launch_back_t(const BackArgs &p, const int32_t *cu, int *parts, int 
 
 cudaError_t launch_scan(const Args &p, bool f32, const int32_t *cu, int dev, int sms, cudaStream_t s)
 {
+    if (short_sequences(cu, p.N, p.D, f32)) return launch_walk(p, f32, s);
     if (p.rows.g) return f32 ? launch_scan_t<float, true>(p, cu, dev, sms, s) : launch_scan_t<__nv_bfloat16, true>(p, cu, dev, sms, s);
     return f32 ? launch_scan_t<float, false>(p, cu, dev, sms, s) : launch_scan_t<__nv_bfloat16, false>(p, cu, dev, sms, s);
 }
 
 cudaError_t launch_scan_back(const BackArgs &p, bool f32, const int32_t *cu, int *parts, int dev, int sms, cudaStream_t s)
 {
-    if (p.rows.g)
-        return f32 ? launch_back_t<float, true>(p, cu, parts, dev, sms, s) : launch_back_t<__nv_bfloat16, true>(p, cu, parts, dev, sms, s);
-    return f32 ? launch_back_t<float, false>(p, cu, parts, dev, sms, s) : launch_back_t<__nv_bfloat16, false>(p, cu, parts, dev, sms, s);
+    const bool one = one_warp(cu, p.N, (p.D + kSlab - 1) / kSlab, sms);
+    if (f32) {
+        if (p.rows.g) return one ? launch_back_t<float, true, 1>(p, cu, parts, dev, sms, s) : launch_back_t<float, true, kBackWarps>(p, cu, parts, dev, sms, s);
+        return one ? launch_back_t<float, false, 1>(p, cu, parts, dev, sms, s) : launch_back_t<float, false, kBackWarps>(p, cu, parts, dev, sms, s);
+    }
+    if (p.rows.g) return one ? launch_back_t<__nv_bfloat16, true, 1>(p, cu, parts, dev, sms, s) : launch_back_t<__nv_bfloat16, true, kBackWarps>(p, cu, parts, dev, sms, s);
+    return one ? launch_back_t<__nv_bfloat16, false, 1>(p, cu, parts, dev, sms, s) : launch_back_t<__nv_bfloat16, false, kBackWarps>(p, cu, parts, dev, sms, s);
 }
 
 }  // namespace glr

@@ -1,4 +1,5 @@
-// kda_glr_scan.cuh - the launches of the scan along the tokens (kda_glr_scan.cu) and how many blocks share one.
+// kda_glr_scan.cuh - the launches over whole sequences: the scan along the tokens (kda_glr_scan.cu), how many blocks share one,
+// and the walk of short sequences (kda_glr_walk.cu).
 #pragma once
 
 #include "kda_glr.cuh"
@@ -116,6 +117,38 @@ inline int64_t back_parts(int32_t N, int64_t slabs)
 {
     const int64_t groups = back_groups(N, slabs), shared = kMaxShared / slabs;
     return groups > shared ? groups : shared;
+}
+
+inline int32_t longest_of(const int32_t *cu, int32_t N)
+{
+    int32_t n = 0;
+    for (int32_t i = 0; i < N; ++i) n = cu[i + 1] - cu[i] > n ? cu[i + 1] - cu[i] : n;
+    return n;
+}
+
+// Whether a thread takes each sequence of a prefill from end to end (kda_glr_walk.cu), by estimates in microseconds that were
+// fitted to both: 0.17 a token of the longest sequence, or 400 (FP32: 300) channels of a token a ns, against a block's start
+// for every sequence's 64 channels and 500 (234) channels a ns. Both sides, sequences of 0 to n tokens in BF16 with a gate:
+//   300 of 1024 channels  n = 16: 11 us, scan 30   64: 40, 47   128: 77, 72      30 of 256  n = 16: 5.2, 5.6   64: 12, 6
+//   4000 of 4096 channels n = 2: 220 us, scan 1177   16: 464, 1629   64: 1345, 2130    FP32, 300 of 1024: 64: 48, 142
+inline bool short_sequences(const int32_t *cu, int32_t N, int32_t D, bool f32)
+{
+    const double longest = longest_of(cu, N), work = (double)cu[N] * D * 1e-3;
+    const double chain = 0.17 * longest, flow = work / (f32 ? 300 : 400);
+    const double walk = 2 + (chain > flow ? chain + 0.5 * flow : flow + 0.5 * chain);
+    const double units = (double)N * ((D + kSlab - 1) / kSlab);
+    return walk < 5.5 + units * (f32 ? 0.0165 : 0.0036) + work / (f32 ? 234 : 500) + longest / 700;
+}
+cudaError_t launch_walk(const Args &p, bool f32, cudaStream_t s);
+
+// Whether a block of a backward has one warp: where no sequence has more than a warp's 16 tokens, or where they are short and
+// many enough to fill the GPU so (12 a SM). Sequences of 0 to n tokens, BF16 with a gate:
+//   300 of 4096 channels n = 8: 90 us, four warps 194   32: 171, 284   64: 287, 346   128: 508, 552
+//   30 of 1024 channels  n = 16: 9.4 us, four warps 10.3   32: 13, 10   64: 24, 12
+inline bool one_warp(const int32_t *cu, int32_t N, int64_t slabs, int sms)
+{
+    const int32_t longest = longest_of(cu, N);
+    return longest <= kChunk || (longest <= 4 * kChunk && N * slabs >= kBackPerSm * sms);
 }
 
 // cu: the host's cu_seqlens

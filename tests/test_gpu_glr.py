@@ -147,12 +147,20 @@ def test_wide_rows(D, bf16):
     p.check_grads(p.backward())
 
 
-def test_many_short_sequences():
-    lens = list(np.random.default_rng(5).integers(0, 9, 700))
-    p = Problem(lens, 40, True, True, seed=2)
+@pytest.mark.parametrize("count,top,D,bf16,gate,packed", [(700, 8, 40, True, True, False), (300, 16, 256, True, False, True), (2000, 2, 72, False, True, False),
+                                                         (150, 64, 1024, True, True, True), (90, 200, 520, False, True, False), (30, 33, 2048, False, False, True)])
+def test_many_short_sequences(count, top, D, bf16, gate, packed):
+    """Both ways of a prefill, and blocks of one warp and of four in the backward."""
+    lens = list(np.random.default_rng(5).integers(0, top + 1, count))
+    p = Problem(lens, D, bf16, gate, packed, seed=2)
     p.prefill()
     p.check()
-    p.check_grads(p.backward())
+    got = p.backward()
+    p.check_grads(got)
+    first = p.out.clone()
+    p.prefill(starts=False)
+    again = p.backward()
+    assert torch.equal(first, p.out) and all(torch.equal(got[n], again[n]) for n in got)
 
 
 def test_a_long_memory():
