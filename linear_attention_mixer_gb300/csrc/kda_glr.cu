@@ -163,7 +163,15 @@ bool workspace_ok(const void *ws, size_t bytes, size_t need)
     return fail(KDA_ERR_INVALID, "workspace is NULL, not 16-byte aligned, or holds %zu bytes of %zu needed", bytes, need), false;
 }
 
-size_t back_bytes(int32_t N, int32_t D) { return N == 0 ? 0 : (size_t)back_parts(N, slabs_of(D)) * 3 * D * sizeof(float); }
+// The workspace: a backward's partial sums, then what split sequences need.
+size_t sums_bytes(int32_t N, int32_t D) { return N == 0 ? 0 : ((size_t)back_parts(N, slabs_of(D)) * 3 * D * sizeof(float) + 255) / 256 * 256; }
+size_t need_bytes(int32_t N, int32_t D) { return N == 0 ? 256 : 256 + sums_bytes(N, D) + split_bytes(N, slabs_of(D)); }
+void lay_out(Split &split, void *workspace, int32_t N, int32_t D)
+{
+    char *at = static_cast<char *>(workspace) + sums_bytes(N, D);
+    split.pairs = reinterpret_cast<float4 *>(at);
+    split.S0 = reinterpret_cast<float *>(at + split_pairs_bytes(N, slabs_of(D)));
+}
 
 }  // namespace
 }  // namespace glr
@@ -211,7 +219,7 @@ kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *par
 size_t kda_glr_workspace_bytes(const kda_glr_config_t *cfg, const int32_t *cu_seqlens_host, int32_t N)
 {
     if (!glr::cfg_ok(cfg) || !glr::lengths_ok(cu_seqlens_host, N)) return 0;
-    return 256 + glr::back_bytes(N, cfg->dim);
+    return glr::need_bytes(N, cfg->dim);
 }
 
 int64_t kda_glr_chunks(const int32_t *cu_seqlens_host, int32_t N)
@@ -230,11 +238,12 @@ kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *pa
     const int64_t T = cu_seqlens_host[N];
     if (!glr::call_ok(cfg, params, S, max_slots, src_slots, dst_slots, rows, T) || !glr::f32_or_null_ok("starts", starts)) return KDA_ERR_INVALID;
     if (N * glr::slabs_of(cfg->dim) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
-    if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(N, cfg->dim))) return KDA_ERR_INVALID;
+    if (!glr::workspace_ok(workspace, workspace_bytes, glr::need_bytes(N, cfg->dim))) return KDA_ERR_INVALID;
     glr::Args p = glr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, N, rows, err);
     p.cu = cu_seqlens;
     p.total_T = T;
     p.starts = starts;
+    glr::lay_out(p.split, workspace, N, cfg->dim);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int dev = 0, sms = 0;
     cudaError_t e = current_sms(&dev, &sms);
@@ -269,12 +278,13 @@ kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *p
             if (r->g && (!glr::row_ok("g", r->g, r->g_stride, T, cfg) || !glr::row_ok("dg", r->dg, r->dg_stride, T, cfg))) return KDA_ERR_INVALID;
         }
         if (N * glr::slabs_of(D) > INT_MAX / 16) return glr::fail(KDA_ERR_INVALID, "N * dim is too large");
-        if (!glr::workspace_ok(workspace, workspace_bytes, 256 + glr::back_bytes(N, D))) return KDA_ERR_INVALID;
+        if (!glr::workspace_ok(workspace, workspace_bytes, glr::need_bytes(N, D))) return KDA_ERR_INVALID;
         glr::BackArgs p = {};
         p.err = err; p.cu = cu_seqlens; p.N = N; p.total_T = T; p.D = D;
         p.A_log = params->A_log; p.a_bias = params->a_bias; p.b_bias = params->b_bias;
         p.starts = starts; p.rows = *rows; p.dS_last = dS_last; p.dS_first = dS_first;
         p.part = static_cast<float *>(workspace);
+        glr::lay_out(p.split, workspace, N, D);
         p.groups = glr::back_groups(N, glr::slabs_of(D));
         int dev = 0, sms = 0;
         if ((e = current_sms(&dev, &sms)) == cudaSuccess) e = glr::launch_scan_back(p, cfg->io_dtype == KDA_F32, cu_seqlens_host, &parts, dev, sms, s);
@@ -285,7 +295,6 @@ kda_status kda_glr_backward(const kda_glr_config_t *cfg, const kda_glr_params *p
         // without sequences no kernel of this call comes before it
         if (parts > 0) e = launch_after(glr::glr_param_sums_kernel, grid, sum_block(parts), 0, s, part, parts, D, dA_log, da_bias, db_bias);
         else glr::glr_param_sums_kernel<<<grid, sum_block(0), 0, s>>>(part, 0, D, dA_log, da_bias, db_bias), e = cudaGetLastError();
-
     }
     return e == cudaSuccess ? KDA_OK : glr::fail(KDA_ERR_CUDA, "kda_glr_backward: %s", cudaGetErrorString(e));
 }

@@ -19,6 +19,16 @@ namespace glr {
 constexpr int kChunk = 16;   // tokens between the states that a forward keeps for its backward
 constexpr int kSlab = 64;    // channels of a warp
 
+// A long sequence of few channels in parts that different clusters take at once. A part's first state is folded from the
+// pairs (A, H) of the `sub` tokens each before it, which another kernel works out before.
+struct Split {
+    int32_t parts;   // of a sequence; 1: not split
+    int32_t plen;    // tokens of a part, a multiple of sub; the last part has what is left
+    int32_t sub, subs;
+    float4 *pairs;   // [N][subs][D / 2]
+    float *S0;       // [N][D]: the states at the start, since the call writes to the slots
+};
+
 struct Args {
     float *S;  // [max_slots][D]
     int32_t max_slots;
@@ -31,6 +41,7 @@ struct Args {
     const float *A_log, *a_bias, *b_bias;
     kda_glr_rows rows;
     float *starts;  // may be null
+    Split split;
 };
 
 struct BackArgs {
@@ -45,7 +56,8 @@ struct BackArgs {
     const float *dS_last;  // may be null: zeros
     float *dS_first;       // may be null
     float *part;           // sums over tokens: [groups x blocks a cluster][3][D]
-    int32_t groups;        // sequences in work at once
+    int32_t groups;        // parts of sequences in work at once
+    Split split;
 };
 
 __device__ __forceinline__ void set_err(int32_t *err, int32_t what = kErrBadSlot)

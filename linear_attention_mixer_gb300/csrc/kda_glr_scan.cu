@@ -132,6 +132,27 @@ __device__ __forceinline__ float2 meet(Exchange<W, MAX> &ex, const Lin &pre, con
     carry = h;
     return pre.at(mine);
 }
+// What the pairs q0 .. q1 - 1 of a split sequence make of `carry` (BACK: from the last of them on). Each warp folds its share of them;
+// all threads of the block take part, before its first window.
+template <bool BACK, int W, int MAX>
+__device__ __forceinline__ float2 fold(Exchange<W, MAX> &ex, const Split &split, int row, int D, int c, bool live, int q0, int q1, float2 carry)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = q1 - q0;
+    const int a = q0 + n * warp / W, b = q0 + n * (warp + 1) / W;
+    Lin own = lin_identity();
+    if (live) {
+        const float4 *pair = split.pairs + (size_t)row * split.subs * (D / 2) + c / 2;
+#pragma unroll 8
+        for (int i = 0; i < b - a; ++i) own.then(ld_lin(pair + (size_t)(BACK ? b - 1 - i : a + i) * (D / 2)));
+    }
+    __syncthreads();  // a backward's part before this one has read what is written here
+    ex.warp[1][warp][lane] = as_float4(own);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) carry = ld_lin(&ex.warp[1][BACK ? W - 1 - i : i][lane]).at(carry);
+    __syncthreads();  // and the windows write it again
+    return carry;
+}
 // Before a block of a cluster ends: none sends to it any more. What was sent to it has arrived, as it has waited for that;
 // where a wait gave up, it gets some time to.
 __device__ __forceinline__ void leave(int nc, bool joined, bool good)
@@ -197,6 +218,101 @@ __device__ __forceinline__ void all_gates(const Chan &ch, const unsigned char *x
     __syncwarp();
 }
 
+// ---------------------------------------------------------------- pairs of a split sequence
+// The pair of `sub` tokens of 64 channels: each of eight warps takes an eighth of them, 16 at a time with the next 16 on their way.
+// BACK: from the gradient of the state behind the tokens to that before them, else from the state before to that behind.
+constexpr int kPairWarps = 8;
+template <typename T, bool BACK, bool G>
+__global__ void __launch_bounds__(32 * kPairWarps) glr_pairs_kernel(const __grid_constant__ Args p, const void *dout, int64_t dout_stride)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float4 sh[kPairWarps][32];
+    using Tl = Tile<T, kChunk>;
+    constexpr int kTiles = BACK ? (G ? 3 : 2) : 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slabs = (p.D + kSlab - 1) / kSlab, q = blockIdx.x % p.split.subs, u = blockIdx.x / p.split.subs;
+    const int row = u / slabs, c0 = (u - row * slabs) * kSlab, c = c0 + 2 * lane;
+    int src = -1, dst, s0, s1;
+    if (!bounds_ok(p.cu, row, p.N, p.total_T, s0, s1) || (!BACK && !slots_ok(p, row, src, dst))) return;  // the kernel behind this one says so
+    const bool live = c < p.D;
+    if (!BACK && q == 0 && warp == 0 && live)
+        *reinterpret_cast<float2 *>(p.split.S0 + (size_t)row * p.D + c) = src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
+    const int len = s1 - s0, off = q * p.split.sub;
+    if (off >= len) return;
+    Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
+    if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
+    const int each = p.split.sub / kPairWarps;  // a multiple of 16
+    const int t0 = off + warp * each;
+    // the last pair of a backward has all that is left
+    const int t1 = BACK && q == p.split.subs - 1 && warp == kPairWarps - 1 ? len : min(len, t0 + each);
+    unsigned char *tile = smem + (size_t)warp * 2 * kTiles * Tl::kBytes;
+    const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tl::kUnits) < p.D;
+    auto fetch = [&](int t, int stage) {
+        const int nv = t1 - t;
+        unsigned char *to = tile + stage * kTiles * Tl::kBytes;
+        const int64_t r = (int64_t)s0 + t;
+        if (nv > 0) {
+            Tl::fetch(to, static_cast<const T *>(p.rows.a) + r * p.rows.a_stride + c0, p.rows.a_stride, nv, col_ok);
+            if (BACK) {
+                Tl::fetch(to + Tl::kBytes, static_cast<const T *>(dout) + r * dout_stride + c0, dout_stride, nv, col_ok);
+                if (G) Tl::fetch(to + 2 * Tl::kBytes, static_cast<const T *>(p.rows.g) + r * p.rows.g_stride + c0, p.rows.g_stride, nv, col_ok);
+            } else {
+                Tl::fetch(to + Tl::kBytes, static_cast<const T *>(p.rows.x) + r * p.rows.x_stride + c0, p.rows.x_stride, nv, col_ok);
+                Tl::fetch(to + 2 * Tl::kBytes, static_cast<const T *>(p.rows.b) + r * p.rows.b_stride + c0, p.rows.b_stride, nv, col_ok);
+            }
+        }
+        commit();
+    };
+    Lin own = lin_identity();
+    fetch(t0, 0);
+    int stage = 0;
+#pragma unroll 1
+    for (int t = t0; t < t1; t += kChunk, stage ^= 1) {
+        fetch(t + kChunk, stage ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const unsigned char *a = tile + stage * kTiles * Tl::kBytes;
+        const int nv = min(kChunk, t1 - t);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            if (i < nv) {
+                if (BACK) {
+                    const float2 e = expm1_neg(f2_mul(ch.nA, rcp2(f2_add(neg_exp(Tl::get(a, i), ch.ca), f2(1.f)))));
+                    float2 dh = Tl::get(a + Tl::kBytes, i);
+                    if (G) dh = f2_mul(dh, silu2(Tl::get(a + 2 * Tl::kBytes, i)));
+                    own.A = f2_fma(own.A, e, own.A);
+                    own.H = f2_fma(own.A, dh, own.H);
+                } else {
+                    float2 e, u2;
+                    gates(ch, Tl::get(a + Tl::kBytes, i), Tl::get(a, i), Tl::get(a + 2 * Tl::kBytes, i), e, u2);
+                    own.H = step(own.H, e, u2);
+                    own.A = f2_fma(own.A, e, own.A);
+                }
+            }
+        __syncwarp();
+    }
+    cp_async_wait_all();
+    sh[warp][lane] = as_float4(own);
+    __syncthreads();
+    if (warp != 0 || !live) return;
+    Lin run = lin_identity();
+#pragma unroll
+    for (int i = 0; i < kPairWarps; ++i) run.then(ld_lin(&sh[BACK ? kPairWarps - 1 - i : i][lane]));
+    p.split.pairs[((size_t)row * p.split.subs + q) * (p.D / 2) + c / 2] = as_float4(run);
+}
+
+template <typename T, bool BACK, bool G>
+cudaError_t launch_pairs(const Args &p, const void *dout, int64_t dout_stride, int dev, cudaStream_t s)
+{
+    static std::atomic<uint64_t> raised;
+    const int smem = kPairWarps * 2 * (BACK ? (G ? 3 : 2) : 3) * Tile<T, kChunk>::kBytes;
+    const cudaError_t e = raise_smem_on(raised, dev, glr_pairs_kernel<T, BACK, G>, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t slabs = (p.D + kSlab - 1) / kSlab;
+    glr_pairs_kernel<T, BACK, G><<<(unsigned)(p.N * slabs * p.split.subs), 32 * kPairWarps, smem, s>>>(p, dout, dout_stride);
+    return cudaGetLastError();
+}
+
 // ---------------------------------------------------------------- prefill
 template <typename T, bool G, int W, int R>
 __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
@@ -207,15 +323,26 @@ __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(
     using Tl = Tile<T, R>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
-    const int row = cid / slabs, c0 = (cid - row * slabs) * kSlab, c = c0 + 2 * lane;
+    const int unit = cid / slabs, c0 = (cid - unit * slabs) * kSlab, c = c0 + 2 * lane;
+    const int row = unit / p.split.parts, part = unit - row * p.split.parts;
     int src, dst, s0, s1;
     if (!bounds_ok(p.cu, row, p.N, p.total_T, s0, s1) || !slots_ok(p, row, src, dst)) {  // the same for the whole cluster
         if (threadIdx.x == 0 && rank == 0) set_err(p.err);
         return;
     }
     const bool live = c < p.D;
-    float2 carry = live && src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
-    const int len = s1 - s0;
+    const int off = part * p.split.plen;  // this part's first token
+    if (part > 0 && off >= s1 - s0) return;
+    const bool to_end = part == p.split.parts - 1 || s1 - s0 - off <= p.split.plen;
+    const int len = to_end ? s1 - s0 - off : p.split.plen;
+    float2 carry = f2(0.f);
+    if (p.split.parts == 1) {
+        if (live && src >= 0) carry = *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c);
+    } else {
+        if (live) carry = *reinterpret_cast<const float2 *>(p.split.S0 + (size_t)row * p.D + c);
+        carry = fold<false>(ex, p.split, row, p.D, c, live, 0, off / p.split.sub, carry);
+    }
+    s0 += off;
     if (len > 0) {
         if (nc > 1) {
             if (threadIdx.x == 0) ex.open();
@@ -232,7 +359,7 @@ __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(
         const T *xp = static_cast<const T *>(p.rows.x) + (int64_t)s0 * p.rows.x_stride + c0, *ap = static_cast<const T *>(p.rows.a) + (int64_t)s0 * p.rows.a_stride + c0;
         const T *bp = static_cast<const T *>(p.rows.b) + (int64_t)s0 * p.rows.b_stride + c0, *gp = G ? static_cast<const T *>(p.rows.g) + (int64_t)s0 * p.rows.g_stride + c0 : nullptr;
         T *op = static_cast<T *>(p.rows.out) + (int64_t)s0 * p.rows.out_stride + c;
-        float *st = p.starts ? p.starts + first_chunk(s0, row) * p.D + c : nullptr;
+        float *st = p.starts ? p.starts + (first_chunk(s0 - off, row) + off / kChunk) * p.D + c : nullptr;
         auto fetch = [&](int at) {
             const int nv = len - at;
             if (nv > 0) {
@@ -297,7 +424,7 @@ __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(
         leave(nc, true, good);
         if (!good && lane == 0) set_err(p.err, KDA_ERR_TIMEOUT);
     }
-    if (rank == 0 && warp == 0 && live) *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = carry;
+    if (to_end && rank == 0 && warp == 0 && live) *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = carry;
 }
 
 template <typename T, bool G>
@@ -310,14 +437,20 @@ cudaError_t launch_scan_t(const Args &p, const int32_t *cu, int dev, int sms, cu
     const cudaError_t e = raise_smem_on(raised, dev, glr_scan_kernel<T, G, W, R>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;
-    const int nc = choose_cluster(cu, p.N, p.N, slabs, R * W, max_cluster<T>(), sms, [&](int n) { return room.of(glr_scan_kernel<T, G, W, R>, n, 32 * W, smem, dev); });
-    return launch_cluster(glr_scan_kernel<T, G, W, R>, (unsigned)(p.N * slabs * nc), nc, 32 * W, smem, s, p, nc);
+    Args q = p;
+    const int nc = choose_parts(cu, p.N, p.N, slabs, R * W, max_cluster<T>(), sms, false, q.split,
+                                [&](int n) { return room.of(glr_scan_kernel<T, G, W, R>, n, 32 * W, smem, dev); });
+    if (q.split.parts > 1) {
+        const cudaError_t first = launch_pairs<T, false, false>(q, nullptr, 0, dev, s);
+        if (first != cudaSuccess) return first;
+    }
+    return launch_cluster(glr_scan_kernel<T, G, W, R>, (unsigned)(p.N * q.split.parts * slabs * nc), nc, 32 * W, smem, s, q, nc);
 }
 
 // ---------------------------------------------------------------- backward
 // The same from the last window to the first, with c the gradient of the state behind a token: c -> alpha (dh + c) is linear
 // too. What a token's gradients need beside it is the state before it, which a warp walks again from the one that the
-// forward kept for its 16 tokens. A cluster has the sequences group, group + groups, .. and adds up its tokens' shares of
+// forward kept for its 16 tokens. A cluster has the sequences (or their parts) group, group + groups, .. and adds up its tokens' shares of
 // the parameters' gradients in registers: one row of partial sums a block.
 template <typename T, bool G, int W>
 __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
@@ -344,19 +477,26 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
         cluster_arrive();
     }
 #pragma unroll 1
-    for (int row = group; row < p.N; row += p.groups) {
+    for (int unit = group; unit < p.N * p.split.parts; unit += p.groups) {
+        const int row = unit / p.split.parts, part = unit - row * p.split.parts;
         int s0, s1;
         if (!bounds_ok(p.cu, row, p.N, p.total_T, s0, s1)) {  // the same for the whole cluster
             if (threadIdx.x == 0 && rank == 0) set_err(p.err);
             continue;
         }
-        const int len = s1 - s0;
+        const int off = part * p.split.plen;  // this part's first token
+        if (part > 0 && off >= s1 - s0) continue;
+        const bool to_end = part == p.split.parts - 1 || s1 - s0 - off <= p.split.plen;
+        const int len = to_end ? s1 - s0 - off : p.split.plen;
         float2 carry = live && p.dS_last ? *reinterpret_cast<const float2 *>(p.dS_last + (size_t)row * p.D + c) : f2(0.f);
         if (len == 0) {  // no window, and no row that could be asked for
             if (rank == 0 && warp == 0 && live && p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = carry;
             continue;
         }
-        const float *st = p.starts + first_chunk(s0, row) * p.D + c;
+        if (!to_end)
+            carry = fold<true>(ex, p.split, row, p.D, c, live, (off + len) / p.split.sub, min((s1 - s0 + p.split.sub - 1) / p.split.sub, p.split.subs), carry);
+        const float *st = p.starts + (first_chunk(s0, row) + off / kChunk) * p.D + c;
+        s0 += off;
         auto fetch = [&](int at) {
             const int nv = len - at;
             const int64_t r = (int64_t)s0 + at;
@@ -448,7 +588,7 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
             }
             if (t >= own_t + window) fetch(t - window);
         }
-        if (rank == 0 && warp == 0 && live && p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = carry;
+        if (part == 0 && rank == 0 && warp == 0 && live && p.dS_first) *reinterpret_cast<float2 *>(p.dS_first + (size_t)row * p.D + c) = carry;
     }
     leave(nc, turn > 0, good);
     if (!good && lane == 0) set_err(p.err, KDA_ERR_TIMEOUT);
@@ -477,9 +617,19 @@ cudaError_t launch_back_t(const BackArgs &p, const int32_t *cu, int *parts, int 
     const cudaError_t e = raise_smem_on(raised, dev, glr_back_kernel<T, G, W>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;
-    const int nc = choose_cluster(cu, p.N, p.groups, slabs, kChunk * W, W == 1 ? 1 : max_cluster<T>(), sms, [&](int n) { return room.of(glr_back_kernel<T, G, W>, n, 32 * W, smem, dev); });
-    *parts = p.groups * nc;
-    return launch_cluster(glr_back_kernel<T, G, W>, (unsigned)(p.groups * slabs * nc), nc, 32 * W, smem, s, p, nc);
+    BackArgs q = p;
+    const int nc = choose_parts(cu, p.N, p.groups, slabs, kChunk * W, W == 1 ? 1 : max_cluster<T>(), sms, true, q.split,
+                                [&](int n) { return room.of(glr_back_kernel<T, G, W>, n, 32 * W, smem, dev); });
+    if (q.split.parts > 1) {
+        Args f = {};
+        f.cu = p.cu; f.N = p.N; f.total_T = p.total_T; f.D = p.D; f.A_log = p.A_log; f.a_bias = p.a_bias; f.b_bias = p.b_bias; f.split = q.split;
+        f.rows.a = p.rows.a; f.rows.a_stride = p.rows.a_stride; f.rows.g = p.rows.g; f.rows.g_stride = p.rows.g_stride;
+        const cudaError_t first = launch_pairs<T, true, G>(f, p.rows.dout, p.rows.dout_stride, dev, s);
+        if (first != cudaSuccess) return first;
+        q.groups = p.N * q.split.parts;
+    }
+    *parts = q.groups * nc;
+    return launch_cluster(glr_back_kernel<T, G, W>, (unsigned)(q.groups * slabs * nc), nc, 32 * W, smem, s, q, nc);
 }
 
 }  // namespace

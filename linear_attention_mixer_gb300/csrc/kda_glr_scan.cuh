@@ -77,10 +77,9 @@ struct ClusterRoom {
 // and the work of all of the SM's blocks; where all clusters run at once the longest sequence's windows count,
 // else the work of all. Any number, or, to look at many sequences quickly, powers of two.
 template <typename Room>
-inline int choose_cluster(const int32_t *cu, int32_t N, int32_t groups, int64_t slabs, int tile, int most, int sms, Room room)
+inline int choose_cluster(const int32_t *cu, int32_t N, int32_t groups, int64_t slabs, int tile, int most, int sms, Room room, double &least)
 {
     int best = 1;
-    double least = 0;
     for (int nc = 1; nc <= most; nc += N > 64 ? nc : 1) {
         if (nc > 1 && groups * slabs * nc > kMaxShared) break;
         const int at_once = room(nc);
@@ -105,6 +104,61 @@ inline int choose_cluster(const int32_t *cu, int32_t N, int32_t groups, int64_t 
     return best;
 }
 
+inline int32_t longest_of(const int32_t *cu, int32_t N)
+{
+    int32_t n = 0;
+    for (int32_t i = 0; i < N; ++i) n = cu[i + 1] - cu[i] > n ? cu[i + 1] - cu[i] : n;
+    return n;
+}
+
+// Sequences of up to so many times 64 channels may be split, into so many pairs of tokens' (A, H) at most.
+constexpr int kSplitUnits = 152, kSplitPairs = 4864;
+inline size_t split_pairs_bytes(int32_t N, int64_t slabs) { return N * slabs <= kSplitUnits ? (size_t)kSplitPairs * (kSlab / 2) * sizeof(float4) : 0; }
+inline size_t split_bytes(int32_t N, int64_t slabs)
+{
+    return N * slabs <= kSplitUnits ? split_pairs_bytes(N, slabs) + (size_t)N * slabs * kSlab * sizeof(float) : 0;
+}
+
+// choose_cluster, and whether each sequence is split into parts that run at once: where that pays for reading the rows twice, by
+// the same estimate. The pairs' kernel takes a start (300), its blocks' 16 tokens one after the other, and the fold.
+//   65536 tokens in BF16: 64 channels 27 us, in one part 137   256: 70, 139   1024: 205, 220   8192 tokens: 64: 19, 21   256: 21, 21
+//   (with the backward 65536: 68, 426   206, 453   8192: 38, 61   46, 61)
+template <typename Room>
+inline int choose_parts(const int32_t *cu, int32_t N, int32_t groups, int64_t slabs, int tile, int most, int sms, bool back, Split &split, Room room)
+{
+    double least = 0;
+    int best = choose_cluster(cu, N, groups, slabs, tile, most, sms, room, least);
+    split.parts = 1;
+    const int32_t longest = longest_of(cu, N);
+    split.plen = longest;
+    split.sub = 512;
+    split.subs = 0;
+    if (N * slabs > kSplitUnits || groups < N || longest < 4096 || longest > 1 << 24) return best;
+    while (longest > 128 * split.sub) split.sub *= 2;
+    const int sub = split.sub;
+    least *= 0.9;
+    for (int parts = 2; parts <= 32; parts *= 2) {
+        const int plen = (longest / parts + sub - 1) / sub * sub, subs = (parts - 1 + back) * (plen / sub);
+        if ((int64_t)plen * (parts - 1) >= longest || N * subs * slabs > kSplitPairs) break;
+        const double pairs = 500 + sub / 128 * (110.0 + 64.0 * N * subs * slabs / sms) + 3.0 * subs;
+        int64_t clusters = 0;  // that have tokens
+        for (int32_t i = 0; i < N; ++i) {
+            const int n = (cu[i + 1] - cu[i] + plen - 1) / plen;
+            clusters += (n < 1 ? 1 : n < parts ? n : parts) * slabs;
+        }
+        for (int nc = 1; nc <= most; nc *= 2) {
+            if (N * parts * slabs * nc > kMaxShared || clusters > room(nc)) continue;
+            const int path = ((plen > longest - (parts - 1) * plen ? plen : longest - (parts - 1) * plen) + tile * nc - 1) / (tile * nc);
+            const double cost = pairs + path * ((nc == 1 ? 128.0 : 192.0) + tile * (double)(clusters * nc) / sms);
+            if (cost < least) {
+                least = cost, best = nc;
+                split.parts = parts, split.plen = plen, split.subs = subs;
+            }
+        }
+    }
+    return best;
+}
+
 // Sequences that are in work at once in a backward: as many as give every SM's blocks several turns. Each has its rows
 // of partial sums, so that these stay few beside the tokens' rows.
 inline int back_groups(int32_t N, int64_t slabs)
@@ -117,13 +171,6 @@ inline int64_t back_parts(int32_t N, int64_t slabs)
 {
     const int64_t groups = back_groups(N, slabs), shared = kMaxShared / slabs;
     return groups > shared ? groups : shared;
-}
-
-inline int32_t longest_of(const int32_t *cu, int32_t N)
-{
-    int32_t n = 0;
-    for (int32_t i = 0; i < N; ++i) n = cu[i + 1] - cu[i] > n ? cu[i + 1] - cu[i] : n;
-    return n;
 }
 
 // Whether a thread takes each sequence of a prefill from end to end (kda_glr_walk.cu), by estimates in microseconds that were

@@ -139,6 +139,24 @@ def test_prefill_and_backward(lens, D, bf16, gate, packed):
     p.check_grads(p.backward())
 
 
+@pytest.mark.parametrize("lens,D,bf16,gate,packed,slow", [([20000], 72, True, True, False, True), ([9000, 3, 0, 16384], 64, False, False, True, False),
+                                                          ([0, 33000, 1025], 8, True, False, True, True), ([5000, 12288, 4097], 200, True, True, False, False),
+                                                          ([70001], 4, False, True, False, True)])
+def test_long_sequences_of_few_channels(lens, D, bf16, gate, packed, slow):
+    """Sequences in parts that are worked on at once, also into the slots that they came from."""
+    p = Problem(lens, D, bf16, gate, packed, seed=17, slow=slow)
+    p.dst = p.src
+    p.prefill()
+    p.check()
+    got = p.backward()
+    p.check_grads(got)
+    first = p.out.clone()
+    p.S[:p.N] = p.dev["h0"]
+    p.prefill(starts=False)
+    again = p.backward()
+    assert torch.equal(first, p.out) and all(torch.equal(got[n], again[n]) for n in got)
+
+
 @pytest.mark.parametrize("D,bf16", [(12288, True), (7168, False)])
 def test_wide_rows(D, bf16):
     p = Problem([150, 20], D, bf16, seed=1)
