@@ -35,13 +35,16 @@ __device__ __forceinline__ void st_remote(const float4 *mine, const uint64_t *ba
 #ifndef KDA_GLR_WAIT_LIMIT
 #define KDA_GLR_WAIT_LIMIT (1u << 24)
 #endif
-// Until what other blocks of the cluster sent has arrived; false when the limit ran out.
-__device__ __forceinline__ bool wait_cluster(const uint64_t *bar, uint32_t parity)
+// Until what other blocks of the cluster sent has arrived; false when the limit ran out, or another warp of the cluster's
+// did (`stop`): what is missing may then never be sent.
+__device__ __forceinline__ bool wait_cluster(const uint64_t *bar, uint32_t parity, const volatile int32_t *stop)
 {
     uint32_t ok = 0;
-    for (uint32_t i = 0; i < KDA_GLR_WAIT_LIMIT && !ok; ++i)
+    for (uint32_t i = 0; i < KDA_GLR_WAIT_LIMIT && !ok; ++i) {
         asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (!ok && *stop) break;
+    }
     return __all_sync(0xFFFFFFFFu, ok != 0);
 }
 
@@ -70,8 +73,10 @@ struct Exchange {
     float4 warp[2][W][32];
     float4 block[2][MAX][32];
     uint64_t bar[2];
+    int32_t stop;  // set in every block of the cluster by a warp that gave up
     __device__ __forceinline__ void open()  // one thread
     {
+        stop = 0;
         mbar_init(&bar[0], 1);
         mbar_init(&bar[1], 1);
         fence_mbar_init();
@@ -115,7 +120,15 @@ __device__ __forceinline__ float2 meet(Exchange<W, MAX> &ex, const Lin &pre, con
         carry = all.at(carry);
         return h;
     }
-    if (good) good = wait_cluster(&ex.bar[par], (uint32_t)(turn >> 1) & 1);
+    if (good) {
+        good = wait_cluster(&ex.bar[par], (uint32_t)(turn >> 1) & 1, &ex.stop);
+        if (!good && lane < nc) {
+            uint32_t a;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&ex.stop)), "r"(lane));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(1) : "memory");
+        }
+        __syncwarp();
+    }
     float2 h = carry, mine = carry;
 #pragma unroll
     for (int j = 0; j < MAX; j += 4) {
