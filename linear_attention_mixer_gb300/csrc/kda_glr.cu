@@ -12,12 +12,13 @@ namespace kda {
 namespace glr {
 namespace {
 
-// Decode: one thread has two channels of one row through its n <= N tokens, all of which it asks for before it begins.
+// Decode: one thread has four channels of one row through its n <= N tokens, all of which it asks for before it begins.
 template <typename T, bool G, int N>
 __global__ void __launch_bounds__(128) glr_decode_kernel(const __grid_constant__ Args p)
 {
-    const int half = p.D / 2, unit = blockIdx.x * 128 + threadIdx.x;
-    const int row = unit / half, c = 2 * (unit - row * half);
+    using Q = Quad<T>;
+    const int quarter = p.D / 4, unit = blockIdx.x * 128 + threadIdx.x;
+    const int row = unit / quarter, c = 4 * (unit - row * quarter);
     if (row >= p.N) return;
     int src, dst;
     const bool ok = slots_ok(p, row, src, dst);
@@ -25,31 +26,38 @@ __global__ void __launch_bounds__(128) glr_decode_kernel(const __grid_constant__
     const T *xp = static_cast<const T *>(p.rows.x) + t0 * p.rows.x_stride + c, *ap = static_cast<const T *>(p.rows.a) + t0 * p.rows.a_stride + c;
     const T *bp = static_cast<const T *>(p.rows.b) + t0 * p.rows.b_stride + c, *gp = G ? static_cast<const T *>(p.rows.g) + t0 * p.rows.g_stride + c : nullptr;
     T *op = static_cast<T *>(p.rows.out) + t0 * p.rows.out_stride + c;
-    typename Pair<T>::Raw x[N], a[N], b[N], g[N];
+    typename Q::Raw x[N], a[N], b[N], g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
         if (i < p.n) {
-            x[i] = ld_pair(xp + i * p.rows.x_stride);
-            a[i] = ld_pair(ap + i * p.rows.a_stride);
-            b[i] = ld_pair(bp + i * p.rows.b_stride);
-            if (G) g[i] = ld_pair(gp + i * p.rows.g_stride);
+            x[i] = ld_quad(xp + i * p.rows.x_stride);
+            a[i] = ld_quad(ap + i * p.rows.a_stride);
+            b[i] = ld_quad(bp + i * p.rows.b_stride);
+            if (G) g[i] = ld_quad(gp + i * p.rows.g_stride);
         }
     if (!ok) {
         if (c == 0) set_err(p.err);
         return;
     }
-    float2 h = src >= 0 ? *reinterpret_cast<const float2 *>(p.S + (size_t)src * p.D + c) : f2(0.f);
-    Chan ch;
-    ch.load(p.A_log, p.a_bias, p.b_bias, c);
+    const float4 S = src >= 0 ? *reinterpret_cast<const float4 *>(p.S + (size_t)src * p.D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float2 h[2] = {make_float2(S.x, S.y), make_float2(S.z, S.w)};
+    Chan ch[2];
+    ch[0].load(p.A_log, p.a_bias, p.b_bias, c);
+    ch[1].load(p.A_log, p.a_bias, p.b_bias, c + 2);
 #pragma unroll
     for (int i = 0; i < N; ++i)
         if (i < p.n) {
-            float2 e, u;
-            gates(ch, Pair<T>::get(x[i]), Pair<T>::get(a[i]), Pair<T>::get(b[i]), e, u);
-            h = step(h, e, u);
-            st_pair(op + i * p.rows.out_stride, G ? f2_mul(h, silu2(Pair<T>::get(g[i]))) : h);
+            float2 o[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float2 e, u;
+                gates(ch[j], Q::get(x[i], j), Q::get(a[i], j), Q::get(b[i], j), e, u);
+                h[j] = step(h[j], e, u);
+                o[j] = G ? f2_mul(h[j], silu2(Q::get(g[i], j))) : h[j];
+            }
+            *reinterpret_cast<typename Q::Raw *>(op + i * p.rows.out_stride) = Q::put(o[0], o[1]);
         }
-    *reinterpret_cast<float2 *>(p.S + (size_t)dst * p.D + c) = h;
+    *reinterpret_cast<float4 *>(p.S + (size_t)dst * p.D + c) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
 }
 
 template <typename T, bool G>
@@ -201,8 +209,8 @@ kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *par
     glr::Args p = glr::make_args(cfg, params, S, max_slots, src_slots, dst_slots, B, rows, err);
     p.n = n;
     p.total_T = (int64_t)B * n;
-    if ((int64_t)B * (cfg->dim / 2) > INT_MAX - 128) return glr::fail(KDA_ERR_INVALID, "B * dim is too large");
-    const int64_t blocks = ((int64_t)B * (cfg->dim / 2) + 127) / 128;
+    if ((int64_t)B * (cfg->dim / 4) > INT_MAX - 128) return glr::fail(KDA_ERR_INVALID, "B * dim is too large");
+    const int64_t blocks = ((int64_t)B * (cfg->dim / 4) + 127) / 128;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = cfg->io_dtype == KDA_F32;
     if (rows->g) {

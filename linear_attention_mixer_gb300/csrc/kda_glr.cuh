@@ -111,6 +111,23 @@ template <typename T> __device__ __forceinline__ void st_pair(T *p, float2 f)
     *reinterpret_cast<typename Pair<T>::Raw *>(p) = Pair<T>::put(f);
 }
 
+// four channels of a row
+template <typename T> struct Quad;
+template <> struct Quad<__nv_bfloat16> {
+    typedef uint2 Raw;
+    static __device__ __forceinline__ float2 get(const Raw &r, int i) { return Pair<__nv_bfloat16>::get(i ? r.y : r.x); }
+    static __device__ __forceinline__ Raw put(float2 a, float2 b) { return make_uint2(Pair<__nv_bfloat16>::put(a), Pair<__nv_bfloat16>::put(b)); }
+};
+template <> struct Quad<float> {
+    typedef float4 Raw;
+    static __device__ __forceinline__ float2 get(const Raw &r, int i) { return i ? make_float2(r.z, r.w) : make_float2(r.x, r.y); }
+    static __device__ __forceinline__ Raw put(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
+};
+template <typename T> __device__ __forceinline__ typename Quad<T>::Raw ld_quad(const T *p)
+{
+    return __ldg(reinterpret_cast<const typename Quad<T>::Raw *>(p));
+}
+
 __device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float ex2_ftz(float x)
 {
