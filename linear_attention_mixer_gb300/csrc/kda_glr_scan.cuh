@@ -16,7 +16,7 @@ template <typename T> constexpr int scan_warps() { return sizeof(T) == 4 ? 8 : 4
 // Blocks of a cluster at most. FP32 rows leave no room in shared memory for the pairs of more than 8.
 template <typename T> constexpr int max_cluster() { return sizeof(T) == 4 ? 8 : 16; }
 // Blocks that work on clusters of more than one, over all channels and sequences, at most: what bounds the workspace.
-constexpr int kMaxShared = 2432;
+constexpr int kMaxShared = 16384;
 
 inline cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *at, unsigned grid, int nc, int threads, size_t smem, cudaStream_t stream)
 {
@@ -74,8 +74,8 @@ struct ClusterRoom {
 
 // Blocks that share a sequence's 64 channels, of `groups` sequences at once: as many as make the call shortest. A window
 // takes a while however few blocks an SM has (about as long as 192 tokens of one block's work, less without a cluster)
-// and the work of all of the SM's blocks; where all clusters run at once the longest sequence's windows count,
-// else the work of all. Any number, or, to look at many sequences quickly, powers of two.
+// and the work of all of the SM's blocks; where all clusters of long sequences run at once the longest one's windows
+// count, else the work of all. Any number, or, to look at many sequences quickly, powers of two.
 template <typename Room>
 inline int choose_cluster(const int32_t *cu, int32_t N, int32_t groups, int64_t slabs, int tile, int most, int sms, Room room, double &least)
 {
@@ -93,10 +93,15 @@ inline int choose_cluster(const int32_t *cu, int32_t N, int32_t groups, int64_t 
             all += w;
             if (w > path) path = w;
         }
+        int64_t heavy = 0;  // sequences that take long
+        for (int32_t i = 0; i < N; ++i) {
+            const uint32_t n = (uint32_t)(cu[i + 1] - cu[i]);
+            heavy += 8 * (uint64_t)n >= (uint64_t)(path - 1) * span && n > 0;
+        }
         const double still = nc == 1 ? 128.0 : 192.0;  // in tokens
-        double cost = path * (still + tile * (double)(groups * slabs * nc) / sms);
+        double cost = path * (still + tile * (double)(heavy * slabs * nc) / sms);
         // not all at once: the SMs are full, with `at_once` clusters on them, until the work is done
-        if (groups < N || groups * slabs > at_once)
+        if (groups < N || heavy * slabs > at_once)
             cost = (double)all * slabs / at_once * (still + tile * (double)at_once * nc / sms) + 0.25 * path * (still + tile);
         if (nc == 1 || cost < 0.97 * least) least = cost, best = nc;
         if (path <= 1) break;  // more blocks would stand idle
@@ -140,12 +145,13 @@ inline int choose_parts(const int32_t *cu, int32_t N, int32_t groups, int64_t sl
     for (int parts = 2; parts <= 32; parts *= 2) {
         const int plen = (longest / parts + sub - 1) / sub * sub, subs = (parts - 1 + back) * (plen / sub);
         if ((int64_t)plen * (parts - 1) >= longest || N * subs * slabs > kSplitPairs) break;
-        const double pairs = 500 + sub / 128 * (110.0 + 64.0 * N * subs * slabs / sms) + 3.0 * subs;
-        int64_t clusters = 0;  // that have tokens
+        int64_t clusters = 0, blocks = 0;  // that have tokens
         for (int32_t i = 0; i < N; ++i) {
-            const int n = (cu[i + 1] - cu[i] + plen - 1) / plen;
-            clusters += (n < 1 ? 1 : n < parts ? n : parts) * slabs;
+            const int n = cu[i + 1] - cu[i], in = (n + plen - 1) / plen, of = (n + sub - 1) / sub;
+            clusters += (8 * (int64_t)n < longest / parts ? 0 : in < parts ? in : parts) * slabs;
+            blocks += (of < subs ? of : subs) * slabs;
         }
+        const double pairs = 500 + sub / 128 * (110.0 + 64.0 * blocks / sms) + 3.0 * subs;
         for (int nc = 1; nc <= most; nc *= 2) {
             if (N * parts * slabs * nc > kMaxShared || clusters > room(nc)) continue;
             const int path = ((plen > longest - (parts - 1) * plen ? plen : longest - (parts - 1) * plen) + tile * nc - 1) / (tile * nc);
