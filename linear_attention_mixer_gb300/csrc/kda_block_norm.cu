@@ -615,7 +615,10 @@ template <typename T, bool F8>
 cudaError_t launch(const Args &p, int dev, int sms, cudaStream_t s)
 {
     const unsigned M = (unsigned)p.M, M4 = (unsigned)((p.M + 3) / 4);
-    if (p.M >= 8 * sms && p.D > 512 && p.D <= 8192 && p.r.y && p.r.h) {
+    // Blocks that stay from about 2.4 million channels of rows on (BF16 without a gate, M = 600, 1200, 2400, 9600): D = 600 3.1, 3.7, 4.6,
+    // 10.7 us for 3.1, 3.5, 5.4, 13.4 with a block each; 4096 6.2, 7.8, 11.7, 50.9 for 5.4, 9.7, 17.6, 64.7; 7168 7.6, 10.9, 23.8, 92.8
+    // for 8.9, 16.8, 35.3, 129.8. FP32 turns at the same M.
+    if (p.M >= 4 * sms && p.M * p.D >= 2400000 && p.D > 512 && p.D <= 8192 && p.r.y && p.r.h) {
         if (p.D <= 1024) return launch_rows<T, 64, 2, F8>(p, dev, sms, s);
         if (p.D <= 2048) return launch_rows<T, 128, 2, F8>(p, dev, sms, s);
         if (p.D <= 4096) return launch_rows<T, 128, 4, F8>(p, dev, sms, s);
@@ -651,7 +654,9 @@ template <typename T>
 cudaError_t launch_back(const BackArgs &p, int *parts, int dev, int sms, cudaStream_t s)
 {
     const unsigned n = (unsigned)*parts, n4 = (unsigned)((*parts + 3) / 4);
-    if (p.M >= 8 * sms && p.D > 512 && p.D <= 8192 && p.r.y && p.r.dh && p.r.dx1) {
+    // Staged rows wherever a block has more than one (BF16, M = 150, 300, 1200, 9600): D = 600 5.6, 6.6, 9.1, 32 us for 5.6, 7.0, 10.7, 58
+    // straight from global memory; 7168 14.3, 15.6, 29.6, 138 for 14.2, 23.7, 47.6, 267; FP32 19.3, 21.2, 49.9, 287 for 19.4, 35.6, 95.7, 641.
+    if (p.M > sms && p.D > 512 && p.D <= 8192 && p.r.y && p.r.dh && p.r.dx1) {
         if (p.D <= 1024) return launch_back_rows<T, 128, 1>(p, parts, dev, sms, s);
         if (p.D <= 2048) return launch_back_rows<T, 128, 2>(p, parts, dev, sms, s);
         if (p.D <= 4096) return launch_back_rows<T, 256, 2>(p, parts, dev, sms, s);

@@ -7,6 +7,11 @@
 // shared memory, the blocks' through distributed shared memory, in the tokens' order (so results do not depend on timing);
 // then each warp walks its tokens from the state that it now knows, with e and u still in registers. The rows are read
 // once. No block waits for one of another cluster.
+//
+// 65536 tokens of 4096 channels in BF16: 503 us, 4.3 TB/s. Instructions (55% issued on the average), special functions
+// and the FP32 pipe (35 to 41%) and the latency of a window's exchange share it, on 3.4 of the 4 blocks that an SM has room
+// for. Eight sequences of 0 to 2048 tokens, 7168 channels in FP32: 95 us, 5.7 TB/s. With 8 tokens a warp (and 24 warps an SM)
+// the first took 670 us where this took 566.
 #include "kda_glr_scan.cuh"
 
 namespace kda {
@@ -190,25 +195,25 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-// Copies of R rows of 64 channels, asked for by 16-byte units; what lies past the sequence or past the row's end is 0.
-template <typename T, int R>
+// Copies of 16 rows of 64 channels, asked for by 16-byte units; what lies past the sequence or past the row's end is 0.
+template <typename T>
 struct Tile {
     static constexpr int kUnits = kSlab * (int)sizeof(T) / 16;  // of a row
     static constexpr int kRowsAt = 32 / kUnits;                 // rows that a warp asks for at once
-    static constexpr int kBytes = R * kSlab * (int)sizeof(T);
+    static constexpr int kBytes = kChunk * kSlab * (int)sizeof(T);
 
     // row0: the first row's place in the slab, of nv rows that exist
     static __device__ __forceinline__ void fetch(unsigned char *to, const T *row0, int64_t stride, int nv, bool col_ok)
     {
         const int lane = threadIdx.x & 31, r0 = lane / kUnits;
         const T *at = row0 + r0 * stride + (16 / (int)sizeof(T)) * (lane % kUnits);
-        if (nv >= R && col_ok) {  // all of this lane's rows
+        if (nv >= kChunk && col_ok) {  // all of this lane's rows
 #pragma unroll
-            for (int i = 0; i < R / kRowsAt; ++i, advance(at, kRowsAt * stride)) cp_async16(to + (size_t)(lane + 32 * i) * 16, at);
+            for (int i = 0; i < kChunk / kRowsAt; ++i, advance(at, kRowsAt * stride)) cp_async16(to + (size_t)(lane + 32 * i) * 16, at);
             return;
         }
 #pragma unroll
-        for (int i = 0; i < R / kRowsAt; ++i, advance(at, kRowsAt * stride)) {
+        for (int i = 0; i < kChunk / kRowsAt; ++i, advance(at, kRowsAt * stride)) {
             const bool ok = col_ok && r0 + i * kRowsAt < nv;
             kda::cp_async16(to + (size_t)(lane + 32 * i) * 16, ok ? at : row0, ok ? 16 : 0);
         }
@@ -220,14 +225,14 @@ struct Tile {
 };
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// e and u of a warp's R tokens. (A reciprocal each for the two sigmoids: one for their product costs five multiplications
+// e and u of a warp's 16 tokens. (A reciprocal each for the two sigmoids: one for their product costs five multiplications
 // and a test of its range, which is more than the special function unit's time for another; 574 us for 535.)
-template <typename T, int R>
+template <typename T>
 __device__ __forceinline__ void all_gates(const Chan &ch, const unsigned char *x, const unsigned char *a, const unsigned char *b,
-                                          float2 (&e)[R], float2 (&u)[R])
+                                          float2 (&e)[kChunk], float2 (&u)[kChunk])
 {
 #pragma unroll
-    for (int t = 0; t < R; ++t) gates(ch, Tile<T, R>::get(x, t), Tile<T, R>::get(a, t), Tile<T, R>::get(b, t), e[t], u[t]);
+    for (int t = 0; t < kChunk; ++t) gates(ch, Tile<T>::get(x, t), Tile<T>::get(a, t), Tile<T>::get(b, t), e[t], u[t]);
     __syncwarp();
 }
 
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(32 * kPairWarps) glr_pairs_kernel(const __grid
 {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float4 sh[kPairWarps][32];
-    using Tl = Tile<T, kChunk>;
+    using Tl = Tile<T>;
     constexpr int kTiles = BACK ? (G ? 3 : 2) : 3;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.D + kSlab - 1) / kSlab, q = blockIdx.x % p.split.subs, u = blockIdx.x / p.split.subs;
@@ -318,7 +323,7 @@ template <typename T, bool BACK, bool G>
 cudaError_t launch_pairs(const Args &p, const void *dout, int64_t dout_stride, int dev, cudaStream_t s)
 {
     static std::atomic<uint64_t> raised;
-    const int smem = kPairWarps * 2 * (BACK ? (G ? 3 : 2) : 3) * Tile<T, kChunk>::kBytes;
+    const int smem = kPairWarps * 2 * (BACK ? (G ? 3 : 2) : 3) * Tile<T>::kBytes;
     const cudaError_t e = raise_smem_on(raised, dev, glr_pairs_kernel<T, BACK, G>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;
@@ -327,13 +332,13 @@ cudaError_t launch_pairs(const Args &p, const void *dout, int64_t dout_stride, i
 }
 
 // ---------------------------------------------------------------- prefill
-template <typename T, bool G, int W, int R>
-__global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
+template <typename T, bool G, int W>
+__global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const __grid_constant__ Args p, int nc)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ Exchange<W, max_cluster<T>()> ex;
     constexpr int kTiles = G ? 4 : 3;
-    using Tl = Tile<T, R>;
+    using Tl = Tile<T>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.D + kSlab - 1) / kSlab, cid = blockIdx.x / nc, rank = nc > 1 ? (int)cluster_rank() : 0;
     const int unit = cid / slabs, c0 = (cid - unit * slabs) * kSlab, c = c0 + 2 * lane;
@@ -367,8 +372,8 @@ __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(
         if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
         unsigned char *tx = smem + (size_t)warp * kTiles * Tl::kBytes, *ta = tx + Tl::kBytes, *tb = ta + Tl::kBytes, *tg = tb + Tl::kBytes;
         const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tl::kUnits) < p.D;
-        const int window = R * W * nc;
-        int t = R * (rank * W + warp);  // this warp's first token of the window
+        const int window = kChunk * W * nc;
+        int t = kChunk * (rank * W + warp);  // this warp's first token of the window
         const T *xp = static_cast<const T *>(p.rows.x) + (int64_t)s0 * p.rows.x_stride + c0, *ap = static_cast<const T *>(p.rows.a) + (int64_t)s0 * p.rows.a_stride + c0;
         const T *bp = static_cast<const T *>(p.rows.b) + (int64_t)s0 * p.rows.b_stride + c0, *gp = G ? static_cast<const T *>(p.rows.g) + (int64_t)s0 * p.rows.g_stride + c0 : nullptr;
         T *op = static_cast<T *>(p.rows.out) + (int64_t)s0 * p.rows.out_stride + c;
@@ -391,20 +396,20 @@ __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(
         const int windows = (len + window - 1) / window;
 #pragma unroll 1
         for (int k = 0; k < windows; ++k, t += window) {
-            const int nv = min(R, len - t);  // <= 0 behind the sequence's end
-            float2 e[R], u[R];
+            const int nv = min(kChunk, len - t);  // <= 0 behind the sequence's end
+            float2 e[kChunk], u[kChunk];
             cp_async_wait_all();
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
-                all_gates<T, R>(ch, tx, ta, tb, e, u);
-                if (nv < R)
+                all_gates<T>(ch, tx, ta, tb, e, u);
+                if (nv < kChunk)
 #pragma unroll
-                    for (int i = 0; i < R; ++i)
+                    for (int i = 0; i < kChunk; ++i)
                         if (i >= nv) e[i] = u[i] = f2(0.f);
                 fetch(t + window);
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
+                for (int i = 0; i < kChunk; ++i) {
                     own.H = step(own.H, e[i], u[i]);
                     own.A = f2_fma(own.A, e[i], own.A);
                 }
@@ -414,17 +419,17 @@ __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(
             float2 h = meet<false>(ex, pre, all, carry, k, nc, rank, good);
             if (nv > 0) {
                 if (live) {
-                    if (st && (R == kChunk || t % kChunk == 0)) *reinterpret_cast<float2 *>(st + (size_t)(t / kChunk) * p.D) = h;
+                    if (st) *reinterpret_cast<float2 *>(st + (size_t)(t / kChunk) * p.D) = h;
                     T *o = op + t * p.rows.out_stride;
-                    if (nv == R) {
+                    if (nv == kChunk) {
 #pragma unroll
-                        for (int i = 0; i < R; ++i, advance(o, p.rows.out_stride)) {
+                        for (int i = 0; i < kChunk; ++i, advance(o, p.rows.out_stride)) {
                             h = step(h, e[i], u[i]);
                             st_pair(o, G ? f2_mul(h, silu2(Tl::get(tg, i))) : h);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < R; ++i, advance(o, p.rows.out_stride)) {
+                        for (int i = 0; i < kChunk; ++i, advance(o, p.rows.out_stride)) {
                             h = step(h, e[i], u[i]);
                             if (i < nv) st_pair(o, G ? f2_mul(h, silu2(Tl::get(tg, i))) : h);
                         }
@@ -443,28 +448,29 @@ __global__ void __launch_bounds__(32 * W, scan_per_sm<R>() / W) glr_scan_kernel(
 template <typename T, bool G>
 cudaError_t launch_scan_t(const Args &p, const int32_t *cu, int dev, int sms, cudaStream_t s)
 {
-    constexpr int W = scan_warps<T>(), R = scan_rows<T>();
+    constexpr int W = scan_warps<T>();
     static std::atomic<uint64_t> raised;
     static ClusterRoom room;
-    const int smem = W * (G ? 4 : 3) * Tile<T, R>::kBytes;
-    const cudaError_t e = raise_smem_on(raised, dev, glr_scan_kernel<T, G, W, R>, smem);
+    const int smem = W * (G ? 4 : 3) * Tile<T>::kBytes;
+    const cudaError_t e = raise_smem_on(raised, dev, glr_scan_kernel<T, G, W>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;
     Args q = p;
-    const int nc = choose_parts(cu, p.N, p.N, slabs, R * W, max_cluster<T>(), sms, false, q.split,
-                                [&](int n) { return room.of(glr_scan_kernel<T, G, W, R>, n, 32 * W, smem, dev); });
+    const int nc = choose_parts(cu, p.N, p.N, slabs, kChunk * W, max_cluster<T>(), sms, false, q.split,
+                                [&](int n) { return room.of(glr_scan_kernel<T, G, W>, n, 32 * W, smem, dev); });
     if (q.split.parts > 1) {
         const cudaError_t first = launch_pairs<T, false, false>(q, nullptr, 0, dev, s);
         if (first != cudaSuccess) return first;
     }
-    return launch_cluster(glr_scan_kernel<T, G, W, R>, (unsigned)(p.N * q.split.parts * slabs * nc), nc, 32 * W, smem, s, q, nc);
+    return launch_cluster(glr_scan_kernel<T, G, W>, (unsigned)(p.N * q.split.parts * slabs * nc), nc, 32 * W, smem, s, q, nc);
 }
 
 // ---------------------------------------------------------------- backward
 // The same from the last window to the first, with c the gradient of the state behind a token: c -> alpha (dh + c) is linear
 // too. What a token's gradients need beside it is the state before it, which a warp walks again from the one that the
 // forward kept for its 16 tokens. A cluster has the sequences (or their parts) group, group + groups, .. and adds up its tokens' shares of
-// the parameters' gradients in registers: one row of partial sums a block.
+// the parameters' gradients in registers: one row of partial sums a block. 8192 tokens of 4096 channels in BF16 with an output gate:
+// 190 us (569 MB, 3.0 TB/s), by latency and instructions (half of them issued) of 12 warps an SM.
 template <typename T, bool G, int W>
 __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
 {
@@ -477,9 +483,9 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
     const bool live = c < p.D;
     Chan ch = {f2(0.f), f2(0.f), f2(0.f)};
     if (live) ch.load(p.A_log, p.a_bias, p.b_bias, c);
-    unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T, kChunk>::kBytes, *ta = tx + Tile<T, kChunk>::kBytes, *tb = ta + Tile<T, kChunk>::kBytes;
-    unsigned char *td = tb + Tile<T, kChunk>::kBytes, *tg = td + Tile<T, kChunk>::kBytes;
-    const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T, kChunk>::kUnits) < p.D;
+    unsigned char *tx = smem + (size_t)warp * kTiles * Tile<T>::kBytes, *ta = tx + Tile<T>::kBytes, *tb = ta + Tile<T>::kBytes;
+    unsigned char *td = tb + Tile<T>::kBytes, *tg = td + Tile<T>::kBytes;
+    const bool col_ok = c0 + (16 / (int)sizeof(T)) * (lane % Tile<T>::kUnits) < p.D;
     const int window = kChunk * W * nc, own_t = kChunk * (rank * W + warp);
     float2 sA = f2(0.f), sa = sA, sb = sA;
     int turn = 0;
@@ -514,11 +520,11 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
             const int nv = len - at;
             const int64_t r = (int64_t)s0 + at;
             if (nv > 0) {
-                Tile<T, kChunk>::fetch(tx, static_cast<const T *>(p.rows.x) + r * p.rows.x_stride + c0, p.rows.x_stride, nv, col_ok);
-                Tile<T, kChunk>::fetch(ta, static_cast<const T *>(p.rows.a) + r * p.rows.a_stride + c0, p.rows.a_stride, nv, col_ok);
-                Tile<T, kChunk>::fetch(tb, static_cast<const T *>(p.rows.b) + r * p.rows.b_stride + c0, p.rows.b_stride, nv, col_ok);
-                Tile<T, kChunk>::fetch(td, static_cast<const T *>(p.rows.dout) + r * p.rows.dout_stride + c0, p.rows.dout_stride, nv, col_ok);
-                if (G) Tile<T, kChunk>::fetch(tg, static_cast<const T *>(p.rows.g) + r * p.rows.g_stride + c0, p.rows.g_stride, nv, col_ok);
+                Tile<T>::fetch(tx, static_cast<const T *>(p.rows.x) + r * p.rows.x_stride + c0, p.rows.x_stride, nv, col_ok);
+                Tile<T>::fetch(ta, static_cast<const T *>(p.rows.a) + r * p.rows.a_stride + c0, p.rows.a_stride, nv, col_ok);
+                Tile<T>::fetch(tb, static_cast<const T *>(p.rows.b) + r * p.rows.b_stride + c0, p.rows.b_stride, nv, col_ok);
+                Tile<T>::fetch(td, static_cast<const T *>(p.rows.dout) + r * p.rows.dout_stride + c0, p.rows.dout_stride, nv, col_ok);
+                if (G) Tile<T>::fetch(tg, static_cast<const T *>(p.rows.g) + r * p.rows.g_stride + c0, p.rows.g_stride, nv, col_ok);
             }
             commit();
         };
@@ -533,15 +539,15 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
-                all_gates<T, kChunk>(ch, tx, ta, tb, e, u);
+                all_gates<T>(ch, tx, ta, tb, e, u);
                 if (nv < kChunk)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i)
                         if (i >= nv) e[i] = u[i] = f2(0.f);
 #pragma unroll
                 for (int i = kChunk - 1; i >= 0; --i) {  // the rows of dout past the end are 0
-                    float2 dh = Tile<T, kChunk>::get(td, i);
-                    if (G) dh = f2_mul(dh, silu2(Tile<T, kChunk>::get(tg, i)));
+                    float2 dh = Tile<T>::get(td, i);
+                    if (G) dh = f2_mul(dh, silu2(Tile<T>::get(tg, i)));
                     own.H = f2_add(own.H, dh);
                     own.H = f2_fma(e[i], own.H, own.H);
                     own.A = f2_fma(own.A, e[i], own.A);
@@ -566,12 +572,12 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
 #pragma unroll
                 for (int i = kChunk - 1; i >= 0; --i) {
                     if (i < nv) {
-                        const float2 x = Tile<T, kChunk>::get(tx, i);
-                        float2 dh = Tile<T, kChunk>::get(td, i);
+                        const float2 x = Tile<T>::get(tx, i);
+                        float2 dh = Tile<T>::get(td, i);
                         Back bk;
-                        bk.gates(ch, e[i], Tile<T, kChunk>::get(ta, i), Tile<T, kChunk>::get(tb, i));
+                        bk.gates(ch, e[i], Tile<T>::get(ta, i), Tile<T>::get(tb, i));
                         if (G) {
-                            const float2 g = Tile<T, kChunk>::get(tg, i);
+                            const float2 g = Tile<T>::get(tg, i);
                             float2 s, ns;
                             both_sigmoids(neg_exp(g, f2(0.f)), s, ns);
                             if (live) st_pair(dgp, f2_mul(f2_mul(dh, h), f2_mul(s, f2_fma(g, ns, f2(1.f)))));
@@ -626,7 +632,7 @@ cudaError_t launch_back_t(const BackArgs &p, const int32_t *cu, int *parts, int 
 {
     static std::atomic<uint64_t> raised;
     static ClusterRoom room;
-    const int smem = W * (G ? 5 : 4) * Tile<T, kChunk>::kBytes;
+    const int smem = W * (G ? 5 : 4) * Tile<T>::kBytes;
     const cudaError_t e = raise_smem_on(raised, dev, glr_back_kernel<T, G, W>, smem);
     if (e != cudaSuccess) return e;
     const int64_t slabs = (p.D + kSlab - 1) / kSlab;

@@ -9,9 +9,9 @@ namespace kda {
 namespace glr {
 
 constexpr int kBackWarps = 4;                        // warps of a block: 64 tokens
-constexpr int kBackPerSm = 12;                       // warps that an SM's registers hold, 168 a thread
-template <int R> constexpr int scan_per_sm() { return R == 16 ? 16 : 24; }
-template <typename T> constexpr int scan_rows() { return 16; }
+constexpr int kScanPerSm = 16, kBackPerSm = 12;      // warps that an SM's registers hold (128 and 168 a thread)
+// Warps of a prefill's block. FP32 rows fill shared memory with two blocks of eight; BF16 rows are faster in four of four
+// (65536 tokens of 4096 channels 569 us where two of eight took 597).
 template <typename T> constexpr int scan_warps() { return sizeof(T) == 4 ? 8 : 4; }
 // Blocks of a cluster at most. FP32 rows leave no room in shared memory for the pairs of more than 8.
 template <typename T> constexpr int max_cluster() { return sizeof(T) == 4 ? 8 : 16; }
