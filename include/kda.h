@@ -493,7 +493,7 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
  *   h = alpha h + sqrt(1 - alpha^2) beta x,  out = h, or with an output gate h silu(g)
  * a = -inf keeps the state as it is (alpha = 1), b = -inf lets nothing in; exp(A_log) must be finite in FP32, and a sigmoid
  * below 2^-126 counts as 0. What is not finite in a row reaches no earlier token, no other channel and no other sequence
- * (a state that has become infinite is NaN from the next token on).
+ * (a state that has become infinite stays infinite or becomes NaN).
  *
  * States are caller-owned, device FP32 [max_slots][dim], 16-byte aligned, read and written by slots as the gated delta
  * rule's are (src_slots, dst_slots, err with KDA_ERR_TIMEOUT too; KDA_ERR_DEVICE also where a sequence's bounds in cu_seqlens do not rise within
@@ -567,7 +567,7 @@ kda_status kda_glr_prefill(const kda_glr_config_t *cfg, const kda_glr_params *pa
  *   rows.dout  the gradient of out          dS_last   device FP32 [N][dim], that of the final states, or NULL: zeros
  *   rows.dx, .da, .db, .dg  io_dtype        dS_first  device FP32 [N][dim], that of the states at the start, or NULL
  *   dA_log, da_bias, db_bias  device FP32 [dim], sums over all tokens, each or NULL; overwritten (zeros for N == 0)
- * dS_last, dS_first and the three sums 16-byte aligned. Sums are FP32, and results do not depend on timing. A sequence
+ * dS_last, dS_first and the three sums 16-byte aligned; nothing that is written overlaps what is read. Sums are FP32, and results do not depend on timing. A sequence
  * whose bounds are wrong is left alone, as in the prefill, and adds nothing to the sums. Errors: KDA_ERR_INVALID,
  * KDA_ERR_CUDA.
  */

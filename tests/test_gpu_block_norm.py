@@ -242,3 +242,34 @@ def test_no_rows():
     p.forward()
     g = p.backward()
     assert all(bool((g[n] == 0).all()) for n in ("dpost_w", "dscale", "dpre_w"))
+
+
+def test_refusals_of_the_binding():
+    p = Problem(20, 64, True, True, seed=9)
+    d = p.dev
+
+    def forward(**e):
+        v = dict(x=d["x"], y=d["y"], g=d["g"], x_out=p.new(), h=p.new(), hs=None, prm=p.params) | e
+        K.kda_block_norm(p.cfg, v["prm"], v["x"], y=v["y"], g=v["g"], x_out=v["x_out"], h=v["h"], hs=v["hs"])
+
+    hs = torch.zeros(20, 1, device="cuda")
+    q = torch.zeros(20, 64, device="cuda", dtype=torch.float8_e4m3fn)
+    for e in ({"x": d["x"].float()}, {"y": d["y"][:3]}, {"g": d["g"].cpu()}, {"x_out": None}, {"h": q}, {"hs": hs}, {"h": q, "hs": hs[:, 0]}, {"h": q, "hs": hs.half()},
+              {"h": None, "hs": hs}, {"y": None}, {"y": None, "g": None, "x_out": None, "h": None}, {"x": d["x"].t()},
+              {"prm": K.kda_block_norm_params_from(*(torch.zeros(72, device="cuda") for _ in range(3)))},
+              {"prm": K.kda_block_norm_params(p.params.post_w, p.params.scale, p.params.pre_w)}):
+        with pytest.raises((TypeError, ValueError, K.KdaError)):
+            forward(**e)
+    forward(h=q, hs=hs)
+    work = torch.empty(K.kda_block_norm_workspace_bytes(p.cfg, 20), dtype=torch.uint8, device="cuda")
+
+    def backward(**e):
+        v = dict(x_out=d["x"], dh=d["dh"], dx1=d["dx1"], dx=p.new(), work=work, y=d["y"], g=d["g"], dy=p.new(), dg=p.new(), dscale=None) | e
+        K.kda_block_norm_backward(p.cfg, p.params, v["x_out"], v["dh"], v["dx1"], v["dx"], v["work"], y=v["y"], g=v["g"], dy=v["dy"], dg=v["dg"], dscale=v["dscale"])
+
+    for e in ({"x_out": None}, {"dh": d["dh"][:2]}, {"dx1": d["dx1"].float()}, {"work": work[:100]}, {"dy": None}, {"dg": None}, {"g": None}, {"y": None},
+              {"dscale": torch.zeros(63, device="cuda")}):
+        with pytest.raises((TypeError, ValueError, K.KdaError)):
+            backward(**e)
+    backward()
+    torch.cuda.synchronize()

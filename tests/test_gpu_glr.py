@@ -383,3 +383,82 @@ def test_no_sequences():
                        dA_log=sums[0], da_bias=sums[1], db_bias=sums[2])
     torch.cuda.synchronize()
     assert bool((S == 1).all()) and all(bool((s == 0).all()) for s in sums)
+
+
+def test_refusals_of_the_binding():
+    p = Problem([20, 5], 64, True, True, seed=18)
+    x, a, b, g = p.rows()
+    out = p.out[:p.T]
+
+    def prefill(S=p.S, src=p.src, dst=p.dst, cu=p.cu_dev, cuh=p.cu, x=x, a=a, b=b, g=g, out=out, ws=p.work, starts=p.starts, prm=p.params, err=p.err):
+        K.kda_glr_prefill(p.cfg, prm, S, src, dst, cu, cuh, x, a, b, g, out, ws, starts=starts, err=err)
+
+    def backward(**e):
+        v = p.make_grads() | {"starts": p.starts, "dS_last": p.dev["dS"], "dout": p.dev["dout"], "x": x} | e
+        K.kda_glr_backward(p.cfg, p.params, p.cu_dev, p.cu, v["starts"], v["x"], a, b, g, v["dout"], v["dx"][:p.T], v["da"][:p.T], v["db"][:p.T], v["dg"][:p.T],
+                           p.work, dS_last=v["dS_last"], dA_log=v["dA_log"])
+
+    other = K.kda_glr_params_from(*(torch.zeros(72, device="cuda") for _ in range(3)))
+    by_hand = K.kda_glr_params(p.params.A_log, p.params.a_bias, p.params.b_bias)
+    for e in ({"x": x.float()}, {"x": x[:-1]}, {"a": a.t()}, {"b": b.cpu()}, {"g": g[:, :32]}, {"out": torch.zeros(p.T, 128, dtype=p.dt, device="cuda")[:, ::2]},
+              {"S": p.S[:, :32]}, {"S": p.S.double()}, {"src": p.src.long()}, {"dst": p.dst[:1]}, {"cu": p.cu_dev[:-1]}, {"cuh": [0, 20]}, {"cuh": [0, 20, 26]},
+              {"starts": p.starts[:1]}, {"starts": p.starts.half()}, {"ws": p.work[:100]}, {"ws": p.work.cpu()}, {"prm": other}, {"prm": by_hand}, {"err": p.src.cpu()},
+              {"x": None}, {"x": 3}, {"cuh": [0, 30, 25]}):
+        with pytest.raises((TypeError, ValueError, AttributeError, K.KdaError)):
+            prefill(**e)
+    for e in ({"x": x.float()}, {"dout": p.dev["dout"][:3]}, {"starts": p.starts[:1]}, {"dS_last": p.dev["dS"][:1]}, {"dA_log": torch.zeros(63, device="cuda")}):
+        with pytest.raises((TypeError, ValueError, K.KdaError)):
+            backward(**e)
+    with pytest.raises(ValueError):
+        K.kda_glr_params_from(*(torch.zeros(n, device="cuda") for n in (64, 64, 72)))
+    with pytest.raises(TypeError):
+        K.kda_glr_params_from(*(torch.zeros(64, device="cuda", dtype=torch.float64) for _ in range(3)))
+    for n in (0, 9):
+        with pytest.raises((K.KdaError, ValueError)):
+            K.kda_glr_decode(p.cfg, p.params, p.S, p.src, p.dst, n, *p.rows(), out)
+    p.prefill()  # nothing was touched
+    p.check()
+
+
+FIRST = """
+import torch
+import linear_attention_mixer_gb300 as K
+f32 = dict(device="cuda")
+cfg, T, D, cu_h = K.kda_glr_config(72), 700, 72, [0, 700]
+v = [torch.randn(D, **f32) for _ in range(3)]
+prm = K.kda_glr_params_from(*v)
+rows = [torch.randn(T, D, **f32).bfloat16() for _ in range(5)]
+out, dx, da, db, dg = (torch.empty_like(rows[0]) for _ in range(5))
+S, slot, cu = torch.zeros(1, D, **f32), torch.zeros(1, dtype=torch.int32, **f32), torch.tensor(cu_h, dtype=torch.int32, **f32)
+ws = torch.empty(K.kda_glr_workspace_bytes(cfg, cu_h), dtype=torch.uint8, **f32)
+starts, dA = torch.empty(K.kda_glr_chunks(cu_h), D, **f32), torch.empty(D, **f32)
+nc, np_ = K.kda_block_norm_config(D), K.kda_block_norm_params_from(*v)
+h, x1 = torch.empty_like(out), torch.empty_like(out)
+
+def step():
+    K.kda_glr_prefill(cfg, prm, S, slot, slot, cu, cu_h, *rows[:4], out, ws, starts=starts)
+    K.kda_glr_backward(cfg, prm, cu, cu_h, starts, *rows, dx, da, db, dg, ws, dA_log=dA)
+    K.kda_block_norm(nc, np_, rows[0], y=out, x_out=x1, h=h)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (out, dx, da, db, dg, dA, h, x1)]
+S.zero_()
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (out, dx, da, db, dg, dA, h, x1)))
+print("same")
+"""
+
+
+def test_the_first_call_of_a_process_is_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
