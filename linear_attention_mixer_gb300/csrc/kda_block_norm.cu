@@ -7,6 +7,7 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include "kda_cluster.cuh"
 #include "kda_colsum.cuh"
 #include "kda_internal.cuh"
 #include "kda_launch.cuh"
@@ -112,23 +113,57 @@ __device__ __forceinline__ float2 sigmoid2(float2 g) { return make_float2(sigmoi
 // 1 / sqrt(sum / D + eps), rounded as well as FP32 can: it is one number a row, and every element's
 __device__ __forceinline__ float rstd(float sum, int D, float eps) { return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)D), eps)); }
 
-// Sums over the NT threads that have a row; each thread gets them. A block of more than one warp has one row.
-template <int NT, int K>
+// v to where `mine` (shared memory) is in the other block of a cluster of two
+__device__ __forceinline__ void st_other(const float *mine, float v)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(cluster_rank() ^ 1u));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// A thread's columns, 8 at first + 8 NT i up to end. A backward row of more than 8192 channels has a cluster of
+// two blocks (CL), half the columns each: the parameters' sums of all of them find no room in one SM's registers.
+constexpr int kWide = 8192;
+template <int CL>
+struct Cols {
+    int first, end;
+    __device__ __forceinline__ Cols(int tid, int D) : first(8 * tid), end(D)
+    {
+        if (CL == 1) return;
+        const int half = (D / 2 + 7) & ~7;
+        if (cluster_rank() == 0) end = half;
+        else first += half;
+    }
+};
+
+// Sums over the NT threads (of each block of the cluster) that have a row; each thread gets them. A block of more than one warp
+// has one row. Blocks of a cluster put their sums into both and meet: what follows finds all of them, and neither ends before
+// the other has written.
+template <int NT, int CL, int K>
 __device__ __forceinline__ void row_sum(float (&s)[K], float (*sh)[K])
 {
 #pragma unroll
     for (int k = 0; k < K; ++k) s[k] = warp_sum(s[k]);
     if (NT == 32) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = CL == 1 ? warp : (int)cluster_rank() * (NT / 32) + warp;
     if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) sh[warp][k] = s[k];
-    __syncthreads();
+        for (int k = 0; k < K; ++k) {
+            sh[slot][k] = s[k];
+            if (CL == 2) st_other(&sh[slot][k], s[k]);
+        }
+    if (CL == 1) {
+        __syncthreads();
+    } else {
+        cluster_arrive();
+        cluster_wait();
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        float v = lane < NT / 32 ? sh[lane][k] : 0.f;
+        float v = lane < CL * NT / 32 ? sh[lane][k] : 0.f;
 #pragma unroll
-        for (int o = NT / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        for (int o = CL * NT / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         s[k] = __shfl_sync(0xFFFFFFFFu, v, 0);
     }
 }
@@ -139,7 +174,7 @@ enum { kAny, kNoGate, kAll };
 // What is done to a row once its channels are in registers. W: pairs of the parameters of vector i: post_w times scale, and
 // pre_w. sh: room for two sums a warp.
 template <int HAS, typename T, int NT, int VPT, bool F8, typename PostW, typename PreW>
-__device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, V8<T> (&x)[VPT], const V8<T> (&y)[VPT], const V8<T> (&g)[VPT],
+__device__ __forceinline__ void finish_row(const Args &p, int64_t row, const Cols<1> &cols, V8<T> (&x)[VPT], const V8<T> (&y)[VPT], const V8<T> (&g)[VPT],
                                            float (*sh0)[1], float (*sh1)[1], PostW post_w, PreW pre_w)
 {
     const bool has_y = HAS != kAny || p.r.y, has_g = HAS == kAny ? p.r.g != nullptr : HAS == kAll, has_h = HAS != kAny || p.r.h;
@@ -148,7 +183,7 @@ __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, 
     if (has_y) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (8 * (tid + i * NT) < p.D)
+            if (cols.first + 8 * NT * i < cols.end)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q = f2_fma(y[i].get(j), y[i].get(j), q);
         s[0] = q.x + q.y;
@@ -159,8 +194,8 @@ __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, 
     q = f2(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (c >= p.D) continue;
+        const int c = cols.first + 8 * NT * i;
+        if (c >= cols.end) continue;
         W8 w;
         if (has_y) w = post_w(i, c);
 #pragma unroll
@@ -182,10 +217,10 @@ __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, 
     const float rx = rstd(s[0], p.D, p.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (!F8 && c >= p.D) continue;
+        const int c = cols.first + 8 * NT * i;
+        if (!F8 && c >= cols.end) continue;
         W8 w;
-        if (c < p.D) w = pre_w(i, c);
+        if (c < cols.end) w = pre_w(i, c);
         if (!F8) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[i].set(j, f2_mul(w.get(j), f2_mul(f[i][j], f2(rx))));
@@ -193,7 +228,7 @@ __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, 
         } else {  // 16 lanes have 128 columns; every lane of the warp takes part
             Q8<float> v;
             v.zero();
-            if (c < p.D) {
+            if (c < cols.end) {
                 float2 o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[j] = f2_mul(w.get(j), f2_mul(f[i][j], f2(rx)));
@@ -211,7 +246,7 @@ __device__ __forceinline__ void finish_row(const Args &p, int64_t row, int tid, 
             }
             float sc, inv;
             q8_scale(m, sc, inv);
-            if (c < p.D) {
+            if (c < cols.end) {
                 *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.r.h) + row * p.r.h_stride + c) = q8_codes(v, inv, odd);
                 if ((threadIdx.x & 15) == 0) p.r.hs[row * ((p.D + kQb - 1) / kQb) + c / kQb] = sc;
             }
@@ -228,17 +263,18 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_kernel(const _
     const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int64_t row = (int64_t)blockIdx.x * kRows + (NT == 32 ? threadIdx.x >> 5 : 0);
     if (row >= p.M) return;  // a whole warp
+    const Cols<1> cols(tid, p.D);
     V8<T> x[VPT], y[VPT], g[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (c < p.D) {
+        const int c = cols.first + 8 * NT * i;
+        if (c < cols.end) {
             load8(x[i], p.r.x, row * p.r.x_stride + c, c, p.D);
             if (p.r.y) load8(y[i], p.r.y, row * p.r.y_stride + c, c, p.D);
             if (p.r.g) load8(g[i], p.r.g, row * p.r.g_stride + c, c, p.D);
         }
     }
-    finish_row<kAny, T, NT, VPT, F8>(p, row, tid, x, y, g, sh[0], sh[1],
+    finish_row<kAny, T, NT, VPT, F8>(p, row, cols, x, y, g, sh[0], sh[1],
         [&](int, int c) {
             W8 w, sc;
             w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
@@ -276,11 +312,12 @@ __global__ void __launch_bounds__(NT, 512 / NT) block_norm_rows_kernel(const __g
     Stage<T, NT, VPT> &st = *reinterpret_cast<Stage<T, NT, VPT> *>(smem);
     __shared__ float sh[2][2][32][1];
     const int tid = threadIdx.x;
+    const Cols<1> cols(tid, p.D);
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (tid + i * NT);
-            if (c >= p.D) continue;
+            const int c = cols.first + 8 * NT * i;
+            if (c >= cols.end) continue;
             copy8(&st.rows[0][i][tid], p.r.x, row * p.r.x_stride + c, c, p.D);
             copy8(&st.rows[1][i][tid], p.r.y, row * p.r.y_stride + c, c, p.D);
             if (HAS == kAll) copy8(&st.rows[2][i][tid], p.r.g, row * p.r.g_stride + c, c, p.D);
@@ -289,8 +326,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) block_norm_rows_kernel(const __g
     fetch(blockIdx.x);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (c >= p.D) continue;
+        const int c = cols.first + 8 * NT * i;
+        if (c >= cols.end) continue;
         W8 w, sc;
         w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
         w = w.times(sc);
@@ -310,7 +347,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) block_norm_rows_kernel(const __g
             if (HAS == kAll) g[i] = st.rows[2][i][tid];
         }
         if (row + gridDim.x < p.M) fetch(row + gridDim.x);
-        finish_row<HAS, T, NT, VPT, F8>(p, row, tid, x, y, g, sh[turn][0], sh[turn][1],
+        finish_row<HAS, T, NT, VPT, F8>(p, row, cols, x, y, g, sh[turn][0], sh[turn][1],
             [&](int i, int) { return W8{{st.w[0][i][tid], st.w[1][i][tid]}}; }, [&](int i, int) { return W8{{st.w[2][i][tid], st.w[3][i][tid]}}; });
     }
 }
@@ -318,8 +355,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) block_norm_rows_kernel(const __g
 // Gradients, a row at a time: with n = z / rms(z) a norm's gradient is dz = (w - n mean(w n)) / rms(z), w that of n.
 //   dx = dx' + (gradient of h's norm),  d(scale sigmoid(g) post_w n_y) = dx
 // A thread adds up its columns' sums over the block's rows, sq for post_w and scale, sp for pre_w.
-template <int HAS, typename T, int NT, int VPT, typename PostW, typename PreW>
-__device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, int tid, V8<T> (&x)[VPT], const V8<T> (&dh)[VPT], const V8<T> (&dx1)[VPT],
+template <int HAS, typename T, int NT, int VPT, int CL, typename PostW, typename PreW>
+__device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, const Cols<CL> &cols, V8<T> (&x)[VPT], const V8<T> (&dh)[VPT], const V8<T> (&dx1)[VPT],
                                          V8<T> (&y)[VPT], V8<T> (&g)[VPT], float2 (&sq)[VPT][4], float2 (&sp)[VPT][4], float (*sh)[3], float (*sh1)[1],
                                          PostW post_w, PreW pre_w)
 {
@@ -329,8 +366,8 @@ __device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, int tid
     float2 s0 = f2(0.f), s1 = s0, s2 = s0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (c >= p.D) continue;
+        const int c = cols.first + 8 * NT * i;
+        if (c >= cols.end) continue;
         W8 w;
         if (has_h) w = pre_w(i, c);
 #pragma unroll
@@ -343,14 +380,14 @@ __device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, int tid
         }
     }
     s[0] = s0.x + s0.y, s[1] = s1.x + s1.y, s[2] = s2.x + s2.y;
-    row_sum<NT, 3>(s, sh);
+    row_sum<NT, CL>(s, sh);
     const float rx = rstd(s[0], p.D, p.eps), ry = rstd(s[2], p.D, p.eps);
     const float mx = s[1] * rx * inv_D;  // mean(w n)
     float2 m = f2(0.f), d[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (c >= p.D) continue;
+        const int c = cols.first + 8 * NT * i;
+        if (c >= cols.end) continue;
         W8 w, pw;
         if (has_h) w = pre_w(i, c);
         if (has_y) pw = post_w(i, c);
@@ -382,12 +419,12 @@ __device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, int tid
     }
     if (!has_y) return;
     float t[1] = {m.x + m.y};
-    row_sum<NT, 1>(t, sh1);
+    row_sum<NT, CL>(t, sh1);
     const float my = t[0] * inv_D;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
-        if (c >= p.D) continue;
+        const int c = cols.first + 8 * NT * i;
+        if (c >= cols.end) continue;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 n = f2_mul(y[i].get(j), f2(ry));
@@ -397,31 +434,36 @@ __device__ __forceinline__ void back_row(const BackArgs &p, int64_t row, int tid
     }
 }
 
-template <int NT, int VPT>
-__device__ __forceinline__ void store_sums(const BackArgs &p, int part, int tid, const float2 (&sq)[VPT][4], const float2 (&sp)[VPT][4])
+template <int NT, int VPT, int CL>
+__device__ __forceinline__ void store_sums(const BackArgs &p, int part, const Cols<CL> &cols, const float2 (&sq)[VPT][4], const float2 (&sp)[VPT][4])
 {
     float *out = p.part + (int64_t)part * 2 * p.D;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
+        const int c = cols.first + 8 * NT * i;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c + 2 * j < p.D) {
+            if (c + 2 * j < cols.end) {
                 *reinterpret_cast<float2 *>(out + c + 2 * j) = sq[i][j];
                 *reinterpret_cast<float2 *>(out + p.D + c + 2 * j) = sp[i][j];
             }
     }
 }
 
-// Rows straight from global memory: a warp each for the shortest ones, and those too long for the kernel below.
-template <typename T, int NT, int VPT>
+// Rows straight from global memory: a warp each for the shortest ones.
+template <typename T, int NT, int VPT, int CL>
 __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_back_kernel(const __grid_constant__ BackArgs p, int parts)
 {
     constexpr int kRows = NT == 32 ? 4 : 1;
     __shared__ float sh[2][32][3], sh1[2][32][1];
     const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int part = blockIdx.x * kRows + (NT == 32 ? threadIdx.x >> 5 : 0);
-    if (part >= parts) return;
+    const int part = blockIdx.x / CL * kRows + (NT == 32 ? threadIdx.x >> 5 : 0);
+    if (part >= parts) return;  // a whole warp
+    const Cols<CL> cols(tid, p.D);
+    if (CL == 2) {
+        cluster_arrive();
+        cluster_wait();
+    }
     float2 sq[VPT][4], sp[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -432,8 +474,8 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_back_kernel(co
         V8<T> x[VPT], dh[VPT], dx1[VPT], y[VPT], g[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (tid + i * NT);
-            if (c >= p.D) continue;
+            const int c = cols.first + 8 * NT * i;
+            if (c >= cols.end) continue;
             if (p.r.dh) {
                 load8(x[i], p.r.x_out, row * p.r.x_out_stride + c, c, p.D);
                 load8(dh[i], p.r.dh, row * p.r.dh_stride + c, c, p.D);
@@ -442,7 +484,7 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_back_kernel(co
             if (p.r.y) load8(y[i], p.r.y, row * p.r.y_stride + c, c, p.D);
             if (p.r.g) load8(g[i], p.r.g, row * p.r.g_stride + c, c, p.D);
         }
-        back_row<kAny, T, NT, VPT>(p, row, tid, x, dh, dx1, y, g, sq, sp, sh[turn], sh1[turn],
+        back_row<kAny, T, NT, VPT, CL>(p, row, cols, x, dh, dx1, y, g, sq, sp, sh[turn], sh1[turn],
             [&](int, int c) {
                 W8 w, sc;
                 w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
@@ -454,7 +496,7 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_back_kernel(co
                 return w;
             });
     }
-    store_sums<NT, VPT>(p, part, tid, sq, sp);
+    store_sums<NT, VPT>(p, part, cols, sq, sp);
 }
 
 // As block_norm_rows_kernel: the parameters and the next row in shared memory.
@@ -463,18 +505,20 @@ struct BackStage {
     float4 w[4][VPT][NT];    // post_w scale, pre_w: four channels each
     V8<T> rows[5][VPT][NT];  // x', dh, dx', y, g
 };
-template <typename T, int NT, int VPT, int HAS>
+template <typename T, int NT, int VPT, int CL, int HAS>
 __global__ void __launch_bounds__(NT, 512 / NT) block_norm_back_rows_kernel(const __grid_constant__ BackArgs p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     BackStage<T, NT, VPT> &st = *reinterpret_cast<BackStage<T, NT, VPT> *>(smem);
     __shared__ float sh[2][32][3], sh1[2][32][1];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, part = blockIdx.x / CL, parts = gridDim.x / CL;
+    const Cols<CL> cols(tid, p.D);
+    if (CL == 2) cluster_arrive();
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (tid + i * NT);
-            if (c >= p.D) continue;
+            const int c = cols.first + 8 * NT * i;
+            if (c >= cols.end) continue;
             copy8(&st.rows[0][i][tid], p.r.x_out, row * p.r.x_out_stride + c, c, p.D);
             copy8(&st.rows[1][i][tid], p.r.dh, row * p.r.dh_stride + c, c, p.D);
             copy8(&st.rows[2][i][tid], p.r.dx1, row * p.r.dx1_stride + c, c, p.D);
@@ -482,14 +526,14 @@ __global__ void __launch_bounds__(NT, 512 / NT) block_norm_back_rows_kernel(cons
             if (HAS == kAll) copy8(&st.rows[4][i][tid], p.r.g, row * p.r.g_stride + c, c, p.D);
         }
     };
-    fetch(blockIdx.x);
+    fetch(part);
     float2 sq[VPT][4], sp[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = 8 * (tid + i * NT);
+        const int c = cols.first + 8 * NT * i;
 #pragma unroll
         for (int j = 0; j < 4; ++j) sq[i][j] = sp[i][j] = f2(0.f);
-        if (c >= p.D) continue;
+        if (c >= cols.end) continue;
         W8 w, sc;
         w.load(p.post_w, c, p.D), sc.load(p.scale, c, p.D);
         w = w.times(sc);
@@ -497,9 +541,10 @@ __global__ void __launch_bounds__(NT, 512 / NT) block_norm_back_rows_kernel(cons
         w.load(p.pre_w, c, p.D);
         st.w[2][i][tid] = w.r[0], st.w[3][i][tid] = w.r[1];
     }
+    if (CL == 2) cluster_wait();  // the other block runs, and has shared memory
     int turn = 0;
 #pragma unroll 1
-    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
+    for (int64_t row = part; row < p.M; row += parts, turn ^= 1) {
         V8<T> x[VPT], dh[VPT], dx1[VPT], y[VPT], g[VPT];
         cp_async_wait_all();
 #pragma unroll
@@ -509,11 +554,11 @@ __global__ void __launch_bounds__(NT, 512 / NT) block_norm_back_rows_kernel(cons
             y[i] = st.rows[3][i][tid];
             if (HAS == kAll) g[i] = st.rows[4][i][tid];
         }
-        if (row + gridDim.x < p.M) fetch(row + gridDim.x);
-        back_row<HAS, T, NT, VPT>(p, row, tid, x, dh, dx1, y, g, sq, sp, sh[turn], sh1[turn],
+        if (row + parts < p.M) fetch(row + parts);
+        back_row<HAS, T, NT, VPT, CL>(p, row, cols, x, dh, dx1, y, g, sq, sp, sh[turn], sh1[turn],
             [&](int i, int) { return W8{{st.w[0][i][tid], st.w[1][i][tid]}}; }, [&](int i, int) { return W8{{st.w[2][i][tid], st.w[3][i][tid]}}; });
     }
-    store_sums<NT, VPT>(p, blockIdx.x, tid, sq, sp);
+    store_sums<NT, VPT>(p, part, cols, sq, sp);
 }
 
 __global__ void __launch_bounds__(kSumCols *kSumGroups)
@@ -617,12 +662,15 @@ cudaError_t launch(const Args &p, int dev, int sms, cudaStream_t s)
     const unsigned M = (unsigned)p.M, M4 = (unsigned)((p.M + 3) / 4);
     // Blocks that stay from about 2.4 million channels of rows on (BF16 without a gate, M = 600, 1200, 2400, 9600): D = 600 3.1, 3.7, 4.6,
     // 10.7 us for 3.1, 3.5, 5.4, 13.4 with a block each; 4096 6.2, 7.8, 11.7, 50.9 for 5.4, 9.7, 17.6, 64.7; 7168 7.6, 10.9, 23.8, 92.8
-    // for 8.9, 16.8, 35.3, 129.8. FP32 turns at the same M.
-    if (p.M >= 4 * sms && p.M * p.D >= 2400000 && p.D > 512 && p.D <= 8192 && p.r.y && p.r.h) {
+    // for 8.9, 16.8, 35.3, 129.8. FP32 turns at the same M. 16384 channels (M = 1200, 4800): 28.2, 109 for 44.9, 165 us; in FP32 the
+    // parameters find no room there, and the rows alone gain 5% (77, 278 us with a block each). A cluster of two blocks a row takes 38.5, 127.
+    constexpr bool kStageWide = sizeof(T) == 2;
+    if (p.M >= 4 * sms && p.M * p.D >= 2400000 && p.D > 512 && (p.D <= kWide || kStageWide) && p.r.y && p.r.h) {
         if (p.D <= 1024) return launch_rows<T, 64, 2, F8>(p, dev, sms, s);
         if (p.D <= 2048) return launch_rows<T, 128, 2, F8>(p, dev, sms, s);
         if (p.D <= 4096) return launch_rows<T, 128, 4, F8>(p, dev, sms, s);
-        return launch_rows<T, 256, 4, F8>(p, dev, sms, s);
+        if (p.D <= kWide) return launch_rows<T, 256, 4, F8>(p, dev, sms, s);
+        if constexpr (kStageWide) return launch_rows<T, 512, 4, F8>(p, dev, sms, s);
     }
     if (p.D <= 256) block_norm_kernel<T, 32, 1, F8><<<M4, 128, 0, s>>>(p);
     else if (p.D <= 512) block_norm_kernel<T, 32, 2, F8><<<M4, 128, 0, s>>>(p);
@@ -634,19 +682,19 @@ cudaError_t launch(const Args &p, int dev, int sms, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <typename T, int NT, int VPT, int HAS = kAny>
+template <typename T, int NT, int VPT, int CL = 1, int HAS = kAny>
 cudaError_t launch_back_rows(const BackArgs &p, int *parts, int dev, int sms, cudaStream_t s)
 {
-    if (HAS == kAny) return p.r.g ? launch_back_rows<T, NT, VPT, kAll>(p, parts, dev, sms, s) : launch_back_rows<T, NT, VPT, kNoGate>(p, parts, dev, sms, s);
+    if (HAS == kAny) return p.r.g ? launch_back_rows<T, NT, VPT, CL, kAll>(p, parts, dev, sms, s) : launch_back_rows<T, NT, VPT, CL, kNoGate>(p, parts, dev, sms, s);
     constexpr int kHas = HAS == kAny ? kAll : HAS;
     static std::atomic<uint64_t> raised;
     const int smem = (int)sizeof(BackStage<T, NT, VPT>);
-    const cudaError_t e = raise_smem_on(raised, dev, block_norm_back_rows_kernel<T, NT, VPT, kHas>, smem);
+    const auto kernel = block_norm_back_rows_kernel<T, NT, VPT, CL, kHas>;
+    const cudaError_t e = raise_smem_on(raised, dev, kernel, smem);
     if (e != cudaSuccess) return e;
-    const int64_t most = (int64_t)sms * blocks_per_sm(512, NT, sizeof(BackStage<T, NT, VPT>));
+    const int64_t most = (int64_t)sms * blocks_per_sm(512, NT, sizeof(BackStage<T, NT, VPT>)) / CL;
     *parts = (int)(most < *parts ? most : *parts);
-    block_norm_back_rows_kernel<T, NT, VPT, kHas><<<(unsigned)*parts, NT, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_cluster(kernel, (unsigned)*parts * CL, CL, NT, smem, s, p);
 }
 
 // parts: rows of partial sums that the workspace has room for, and then those that are written
@@ -656,19 +704,22 @@ cudaError_t launch_back(const BackArgs &p, int *parts, int dev, int sms, cudaStr
     const unsigned n = (unsigned)*parts, n4 = (unsigned)((*parts + 3) / 4);
     // Staged rows wherever a block has more than one (BF16, M = 150, 300, 1200, 9600): D = 600 5.6, 6.6, 9.1, 32 us for 5.6, 7.0, 10.7, 58
     // straight from global memory; 7168 14.3, 15.6, 29.6, 138 for 14.2, 23.7, 47.6, 267; FP32 19.3, 21.2, 49.9, 287 for 19.4, 35.6, 95.7, 641.
-    if (p.M > sms && p.D > 512 && p.D <= 8192 && p.r.y && p.r.dh && p.r.dx1) {
+    // Two blocks a row (BF16, M = 40, 300, 1200, 4800): D = 8200 12.8, 21.0, 60, 216 us; 16384 18.9, 28.5, 81, 259; FP32 24, 49, 135, 458.
+    // One block, its sums in shared memory and the row read three times: 13.9, 20.6, 66, 308; 21.3, 40.8, 138, 506; 25, 49, 163, 603.
+    if (p.M > (p.D <= kWide ? sms : sms / 2) && p.D > 512 && p.r.y && p.r.dh && p.r.dx1) {
         if (p.D <= 1024) return launch_back_rows<T, 128, 1>(p, parts, dev, sms, s);
         if (p.D <= 2048) return launch_back_rows<T, 128, 2>(p, parts, dev, sms, s);
         if (p.D <= 4096) return launch_back_rows<T, 256, 2>(p, parts, dev, sms, s);
-        return launch_back_rows<T, 512, 2>(p, parts, dev, sms, s);
+        if (p.D <= kWide) return launch_back_rows<T, 512, 2>(p, parts, dev, sms, s);
+        return launch_back_rows<T, 512, 2, 2>(p, parts, dev, sms, s);
     }
-    if (p.D <= 256) block_norm_back_kernel<T, 32, 1><<<n4, 128, 0, s>>>(p, *parts);
-    else if (p.D <= 512) block_norm_back_kernel<T, 32, 2><<<n4, 128, 0, s>>>(p, *parts);
-    else if (p.D <= 1024) block_norm_back_kernel<T, 128, 1><<<n, 128, 0, s>>>(p, *parts);
-    else if (p.D <= 2048) block_norm_back_kernel<T, 128, 2><<<n, 128, 0, s>>>(p, *parts);
-    else if (p.D <= 4096) block_norm_back_kernel<T, 256, 2><<<n, 256, 0, s>>>(p, *parts);
-    else if (p.D <= 8192) block_norm_back_kernel<T, 512, 2><<<n, 512, 0, s>>>(p, *parts);
-    else block_norm_back_kernel<T, 1024, 2><<<n, 1024, 0, s>>>(p, *parts);
+    if (p.D <= 256) block_norm_back_kernel<T, 32, 1, 1><<<n4, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 512) block_norm_back_kernel<T, 32, 2, 1><<<n4, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 1024) block_norm_back_kernel<T, 128, 1, 1><<<n, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 2048) block_norm_back_kernel<T, 128, 2, 1><<<n, 128, 0, s>>>(p, *parts);
+    else if (p.D <= 4096) block_norm_back_kernel<T, 256, 2, 1><<<n, 256, 0, s>>>(p, *parts);
+    else if (p.D <= kWide) block_norm_back_kernel<T, 512, 2, 1><<<n, 512, 0, s>>>(p, *parts);
+    else return launch_cluster(block_norm_back_kernel<T, 512, 2, 2>, 2 * n, 2, 512, 0, s, p, *parts);
     return cudaGetLastError();
 }
 

@@ -19,14 +19,6 @@ namespace glr {
 namespace {
 
 // ---------------------------------------------------------------- clusters
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The float4 at `mine` (shared memory) in block `rank` of the cluster, counted by its barrier at `bar`.
 __device__ __forceinline__ void st_remote(const float4 *mine, const uint64_t *bar, uint32_t rank, float4 v)
 {

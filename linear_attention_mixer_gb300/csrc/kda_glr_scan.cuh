@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kda_glr.cuh"
+#include "kda_cluster.cuh"
 #include "kda_launch.cuh"
 
 namespace kda {
@@ -17,30 +18,6 @@ template <typename T> constexpr int scan_warps() { return sizeof(T) == 4 ? 8 : 4
 template <typename T> constexpr int max_cluster() { return sizeof(T) == 4 ? 8 : 16; }
 // Blocks that work on clusters of more than one, over all channels and sequences, at most: what bounds the workspace.
 constexpr int kMaxShared = 16384;
-
-inline cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *at, unsigned grid, int nc, int threads, size_t smem, cudaStream_t stream)
-{
-    at->id = cudaLaunchAttributeClusterDimension;
-    at->val.clusterDim.x = (unsigned)nc;
-    at->val.clusterDim.y = at->val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = nc > 1 ? 1 : 0;
-    return cfg;
-}
-
-// A launch of clusters of nc blocks (nc 1: without).
-template <typename... P, typename... A>
-inline cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, int nc, int threads, size_t smem, cudaStream_t stream, A &&...args)
-{
-    cudaLaunchAttribute at = {};
-    const cudaLaunchConfig_t cfg = cluster_config(&at, grid, nc, threads, smem, stream);
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
-}
 
 // How many clusters of n blocks of a kernel run at once, asked once for each device and n. Not n times fewer than single
 // blocks: a cluster stays within a group of SMs, and what does not divide there stays idle.

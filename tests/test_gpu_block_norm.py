@@ -138,6 +138,26 @@ def test_many_rows(D, bf16, gate, strided):
         p.check_back(p.backward(**kw), **kw)
 
 
+@pytest.mark.parametrize("M,D,bf16,gate,strided", [(1, 8200, True, False, False), (76, 16384, False, True, True), (77, 12288, True, True, False),
+                                                   (153, 8196, False, False, True), (701, 8200, True, True, True), (650, 16380, False, True, False),
+                                                   (611, 16384, True, False, False)])
+def test_wide_rows(M, D, bf16, gate, strided):
+    """Rows of more than 8192 channels, which two blocks share."""
+    p = Problem(M, D, bf16, gate, seed=11, strided=strided)
+    x1, h = p.forward()
+    r = p.ref()
+    near(x1, r["x1"], r["x1_err"], bf16)
+    near(h, r["h"], r["h_err"], bf16)
+    got = p.backward()
+    p.check_back(got)
+    again = p.backward()
+    assert all(torch.equal(got[n], again[n]) for n in got)
+    for t in (x1, h, got["dx"], got["dy"]):  # the row behind the last
+        assert bool((torch.as_strided(t, (1, D), (1, 1), t.storage_offset() + M * t.stride(0)) == -7.0).all())
+    for kw in ({"y": False}, {"dh": False}, {"dx1": False}):
+        p.check_back(p.backward(**kw), **kw)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_only_one_of_the_norms(bf16):
     p = Problem(40, 200, bf16, True, seed=2)
@@ -191,6 +211,16 @@ def test_fp8_rows_are_those_of_the_quantiser():
     _, h = p.forward()
     q, q2 = (torch.zeros(130, 1040, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
     s, s2 = (torch.zeros(130, 9, device="cuda") for _ in range(2))
+    K.kda_block_norm(p.cfg, p.params, p.dev["x"], y=p.dev["y"], g=p.dev["g"], x_out=p.new(), h=q, hs=s)
+    K.kda_quant_fp8(h, q2, s2)
+    assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+
+
+def test_wide_fp8_rows_are_those_of_the_quantiser():
+    p = Problem(640, 8208, False, True, seed=12)
+    _, h = p.forward()
+    q, q2 = (torch.zeros(640, 8208, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    s, s2 = (torch.zeros(640, 65, device="cuda") for _ in range(2))
     K.kda_block_norm(p.cfg, p.params, p.dev["x"], y=p.dev["y"], g=p.dev["g"], x_out=p.new(), h=q, hs=s)
     K.kda_quant_fp8(h, q2, s2)
     assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
