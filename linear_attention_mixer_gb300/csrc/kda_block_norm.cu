@@ -4,6 +4,7 @@
 // h (the next block's input) in the rows' type or in E4M3 with a power-of-two scale for each 128 columns. And the
 // gradients of that.
 #include <climits>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 
@@ -450,7 +451,7 @@ __device__ __forceinline__ void store_sums(const BackArgs &p, int part, const Co
     }
 }
 
-// Rows straight from global memory: a warp each for the shortest ones.
+// Rows straight from global memory, in the forms that lack some: a warp each for the shortest ones.
 template <typename T, int NT, int VPT, int CL>
 __global__ void __launch_bounds__(NT == 32 ? 128 : NT) block_norm_back_kernel(const __grid_constant__ BackArgs p, int parts)
 {
@@ -628,10 +629,14 @@ bool rows_ok(int64_t M)
     return true;
 }
 
+// Rows of partial sums. One more costs the sums' kernel what some M / 100 of a row fewer save a block, so the time is least
+// near 10 sqrt(M) of them (BF16, 256 channels, M = 9600, in 608, 912, 1216, 1824: 15.4, 14.2, 13.8, 15.5 us; 1024 channels, M = 300, in
+// 152, 300: 6.0, 7.0; M = 2400, in 304, 456, 608: 12.7, 12.0, 12.7): a whole number for each of the 152 SMs, up to what runs at once.
 int64_t parts_of(int32_t D, int64_t M)
 {
-    const int64_t most = D <= 512 ? 1216 : 304;
-    return M < most ? M : most;
+    const int64_t most = D <= 256 ? 2432 : D <= 512 ? 1216 : D <= 2048 ? 608 : 304, even = (int64_t)(10 * sqrt((double)M) / 152 + 0.5) * 152;
+    const int64_t n = even < 152 ? 152 : even < most ? even : most;
+    return M < n ? M : n;
 }
 size_t back_bytes(int32_t D, int64_t M) { return 256 + (size_t)parts_of(D, M) * 2 * D * sizeof(float); }
 
@@ -702,11 +707,13 @@ template <typename T>
 cudaError_t launch_back(const BackArgs &p, int *parts, int dev, int sms, cudaStream_t s)
 {
     const unsigned n = (unsigned)*parts, n4 = (unsigned)((*parts + 3) / 4);
-    // Staged rows wherever a block has more than one (BF16, M = 150, 300, 1200, 9600): D = 600 5.6, 6.6, 9.1, 32 us for 5.6, 7.0, 10.7, 58
-    // straight from global memory; 7168 14.3, 15.6, 29.6, 138 for 14.2, 23.7, 47.6, 267; FP32 19.3, 21.2, 49.9, 287 for 19.4, 35.6, 95.7, 641.
+    // Staged rows wherever a call has all of them (BF16, M = 20, 150, 9600): D = 512 4.5, 5.0, 18.1 us for 6.4, 6.8, 26.3 straight from
+    // global memory; 7168 11.9, 14.0, 138 for 12.4, 14.3, 267; FP32 14.4, 17.2, 282 for 17.4, 19.2, 641.
     // Two blocks a row (BF16, M = 40, 300, 1200, 4800): D = 8200 12.8, 21.0, 60, 216 us; 16384 18.9, 28.5, 81, 259; FP32 24, 49, 135, 458.
     // One block, its sums in shared memory and the row read three times: 13.9, 20.6, 66, 308; 21.3, 40.8, 138, 506; 25, 49, 163, 603.
-    if (p.M > (p.D <= kWide ? sms : sms / 2) && p.D > 512 && p.r.y && p.r.dh && p.r.dx1) {
+    if (p.r.y && p.r.dh && p.r.dx1) {
+        if (p.D <= 256) return launch_back_rows<T, 32, 1>(p, parts, dev, sms, s);
+        if (p.D <= 512) return launch_back_rows<T, 64, 1>(p, parts, dev, sms, s);
         if (p.D <= 1024) return launch_back_rows<T, 128, 1>(p, parts, dev, sms, s);
         if (p.D <= 2048) return launch_back_rows<T, 128, 2>(p, parts, dev, sms, s);
         if (p.D <= 4096) return launch_back_rows<T, 256, 2>(p, parts, dev, sms, s);

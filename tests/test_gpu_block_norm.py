@@ -138,6 +138,29 @@ def test_many_rows(D, bf16, gate, strided):
         p.check_back(p.backward(**kw), **kw)
 
 
+@pytest.mark.parametrize("M,D,bf16,gate,strided", [(1, 264, True, True, False), (151, 16, True, False, True), (305, 4, False, True, False), (2433, 256, True, True, False),
+                                                   (3001, 252, False, False, True), (3001, 512, True, True, True), (1217, 508, False, True, False)])
+def test_many_short_rows(M, D, bf16, gate, strided):
+    p = Problem(M, D, bf16, gate, seed=13, strided=strided)
+    got = p.backward()
+    p.check_back(got)
+    again = p.backward()
+    assert all(torch.equal(got[n], again[n]) for n in got)
+    for n in ("dx", "dy"):  # the row behind the last
+        t = got[n]
+        assert bool((torch.as_strided(t, (1, D), (1, 1), t.storage_offset() + M * t.stride(0)) == -7.0).all())
+    for kw in ({"y": False}, {"dh": False}, {"dx1": False}):
+        p.check_back(p.backward(**kw), **kw)
+
+
+def test_workspace_grows_with_the_rows():
+    """Room for many rows serves fewer."""
+    for D in (16, 512, 2048, 8200):
+        cfg = K.kda_block_norm_config(D, K.KDA_BF16)
+        need = [K.kda_block_norm_workspace_bytes(cfg, M) for M in (*range(1, 2000), 5000, 10000, 59000, 100000, 2 ** 31 - 1)]
+        assert need == sorted(need)
+
+
 @pytest.mark.parametrize("M,D,bf16,gate,strided", [(1, 8200, True, False, False), (76, 16384, False, True, True), (77, 12288, True, True, False),
                                                    (153, 8196, False, False, True), (701, 8200, True, True, True), (650, 16380, False, True, False),
                                                    (611, 16384, True, False, False)])
