@@ -544,7 +544,8 @@ kda_status kda_glr_decode(const kda_glr_config_t *cfg, const kda_glr_params *par
 /*
  * N sequences packed along the token axis; cu_seqlens (device int32 [N+1]) and cu_seqlens_host as for kda_prefill. An
  * empty sequence copies its src state (or zeros) to its dst. Nothing outside the rows [0, cu[N]) of out is written. All
- * arithmetic is FP32 (the state within 2.4e-7 of FP64 in the 2-norm over 65536 tokens), and results do not depend on timing.
+ * arithmetic is FP32, and results do not depend on timing. Over 65536 tokens of steady decays, 1 - alpha from 1e-2 to 1e-7, the final
+ * state and its gradient are within 6.3e-7 of FP64 in the 2-norm (token by token, kda_glr_decode: 6.5e-6).
  * Long sequences are taken in windows by clusters of blocks, and in parts at once where the channels are few; short ones a
  * thread for two channels each.
  *   starts     device FP32 [kda_glr_chunks(cu_seqlens_host, N)][dim], 16-byte aligned, or NULL. Receives states that

@@ -7,7 +7,7 @@
 // A lane has two neighbouring channels, as FP32 pairs. The decay is held as e = alpha - 1 and a step taken as
 // h + (e h + u): near alpha = 1, where a state remembers 1 / (1 - alpha) tokens, alpha itself in FP32 would be
 // wrong by 2^-25 at each of them (the steady state of 1 - alpha = 1e-4 by 3e-4), e is not. m^2 = -e (2 + e) has
-// no cancellation either. What it costs: where alpha is far below 1, h's part of the sum is off by 2^-24 |h|.
+// no cancellation either. (The scan keeps its products of alphas in a like way.) What it costs: where alpha is far below 1, h's part of the sum is off by 2^-24 |h|.
 #pragma once
 
 #include "kda_internal.cuh"

@@ -1,17 +1,17 @@
 // kda_glr_scan.cu - the gated linear recurrence over packed sequences: prefill and backward, by a scan along the tokens.
 //
 // A step h -> (1 + e) h + u is linear, so 16 of them are h -> A h + H with A the product of the (1 + e) and H what becomes
-// of h = 0, and such pairs join as (A2 A1, A2 H1 + H2). A warp has 16 tokens of 64 channels (two channels a lane), a block
+// of h = 0, and such pairs join as (A2 A1, A2 H1 + H2), with A or A - 1 held, whichever is the smaller. A warp has 16 tokens of 64 channels (two channels a lane), a block
 // of W warps 16 W tokens, a cluster of nc blocks a window of 16 W nc tokens, and it goes through its sequence window by
 // window. For each: every warp works out its tokens' e and u, once, and its pair; the warps' pairs are joined through
 // shared memory, the blocks' through distributed shared memory, in the tokens' order (so results do not depend on timing);
 // then each warp walks its tokens from the state that it now knows, with e and u still in registers. The rows are read
 // once. No block waits for one of another cluster.
 //
-// 65536 tokens of 4096 channels in BF16: 503 us, 4.3 TB/s. Instructions (55% issued on the average), special functions
-// and the FP32 pipe (35 to 41%) and the latency of a window's exchange share it, on 3.4 of the 4 blocks that an SM has room
-// for. Eight sequences of 0 to 2048 tokens, 7168 channels in FP32: 95 us, 5.7 TB/s. With 8 tokens a warp (and 24 warps an SM)
-// the first took 670 us where this took 566.
+// 65536 tokens of 4096 channels in BF16: 531 us, 4.0 TB/s (506 with A alone, which is wrong for states that are kept long). Instructions,
+// special functions and the FP32 pipe and the latency of a window's exchange share it, on 3.4 of the 4 blocks that an SM has room
+// for. Eight sequences of 0 to 2048 tokens, 7168 channels in FP32: 99 us, 5.5 TB/s. With 8 tokens a warp (and 24 warps an SM)
+// the first took 670 us where 16 took 566.
 #include "kda_glr_scan.cuh"
 
 namespace kda {
@@ -46,22 +46,40 @@ __device__ __forceinline__ bool wait_cluster(const uint64_t *bar, uint32_t parit
 }
 
 // ---------------------------------------------------------------- pairs
-struct Lin {  // h -> A h + H
-    float2 A, H;
-    __device__ __forceinline__ float2 at(float2 h) const { return f2_fma(A, h, H); }
+// h -> A h + H. What is held of A is v: A - 1 (below 0) where A >= 1/2, else A. Near 1, where a state is kept over many pairs,
+// A itself in FP32 would be wrong by 2^-25 at each with a sign that a steady decay repeats (65536 tokens of 1 - alpha = 1e-6 to
+// 1e-7: states off by 1e-3; so, by 6e-7); near 0 a difference from 1 would leave 2^-24 of a state that has gone.
+constexpr float kKept = -0x1p-100f;  // v where A is 1: it changes no h, and is below 0
+constexpr float kForm = -0x1p110f;
+__device__ __forceinline__ float2 form(float2 v) { return make_float2(__saturatef(v.x * kForm), __saturatef(v.y * kForm)); }  // 1 for A - 1, 0 for A
+struct Lin {
+    float2 v, H;
+    __device__ __forceinline__ float2 at(float2 h) const { return f2_fma(form(v), h, f2_fma(v, h, H)); }
     __device__ __forceinline__ void then(const Lin &n)  // first this, then n
     {
-        H = f2_fma(n.A, H, n.H);
-        A = f2_mul(A, n.A);
+        H = n.at(H);
+        v = f2_fma(form(n.v), v, f2_fma(v, n.v, f2_mul(form(v), n.v)));  // the product in either's form, A - 1 only if both are
+        v = make_float2(v.x < -0.5f ? v.x + 1.f : v.x, v.y < -0.5f ? v.y + 1.f : v.y);
     }
 };
-__device__ __forceinline__ Lin lin_identity() { return Lin{f2(1.f), f2(0.f)}; }
+__device__ __forceinline__ Lin lin_identity() { return Lin{f2(kKept), f2(0.f)}; }
+// The product A of up to 16 decays 1 + e, and E = A - 1 without the difference.
+struct Decays {
+    float2 A, E;
+    __device__ __forceinline__ Decays() : A(f2(1.f)), E(f2(0.f)) {}
+    __device__ __forceinline__ void add(float2 e)
+    {
+        E = f2_fma(A, e, E);
+        A = f2_fma(A, e, A);
+    }
+    __device__ __forceinline__ float2 v() const { return make_float2(A.x >= 0.5f ? fminf(E.x, kKept) : A.x, A.y >= 0.5f ? fminf(E.y, kKept) : A.y); }
+};
 __device__ __forceinline__ Lin ld_lin(const float4 *p)
 {
     const float4 v = *p;
     return Lin{make_float2(v.x, v.y), make_float2(v.z, v.w)};
 }
-__device__ __forceinline__ float4 as_float4(const Lin &l) { return make_float4(l.A.x, l.A.y, l.H.x, l.H.y); }
+__device__ __forceinline__ float4 as_float4(const Lin &l) { return make_float4(l.v.x, l.v.y, l.H.x, l.H.y); }
 
 // The places through which pairs are joined, for two windows in turn: a block sends for a window when it has joined the
 // one before, to which every block sends when all its warps have read the one before that.
@@ -81,66 +99,64 @@ struct Exchange {
 };
 
 // Joining the pairs of a window's warps, in two parts, so that a warp has something to do while they travel.
-// post: this warp's own pair goes to the others. Returns what comes before its tokens within the block (BACK: behind them)
-// and, in a cluster, sends the block's pair to all its blocks; without one `all` becomes it.
-// meet: the state before the warp's tokens (behind them), from `carry`, that at the window's start, which becomes that at its end.
+// post: this warp's own pair goes to the others of the block and, in a cluster, the block's pair to all its blocks: by one warp, in turn,
+// since joining pairs takes three times the instructions of a state's way through them.
+// meet: the state before the warp's tokens (BACK: behind them), from `carry`, that at the window's start, which becomes that at its end.
 // `turn`: windows so far; good: no wait has given up (then nothing more is sent or waited for). All threads of the cluster
 // take part.
 template <bool BACK, int W, int MAX>
-__device__ __forceinline__ Lin post(Exchange<W, MAX> &ex, const Lin &own, Lin &all, int turn, int nc, int rank, bool good)
+__device__ __forceinline__ void post(Exchange<W, MAX> &ex, const Lin &own, int turn, int nc, int rank, bool good)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, par = turn & 1;
     ex.warp[par][warp][lane] = as_float4(own);
     if (nc > 1 && threadIdx.x == 0 && good) mbar_arrive_expect_tx(&ex.bar[par], (uint32_t)nc * 32 * sizeof(float4));
     __syncthreads();
-    Lin run = lin_identity(), pre = run;
+    if (nc == 1) return;
+    if (turn == 0) cluster_wait();  // every block of the cluster runs and has its barriers: theirs is the arrival at the start
+    if (warp != (turn + (int)blockIdx.x) % W || !good) return;
+    Lin all = ld_lin(&ex.warp[par][BACK ? W - 1 : 0][lane]);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const int w = BACK ? W - 1 - i : i;
-        if (w == warp) pre = run;
-        run.then(ld_lin(&ex.warp[par][w][lane]));
-    }
-    all = run;
-    if (nc > 1) {
-        if (turn == 0) cluster_wait();  // every block of the cluster runs and has its barriers: theirs is the arrival at the start
-        if (good)
-            for (int r = warp; r < nc; r += W) st_remote(&ex.block[par][rank][lane], &ex.bar[par], r, as_float4(run));
-    }
-    return pre;
+    for (int i = 1; i < W; ++i) all.then(ld_lin(&ex.warp[par][BACK ? W - 1 - i : i][lane]));
+    for (int r = 0; r < nc; ++r) st_remote(&ex.block[par][rank][lane], &ex.bar[par], r, as_float4(all));
 }
 template <bool BACK, int W, int MAX>
-__device__ __forceinline__ float2 meet(Exchange<W, MAX> &ex, const Lin &pre, const Lin &all, float2 &carry, int turn, int nc, int rank, bool &good)
+__device__ __forceinline__ float2 meet(Exchange<W, MAX> &ex, float2 &carry, int turn, int nc, int rank, bool &good)
 {
-    const int lane = threadIdx.x & 31, par = turn & 1;
-    if (nc == 1) {
-        const float2 h = pre.at(carry);
-        carry = all.at(carry);
-        return h;
-    }
-    if (good) {
-        good = wait_cluster(&ex.bar[par], (uint32_t)(turn >> 1) & 1, &ex.stop);
-        if (!good && lane < nc) {
-            uint32_t a;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&ex.stop)), "r"(lane));
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(1) : "memory");
-        }
-        __syncwarp();
-    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, par = turn & 1;
     float2 h = carry, mine = carry;
-#pragma unroll
-    for (int j = 0; j < MAX; j += 4) {
-        if (j >= nc) break;
-        Lin l[4];  // loaded before they are needed one after the other
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l[i] = j + i < nc ? ld_lin(&ex.block[par][BACK ? nc - 1 - j - i : j + i][lane]) : lin_identity();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if ((BACK ? nc - 1 - j - i : j + i) == rank) mine = h;
-            h = l[i].at(h);
+    if (nc > 1) {
+        if (good) {
+            good = wait_cluster(&ex.bar[par], (uint32_t)(turn >> 1) & 1, &ex.stop);
+            if (!good && lane < nc) {
+                uint32_t a;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&ex.stop)), "r"(lane));
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(1) : "memory");
+            }
+            __syncwarp();
         }
+#pragma unroll
+        for (int j = 0; j < MAX; j += 4) {
+            if (j >= nc) break;
+            Lin l[4];  // loaded before they are needed one after the other
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[i] = j + i < nc ? ld_lin(&ex.block[par][BACK ? nc - 1 - j - i : j + i][lane]) : lin_identity();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((BACK ? nc - 1 - j - i : j + i) == rank) mine = h;
+                h = l[i].at(h);
+            }
+        }
+        carry = h;
+        h = mine;
     }
-    carry = h;
-    return pre.at(mine);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {  // from the block's first token to this warp's, without a cluster to the window's end
+        const int w = BACK ? W - 1 - i : i;
+        if (w == warp) mine = h;
+        if (nc == 1 || (BACK ? w > warp : w < warp)) h = ld_lin(&ex.warp[par][w][lane]).at(h);
+    }
+    if (nc == 1) carry = h;
+    return mine;
 }
 // What the pairs q0 .. q1 - 1 of a split sequence make of `carry` (BACK: from the last of them on). Each warp folds its share of them;
 // all threads of the block take part, before its first window.
@@ -283,6 +299,8 @@ __global__ void __launch_bounds__(32 * kPairWarps) glr_pairs_kernel(const __grid
         __syncwarp();
         const unsigned char *a = tile + stage * kTiles * Tl::kBytes;
         const int nv = min(kChunk, t1 - t);
+        Decays d;
+        Lin some = lin_identity();
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
             if (i < nv) {
@@ -290,15 +308,22 @@ __global__ void __launch_bounds__(32 * kPairWarps) glr_pairs_kernel(const __grid
                     const float2 e = expm1_neg(f2_mul(ch.nA, rcp2(f2_add(neg_exp(Tl::get(a, i), ch.ca), f2(1.f)))));
                     float2 dh = Tl::get(a + Tl::kBytes, i);
                     if (G) dh = f2_mul(dh, silu2(Tl::get(a + 2 * Tl::kBytes, i)));
-                    own.A = f2_fma(own.A, e, own.A);
-                    own.H = f2_fma(own.A, dh, own.H);
+                    d.add(e);
+                    some.H = f2_fma(d.A, dh, some.H);
                 } else {
                     float2 e, u2;
                     gates(ch, Tl::get(a + Tl::kBytes, i), Tl::get(a, i), Tl::get(a + 2 * Tl::kBytes, i), e, u2);
-                    own.H = step(own.H, e, u2);
-                    own.A = f2_fma(own.A, e, own.A);
+                    some.H = step(some.H, e, u2);
+                    d.add(e);
                 }
             }
+        some.v = d.v();
+        if (BACK) {  // what lies behind comes first
+            some.then(own);
+            own = some;
+        } else {
+            own.then(some);
+        }
         __syncwarp();
     }
     cp_async_wait_all();
@@ -394,6 +419,7 @@ __global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const 
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
+                Decays d;
                 all_gates<T>(ch, tx, ta, tb, e, u);
                 if (nv < kChunk)
 #pragma unroll
@@ -403,12 +429,12 @@ __global__ void __launch_bounds__(32 * W, kScanPerSm / W) glr_scan_kernel(const 
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {
                     own.H = step(own.H, e[i], u[i]);
-                    own.A = f2_fma(own.A, e[i], own.A);
+                    d.add(e[i]);
                 }
+                own.v = d.v();
             }
-            Lin all;
-            const Lin pre = post<false>(ex, own, all, k, nc, rank, good);
-            float2 h = meet<false>(ex, pre, all, carry, k, nc, rank, good);
+            post<false>(ex, own, k, nc, rank, good);
+            float2 h = meet<false>(ex, carry, k, nc, rank, good);
             if (nv > 0) {
                 if (live) {
                     if (st) *reinterpret_cast<float2 *>(st + (size_t)(t / kChunk) * p.D) = h;
@@ -462,7 +488,7 @@ cudaError_t launch_scan_t(const Args &p, const int32_t *cu, int dev, int sms, cu
 // too. What a token's gradients need beside it is the state before it, which a warp walks again from the one that the
 // forward kept for its 16 tokens. A cluster has the sequences (or their parts) group, group + groups, .. and adds up its tokens' shares of
 // the parameters' gradients in registers: one row of partial sums a block. 8192 tokens of 4096 channels in BF16 with an output gate:
-// 190 us (569 MB, 3.0 TB/s), by latency and instructions (half of them issued) of 12 warps an SM.
+// 203 us (569 MB, 2.8 TB/s; 190 with A alone), by latency and instructions (half of them issued) of 12 warps an SM.
 template <typename T, bool G, int W>
 __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
 {
@@ -531,6 +557,7 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
             __syncwarp();
             Lin own = lin_identity();
             if (nv > 0) {
+                Decays d;
                 all_gates<T>(ch, tx, ta, tb, e, u);
                 if (nv < kChunk)
 #pragma unroll
@@ -542,11 +569,11 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
                     if (G) dh = f2_mul(dh, silu2(Tile<T>::get(tg, i)));
                     own.H = f2_add(own.H, dh);
                     own.H = f2_fma(e[i], own.H, own.H);
-                    own.A = f2_fma(own.A, e[i], own.A);
+                    d.add(e[i]);
                 }
+                own.v = d.v();
             }
-            Lin all;
-            const Lin pre = post<true>(ex, own, all, turn, nc, rank, good);
+            post<true>(ex, own, turn, nc, rank, good);
             if (nv > 0) {
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {  // u: the state before the token
@@ -555,7 +582,7 @@ __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const 
                     u[i] = before;
                 }
             }
-            float2 lc = meet<true>(ex, pre, all, carry, turn, nc, rank, good);
+            float2 lc = meet<true>(ex, carry, turn, nc, rank, good);
             if (nv > 0) {
                 const int64_t r = (int64_t)s0 + t + nv - 1;
                 T *dxp = static_cast<T *>(p.rows.dx) + r * p.rows.dx_stride + c, *dap = static_cast<T *>(p.rows.da) + r * p.rows.da_stride + c;
