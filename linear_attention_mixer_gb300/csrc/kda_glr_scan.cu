@@ -114,9 +114,19 @@ __device__ __forceinline__ void post(Exchange<W, MAX> &ex, const Lin &own, int t
     if (nc == 1) return;
     if (turn == 0) cluster_wait();  // every block of the cluster runs and has its barriers: theirs is the arrival at the start
     if (warp != (turn + (int)blockIdx.x) % W || !good) return;
-    Lin all = ld_lin(&ex.warp[par][BACK ? W - 1 : 0][lane]);
+    static_assert(W == 1 || W % 4 == 0, "one warp, or whole groups of four");
+    Lin all = ld_lin(&ex.warp[par][0][lane]);
 #pragma unroll
-    for (int i = 1; i < W; ++i) all.then(ld_lin(&ex.warp[par][BACK ? W - 1 - i : i][lane]));
+    for (int i = 0; i + 4 <= W; i += 4) {  // four at a time in pairs: one after the other spilled registers with an output gate
+        Lin l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) l[j] = ld_lin(&ex.warp[par][BACK ? W - 1 - i - j : i + j][lane]);
+        l[0].then(l[1]);
+        l[2].then(l[3]);
+        l[0].then(l[2]);
+        if (i == 0) all = l[0];
+        else all.then(l[0]);
+    }
     for (int r = 0; r < nc; ++r) st_remote(&ex.block[par][rank][lane], &ex.bar[par], r, as_float4(all));
 }
 template <bool BACK, int W, int MAX>
