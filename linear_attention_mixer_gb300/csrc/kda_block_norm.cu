@@ -607,10 +607,11 @@ bool row_ok(const char *name, const void *ptr, int64_t stride, int64_t M, int32_
 {
     const int align = esize == 1 ? 8 : 16;
     if (!ptr) return fail(KDA_ERR_INVALID, "%s is NULL", name), false;
-    if (M > 1 && stride < D) return fail(KDA_ERR_INVALID, "%s_stride must be >= %d (got %lld)", name, D, (long long)stride), false;
-    if (stride < 0 || stride > ((int64_t)1 << 38) || (stride > 0 && M > ((int64_t)1 << 60) / stride))
-        return fail(KDA_ERR_INVALID, "%s_stride out of range (%lld)", name, (long long)stride), false;
     if (reinterpret_cast<uintptr_t>(ptr) % align) return fail(KDA_ERR_INVALID, "%s must be %d-byte aligned", name, align), false;
+    if (M == 1) return true;  // the distance between rows is not used
+    if (stride < D) return fail(KDA_ERR_INVALID, "%s_stride must be >= %d (got %lld)", name, D, (long long)stride), false;
+    if (stride > ((int64_t)1 << 38) || M > ((int64_t)1 << 60) / stride)
+        return fail(KDA_ERR_INVALID, "%s_stride out of range (%lld)", name, (long long)stride), false;
     if ((stride * esize) % align)
         return fail(KDA_ERR_INVALID, "%s_stride must be a multiple of %d elements (got %lld)", name, align / esize, (long long)stride), false;
     return true;

@@ -108,10 +108,11 @@ bool row_ok(const char *name, const void *ptr, int64_t stride, int64_t T, const 
 {
     const int e = c->io_dtype == KDA_BF16 ? 2 : 4;
     if (!ptr) return fail(KDA_ERR_INVALID, "%s is NULL", name), false;
-    if (T > 1 && stride < c->dim)
-        return fail(KDA_ERR_INVALID, "%s_stride must be >= %d (got %lld)", name, c->dim, (long long)stride), false;
-    if (stride < 0 || stride > ((int64_t)1 << 38) || (stride > 0 && T > ((int64_t)1 << 60) / stride)) return fail(KDA_ERR_INVALID, "%s_stride out of range (%lld)", name, (long long)stride), false;
     if (reinterpret_cast<uintptr_t>(ptr) % 16) return fail(KDA_ERR_INVALID, "%s must be 16-byte aligned", name), false;
+    if (T == 1) return true;  // the distance between tokens is not used
+    if (stride < c->dim)
+        return fail(KDA_ERR_INVALID, "%s_stride must be >= %d (got %lld)", name, c->dim, (long long)stride), false;
+    if (stride > ((int64_t)1 << 38) || T > ((int64_t)1 << 60) / stride) return fail(KDA_ERR_INVALID, "%s_stride out of range (%lld)", name, (long long)stride), false;
     if ((stride * e) % 16) return fail(KDA_ERR_INVALID, "%s_stride must be a multiple of %d elements (got %lld)", name, 16 / e, (long long)stride), false;
     return true;
 }
