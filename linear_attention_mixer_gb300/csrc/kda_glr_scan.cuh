@@ -102,9 +102,9 @@ inline size_t split_bytes(int32_t N, int64_t slabs)
 }
 
 // choose_cluster, and whether each sequence is split into parts that run at once: where that pays for reading the rows twice, by
-// the same estimate. The pairs' kernel takes a start (300), its blocks' 16 tokens one after the other, and the fold.
-//   65536 tokens in BF16: 64 channels 27 us, in one part 137   256: 70, 139   1024: 205, 220   8192 tokens: 64: 19, 21   256: 21, 21
-//   (with the backward 65536: 68, 426   206, 453   8192: 38, 61   46, 61)
+// the same estimate. The pairs' kernel takes a start, its blocks' 16 tokens one after the other, and the fold.
+//   65536 tokens in BF16: 64 channels 31 us, in one part 141   256: 74, 143   1024: 225, 223   8192 tokens: 64: 21, 22.6
+//   (with the backward 65536: 72, 441   217, 467   8192: 41, 64); not taken: 8192 tokens of 256 channels, 24.6 for 22.6
 template <typename Room>
 inline int choose_parts(const int32_t *cu, int32_t N, int32_t groups, int64_t slabs, int tile, int most, int sms, bool back, Split &split, Room room)
 {
@@ -128,7 +128,7 @@ inline int choose_parts(const int32_t *cu, int32_t N, int32_t groups, int64_t sl
             clusters += (8 * (int64_t)n < longest / parts ? 0 : in < parts ? in : parts) * slabs;
             blocks += (of < subs ? of : subs) * slabs;
         }
-        const double pairs = 500 + sub / 128 * (110.0 + 64.0 * blocks / sms) + 3.0 * subs;
+        const double pairs = 600 + sub / 128 * (110.0 + 64.0 * blocks / sms) + 3.0 * subs;
         for (int nc = 1; nc <= most; nc *= 2) {
             if (N * parts * slabs * nc > kMaxShared || clusters > room(nc)) continue;
             const int path = ((plen > longest - (parts - 1) * plen ? plen : longest - (parts - 1) * plen) + tile * nc - 1) / (tile * nc);
