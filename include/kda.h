@@ -492,8 +492,9 @@ kda_status kda_gdr_prefill(const kda_gdr_config_t *cfg, const kda_gdr_params *pa
  *   gk = -exp(A_log) sigmoid(a + a_bias),  alpha = exp(gk),  beta = sigmoid(b + b_bias)
  *   h = alpha h + sqrt(1 - alpha^2) beta x,  out = h, or with an output gate h silu(g)
  * a = -inf keeps the state as it is (alpha = 1), b = -inf lets nothing in; exp(A_log) must be finite in FP32, and a sigmoid
- * below 2^-126 counts as 0. What is not finite in a row reaches no earlier token, no other channel and no other sequence
- * (a state that has become infinite stays infinite or becomes NaN).
+ * below 2^-126 counts as 0. A token's step rounds h + ((alpha - 1) h + u): however small alpha, it is off by up to 2^-24 of
+ * the state before it. What is not finite in a row reaches no earlier token, no other channel and no other sequence (a state that
+ * has become infinite stays infinite or becomes NaN).
  *
  * States are caller-owned, device FP32 [max_slots][dim], 16-byte aligned, read and written by slots as the gated delta
  * rule's are (src_slots, dst_slots, err with KDA_ERR_TIMEOUT too; KDA_ERR_DEVICE also where a sequence's bounds in cu_seqlens do not rise within

@@ -144,8 +144,9 @@ __device__ __forceinline__ float min_nan(float a, float b)  // NaN if either is
 constexpr float kLog2e = 1.4426950408889634f;
 
 // exp(x) - 1 for x <= 0. Above -1/4 it is x q(x), q of degree 4 (Chebyshev interpolation of (exp(x) - 1) / x on [-1/4, 0]; its
-// error is 2.6e-9), to a few 2^-24 however near to 0. Below, the difference loses no more than two bits of the exponential.
-// NaN stays. (Reducing x to k ln 2 + r and a q of degree 5 on |r| <= ln 2 / 2, without the exponential, takes four instructions
+// error is 2.6e-9), to a few 2^-24 however near to 0. Below, the difference loses no more than two bits of the exponential: alpha is
+// off by 2.1 x 2^-24 at most and 0.6 x 2^-24 in the root mean square (measured over x from -20 to -0.2), and is there remembered for no
+// more than four tokens. NaN stays. (Reducing x to k ln 2 + r and a q of degree 5 on |r| <= ln 2 / 2, without the exponential, takes four instructions
 // more for each channel: 65536 tokens of 4096 channels 535 us for 516.)
 __device__ __forceinline__ float2 expm1_neg(float2 x)
 {

@@ -8,9 +8,9 @@
 // then each warp walks its tokens from the state that it now knows, with e and u still in registers. The rows are read
 // once. No block waits for one of another cluster.
 //
-// 65536 tokens of 4096 channels in BF16: 531 us, 4.0 TB/s (506 with A alone, which is wrong for states that are kept long). Instructions,
+// 65536 tokens of 4096 channels in BF16: 529 us, 4.0 TB/s (506 with A alone, which is wrong for states that are kept long). Instructions,
 // special functions and the FP32 pipe and the latency of a window's exchange share it, on 3.4 of the 4 blocks that an SM has room
-// for. Eight sequences of 0 to 2048 tokens, 7168 channels in FP32: 99 us, 5.5 TB/s. With 8 tokens a warp (and 24 warps an SM)
+// for. Eight sequences of 0 to 2048 tokens, 7168 channels in FP32: 97 us, 5.6 TB/s. With 8 tokens a warp (and 24 warps an SM)
 // the first took 670 us where 16 took 566.
 #include "kda_glr_scan.cuh"
 
@@ -48,7 +48,7 @@ __device__ __forceinline__ bool wait_cluster(const uint64_t *bar, uint32_t parit
 // ---------------------------------------------------------------- pairs
 // h -> A h + H. What is held of A is v: A - 1 (below 0) where A >= 1/2, else A. Near 1, where a state is kept over many pairs,
 // A itself in FP32 would be wrong by 2^-25 at each with a sign that a steady decay repeats (65536 tokens of 1 - alpha = 1e-6 to
-// 1e-7: states off by 1e-3; so, by 6e-7); near 0 a difference from 1 would leave 2^-24 of a state that has gone.
+// 1e-7: states off by 1e-3; held so, by 6e-7); near 0 a difference from 1 would leave 2^-24 of a state that has gone.
 constexpr float kKept = -0x1p-100f;  // v where A is 1: it changes no h, and is below 0
 constexpr float kForm = -0x1p110f;
 __device__ __forceinline__ float2 form(float2 v) { return make_float2(__saturatef(v.x * kForm), __saturatef(v.y * kForm)); }  // 1 for A - 1, 0 for A
@@ -498,7 +498,7 @@ cudaError_t launch_scan_t(const Args &p, const int32_t *cu, int dev, int sms, cu
 // too. What a token's gradients need beside it is the state before it, which a warp walks again from the one that the
 // forward kept for its 16 tokens. A cluster has the sequences (or their parts) group, group + groups, .. and adds up its tokens' shares of
 // the parameters' gradients in registers: one row of partial sums a block. 8192 tokens of 4096 channels in BF16 with an output gate:
-// 203 us (569 MB, 2.8 TB/s; 190 with A alone), by latency and instructions (half of them issued) of 12 warps an SM.
+// 199 us (569 MB, 2.9 TB/s; 190 with A alone), by latency and instructions (half of them issued) of 12 warps an SM.
 template <typename T, bool G, int W>
 __global__ void __launch_bounds__(32 * W, kBackPerSm / W) glr_back_kernel(const __grid_constant__ BackArgs p, int nc)
 {

@@ -10,8 +10,10 @@ namespace kda {
 namespace glr {
 
 constexpr int kBackWarps = 4;                        // warps of a block: 64 tokens
-constexpr int kScanPerSm = 16, kBackPerSm = 12;      // warps that an SM's registers hold (128 and 168 a thread)
-// Warps of a prefill's block. FP32 rows fill shared memory with two blocks of eight; BF16 rows are faster in four of four
+// Warps that an SM's registers hold (128 and 168 a thread). With BF16 rows that many run; FP32 rows fill shared memory before: 16 in a
+// prefill without an output gate, 8 with one (131 KB of rows a block), 8 in a backward.
+constexpr int kScanPerSm = 16, kBackPerSm = 12;
+// Warps of a prefill's block: eight with FP32 rows, two blocks an SM without an output gate; BF16 rows are faster in four blocks of four
 // (65536 tokens of 4096 channels 569 us where two of eight took 597).
 template <typename T> constexpr int scan_warps() { return sizeof(T) == 4 ? 8 : 4; }
 // Blocks of a cluster at most. FP32 rows leave no room in shared memory for the pairs of more than 8.
@@ -159,8 +161,8 @@ inline int64_t back_parts(int32_t N, int64_t slabs)
 // Whether a thread takes each sequence of a prefill from end to end (kda_glr_walk.cu), by estimates in microseconds that were
 // fitted to both: 0.17 a token of the longest sequence, or 400 (FP32: 300) channels of a token a ns, against a block's start
 // for every sequence's 64 channels and 500 (234) channels a ns. Both sides, sequences of 0 to n tokens in BF16 with a gate:
-//   300 of 1024 channels  n = 16: 11 us, scan 30   64: 40, 47   128: 77, 72      30 of 256  n = 16: 5.2, 5.6   64: 12, 6
-//   4000 of 4096 channels n = 2: 220 us, scan 1177   16: 464, 1629   64: 1345, 2130    FP32, 300 of 1024: 64: 48, 142
+//   300 of 1024 channels  n = 16: 12 us, scan 33   64: 41, 49   (128: 77, 73)      30 of 256  n = 16: 6.3, 8.2   (64: 12, 8.2)
+//   4000 of 4096 channels n = 2: 225 us, scan 1248   16: 477, 1710   64: 1378, 2240    FP32, 300 of 1024: 64: 50, 147
 inline bool short_sequences(const int32_t *cu, int32_t N, int32_t D, bool f32)
 {
     const double longest = longest_of(cu, N), work = (double)cu[N] * D * 1e-3;
@@ -173,8 +175,8 @@ cudaError_t launch_walk(const Args &p, bool f32, cudaStream_t s);
 
 // Whether a block of a backward has one warp: where no sequence has more than a warp's 16 tokens, or where they are short and
 // many enough to fill the GPU so (12 a SM). Sequences of 0 to n tokens, BF16 with a gate:
-//   300 of 4096 channels n = 8: 90 us, four warps 194   32: 171, 284   64: 287, 346   128: 508, 552
-//   30 of 1024 channels  n = 16: 9.4 us, four warps 10.3   32: 13, 10   64: 24, 12
+//   300 of 4096 channels n = 8: 82 us, four warps 193   32: 172, 286   64: 292, 357   (128: 578 with four)
+//   30 of 1024 channels  n = 16: 12.3 us, four warps 12.4   (32: 16.4 with four; 64: 17.6)
 inline bool one_warp(const int32_t *cu, int32_t N, int64_t slabs, int sms)
 {
     const int32_t longest = longest_of(cu, N);
